@@ -1,0 +1,111 @@
+// qmv_step.cuh -- declarations of the verification-step operators: the 4-bit
+// matvec with group scales and zero points (qmv_w4.cu), the norms between two
+// blocks (qmv_norm.cu), and logits to probabilities to accepted tokens
+// (qmv_sample.cu).  Arguments are checked in qmv_step_abi.cu.
+#pragma once
+#include <cuda_bf16.h>
+
+#include "qmv_internal.cuh"
+
+#define QMV_W4_MAGIC 0x514D3450u
+
+struct qmv_w4pack {
+  uint32_t magic;
+  int N, K, group, scale_bf16, zeros;
+  int G;                      // groups per row: ceil(K / group)
+  size_t bytes;
+  const uint8_t* d_packed;    // bound by qmv_w4_pack or qmv_w4_bind
+};
+
+namespace qmv {
+namespace w4 {
+
+// The packed layout (qmv.h): blocks of ROWS x BK codes, strips of ROWS rows,
+// the blocks of a strip one after another in k.
+constexpr int ROWS = 32, BK = 128, CODE_BYTES = ROWS * BK / 2;
+
+__host__ __device__ constexpr int block_bytes(int group, bool zeros) {
+  return CODE_BYTES + (BK / group) * ROWS * (zeros ? 3 : 2);
+}
+__host__ __device__ constexpr int cdiv(int a, int b) { return (a + b - 1) / b; }
+
+// Where row r (0..31) of a block keeps its scale and zero point inside a
+// group's 32: the four rows that one lane of a warp holds (g, g + 8, g + 16,
+// g + 24 for g = lane / 4) lie side by side.
+__host__ __device__ constexpr int meta_slot(int r) { return (r & 7) * 4 + (r >> 3); }
+
+struct GemvArgs4 {
+  const uint8_t* packed;
+  int N, K, scale_bf16, group, zeros;
+  int M;
+  const void* x;
+  int ldx, x_bf16;
+  void* y;
+  int ldy, y_dtype;
+};
+
+cudaError_t launch_w4_pack(const qmv_w4pack& p, const uint8_t* codes, const uint16_t* scales,
+                           const uint8_t* zeros, uint8_t* packed, cudaStream_t s);
+cudaError_t launch_w4_unpack(const qmv_w4pack& p, uint8_t* codes, cudaStream_t s);
+cudaError_t launch_w4_gemv(const GemvArgs4& a, cudaStream_t s);
+
+}  // namespace w4
+
+struct NormArgs {
+  int M, D;
+  const void* y;
+  int ldy, y_dtype;
+  const void* r;
+  int ldr;
+  const void *gamma_post, *gate;
+  int ldg;
+  float rs, bs;
+  const void* gamma_pre;
+  float goff, eps;
+  void* h;
+  int ldh;
+  void* out;
+  int ldo;
+  int bf16;
+};
+cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t s);
+
+struct SoftmaxArgs {
+  int rows, V;
+  const void* x;
+  int ldx, dtype;
+  const float* t;
+  float t0;
+  float* out;
+  int ldo;
+};
+cudaError_t launch_softmax(const SoftmaxArgs& a, cudaStream_t s);
+
+struct VerifyArgs {
+  int B, S, V;
+  const float *p, *q;
+  const int *draft, *n_draft;
+  const float *ua, *us;
+  int *tokens, *n_acc;
+};
+cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s);
+
+// 16-bit elements as fp32 and back (round to nearest even).
+template <typename T>
+__device__ __forceinline__ float to_f(T v);
+template <>
+__device__ __forceinline__ float to_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f<__half>(__half v) { return __half2float(v); }
+template <>
+__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+}  // namespace qmv

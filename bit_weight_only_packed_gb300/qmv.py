@@ -23,7 +23,7 @@ QMV_ERR_SHAPE = -4
 QMV_ERR_CUDA = -5
 QMV_ERR_TIMEOUT = -6
 QMV_ERR_WORKSPACE = -7
-QMV_F32, QMV_F16 = 0, 1
+QMV_F32, QMV_F16, QMV_BF16 = 0, 1, 2
 QMV_FAST, QMV_EXACT = 0, 1
 QMV_PACK_HEADER_BYTES, QMV_PACK_VERSION = 64, 1
 
@@ -58,6 +58,18 @@ SIGNATURES = {
     "qmv_chain_run": (_I, [_P, _P]),
     "qmv_chain_info": (_I, [_P, ctypes.POINTER(_I), ctypes.POINTER(_I), ctypes.POINTER(_I)]),
     "qmv_chain_destroy": (_I, [_P]),
+    "qmv_w4_create": (_I, [ctypes.POINTER(_P), _I, _I, _I, _I, _I, _SZP]),
+    "qmv_w4_pack": (_I, [_P, _P, _P, _P, _P, _P]),
+    "qmv_w4_bind": (_I, [_P, _P]),
+    "qmv_w4_unpack": (_I, [_P, _P, _P]),
+    "qmv_w4_info": (_I, [_P, ctypes.POINTER(_I), ctypes.POINTER(_I), ctypes.POINTER(_I),
+                         ctypes.POINTER(_I), ctypes.POINTER(_I)]),
+    "qmv_w4_destroy": (_I, [_P]),
+    "qmv_w4_gemv": (_I, [_P, _I, _P, _I, _I, _P, _I, _I, _P]),
+    "qmv_block_norm": (_I, [_I, _I, _P, _I, _I, _P, _I, _P, _P, _I, _F, _F, _P, _F, _F, _P, _I, _P, _I, _I,
+                            _P]),
+    "qmv_softmax": (_I, [_I, _I, _P, _I, _I, _P, _F, _P, _I, _P]),
+    "qmv_verify_draft": (_I, [_I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
 }
 
 
@@ -437,3 +449,245 @@ class Chain:
             self.close()
         except Exception:
             pass
+
+
+# ------------------------------------------------- verification-step calls --
+# These take row strides, so a tensor may be any 2-D view whose rows are
+# contiguous; checks come first and raise ValueError before any call.
+
+_DTYPE = {torch.float32: QMV_F32, torch.float16: QMV_F16, torch.bfloat16: QMV_BF16}
+_TORCH = {v: k for k, v in _DTYPE.items()}
+_16BIT = (torch.float16, torch.bfloat16)
+_FLOAT = (torch.float32, torch.float16, torch.bfloat16)
+
+
+def _rows(name, t, dtypes, rows, cols):
+    """Row stride of a [rows, cols] tensor ([cols] will do for one row) of one
+    of dtypes, after checking that the kernels' reads and writes stay inside it."""
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.dim() == 2:
+        r, c = t.shape
+        ld, step = t.stride()
+    elif t.dim() == 1:
+        r, c, ld, step = 1, t.shape[0], t.shape[0], t.stride(0)
+    else:
+        raise ValueError(f"{name}: expected a [rows, columns] tensor, got {tuple(t.shape)}")
+    if r != rows or c != cols:
+        raise ValueError(f"{name}: expected [{rows}, {cols}], got {tuple(t.shape)}")
+    if c > 1 and step != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    if rows == 1:
+        return cols
+    if ld < cols or ld > 0x7fffffff:
+        raise ValueError(f"{name}: rows overlap or their stride {ld} is too large")
+    return ld
+
+
+def _vec(name, t, dtype, n):
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.numel() != n:
+        raise ValueError(f"{name}: needs {n} elements, has {t.numel()}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+
+
+def _place(first, *others):
+    """All tensors lie on the current CUDA device."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError("expected CUDA tensors")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors are on {dev} and {t.device}")
+
+
+def _fresh(shape, dtype, like, stream):
+    """A fresh output; one written on another stream than torch's current one is
+    recorded there, so the allocator does not hand it out again too early."""
+    t = torch.empty(shape, dtype=dtype, device=like.device)
+    if stream is not None:
+        cur = torch.cuda.current_stream(like.device)
+        if _stream(stream) != cur.cuda_stream:
+            t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
+                            torch.cuda.ExternalStream(int(stream), device=like.device))
+    return t
+
+
+class W4Pack:
+    """4-bit weights with a scale and (optionally) a zero point a group: the host
+    descriptor plus the device buffer that holds the packed bytes."""
+
+    def __init__(self, N: int, K: int, group: int = 128, scale_dtype=torch.float16, zeros: bool = True):
+        if scale_dtype not in _16BIT:
+            raise ValueError(f"scale_dtype: expected torch.float16 or torch.bfloat16, got {scale_dtype}")
+        self.handle = None
+        h, nb = _P(), ctypes.c_size_t()
+        _check("qmv_w4_create", _lib.qmv_w4_create(ctypes.byref(h), N, K, group, _DTYPE[scale_dtype],
+                                                   1 if zeros else 0, ctypes.byref(nb)))
+        self.handle = h
+        self.N, self.K, self.group, self.G = N, K, group, -(-K // group)
+        self.scale_dtype, self.zeros = scale_dtype, bool(zeros)
+        self.packed_bytes = nb.value
+        self.packed = None
+
+    def pack_weights(self, codes, scales, zeros=None, stream=None):
+        """codes: device uint8 [N, K], 0..15; scales: device fp16/bf16 [N, K/group];
+        zeros: device uint8 [N, K/group] where the pack has zero points."""
+        _vec("codes", codes, torch.uint8, self.N * self.K)
+        _vec("scales", scales, self.scale_dtype, self.N * self.G)
+        if self.zeros != (zeros is not None):
+            raise ValueError("zeros: given exactly when the pack has zero points")
+        if zeros is not None:
+            _vec("zeros", zeros, torch.uint8, self.N * self.G)
+        _place(codes, scales, zeros)
+        packed = _fresh((self.packed_bytes,), torch.uint8, codes, stream)
+        _check("qmv_w4_pack", _lib.qmv_w4_pack(self.handle, codes.data_ptr(), scales.data_ptr(),
+                                               None if zeros is None else zeros.data_ptr(), packed.data_ptr(),
+                                               _stream(stream)))
+        self.packed = packed
+        return self
+
+    def bind_packed(self, packed):
+        """packed: a device uint8 buffer with the packed bytes of this shape."""
+        _vec("packed", packed, torch.uint8, self.packed_bytes)
+        _place(packed)
+        _check("qmv_w4_bind", _lib.qmv_w4_bind(self.handle, packed.data_ptr()))
+        self.packed = packed
+        return self
+
+    def unpack_codes(self, stream=None):
+        if self.packed is None:
+            raise ValueError("the pack holds no weights yet")
+        _place(self.packed)
+        out = _fresh((self.N, self.K), torch.uint8, self.packed, stream)
+        _check("qmv_w4_unpack", _lib.qmv_w4_unpack(self.handle, out.data_ptr(), _stream(stream)))
+        return out
+
+    def info(self):
+        """(N, K, group, scale dtype, has zero points) as the library holds them."""
+        v = [_I() for _ in range(5)]
+        _check("qmv_w4_info", _lib.qmv_w4_info(self.handle, *map(ctypes.byref, v)))
+        n, k, g, d, z = (i.value for i in v)
+        return n, k, g, _TORCH[d], bool(z)
+
+    def close(self):
+        if self.handle is not None and self.handle.value:
+            _lib.qmv_w4_destroy(self.handle)
+        self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def qmv_w4_gemv(p: W4Pack, x, y=None, y_dtype=QMV_F32, stream=None):
+    """y [M, N] = x [M, K] . W^T for a W4Pack; x is fp16 or bf16 ([K] counts as M = 1)."""
+    M = x.shape[0] if x.dim() == 2 else 1
+    ldx = _rows("x", x, _16BIT, M, p.K)
+    if p.packed is None:
+        raise ValueError("the pack holds no weights yet")
+    if y_dtype not in _TORCH:
+        raise ValueError(f"y_dtype: unknown value {y_dtype!r}")
+    ldy = p.N if y is None else _rows("y", y, (_TORCH[y_dtype],), M, p.N)
+    _place(x, p.packed, y)
+    if y is None:
+        y = _fresh((M, p.N), _TORCH[y_dtype], x, stream)
+    _check("qmv_w4_gemv", _lib.qmv_w4_gemv(p.handle, M, x.data_ptr(), ldx, _DTYPE[x.dtype], y.data_ptr(), ldy,
+                                           y_dtype, _stream(stream)))
+    return y
+
+
+def qmv_block_norm(y, residual, gamma_pre, gamma_post=None, gate=None, residual_scale=1.0, branch_scale=1.0,
+                   gamma_offset=0.0, eps=1e-6, h_out=None, out=None, stream=None):
+    """(h, out): h = residual_scale * residual + branch_scale * gate * norm(y), out
+    = norm(h); the first norm where gamma_post is given, the gate [D] or [M, D]."""
+    if residual.dim() not in (1, 2):
+        raise ValueError(f"residual: expected a [rows, columns] tensor, got {tuple(residual.shape)}")
+    dt = residual.dtype
+    M, D = (1, residual.shape[0]) if residual.dim() == 1 else residual.shape
+    ldr = _rows("residual", residual, _16BIT, M, D)
+    ldy = _rows("y", y, _FLOAT, M, D)
+    _vec("gamma_pre", gamma_pre, dt, D)
+    ldg = 0
+    if gamma_post is not None:
+        _vec("gamma_post", gamma_post, dt, D)
+    if gate is not None:
+        if gate.dim() == 1:
+            _vec("gate", gate, dt, D)
+        else:
+            ldg = _rows("gate", gate, (dt,), M, D)
+    ldh = D if h_out is None else _rows("h_out", h_out, (dt,), M, D)
+    ldo = D if out is None else _rows("out", out, (dt,), M, D)
+    _place(y, residual, gamma_pre, gamma_post, gate, h_out, out)
+    if h_out is None:
+        h_out = _fresh((M, D), dt, y, stream)
+    if out is None:
+        out = _fresh((M, D), dt, y, stream)
+    _check("qmv_block_norm", _lib.qmv_block_norm(
+        M, D, y.data_ptr(), ldy, _DTYPE[y.dtype], residual.data_ptr(), ldr,
+        None if gamma_post is None else gamma_post.data_ptr(), None if gate is None else gate.data_ptr(), ldg,
+        residual_scale, branch_scale, gamma_pre.data_ptr(), gamma_offset, eps, h_out.data_ptr(), ldh,
+        out.data_ptr(), ldo, _DTYPE[dt], _stream(stream)))
+    return h_out, out
+
+
+def qmv_softmax(logits, temperature=1.0, out=None, stream=None):
+    """fp32 probabilities [rows, V] of logits at a temperature (a number, or a
+    device fp32 tensor [rows]); out may be the fp32 logits themselves."""
+    if logits.dim() not in (1, 2):
+        raise ValueError(f"logits: expected a [rows, columns] tensor, got {tuple(logits.shape)}")
+    rows, V = (1, logits.shape[0]) if logits.dim() == 1 else logits.shape
+    ldl = _rows("logits", logits, _FLOAT, rows, V)
+    t, t0 = None, 1.0
+    if torch.is_tensor(temperature):
+        t = temperature
+        _vec("temperature", t, torch.float32, rows)
+    else:
+        t0 = float(temperature)
+    ldo = V if out is None else _rows("out", out, (torch.float32,), rows, V)
+    _place(logits, t, out)
+    if out is None:
+        out = _fresh((rows, V), torch.float32, logits, stream)
+    _check("qmv_softmax", _lib.qmv_softmax(rows, V, logits.data_ptr(), ldl, _DTYPE[logits.dtype],
+                                           None if t is None else t.data_ptr(), t0, out.data_ptr(), ldo,
+                                           _stream(stream)))
+    return out
+
+
+def qmv_verify_draft(target, draft_probs, draft, u_accept, u_sample, n_draft=None, tokens=None, n_accepted=None,
+                     stream=None):
+    """(tokens [B, S+1], n_accepted [B]): target fp32 [B, S+1, V], draft_probs
+    fp32 [B, S, V] or None (a drafter that is sure of its tokens), draft int32
+    [B, S], u_accept fp32 [B, S], u_sample fp32 [B], n_draft int32 [B] or None."""
+    if target.dim() != 3 or target.shape[1] < 1:
+        raise ValueError(f"target: expected [B, S+1, V], got {tuple(target.shape)}")
+    B, S1, V = target.shape
+    S = S1 - 1
+    _vec("target", target, torch.float32, B * S1 * V)
+    if draft_probs is not None:
+        _vec("draft_probs", draft_probs, torch.float32, B * S * V)
+    _vec("draft", draft, torch.int32, B * S)
+    _vec("u_accept", u_accept, torch.float32, B * S)
+    _vec("u_sample", u_sample, torch.float32, B)
+    if n_draft is not None:
+        _vec("n_draft", n_draft, torch.int32, B)
+    if tokens is not None:
+        _vec("tokens", tokens, torch.int32, B * S1)
+    if n_accepted is not None:
+        _vec("n_accepted", n_accepted, torch.int32, B)
+    _place(target, draft_probs, draft, u_accept, u_sample, n_draft, tokens, n_accepted)
+    if tokens is None:
+        tokens = _fresh((B, S1), torch.int32, target, stream)
+    if n_accepted is None:
+        n_accepted = _fresh((B,), torch.int32, target, stream)
+    _check("qmv_verify_draft", _lib.qmv_verify_draft(
+        B, S, V, target.data_ptr(), None if draft_probs is None else draft_probs.data_ptr(), draft.data_ptr(),
+        None if n_draft is None else n_draft.data_ptr(), u_accept.data_ptr(), u_sample.data_ptr(),
+        tokens.data_ptr(), n_accepted.data_ptr(), _stream(stream)))
+    return tokens, n_accepted

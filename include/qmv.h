@@ -76,6 +76,7 @@ extern "C" {
 
 typedef struct qmv_pack qmv_pack;   /* opaque host descriptor; owns no device memory */
 typedef struct qmv_chain qmv_chain; /* opaque host descriptor of a matvec chain */
+typedef struct qmv_w4pack qmv_w4pack; /* opaque host descriptor of 4-bit weights with zero points */
 
 typedef enum {
     QMV_OK = 0,
@@ -88,7 +89,9 @@ typedef enum {
     QMV_ERR_WORKSPACE = -7      /* the call needs a larger workspace (qmv_workspace_bytes) */
 } qmv_status;
 
-typedef enum { QMV_F32 = 0, QMV_F16 = 1 } qmv_dtype;      /* output element type */
+/* element types; QMV_BF16 is taken by the verification-step calls only (the
+ * qmv_w4_*, qmv_block_norm, qmv_softmax and qmv_verify_draft entry points) */
+typedef enum { QMV_F32 = 0, QMV_F16 = 1, QMV_BF16 = 2 } qmv_dtype;
 typedef enum { QMV_FAST = 0, QMV_EXACT = 1 } qmv_mode;    /* accumulation mode */
 
 /*
@@ -406,6 +409,156 @@ QMV_API int qmv_chain_info(const qmv_chain *c, int *n_ops, int *n_barriers, int 
 
 /* qmv_chain_destroy -- free the host descriptor (never the workspace). */
 QMV_API int qmv_chain_destroy(qmv_chain *c);
+
+/*
+ * The verification step of drafted tokens: a chunk of M = S + 1 tokens (S
+ * drafted ones and the last accepted one) goes through the blocks at once, and
+ * its logits decide how many of the drafted tokens stand ([A19] "The parked
+ * levers", the multi-token-prediction item; [PLAY] prefill-regimes table, S = 4
+ * chunks on the verify lane).  Four operators of that step: the matvec for
+ * 4-bit weights with a scale and a zero point a group, the norms between two
+ * blocks, logits to probabilities, and the verification itself.  These calls
+ * take row strides (ld*, in elements, at least the row's length), fp16 and
+ * bf16, and pointers aligned to their element; the conventions at the top of
+ * this file hold for the rest.  They keep no device state and need no
+ * workspace, so calls may overlap on several streams.
+ */
+
+/*
+ * qmv_w4_create -- describe 4-bit weights w[n][k] = (q[n][k] - z[n][g]) * s[n][g]
+ * with g = k / group.
+ *   N, K         output and input features; N >= 1, K >= 32, K % 32 == 0.
+ *   group        32, 64 or 128 consecutive k of a row (the last group of a row
+ *                is short where K is not a multiple).
+ *   scale_dtype  QMV_F16 or QMV_BF16.
+ *   has_zeros    0: symmetric weights, every z is 8.
+ *   packed_bytes (out, nullable) bytes the caller must allocate for the packed
+ *                weights, codes, scales and zero points together.
+ * Packed layout: blocks of 32 rows x 128 k, in k order within 32 rows.  A block
+ * holds its codes as the tensor cores read them (two 16-row halves, two 64-k
+ * tiles, 16 bytes for each lane of a warp), then its scales (groups x 32 x
+ * fp16/bf16), then its zero points (groups x 32 bytes).  Rows and k past the
+ * end are padded with zero scales.
+ * Errors: INVALID_ARG (out NULL, group or scale_dtype not allowed), SHAPE.
+ * Host only.
+ */
+QMV_API int qmv_w4_create(qmv_w4pack **out, int N, int K, int group, int scale_dtype,
+                          int has_zeros, size_t *packed_bytes);
+
+/*
+ * qmv_w4_pack -- pack on the device and bind the pack to d_packed.
+ *   d_codes_in   device uint8 [N][K], one code a byte, 0..15 (masked to 4 bits),
+ *                8-byte aligned.
+ *   d_scales_in  device fp16/bf16 [N][ceil(K/group)].
+ *   d_zeros_in   device uint8 [N][ceil(K/group)], 0..15 (masked); NULL exactly
+ *                when has_zeros was 0.
+ *   d_packed     device, packed_bytes, 16-byte aligned; the pack keeps it.
+ * Errors: INVALID_ARG, ALIGNMENT, CUDA.
+ */
+QMV_API int qmv_w4_pack(qmv_w4pack *p, const uint8_t *d_codes_in, const void *d_scales_in,
+                        const uint8_t *d_zeros_in, void *d_packed, void *stream);
+
+/* qmv_w4_bind -- bind a device buffer that already holds the packed bytes of
+ * this shape (as qmv_w4_pack left them).  Errors: INVALID_ARG, ALIGNMENT.  Host only. */
+QMV_API int qmv_w4_bind(qmv_w4pack *p, void *d_packed);
+
+/* qmv_w4_unpack -- the codes back as device uint8 [N][K] (a check of the
+ * layout, not on the hot path).  Errors: INVALID_ARG, CUDA. */
+QMV_API int qmv_w4_unpack(const qmv_w4pack *p, uint8_t *d_codes_out, void *stream);
+
+/* qmv_w4_info -- read back a pack's description (any out pointer may be NULL). */
+QMV_API int qmv_w4_info(const qmv_w4pack *p, int *N, int *K, int *group, int *scale_dtype,
+                        int *has_zeros);
+
+/* qmv_w4_destroy -- free the host descriptor (never the device buffer). */
+QMV_API int qmv_w4_destroy(qmv_w4pack *p);
+
+/*
+ * qmv_w4_gemv -- y[m][n] = sum_g s[n][g] * sum_{k in g} x[m][k] * (q[n][k] - z[n][g])
+ * for M columns.  q - z is exact in x's type, products are exact and sums are
+ * fp32 (tensor-core order inside a group, then over the groups); one rounding
+ * to y's type at the end.  Repeated calls give the same bits.
+ *   M        1 .. 4096.
+ *   x        device [M][K] of x_dtype (QMV_F16 or QMV_BF16, any mix with the
+ *            scales' type), row stride ldx.
+ *   y        device [M][N] of y_dtype, row stride ldy; must not overlap x.
+ * Errors: INVALID_ARG, SHAPE (ldx < K or ldy < N), ALIGNMENT, CUDA.
+ */
+QMV_API int qmv_w4_gemv(const qmv_w4pack *p, int M, const void *x, int ldx, int x_dtype, void *y,
+                        int ldy, int y_dtype, void *stream);
+
+/*
+ * qmv_block_norm -- from a block's output y to the next block's input, for M
+ * rows of D:
+ *   u = y;  with gamma_post: u = u / sqrt(mean(u^2) + eps) * (gamma_post + gamma_offset);
+ *   with gate: u = gate * u;
+ *   h = round(residual_scale * residual + branch_scale * u)          (h_out)
+ *   z = round(h / sqrt(mean(h^2) + eps) * (gamma_pre + gamma_offset)) (out)
+ * with every step in fp32 but the two roundings to dtype; the second norm takes
+ * h as it is stored, as qmv_fused_rmsnorm_gemv does.
+ *   y          device [M][D] of y_dtype (QMV_F32, QMV_F16 or QMV_BF16), row stride ldy.
+ *   residual   device [M][D] of dtype (QMV_F16 or QMV_BF16), row stride ldr.
+ *   gamma_post, gamma_pre  device [D] of dtype; gamma_post nullable.
+ *   gate       nullable device [M][D] of dtype, row stride ldg; ldg = 0 takes one
+ *              row [D] for every m.
+ *   h_out      nullable device [M][D] of dtype, row stride ldh; may be residual
+ *              itself (same pointer, ldh == ldr).
+ *   out        device [M][D] of dtype, row stride ldo.
+ *   D          1 .. 65536.  eps >= 0.
+ * out overlaps nothing; h_out overlaps nothing but residual as above.
+ * Errors: INVALID_ARG, SHAPE (a stride below D), UNSUPPORTED (D), ALIGNMENT, CUDA.
+ */
+QMV_API int qmv_block_norm(int M, int D, const void *y, int ldy, int y_dtype, const void *residual,
+                           int ldr, const void *gamma_post, const void *gate, int ldg,
+                           float residual_scale, float branch_scale, const void *gamma_pre,
+                           float gamma_offset, float eps, void *h_out, int ldh, void *out, int ldo,
+                           int dtype, void *stream);
+
+/*
+ * qmv_softmax -- rows of logits to probabilities:
+ * out[r][v] = exp((x[r][v] - max_r) / T_r) / sum_v exp((x[r][v] - max_r) / T_r).
+ *   logits  device [rows][V] of dtype (QMV_F32, QMV_F16 or QMV_BF16), row stride ldl.
+ *   d_temperature  nullable device fp32 [rows]: T_r; NULL takes `temperature`
+ *           for every row.  T = 0 gives 1 to the row's first maximum and 0 to
+ *           the rest; a negative or NaN T of d_temperature counts as 0.
+ *   out     device fp32 [rows][V], row stride ldo; may be logits itself (fp32,
+ *           same pointer, ldo == ldl).
+ * A logit of -inf gets 0; a row of nothing but -inf gets all zeros.  A row that
+ * holds NaN or +inf gives NaN in every place.
+ * Errors: INVALID_ARG (also temperature < 0 or NaN), SHAPE, ALIGNMENT, CUDA.
+ */
+QMV_API int qmv_softmax(int rows, int V, const void *logits, int ldl, int dtype,
+                        const float *d_temperature, float temperature, float *out, int ldo,
+                        void *stream);
+
+/*
+ * qmv_verify_draft -- verification of drafted tokens against the target's
+ * probabilities, for B sequences of n = n_draft[b] drafted tokens (S without
+ * n_draft; values are clamped to 0..S):
+ *   drafted token i stands while u_accept[b][i] * q_i(d_i) < p_i(d_i), compared
+ *   exactly; at the first that does not, j, the new token is drawn from
+ *   max(p_j - q_j, 0) (from p_j where that has no mass); with none refused, from p_n.
+ * The draw: each weight, clamped to 0..1, counts in whole units of 2^-42
+ * (truncated), T is their total, U = floor(2^31 * u_sample[b]), and the token is
+ * the lowest id whose running sum is above floor(U * T / 2^31).  Sums of whole
+ * numbers do not depend on their order, so the result is the same on every run.
+ *   target      device fp32 [B][S+1][V], p_0 .. p_S.
+ *   draft_probs device fp32 [B][S][V], q; NULL for a drafter that is sure of
+ *               its tokens (q is 1 at d_i and 0 elsewhere).
+ *   draft       device int32 [B][S]; an id outside [0, V) is refused.
+ *   n_draft     nullable device int32 [B].
+ *   u_accept    device fp32 [B][S], u_sample device fp32 [B], in [0, 1).
+ *   tokens      device int32 [B][S+1]: the accepted tokens, the new one, then -1.
+ *               The new token is -1 where p has no mass at all.
+ *   n_accepted  device int32 [B]: drafted tokens that stand.
+ * S may be 0 (draft, draft_probs and u_accept are then not read and may be NULL).
+ *   B 1 .. 65535, S 0 .. 1024, V 1 .. 2^20.
+ * NaN in p or q counts as 0 in the draw and refuses its token.
+ * Errors: INVALID_ARG, UNSUPPORTED (sizes), ALIGNMENT (4 bytes), CUDA.
+ */
+QMV_API int qmv_verify_draft(int B, int S, int V, const float *target, const float *draft_probs,
+                             const int *draft, const int *n_draft, const float *u_accept,
+                             const float *u_sample, int *tokens, int *n_accepted, void *stream);
 
 #ifdef __cplusplus
 }
