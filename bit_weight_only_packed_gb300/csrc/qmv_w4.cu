@@ -7,9 +7,22 @@
 // h = 0, 1), so the words of a warp are 512 consecutive bytes and no code
 // moves between lanes.  Inside a 32-bit word code i sits at nibble
 // i / 2 + 4 * (i % 2), so that one mask yields a pair (k, k + 1).
+#include "qmv_pipe.cuh"
 #include "qmv_step.cuh"
 
 namespace qmv {
+
+__device__ int g_w4_error = 0;
+
+int read_w4_error(int clear, int* out) {
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_w4_error, sizeof(int));
+  if (e == cudaSuccess && clear && *out) {
+    const int z = 0;
+    e = cudaMemcpyToSymbol(g_w4_error, &z, sizeof(int));
+  }
+  return (int)e;
+}
+
 namespace w4 {
 
 __host__ __device__ constexpr int nibble_of(int i) { return (i >> 1) + 4 * (i & 1); }
@@ -179,93 +192,185 @@ __device__ __forceinline__ void store_y(void* y, int64_t at, int dtype, float v)
     ((__nv_bfloat16*)y)[at] = __float2bfloat16_rn(v);
 }
 
-// One CTA a strip of 32 rows and 8 columns; its warps take every WARPS-th
-// block of k and their sums meet in shared memory.
-constexpr int WARPS = 8;
+// ------------------------------------------------------------------ matvec --
 
-template <bool BF16, int GROUP>
-__global__ void __launch_bounds__(WARPS * 32) gemv_kernel(GemvArgs4 a) {
+__device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   pipe::sa(dst)),
+               "l"(src), "r"(bytes), "r"(pipe::sa(bar))
+               : "memory");
+}
+
+constexpr int WARPS = 8, NT = WARPS * 32, MAX_SLOTS = 3;
+constexpr int PART_LD = 36;     // floats between the columns of a warp's sums: no bank conflicts
+
+// Eight activations of a column, k .. k + 7, as the tensor cores take them.
+__device__ __forceinline__ uint4 load_x8(const uint16_t* p, bool vec) {
+  if (vec) return *reinterpret_cast<const uint4*>(p);
+  uint32_t v[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = (uint32_t)p[2 * e] | ((uint32_t)p[2 * e + 1] << 16);
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// One CTA a strip of 32 rows and 8 * NB columns; warp w takes blocks w, w + 8,
+// ... of the strip's k through a ring of its own: lane 0 keeps `slots` bulk
+// copies in flight, one block each, and refills a slot as soon as its codes are
+// in registers.  Warps meet only once, to add their sums.
+template <bool BF16, int GROUP, int NB>
+__global__ void __launch_bounds__(NT) gemv_kernel(GemvArgs4 a, int slots, int vec) {
   constexpr int GPB = BK / GROUP, HPG = GROUP / 32;      // groups a block, 32-k steps a group
-  __shared__ float part[WARPS][ROWS][8];
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t full[WARPS][MAX_SLOTS];
+  __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int KB = cdiv(a.K, BK), strip = blockIdx.x, m0 = blockIdx.y * 8;
+  const int KB = cdiv(a.K, BK), strip = blockIdx.x, m0 = blockIdx.y * 8 * NB;
   const int bb = block_bytes(GROUP, a.zeros != 0);
-  const uint16_t* x = (const uint16_t*)a.x + (int64_t)(m0 + g) * a.ldx;
-  const bool col = m0 + g < a.M;
-  float tot[2][4] = {};
-  for (int b = warp; b < KB; b += WARPS) {
-    const uint8_t* blk = a.packed + ((int64_t)strip * KB + b) * bb;
-    const uint8_t* meta = blk + CODE_BYTES;
+  const int n = warp < KB ? (KB - warp + WARPS - 1) / WARPS : 0;
+  const uint8_t* src = a.packed + ((int64_t)strip * KB + warp) * bb;
+  uint8_t* ring = smem + (size_t)warp * slots * bb;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) abort_flag = 0;
+  if (lane == 0) {
+    for (int i = 0; i < slots; ++i) pipe::mbar_init(&full[warp][i], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    for (int i = 0; i < slots && i < n; ++i) {
+      pipe::mbar_arrive_tx(&full[warp][i], bb);
+      bulk_g2s(ring + i * bb, src + (int64_t)i * WARPS * bb, bb, &full[warp][i]);
+    }
+  }
+  __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");     // x may come from the kernel before
+  const uint16_t* x = (const uint16_t*)a.x + (int64_t)(m0 + g) * a.ldx + 8 * t;
+  float tot[2][NB][4] = {};
+  int slot = 0, parity = 0, i = 0;
+  for (; i < n; ++i) {
+    const int k0 = (warp + i * WARPS) * BK;
+    uint4 xv[4][NB];
+#pragma unroll
+    for (int st = 0; st < 4; ++st)
+#pragma unroll
+      for (int c = 0; c < NB; ++c) {
+        xv[st][c] = make_uint4(0, 0, 0, 0);
+        if (m0 + 8 * c + g < a.M && k0 + 32 * st + 8 * t < a.K)
+          xv[st][c] = load_x8(x + (int64_t)(8 * c) * a.ldx + k0 + 32 * st, vec);
+      }
+    if (!pipe::mbar_wait_fast(&full[warp][slot], parity, &abort_flag, pipe::ERR_TIMEOUT_FULL, &g_w4_error)) break;
+    const uint8_t* blk = ring + slot * bb;
     uint4 w[2][2];
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
       for (int j = 0; j < 2; ++j) w[r][j] = *reinterpret_cast<const uint4*>(blk + ((r * 2 + j) * 32 + lane) * 16);
+    const uint8_t* meta = blk + CODE_BYTES;
+    uint2 sc[GPB];
+    uint32_t zp[GPB];
 #pragma unroll
     for (int gi = 0; gi < GPB; ++gi) {
-      const uint2 sc = *reinterpret_cast<const uint2*>(meta + 2 * (gi * ROWS + g * 4));
-      uint32_t z = 0x08080808u;
-      if (a.zeros) z = *reinterpret_cast<const uint32_t*>(meta + 2 * GPB * ROWS + gi * ROWS + g * 4);
-      uint32_t lo[4], hi[4];     // rows g, g + 8, g + 16, g + 24
+      sc[gi] = *reinterpret_cast<const uint2*>(meta + 2 * (gi * ROWS + g * 4));
+      zp[gi] = a.zeros ? *reinterpret_cast<const uint32_t*>(meta + 2 * GPB * ROWS + gi * ROWS + g * 4) : 0x08080808u;
+    }
+    __syncwarp();
+    if (lane == 0 && i + slots < n) {
+      pipe::mbar_arrive_tx(&full[warp][slot], bb);
+      bulk_g2s(ring + slot * bb, src + (int64_t)(i + slots) * WARPS * bb, bb, &full[warp][slot]);
+    }
+    if (++slot == slots) slot = 0, parity ^= 1;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) zero_consts<BF16>((z >> (8 * i)) & 255u, lo[i], hi[i]);
-      float acc[2][4] = {};
+    for (int gi = 0; gi < GPB; ++gi) {
 #pragma unroll
-      for (int hh = 0; hh < HPG; ++hh) {
-        const int step = gi * HPG + hh, j = step >> 1, h = step & 1;   // 32 k of the block
-        const int k = b * BK + 32 * step + 8 * t;
-        uint32_t xv[4] = {};
-        if (col && k < a.K) {
+      for (int r = 0; r < 2; ++r) {
+        uint32_t lo[2], hi[2];     // rows g and g + 8 of the half
+        zero_consts<BF16>((zp[gi] >> (16 * r)) & 255u, lo[0], hi[0]);
+        zero_consts<BF16>((zp[gi] >> (16 * r + 8)) & 255u, lo[1], hi[1]);
+        float acc[NB][4] = {};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) xv[e] = (uint32_t)x[k + 2 * e] | ((uint32_t)x[k + 2 * e + 1] << 16);
-        }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
+        for (int hh = 0; hh < HPG; ++hh) {
+          const int st = gi * HPG + hh, j = st >> 1, h = st & 1;   // 32 k of the block
           uint32_t p[4], q[4];
-          decode<BF16>(h ? w[r][j].y : w[r][j].x, lo[2 * r], hi[2 * r], p);
-          decode<BF16>(h ? w[r][j].w : w[r][j].z, lo[2 * r + 1], hi[2 * r + 1], q);
-          mma16816<BF16>(acc[r], p[0], q[0], p[1], q[1], xv[0], xv[1]);
-          mma16816<BF16>(acc[r], p[2], q[2], p[3], q[3], xv[2], xv[3]);
+          decode<BF16>(h ? w[r][j].y : w[r][j].x, lo[0], hi[0], p);
+          decode<BF16>(h ? w[r][j].w : w[r][j].z, lo[1], hi[1], q);
+#pragma unroll
+          for (int c = 0; c < NB; ++c) {
+            mma16816<BF16>(acc[c], p[0], q[0], p[1], q[1], xv[st][c].x, xv[st][c].y);
+            mma16816<BF16>(acc[c], p[2], q[2], p[3], q[3], xv[st][c].z, xv[st][c].w);
+          }
+        }
+        const uint32_t s2 = r ? sc[gi].y : sc[gi].x;
+        const float s0 = scale_f(s2 & 0xffffu, a.scale_bf16), s1 = scale_f(s2 >> 16, a.scale_bf16);
+#pragma unroll
+        for (int c = 0; c < NB; ++c) {
+          tot[r][c][0] = fmaf(s0, acc[c][0], tot[r][c][0]);
+          tot[r][c][1] = fmaf(s0, acc[c][1], tot[r][c][1]);
+          tot[r][c][2] = fmaf(s1, acc[c][2], tot[r][c][2]);
+          tot[r][c][3] = fmaf(s1, acc[c][3], tot[r][c][3]);
         }
       }
-      const float s[4] = {scale_f(sc.x & 0xffffu, a.scale_bf16), scale_f(sc.x >> 16, a.scale_bf16),
-                          scale_f(sc.y & 0xffffu, a.scale_bf16), scale_f(sc.y >> 16, a.scale_bf16)};
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tot[r][i] = fmaf(s[2 * r + (i >> 1)], acc[r][i], tot[r][i]);
     }
   }
+  // a wait that ran out: let the copies in flight land before the CTA ends
+  if (i < n && lane == 0)
+    for (int j = i; j < n && j < i + slots; ++j) {
+      pipe::mbar_drain(&full[warp][slot], parity, &g_w4_error);
+      if (++slot == slots) slot = 0, parity ^= 1;
+    }
+  __syncthreads();                 // every copy has been read: the rings hold the sums now
+  if (abort_flag) return;
+  float* part = reinterpret_cast<float*>(smem);
+  float* mine = part + warp * (8 * NB * PART_LD);
+  const int cols = min(8 * NB, a.M - m0);
 #pragma unroll
   for (int r = 0; r < 2; ++r)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) part[warp][16 * r + g + 8 * (i >> 1)][2 * t + (i & 1)] = tot[r][i];
-  __syncthreads();
-  // one thread an output: 32 rows x 8 columns
-  const int row = threadIdx.x & 31, m = threadIdx.x >> 5;
-  float v = 0.0f;
+    for (int c = 0; c < NB; ++c)
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) v += part[w][row][m];
-  const int64_t n = (int64_t)strip * ROWS + row;
-  if (n < a.N && m0 + m < a.M) store_y(a.y, (int64_t)(m0 + m) * a.ldy + n, a.y_dtype, v);
-}
-
-template <bool BF16>
-static void run(const GemvArgs4& a, cudaStream_t s) {
-  const dim3 grid(cdiv(a.N, ROWS), cdiv(a.M, 8));
-  switch (a.group) {
-    case 32: gemv_kernel<BF16, 32><<<grid, WARPS * 32, 0, s>>>(a); break;
-    case 64: gemv_kernel<BF16, 64><<<grid, WARPS * 32, 0, s>>>(a); break;
-    default: gemv_kernel<BF16, 128><<<grid, WARPS * 32, 0, s>>>(a); break;
+      for (int e = 0; e < 4; ++e) {
+        const int col = 8 * c + 2 * t + (e & 1);
+        if (col < cols) mine[col * PART_LD + 16 * r + 8 * (e >> 1) + g] = tot[r][c][e];
+      }
+  __syncthreads();
+  for (int o = threadIdx.x; o < 32 * cols; o += NT) {
+    const int row = o & 31, m = o >> 5;
+    const int64_t nn = (int64_t)strip * ROWS + row;
+    if (nn >= a.N) continue;
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) v += part[(w * 8 * NB + m) * PART_LD + row];
+    store_y(a.y, (int64_t)(m0 + m) * a.ldy + nn, a.y_dtype, v);
   }
 }
 
+template <bool BF16, int GROUP, int NB>
+static cudaError_t run(const GemvArgs4& a, cudaStream_t s) {
+  static thread_local KernCache c;
+  const int KB = cdiv(a.K, BK), bb = block_bytes(GROUP, a.zeros != 0);
+  const int per = cdiv(KB, WARPS), slots = per < MAX_SLOTS ? per : MAX_SLOTS;
+  size_t smem = (size_t)WARPS * slots * bb;
+  const size_t part = (size_t)WARPS * 8 * NB * PART_LD * sizeof(float);
+  if (part > smem) smem = part;
+  const cudaError_t e = prep_kernel(gemv_kernel<BF16, GROUP, NB>, c, NT, smem, nullptr);
+  if (e != cudaSuccess) return e;
+  const int vec = a.ldx % 8 == 0 && (uintptr_t)a.x % 16 == 0;
+  return launch_step(gemv_kernel<BF16, GROUP, NB>, dim3(cdiv(a.N, ROWS), cdiv(a.M, 8 * NB)), NT, smem, s, 1, a,
+                     slots, vec);
+}
+
+template <bool BF16, int GROUP>
+static cudaError_t run_m(const GemvArgs4& a, cudaStream_t s) {
+  if (a.M <= 8) return run<BF16, GROUP, 1>(a, s);
+  if (a.M <= 16) return run<BF16, GROUP, 2>(a, s);
+  return run<BF16, GROUP, 4>(a, s);
+}
+
+template <bool BF16>
+static cudaError_t run_g(const GemvArgs4& a, cudaStream_t s) {
+  if (a.group == 32) return run_m<BF16, 32>(a, s);
+  if (a.group == 64) return run_m<BF16, 64>(a, s);
+  return run_m<BF16, 128>(a, s);
+}
+
 cudaError_t launch_w4_gemv(const GemvArgs4& a, cudaStream_t s) {
-  if (a.x_bf16)
-    run<true>(a, s);
-  else
-    run<false>(a, s);
-  return cudaGetLastError();
+  return a.x_bf16 ? run_g<true>(a, s) : run_g<false>(a, s);
 }
 
 }  // namespace w4

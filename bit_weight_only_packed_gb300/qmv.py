@@ -461,9 +461,15 @@ _16BIT = (torch.float16, torch.bfloat16)
 _FLOAT = (torch.float32, torch.float16, torch.bfloat16)
 
 
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _rows(name, t, dtypes, rows, cols):
     """Row stride of a [rows, cols] tensor ([cols] will do for one row) of one
     of dtypes, after checking that the kernels' reads and writes stay inside it."""
+    if t.dtype in dtypes and t.shape == (rows, cols) and t.is_contiguous():
+        return cols                     # the usual case, in as few steps as the host can do it
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
     if t.dim() == 2:
@@ -485,24 +491,27 @@ def _rows(name, t, dtypes, rows, cols):
 
 
 def _vec(name, t, dtype, n):
+    if t.dtype == dtype and t.numel() == n and t.is_contiguous():
+        return
     if t.dtype != dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.numel() != n:
         raise ValueError(f"{name}: needs {n} elements, has {t.numel()}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor")
+    raise ValueError(f"{name}: expected a contiguous tensor")
 
 
-def _place(first, *others):
-    """All tensors lie on the current CUDA device."""
-    dev = first.device
-    if dev.type != "cuda":
+def _place(stream, first, *others):
+    """The stream to launch on, after checking that all tensors lie on the
+    current CUDA device."""
+    dev = first.get_device()
+    if dev < 0:
         raise ValueError("expected CUDA tensors")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+    if dev != _current_device():
+        raise ValueError(f"tensors are on cuda:{dev}, the current device is cuda:{_current_device()}")
     for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors are on {dev} and {t.device}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors are on {first.device} and {t.device}")
+    return _raw_stream(dev) if stream is None else _stream(stream)
 
 
 def _fresh(shape, dtype, like, stream):
@@ -543,18 +552,17 @@ class W4Pack:
             raise ValueError("zeros: given exactly when the pack has zero points")
         if zeros is not None:
             _vec("zeros", zeros, torch.uint8, self.N * self.G)
-        _place(codes, scales, zeros)
+        st = _place(stream, codes, scales, zeros)
         packed = _fresh((self.packed_bytes,), torch.uint8, codes, stream)
         _check("qmv_w4_pack", _lib.qmv_w4_pack(self.handle, codes.data_ptr(), scales.data_ptr(),
-                                               None if zeros is None else zeros.data_ptr(), packed.data_ptr(),
-                                               _stream(stream)))
+                                               None if zeros is None else zeros.data_ptr(), packed.data_ptr(), st))
         self.packed = packed
         return self
 
     def bind_packed(self, packed):
         """packed: a device uint8 buffer with the packed bytes of this shape."""
         _vec("packed", packed, torch.uint8, self.packed_bytes)
-        _place(packed)
+        _place(None, packed)
         _check("qmv_w4_bind", _lib.qmv_w4_bind(self.handle, packed.data_ptr()))
         self.packed = packed
         return self
@@ -562,9 +570,9 @@ class W4Pack:
     def unpack_codes(self, stream=None):
         if self.packed is None:
             raise ValueError("the pack holds no weights yet")
-        _place(self.packed)
+        st = _place(stream, self.packed)
         out = _fresh((self.N, self.K), torch.uint8, self.packed, stream)
-        _check("qmv_w4_unpack", _lib.qmv_w4_unpack(self.handle, out.data_ptr(), _stream(stream)))
+        _check("qmv_w4_unpack", _lib.qmv_w4_unpack(self.handle, out.data_ptr(), st))
         return out
 
     def info(self):
@@ -595,11 +603,11 @@ def qmv_w4_gemv(p: W4Pack, x, y=None, y_dtype=QMV_F32, stream=None):
     if y_dtype not in _TORCH:
         raise ValueError(f"y_dtype: unknown value {y_dtype!r}")
     ldy = p.N if y is None else _rows("y", y, (_TORCH[y_dtype],), M, p.N)
-    _place(x, p.packed, y)
+    st = _place(stream, x, p.packed, y)
     if y is None:
         y = _fresh((M, p.N), _TORCH[y_dtype], x, stream)
     _check("qmv_w4_gemv", _lib.qmv_w4_gemv(p.handle, M, x.data_ptr(), ldx, _DTYPE[x.dtype], y.data_ptr(), ldy,
-                                           y_dtype, _stream(stream)))
+                                           y_dtype, st))
     return y
 
 
@@ -624,7 +632,7 @@ def qmv_block_norm(y, residual, gamma_pre, gamma_post=None, gate=None, residual_
             ldg = _rows("gate", gate, (dt,), M, D)
     ldh = D if h_out is None else _rows("h_out", h_out, (dt,), M, D)
     ldo = D if out is None else _rows("out", out, (dt,), M, D)
-    _place(y, residual, gamma_pre, gamma_post, gate, h_out, out)
+    st = _place(stream, y, residual, gamma_pre, gamma_post, gate, h_out, out)
     if h_out is None:
         h_out = _fresh((M, D), dt, y, stream)
     if out is None:
@@ -633,7 +641,7 @@ def qmv_block_norm(y, residual, gamma_pre, gamma_post=None, gate=None, residual_
         M, D, y.data_ptr(), ldy, _DTYPE[y.dtype], residual.data_ptr(), ldr,
         None if gamma_post is None else gamma_post.data_ptr(), None if gate is None else gate.data_ptr(), ldg,
         residual_scale, branch_scale, gamma_pre.data_ptr(), gamma_offset, eps, h_out.data_ptr(), ldh,
-        out.data_ptr(), ldo, _DTYPE[dt], _stream(stream)))
+        out.data_ptr(), ldo, _DTYPE[dt], st))
     return h_out, out
 
 
@@ -651,12 +659,11 @@ def qmv_softmax(logits, temperature=1.0, out=None, stream=None):
     else:
         t0 = float(temperature)
     ldo = V if out is None else _rows("out", out, (torch.float32,), rows, V)
-    _place(logits, t, out)
+    st = _place(stream, logits, t, out)
     if out is None:
         out = _fresh((rows, V), torch.float32, logits, stream)
     _check("qmv_softmax", _lib.qmv_softmax(rows, V, logits.data_ptr(), ldl, _DTYPE[logits.dtype],
-                                           None if t is None else t.data_ptr(), t0, out.data_ptr(), ldo,
-                                           _stream(stream)))
+                                           None if t is None else t.data_ptr(), t0, out.data_ptr(), ldo, st))
     return out
 
 
@@ -681,7 +688,7 @@ def qmv_verify_draft(target, draft_probs, draft, u_accept, u_sample, n_draft=Non
         _vec("tokens", tokens, torch.int32, B * S1)
     if n_accepted is not None:
         _vec("n_accepted", n_accepted, torch.int32, B)
-    _place(target, draft_probs, draft, u_accept, u_sample, n_draft, tokens, n_accepted)
+    st = _place(stream, target, draft_probs, draft, u_accept, u_sample, n_draft, tokens, n_accepted)
     if tokens is None:
         tokens = _fresh((B, S1), torch.int32, target, stream)
     if n_accepted is None:
@@ -689,5 +696,5 @@ def qmv_verify_draft(target, draft_probs, draft, u_accept, u_sample, n_draft=Non
     _check("qmv_verify_draft", _lib.qmv_verify_draft(
         B, S, V, target.data_ptr(), None if draft_probs is None else draft_probs.data_ptr(), draft.data_ptr(),
         None if n_draft is None else n_draft.data_ptr(), u_accept.data_ptr(), u_sample.data_ptr(),
-        tokens.data_ptr(), n_accepted.data_ptr(), _stream(stream)))
+        tokens.data_ptr(), n_accepted.data_ptr(), st))
     return tokens, n_accepted
