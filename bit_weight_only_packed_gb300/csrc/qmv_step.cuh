@@ -23,6 +23,8 @@ namespace w4 {
 // The packed layout (qmv.h): blocks of ROWS x BK codes, strips of ROWS rows,
 // the blocks of a strip one after another in k.
 constexpr int ROWS = 32, BK = 128, CODE_BYTES = ROWS * BK / 2;
+// The longest row: an eighth of one column of x fits beside the rings.
+constexpr int MAX_K = 131072;
 
 __host__ __device__ constexpr int block_bytes(int group, bool zeros) {
   return CODE_BYTES + (BK / group) * ROWS * (zeros ? 3 : 2);

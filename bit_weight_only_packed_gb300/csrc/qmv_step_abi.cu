@@ -23,9 +23,10 @@ int qmv_w4_create(qmv_w4pack** out, int N, int K, int group, int scale_dtype, in
   *out = nullptr;
   if (group != 32 && group != 64 && group != 128) return QMV_ERR_INVALID_ARG;
   if (!dtype16(scale_dtype)) return QMV_ERR_INVALID_ARG;
-  // strips and blocks are counted in int; the padded sizes must not pass it
-  if (N < 1 || K < 32 || K % 32 != 0 || N > INT32_MAX - 31 || K > INT32_MAX - 127)
+  // strips are counted in int; the padded size must not pass it
+  if (N < 1 || K < 32 || K % 32 != 0 || N > INT32_MAX - 31)
     return QMV_ERR_SHAPE;
+  if (K > qmv::w4::MAX_K) return QMV_ERR_UNSUPPORTED;
   qmv_w4pack* p = new (std::nothrow) qmv_w4pack;
   if (!p) return QMV_ERR_INVALID_ARG;
   memset(p, 0, sizeof(*p));

@@ -427,7 +427,7 @@ QMV_API int qmv_chain_destroy(qmv_chain *c);
 /*
  * qmv_w4_create -- describe 4-bit weights w[n][k] = (q[n][k] - z[n][g]) * s[n][g]
  * with g = k / group.
- *   N, K         output and input features; N >= 1, K >= 32, K % 32 == 0.
+ *   N, K         output and input features; N >= 1, 32 <= K <= 131072, K % 32 == 0.
  *   group        32, 64 or 128 consecutive k of a row (the last group of a row
  *                is short where K is not a multiple).
  *   scale_dtype  QMV_F16 or QMV_BF16.
@@ -439,8 +439,8 @@ QMV_API int qmv_chain_destroy(qmv_chain *c);
  * tiles, 16 bytes for each lane of a warp), then its scales (groups x 32 x
  * fp16/bf16), then its zero points (groups x 32 bytes).  Rows and k past the
  * end are padded with zero scales.
- * Errors: INVALID_ARG (out NULL, group or scale_dtype not allowed), SHAPE.
- * Host only.
+ * Errors: INVALID_ARG (out NULL, group or scale_dtype not allowed), SHAPE,
+ * UNSUPPORTED (K > 131072).  Host only.
  */
 QMV_API int qmv_w4_create(qmv_w4pack **out, int N, int K, int group, int scale_dtype,
                           int has_zeros, size_t *packed_bytes);
@@ -475,9 +475,10 @@ QMV_API int qmv_w4_destroy(qmv_w4pack *p);
 
 /*
  * qmv_w4_gemv -- y[m][n] = sum_g s[n][g] * sum_{k in g} x[m][k] * (q[n][k] - z[n][g])
- * for M columns.  q - z is exact in x's type, products are exact and sums are
- * fp32 (tensor-core order inside a group, then over the groups); one rounding
- * to y's type at the end.  Repeated calls give the same bits.
+ * for M columns, computed as s * (sum(x * q) - z * sum(x)) a group, with exact
+ * products and fp32 sums in a fixed order and one rounding to y's type at the
+ * end.  Infinities and NaN of x act as the definition has them.  Repeated calls
+ * give the same bits.
  *   M        1 .. 4096.
  *   x        device [M][K] of x_dtype (QMV_F16 or QMV_BF16, any mix with the
  *            scales' type), row stride ldx.

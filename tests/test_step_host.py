@@ -21,7 +21,7 @@ def q():
     (64, 256, 16, F16, 1, -1), (64, 256, 256, F16, 1, -1), (64, 256, 0, F16, 1, -1),
     (64, 256, 128, F32, 1, -1), (64, 256, 128, 3, 1, -1),
     (0, 256, 128, F16, 1, -4), (64, 0, 128, F16, 1, -4), (64, 48, 32, F16, 1, -4), (-5, 64, 32, F16, 1, -4),
-    (2**31 - 1, 64, 32, F16, 1, -4),
+    (2**31 - 1, 64, 32, F16, 1, -4), (64, 131072, 32, F16, 1, 0), (64, 131104, 32, F16, 1, -2),
 ])
 def test_w4_create(q, N, K, group, dt, zeros, status):
     h, nb = ctypes.c_void_p(), ctypes.c_size_t()
