@@ -31,6 +31,13 @@ __host__ __device__ constexpr int block_bytes(int group, bool zeros) {
 }
 __host__ __device__ constexpr int cdiv(int a, int b) { return (a + b - 1) / b; }
 
+// The bit of a 32-bit word where code i of its eight begins: the low halves hold
+// codes 0, 4, 2, 6 at bits 3, 7, 11 and 15 (wrapping around), the high halves
+// their odd neighbours.
+__host__ __device__ constexpr int shift_of(int i) {
+  return (3 + 8 * ((i >> 1) & 1) + 4 * (i >> 2) + 16 * (i & 1)) & 31;
+}
+
 // Where row r (0..31) of a block keeps its scale and zero point inside a
 // group's 32: the four rows that one lane of a warp holds (g, g + 8, g + 16,
 // g + 24 for g = lane / 4) lie side by side.
@@ -50,6 +57,10 @@ cudaError_t launch_w4_pack(const qmv_w4pack& p, const uint8_t* codes, const uint
                            const uint8_t* zeros, uint8_t* packed, cudaStream_t s);
 cudaError_t launch_w4_unpack(const qmv_w4pack& p, uint8_t* codes, cudaStream_t s);
 cudaError_t launch_w4_gemv(const GemvArgs4& a, cudaStream_t s);
+template <int GROUP, bool XB>
+cudaError_t launch_group(const GemvArgs4& a, cudaStream_t s);
+template <int GROUP, bool XB>
+cudaError_t read_error(int clear, int* out);
 
 }  // namespace w4
 

@@ -1,0 +1,595 @@
+// qmv_w4_gemv.cuh -- the matvec of the 4-bit weights packed by qmv_w4.cu:
+//   y[m][n] = sum_g s[n][g] * (sum_{k in g} x[m][k] * q[n][k] - z[n][g] * sum_{k in g} x[m][k]).
+// One translation unit a group size and type of x includes it.
+//
+// The products run on m16n8k16 tensor instructions with the weights as the
+// 16-row operand and x as it is, so all products are exact and sums fp32.
+//   fp16: the numbers below 2^-13 are evenly spaced, so a masked code in the low
+//   11 bits of a half is, read as fp16, the code times 2^-21 (at bit 3) or 2^-17
+//   (at bit 7): the operand without any arithmetic, four masks and one rotation
+//   for eight codes.  The two kinds have sums of their own.
+//   bf16: a code at bit 3 under the exponent of 16 reads 16 + q: four masks and
+//   three rotations; the 16 comes off with the zero point.
+// The zero point comes off a group's sum as z * sum(x), as the library's fast
+// form does for its offset; the sums of x are formed once a CTA.
+//
+// The work is bound by HBM once the instructions per code are few, so a CTA a
+// streaming multiprocessor stays for the whole launch and its warps share out
+// its strips evenly, block by block and without meeting: a warp's range may
+// begin and end inside a strip, and only those partial sums are joined, once,
+// at the end.  Every warp keeps a ring of bulk copies of its own in flight.
+#pragma once
+#include "qmv_pipe.cuh"
+#include "qmv_step.cuh"
+
+namespace qmv {
+namespace w4 {
+
+static __device__ int g_w4_error = 0;
+
+constexpr int MAX_SLOTS = 8, MAX_CLUSTER = 8, NBMAX = 4;
+constexpr int PART_LD = 36;     // floats between the columns of a warp's sums: no bank conflicts
+
+// Warps a CTA: with many columns fewer, whose partial sums leave room for x.
+__host__ __device__ constexpr int warps_of(int nb) { return nb <= 2 ? 16 : 8; }
+
+__device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   pipe::sa(dst)),
+               "l"(src), "r"(bytes), "r"(pipe::sa(bar))
+               : "memory");
+}
+
+// D = A . B + C on 16 rows x 8 columns x 16 k.
+template <bool XB>
+__device__ __forceinline__ void mma16816(float (&d)[4], const float* c, uint32_t a0, uint32_t a1,
+                                         uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  if (XB)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+
+// (v & mask) | bits in one instruction; both constants from registers.
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(v), "r"(mask), "r"(bits));
+  return d;
+}
+template <uint32_t V>
+__device__ __forceinline__ uint32_t in_register() {
+  uint32_t d;
+  asm("mov.b32 %0, %1;" : "=r"(d) : "n"(V));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t rot(uint32_t v, int n) { return __funnelshift_r(v, v, n); }
+
+__device__ __forceinline__ float f16_f(uint32_t bits16, int bf16) {
+  return bf16 ? __uint_as_float(bits16 << 16) : __half2float(__ushort_as_half((unsigned short)bits16));
+}
+
+// The zero point in byte i of v on the scale of a group's sum: placed in the
+// mantissa of 4, whose last bit is 2^-21 (fp16), or of 2^23 (bf16: 16 + z).
+template <bool XB>
+__device__ __forceinline__ float zero_f(uint32_t v, int i) {
+  const uint32_t sel = 0x7650u | (uint32_t)i;
+  return XB ? __uint_as_float(__byte_perm(v, 0x4B000000u, sel)) - 8388592.0f
+            : __uint_as_float(__byte_perm(v, 0x40800000u, sel)) - 4.0f;
+}
+
+__device__ __forceinline__ void store_y(void* y, int64_t at, int dtype, float v) {
+  if (dtype == QMV_F32)
+    ((float*)y)[at] = v;
+  else if (dtype == QMV_F16)
+    ((__half*)y)[at] = __float2half_rn(v);
+  else
+    ((__nv_bfloat16*)y)[at] = __float2bfloat16_rn(v);
+}
+
+// How a launch divides the work.  A cluster of ks CTAs takes whole strips, each
+// CTA one ks-th of their k.
+struct Plan {
+  int ks, ks_log, ncl;          // CTAs a cluster (a power of two), clusters
+  int k_share, k_more;          // blocks of k a CTA; so many of them have one more
+  int s_share, s_more;          // strips a cluster, likewise
+  int kbs;                      // blocks of k a CTA, at most
+  int cols;                     // columns a launch row (grid.y) takes
+  int slots, stage;             // ring slots a warp, blocks a slot
+  int rs;                       // strips between two meetings of a cluster
+  int vec;                      // x can be read 16 bytes at a time
+  int pitch;                    // bytes between the columns of x in shared memory
+  int x_off, zero_off, xs_off, part_off, red_off, smem;   // bytes in shared memory; the rings come first
+};
+
+// A sum by its definition: for columns with infinities, NaN or values near
+// the end of fp32's range, where x * q and z * sum(x) apart would give another
+// answer.  x: the column in shared memory, from k0 on.
+static __device__ __noinline__ float plain_sum(const GemvArgs4& a, const uint16_t* x, int n, int k0, int k1) {
+  const int KB = cdiv(a.K, BK), bb = block_bytes(a.group, a.zeros != 0), gpb = BK / a.group;
+  const int row = n & 31, r = row >> 4, hi = (row >> 3) & 1;
+  float v = 0.0f, sum = 0.0f, s = 0.0f;
+  int z = 8;
+  for (int k = k0; k < k1; ++k) {
+    const uint8_t* b = a.packed + ((int64_t)(n >> 5) * KB + (k >> 7)) * bb;
+    if (k % a.group == 0) {
+      v += sum * s;
+      sum = 0.0f;
+      const uint8_t* meta = b + CODE_BYTES;
+      const int at = (k & 127) / a.group * ROWS + meta_slot(row);
+      s = f16_f(reinterpret_cast<const uint16_t*>(meta)[at], a.scale_bf16);
+      if (a.zeros) z = meta[2 * gpb * ROWS + at];
+    }
+    const int j = (k >> 6) & 1, h = (k >> 5) & 1, lane = (row & 7) * 4 + ((k >> 3) & 3);
+    const uint32_t w = reinterpret_cast<const uint32_t*>(b)[((r * 2 + j) * 32 + lane) * 4 + hi * 2 + h];
+    sum = fmaf(f16_f(x[k - k0], a.x_bf16), (float)((int)(rot(w, shift_of(k & 7)) & 15u) - z), sum);
+  }
+  return v + sum * s;
+}
+
+// XB, SB: x and the scales are bf16 (fp16 otherwise).
+template <int GROUP, int NB, bool XB, bool SB>
+__global__ void __launch_bounds__(warps_of(NB) * 32, 1)
+    gemv_kernel(const __grid_constant__ GemvArgs4 a, const __grid_constant__ Plan P) {
+  constexpr int W = warps_of(NB), NT = W * 32;
+  constexpr int GPB = BK / GROUP, HPG = GROUP / 32;      // groups a block, 32-k steps a group
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t full[W][MAX_SLOTS];
+  __shared__ uint64_t x_full;
+  __shared__ int bad[8 * NB];
+  __shared__ int abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int KB = cdiv(a.K, BK), NS = cdiv(a.N, ROWS), bb = block_bytes(GROUP, a.zeros != 0);
+  const int m0 = blockIdx.y * P.cols, mc = min(P.cols, a.M - m0);
+  const int rank = blockIdx.x & (P.ks - 1), cl = blockIdx.x >> P.ks_log;
+  // even shares: the first few CTAs or clusters have one more
+  const int kb0 = rank * P.k_share + min(rank, P.k_more), kbn = P.k_share + (rank < P.k_more);
+  const int S0 = cl * P.s_share + min(cl, P.s_more), S1 = S0 + P.s_share + (cl < P.s_more);
+  const int rounds = P.ks == 1 ? 1 : cdiv(S1 - S0, P.rs);
+  // warp w's blocks of round r, counted through the round's strips
+  const auto strips_of = [&](int r) { return min(P.rs, S1 - S0 - r * P.rs); };
+  const auto first_of = [&](int r, int w) { return (int)((unsigned)(strips_of(r) * kbn) * (unsigned)w / W); };
+  uint8_t* ring = smem + (size_t)warp * P.slots * P.stage * bb;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid < 8 * NB) bad[tid] = 0;
+  if (tid == 0) abort_flag = 0;
+
+  // Lane 0 keeps the ring full.  A copy is up to `stage` neighbouring blocks of a strip.
+  const uint8_t* src = nullptr;
+  int p_round = -1, p_left = 0, p_blk = 0, issued = 0, used = 0;
+  const auto next_round = [&]() {
+    while (p_left == 0 && ++p_round < rounds) {
+      const int lo = first_of(p_round, warp);
+      p_left = first_of(p_round, warp + 1) - lo;
+      const int st = (int)((unsigned)lo / (unsigned)kbn);
+      p_blk = lo - st * kbn;
+      src = a.packed + ((int64_t)(S0 + p_round * P.rs + st) * KB + kb0 + p_blk) * bb;
+    }
+  };
+  const auto issue = [&](int s) {
+    const int cnt = min(P.stage, min(p_left, kbn - p_blk));
+    pipe::mbar_arrive_tx(&full[warp][s], cnt * bb);
+    bulk_g2s(ring + s * P.stage * bb, src, cnt * bb, &full[warp][s]);
+    ++issued;
+    p_left -= cnt;
+    p_blk += cnt;
+    src += (int64_t)cnt * bb;
+    if (p_blk == kbn) p_blk = 0, src += (int64_t)(KB - kbn) * bb;
+    if (p_left == 0) next_round();
+  };
+  if (lane == 0) {
+    for (int i = 0; i < P.slots; ++i) pipe::mbar_init(&full[warp][i], 1);
+    if (warp == 0) pipe::mbar_init(&x_full, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    next_round();
+    for (int i = 0; i < P.slots && p_left > 0; ++i) issue(i);
+  }
+  // x to shared memory as it is, a row a column, P.pitch bytes apart (64 past a
+  // multiple of 128, so that the eight lanes of a 128-byte read touch different banks).
+  uint8_t* xs = smem + P.x_off;
+  const uint16_t* xg = (const uint16_t*)a.x + (int64_t)m0 * a.ldx + (int64_t)kb0 * BK;
+  const int klim = min(kbn * BK, a.K - kb0 * BK);
+  if (tid < 16) reinterpret_cast<uint4*>(smem + P.zero_off)[tid] = make_uint4(0, 0, 0, 0);
+  asm volatile("griddepcontrol.wait;" ::: "memory");     // x may come from the kernel before
+  if (P.vec) {
+    if (warp == 0) {
+      if (lane == 0) pipe::mbar_arrive_tx(&x_full, mc * klim * 2);
+      __syncwarp();
+      for (int m = lane; m < mc; m += 32) bulk_g2s(xs + m * P.pitch, xg + (int64_t)m * a.ldx, klim * 2, &x_full);
+    }
+  } else {
+    for (int m = 0; m < mc; ++m)
+#pragma unroll 4
+      for (int k = tid; k < klim; k += NT) reinterpret_cast<uint16_t*>(xs + m * P.pitch)[k] = xg[(int64_t)m * a.ldx + k];
+  }
+  for (int m = 0; m < mc; ++m)                            // up to 96 k past the end
+    for (int k = klim + tid; k < kbn * BK; k += NT) reinterpret_cast<uint16_t*>(xs + m * P.pitch)[k] = 0;
+  __syncthreads();
+  if (P.vec && !pipe::mbar_wait_fast(&x_full, 0, &abort_flag, pipe::ERR_TIMEOUT_TFULL, &g_w4_error))
+    pipe::mbar_drain(&x_full, 0, &g_w4_error);           // nothing is stored after a wait that ran out
+
+  // The sums of x, a group each: 16 lanes take a block of a column, eight k a lane.
+  float* xsum = reinterpret_cast<float*>(smem + P.xs_off);             // [group][8 * NB]
+  for (int b = 2 * warp + (lane >> 4), m = 0;; b += 2 * W) {
+    while (b >= kbn && m < mc) b -= kbn, ++m;
+    if (__all_sync(~0u, m >= mc)) break;
+    float sum = 0.0f, mag = 0.0f;
+    if (m < mc) {
+      const uint4 v = *reinterpret_cast<const uint4*>(xs + m * P.pitch + b * 256 + (lane & 15) * 16);
+      const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const float u0 = f16_f(in[p] & 0xffffu, XB), u1 = f16_f(in[p] >> 16, XB);
+        sum += u0 + u1;
+        mag += fabsf(u0) + fabsf(u1);
+      }
+      if (!(mag < 1e35f)) bad[m] = 1;
+    }
+#pragma unroll
+    for (int q = GROUP / 16; q; q >>= 1) sum += __shfl_xor_sync(~0u, sum, q);
+    if (m < mc && (lane & (GROUP / 8 - 1)) == 0) xsum[(b * GPB + (lane & 15) / (GROUP / 8)) * (8 * NB) + m] = sum;
+  }
+  __syncthreads();
+
+  // Where a lane reads x; lanes past the last column read zeros.
+  const bool in_last = 8 * (NB - 1) + g < mc;
+  const uint8_t* xp[NB];
+#pragma unroll
+  for (int c = 0; c < NB; ++c) xp[c] = xs + (8 * c + g) * P.pitch + t * 16;
+  if (!in_last) xp[NB - 1] = smem + P.zero_off + t * 16;
+  const int l_step = in_last ? 256 : 0;
+
+  float* red = reinterpret_cast<float*>(smem + P.red_off);             // [2][rs][mc][32], clusters only
+  float* part = reinterpret_cast<float*>(smem + P.part_off);           // [W][mc][PART_LD]
+  // A finished sum goes out (or to the cluster's sum).
+  const auto emit = [&](int round, int s, int m, int row, float v) {
+    if (!XB) v *= 2097152.0f;
+    const int64_t n = (int64_t)(S0 + round * P.rs + s) * ROWS + row;
+    if (bad[m] && n < a.N)
+      v = plain_sum(a, reinterpret_cast<const uint16_t*>(xs + m * P.pitch), (int)n, kb0 * BK, kb0 * BK + klim);
+    if (P.ks > 1)
+      red[(((round & 1) * P.rs + s) * mc + m) * 32 + row] = v;
+    else if (n < a.N && !abort_flag)
+      store_y(a.y, (int64_t)(m0 + m) * a.ldy + n, a.y_dtype, v);
+  };
+
+  const uint32_t bits3 = in_register<0x00780078u>(), sixteen = in_register<0x41804180u>();   // bf16 codes
+  int slot = 0, parity = 0;
+  for (int round = 0; round < rounds; ++round) {
+    const int lo = first_of(round, warp), hi = first_of(round, warp + 1);
+    const int s_lo = (int)((unsigned)lo / (unsigned)kbn);
+    int s = s_lo, blk = lo - s * kbn, f = lo, from = blk;
+    float tot[2][NB][4] = {};
+    bool head = true, tail = false;        // the first strip of the range; its last, left unfinished in tot
+    while (f < hi) {
+      const int cnt = min(P.stage, min(hi - f, kbn - blk));
+      if (!__all_sync(~0u, pipe::mbar_wait_fast(&full[warp][slot], parity, &abort_flag, pipe::ERR_TIMEOUT_FULL, &g_w4_error)))
+        break;
+      const uint8_t* p = ring + slot * P.stage * bb;
+      for (int i = 0; i < cnt; ++i, p += bb) {
+        uint4 w[2][2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) w[r][q] = *reinterpret_cast<const uint4*>(p + ((r * 2 + q) * 32 + lane) * 16);
+        const uint8_t* meta = p + CODE_BYTES;
+        uint2 sc[GPB];
+        uint32_t zp[GPB];
+#pragma unroll
+        for (int gi = 0; gi < GPB; ++gi) {
+          sc[gi] = *reinterpret_cast<const uint2*>(meta + 2 * (gi * ROWS + g * 4));
+          zp[gi] = a.zeros ? *reinterpret_cast<const uint32_t*>(meta + 2 * GPB * ROWS + gi * ROWS + g * 4) : 0x08080808u;
+        }
+        if (i == cnt - 1) {                // every lane has read the slot: fill it again
+          ++used;
+          __syncwarp();
+          if (lane == 0 && p_left > 0) issue(slot);
+        }
+        const int xo = (blk + i) * 256, xl = (blk + i) * l_step;
+        const float* sxp = xsum + (blk + i) * (GPB * 8 * NB) + 2 * t;
+#pragma unroll
+        for (int gi = 0; gi < GPB; ++gi) {
+          constexpr int KINDS = XB ? 1 : 2;          // fp16 codes have two scales
+          float acc[KINDS][2][NB][4];
+          const float none[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int hh = 0; hh < HPG; ++hh) {
+            const int st = gi * HPG + hh, q = st >> 1, h = st & 1;   // 32 k of the block
+            uint4 xv[NB];
+#pragma unroll
+            for (int c = 0; c < NB; ++c)
+              xv[c] = *reinterpret_cast<const uint4*>(xp[c] + (c < NB - 1 ? xo : xl) + st * 64);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const uint32_t u = h ? w[r][q].y : w[r][q].x, v = h ? w[r][q].w : w[r][q].z;   // rows g, g + 8
+              if (XB) {
+                uint32_t p[4], o[4];
+#pragma unroll
+                for (int i4 = 0; i4 < 4; ++i4) {
+                  p[i4] = and_or(i4 ? rot(u, 4 * i4) : u, bits3, sixteen);
+                  o[i4] = and_or(i4 ? rot(v, 4 * i4) : v, bits3, sixteen);
+                }
+#pragma unroll
+                for (int c = 0; c < NB; ++c) {
+                  float(&d)[4] = acc[0][r][c];
+                  mma16816<XB>(d, hh ? d : none, p[0], o[0], p[2], o[2], xv[c].x, xv[c].y);
+                  mma16816<XB>(d, d, p[1], o[1], p[3], o[3], xv[c].z, xv[c].w);
+                }
+              } else {
+                constexpr uint32_t L = 0x00780078u, H = 0x07800780u;
+                const uint32_t u8 = rot(u, 8), v8 = rot(v, 8);
+#pragma unroll
+                for (int c = 0; c < NB; ++c) {
+                  float(&d)[4] = acc[0][r][c];
+                  float(&e)[4] = acc[KINDS - 1][r][c];
+                  mma16816<XB>(d, hh ? d : none, u & L, v & L, u8 & L, v8 & L, xv[c].x, xv[c].y);
+                  mma16816<XB>(e, hh ? e : none, u & H, v & H, u8 & H, v8 & H, xv[c].z, xv[c].w);
+                }
+              }
+            }
+          }
+          float2 sx[NB];
+#pragma unroll
+          for (int c = 0; c < NB; ++c) sx[c] = *reinterpret_cast<const float2*>(sxp + gi * (8 * NB) + 8 * c);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const uint32_t s2 = r ? sc[gi].y : sc[gi].x;
+            const float s0 = f16_f(s2 & 0xffffu, SB), s1 = SB ? __uint_as_float(s2 & 0xffff0000u) : f16_f(s2 >> 16, SB);
+            const float z0 = zero_f<XB>(zp[gi], 2 * r), z1 = zero_f<XB>(zp[gi], 2 * r + 1);
+#pragma unroll
+            for (int c = 0; c < NB; ++c)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float v = acc[0][r][c][e];
+                if (!XB) v = fmaf(acc[KINDS - 1][r][c][e], 0.0625f, v);
+                v = fmaf(-(e < 2 ? z0 : z1), e & 1 ? sx[c].y : sx[c].x, v);
+                tot[r][c][e] = fmaf(e < 2 ? s0 : s1, v, tot[r][c][e]);
+              }
+          }
+        }
+      }
+      if (++slot == P.slots) slot = 0, parity ^= 1;
+      f += cnt;
+      blk += cnt;
+      if (blk == kbn || f == hi) {
+        const bool whole = from == 0 && blk == kbn;
+        tail = !whole && !head;
+        if (!tail) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int c = 0; c < NB; ++c)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int m = 8 * c + 2 * t + (e & 1), row = 16 * r + 8 * (e >> 1) + g;
+                if (m < mc) {
+                  if (whole)
+                    emit(round, s, m, row, tot[r][c][e]);
+                  else
+                    part[(warp * mc + m) * PART_LD + row] = tot[r][c][e];
+                }
+                tot[r][c][e] = 0.0f;
+              }
+          ++s;
+          blk = from = 0;
+          head = false;
+        }
+      }
+    }
+    const int F = strips_of(round) * kbn;
+    if (lo == hi && lo < F)                  // fewer blocks than warps: nothing to add
+      for (int m = 0; m < mc; ++m) part[(warp * mc + m) * PART_LD + lane] = 0.0f;
+    __syncthreads();
+    // Strips that several warps share: the warps w0 .. w0 + nw - 1 whose ranges begin in
+    // the strip share out its columns.  Where the strip itself begins one of the
+    // ranges, its pieces are all in `part`; else its first piece is in the registers of
+    // warp w0 - 1, which finds the sum of the others in w0's place.
+    if (lo < F) {
+      const int st = s_lo, begin = st * kbn, end = begin + kbn;
+      const int w0 = (int)(((unsigned)begin * W + F - 1) / F), nw = (int)(((unsigned)end * W + F - 1) / F) - w0;
+      const bool begins = first_of(round, w0) == begin, whole = first_of(round, w0 + nw - 1) == begin;
+      if (!whole && (begins || nw > 1))      // one warp had the whole strip, or one other piece is there
+        for (int m = warp - w0; m < mc; m += nw) {
+          float v = part[(w0 * mc + m) * PART_LD + lane];
+          for (int q = 1; q < nw; ++q) v += part[((w0 + q) * mc + m) * PART_LD + lane];
+          if (begins)
+            emit(round, st, m, lane, v);
+          else
+            part[(w0 * mc + m) * PART_LD + lane] = v;
+        }
+    }
+    __syncthreads();
+    if (tail) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int c = 0; c < NB; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int m = 8 * c + 2 * t + (e & 1), row = 16 * r + 8 * (e >> 1) + g;
+            if (m < mc) emit(round, s, m, row, tot[r][c][e] + part[((warp + 1) * mc + m) * PART_LD + row]);
+          }
+    }
+    if (P.ks > 1) {
+      // the CTAs of a cluster add theirs, each finishing a share; two buffers, so that the
+      // next round's barrier is the only other one needed
+      __syncwarp();
+      cluster_arrive();
+      cluster_wait();
+      const int items = strips_of(round) * mc;
+      for (int i = rank + P.ks * warp; i < items; i += P.ks * W) {
+        const int st = i / mc, m = i - st * mc;
+        float v = 0.0f;
+        for (int q = 0; q < P.ks; ++q)
+          v += __uint_as_float(ld_cluster32(cluster_addr(red + (((round & 1) * P.rs + st) * mc + m) * 32 + lane, q)));
+        const int64_t n = (int64_t)(S0 + round * P.rs + st) * ROWS + lane;
+        if (n < a.N && !abort_flag) store_y(a.y, (int64_t)(m0 + m) * a.ldy + n, a.y_dtype, v);
+      }
+      __syncwarp();
+    }
+  }
+  // after a wait that ran out: let the copies in flight land before the CTA ends
+  if (lane == 0)
+    for (; used < issued; ++used) {
+      pipe::mbar_drain(&full[warp][slot], parity, &g_w4_error);
+      if (++slot == P.slots) slot = 0, parity ^= 1;
+    }
+  if (P.ks > 1) {                          // the others may still read this CTA's sums
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+  }
+}
+
+// How many clusters of ks CTAs the device holds at once (its GPCs need not hold
+// a whole number of them).  One CTA fills a streaming multiprocessor whatever the
+// shape, so the answer hangs on ks alone.
+template <typename Kern>
+static int clusters_of(Kern kern, int threads, int ks, const DevInfo& d) {
+  struct Seen {
+    int dev = -1, n[MAX_CLUSTER + 1] = {};
+  };
+  static thread_local Seen c;
+  if (ks == 1) return d.sms;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return d.sms / ks;
+  if (c.dev != dev) c = Seen(), c.dev = dev;
+  if (!c.n[ks]) {
+    const int smem = d.max_smem_optin - 4096;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ks;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(ks);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = d.sms / ks;
+    }
+    c.n[ks] = n;
+  }
+  return c.n[ks];
+}
+
+// The shared memory of a plan with ks CTAs along k, or false where it does not fit.
+static bool lay_out(const GemvArgs4& a, int nb, int ks, int ncl, const DevInfo& d, Plan* P) {
+  const int KB = cdiv(a.K, BK), NS = cdiv(a.N, ROWS), bb = block_bytes(a.group, a.zeros != 0), W = warps_of(nb);
+  P->ks = ks;
+  P->ks_log = 0;
+  while (1 << P->ks_log < ks) ++P->ks_log;
+  P->kbs = cdiv(KB, ks);
+  P->ncl = ncl < NS ? ncl : NS;
+  P->k_share = KB / ks;
+  P->k_more = KB % ks;
+  P->s_share = NS / P->ncl;
+  P->s_more = NS % P->ncl;
+  const int strips = cdiv(NS, P->ncl);
+  // a cluster meets after rs strips, whose sums take at most 16 KB a buffer
+  int rs = strips;
+  if (ks > 1) {
+    const int most = 16384 / (P->cols * ROWS * 4);
+    rs = cdiv(strips, cdiv(strips, most < 1 ? 1 : most));
+  }
+  P->rs = rs;
+  const auto up = [](int64_t v) { return (v + 127) & ~(int64_t)127; };
+  P->pitch = P->kbs * 256 + 64;
+  const int64_t x = up((int64_t)P->pitch * P->cols), xs = up((int64_t)P->kbs * (BK / a.group) * 8 * nb * 4),
+                part = up((int64_t)W * P->cols * PART_LD * 4),
+                red = ks > 1 ? up((int64_t)2 * rs * P->cols * ROWS * 4) : 0;
+  const int64_t left = (int64_t)d.max_smem_optin - 4096 - (x + 256 + xs + part + red);
+  const int64_t fit = left / ((int64_t)W * bb);           // blocks a warp's ring can hold
+  if (left < 0 || fit < 2) return false;
+  P->stage = fit >= 6 ? 2 : 1;
+  P->slots = (int)(fit / P->stage < MAX_SLOTS ? fit / P->stage : MAX_SLOTS);
+  P->x_off = (int)up((int64_t)W * P->slots * P->stage * bb);
+  P->zero_off = P->x_off + (int)x;
+  P->xs_off = P->zero_off + 256;
+  P->part_off = P->xs_off + (int)xs;
+  P->red_off = P->part_off + (int)part;
+  P->smem = P->red_off + (int)red;
+  return true;
+}
+
+// What joining the sums of a cluster costs, in blocks that a CTA reads meanwhile.
+constexpr int CLUSTER_COST = 16;
+
+// The number of CTAs along k with the fewest blocks for the busiest CTA, among
+// those whose x fits beside the rings.
+template <int NB, typename Kern>
+static bool choose(const GemvArgs4& a, Kern kern, int cols, Plan* best) {
+  const DevInfo& d = dev_info();
+  const int KB = cdiv(a.K, BK), NS = cdiv(a.N, ROWS);
+  int64_t least = -1;
+  for (int ks = 1; ks <= MAX_CLUSTER && ks <= KB; ks *= 2) {
+    Plan P;
+    P.cols = cols;
+    const int ncl = clusters_of(kern, warps_of(NB) * 32, ks, d);
+    const int64_t cost = (int64_t)cdiv(NS, ncl) * cdiv(KB, ks) + (ks > 1 ? CLUSTER_COST : 0);
+    if ((least < 0 || cost < least) && lay_out(a, NB, ks, ncl, d, &P)) least = cost, *best = P;
+  }
+  return least >= 0;
+}
+
+template <int GROUP, int NB, bool XB, bool SB>
+static cudaError_t run(const GemvArgs4& a, int cols, cudaStream_t s, bool* fits) {
+  const auto kern = gemv_kernel<GROUP, NB, XB, SB>;
+  Plan P;
+  *fits = choose<NB>(a, kern, cols, &P);
+  if (!*fits) return cudaSuccess;
+  P.vec = a.ldx % 8 == 0 && (uintptr_t)a.x % 16 == 0;
+  static thread_local KernCache c;
+  const cudaError_t e = prep_kernel(kern, c, warps_of(NB) * 32, dev_info().max_smem_optin - 4096, nullptr);
+  if (e != cudaSuccess) return e;
+  return launch_step(kern, dim3(P.ncl * P.ks, cdiv(a.M, cols)), warps_of(NB) * 32, P.smem, s, P.ks, a, P);
+}
+
+// Columns in as few launch rows as fit, filled evenly.
+template <int GROUP, bool XB, bool SB>
+static cudaError_t run_m(const GemvArgs4& a, cudaStream_t s) {
+  for (int top = 8 * NBMAX; top >= 1; top = top > 8 ? top - 8 : top / 2) {
+    const int cols = cdiv(a.M, cdiv(a.M, top));
+    bool fits = false;
+    cudaError_t e;
+    switch (cdiv(cols, 8)) {
+      case 1: e = run<GROUP, 1, XB, SB>(a, cols, s, &fits); break;
+      case 2: e = run<GROUP, 2, XB, SB>(a, cols, s, &fits); break;
+      case 3: e = run<GROUP, 3, XB, SB>(a, cols, s, &fits); break;
+      default: e = run<GROUP, 4, XB, SB>(a, cols, s, &fits); break;
+    }
+    if (fits || e != cudaSuccess) return e;
+  }
+  return cudaErrorInvalidConfiguration;    // not reached: one column of MAX_K fits
+}
+
+template <int GROUP, bool XB>
+cudaError_t launch_group(const GemvArgs4& a, cudaStream_t s) {
+  return a.scale_bf16 ? run_m<GROUP, XB, true>(a, s) : run_m<GROUP, XB, false>(a, s);
+}
+
+template <int GROUP, bool XB>
+cudaError_t read_error(int clear, int* out) {
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_w4_error, sizeof(int));
+  if (e == cudaSuccess && clear && *out) {
+    const int z = 0;
+    e = cudaMemcpyToSymbol(g_w4_error, &z, sizeof(int));
+  }
+  return e;
+}
+
+}  // namespace w4
+}  // namespace qmv
