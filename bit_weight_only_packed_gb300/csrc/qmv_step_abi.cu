@@ -106,6 +106,7 @@ int qmv_w4_gemv(const qmv_w4pack* p, int M, const void* x, int ldx, int x_dtype,
   a.y = y;
   a.ldy = ldy;
   a.y_dtype = y_dtype;
+  a.early = qmv::pdl_enabled();
   return done(qmv::w4::launch_w4_gemv(a, (cudaStream_t)stream));
 }
 

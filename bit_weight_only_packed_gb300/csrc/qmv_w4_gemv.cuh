@@ -28,7 +28,11 @@ namespace w4 {
 static __device__ int g_w4_error = 0;
 
 constexpr int MAX_SLOTS = 8, MAX_CLUSTER = 8, NBMAX = 4;
-constexpr int PART_LD = 36;     // floats between the columns of a warp's sums: no bank conflicts
+
+// Where a warp's partial sum of (column m, row) lies: the rows of a column are
+// swapped in eights by column pair, so that the lanes of a warp touch different
+// banks both as the products leave them and row by row.
+__device__ __forceinline__ int part_at(int m, int row) { return m * ROWS + (row ^ (((m >> 1) & 3) << 3)); }
 
 // Warps a CTA: with many columns fewer, whose partial sums leave room for x.
 __host__ __device__ constexpr int warps_of(int nb) { return nb <= 2 ? 16 : 8; }
@@ -135,6 +139,28 @@ static __device__ __noinline__ float plain_sum(const GemvArgs4& a, const uint16_
   return v + sum * s;
 }
 
+// A lane's share of a block: the codes of two 16-row halves and two 64-k tiles,
+// and for each group the scales and zero points of its rows g, g + 8, g + 16, g + 24.
+template <int GPB>
+struct Block {
+  uint4 w[2][2];
+  uint2 sc[GPB];
+  uint32_t zp[GPB];
+  __device__ __forceinline__ void load(const uint8_t* p, int lane, int zeros) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) w[r][q] = *reinterpret_cast<const uint4*>(p + ((r * 2 + q) * 32 + lane) * 16);
+    const uint8_t* meta = p + CODE_BYTES + (lane >> 2) * 8;
+#pragma unroll
+    for (int gi = 0; gi < GPB; ++gi) {
+      sc[gi] = *reinterpret_cast<const uint2*>(meta + gi * (2 * ROWS));
+      zp[gi] = zeros ? *reinterpret_cast<const uint32_t*>(p + CODE_BYTES + 2 * GPB * ROWS + gi * ROWS + (lane >> 2) * 4)
+                     : 0x08080808u;
+    }
+  }
+};
+
 // XB, SB: x and the scales are bf16 (fp16 otherwise).
 template <int GROUP, int NB, bool XB, bool SB>
 __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
@@ -144,7 +170,6 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[W][MAX_SLOTS];
   __shared__ uint64_t x_full;
-  __shared__ int bad[8 * NB];
   __shared__ int abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int KB = cdiv(a.K, BK), NS = cdiv(a.N, ROWS), bb = block_bytes(GROUP, a.zeros != 0);
@@ -159,7 +184,6 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
   const auto first_of = [&](int r, int w) { return (int)((unsigned)(strips_of(r) * kbn) * (unsigned)w / W); };
   uint8_t* ring = smem + (size_t)warp * P.slots * P.stage * bb;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (tid < 8 * NB) bad[tid] = 0;
   if (tid == 0) abort_flag = 0;
 
   // Lane 0 keeps the ring full.  A copy is up to `stage` neighbouring blocks of a strip.
@@ -189,6 +213,7 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
     for (int i = 0; i < P.slots; ++i) pipe::mbar_init(&full[warp][i], 1);
     if (warp == 0) pipe::mbar_init(&x_full, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if (!a.early) asm volatile("griddepcontrol.wait;" ::: "memory");
     next_round();
     for (int i = 0; i < P.slots && p_left > 0; ++i) issue(i);
   }
@@ -210,34 +235,11 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
 #pragma unroll 4
       for (int k = tid; k < klim; k += NT) reinterpret_cast<uint16_t*>(xs + m * P.pitch)[k] = xg[(int64_t)m * a.ldx + k];
   }
-  for (int m = 0; m < mc; ++m)                            // up to 96 k past the end
-    for (int k = klim + tid; k < kbn * BK; k += NT) reinterpret_cast<uint16_t*>(xs + m * P.pitch)[k] = 0;
+  if (klim < kbn * BK && tid < kbn * BK - klim)           // up to 96 k past the end
+    for (int m = 0; m < mc; ++m) reinterpret_cast<uint16_t*>(xs + m * P.pitch)[klim + tid] = 0;
   __syncthreads();
   if (P.vec && !pipe::mbar_wait_fast(&x_full, 0, &abort_flag, pipe::ERR_TIMEOUT_TFULL, &g_w4_error))
     pipe::mbar_drain(&x_full, 0, &g_w4_error);           // nothing is stored after a wait that ran out
-
-  // The sums of x, a group each: 16 lanes take a block of a column, eight k a lane.
-  float* xsum = reinterpret_cast<float*>(smem + P.xs_off);             // [group][8 * NB]
-  for (int b = 2 * warp + (lane >> 4), m = 0;; b += 2 * W) {
-    while (b >= kbn && m < mc) b -= kbn, ++m;
-    if (__all_sync(~0u, m >= mc)) break;
-    float sum = 0.0f, mag = 0.0f;
-    if (m < mc) {
-      const uint4 v = *reinterpret_cast<const uint4*>(xs + m * P.pitch + b * 256 + (lane & 15) * 16);
-      const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const float u0 = f16_f(in[p] & 0xffffu, XB), u1 = f16_f(in[p] >> 16, XB);
-        sum += u0 + u1;
-        mag += fabsf(u0) + fabsf(u1);
-      }
-      if (!(mag < 1e35f)) bad[m] = 1;
-    }
-#pragma unroll
-    for (int q = GROUP / 16; q; q >>= 1) sum += __shfl_xor_sync(~0u, sum, q);
-    if (m < mc && (lane & (GROUP / 8 - 1)) == 0) xsum[(b * GPB + (lane & 15) / (GROUP / 8)) * (8 * NB) + m] = sum;
-  }
-  __syncthreads();
 
   // Where a lane reads x; lanes past the last column read zeros.
   const bool in_last = 8 * (NB - 1) + g < mc;
@@ -247,176 +249,172 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
   if (!in_last) xp[NB - 1] = smem + P.zero_off + t * 16;
   const int l_step = in_last ? 256 : 0;
 
+  // The sums of x over each group, by the same instructions with ones for weights.
+  float* xsum = reinterpret_cast<float*>(smem + P.xs_off);             // [group][8 * NB]
+  for (int b = warp; b < kbn; b += W) {
+    constexpr uint32_t ONE = XB ? 0x3F803F80u : 0x3C003C00u;
+#pragma unroll
+    for (int c = 0; c < NB; ++c)
+#pragma unroll
+      for (int gi = 0; gi < GPB; ++gi) {
+        float d[4] = {};
+#pragma unroll
+        for (int hh = 0; hh < HPG; ++hh) {
+          const uint4 v = *reinterpret_cast<const uint4*>(xp[c] + b * (c < NB - 1 ? 256 : l_step) + (gi * HPG + hh) * 64);
+          mma16816<XB>(d, d, ONE, ONE, ONE, ONE, v.x, v.y);
+          mma16816<XB>(d, d, ONE, ONE, ONE, ONE, v.z, v.w);
+        }
+        if (g == 0) *reinterpret_cast<float2*>(xsum + (b * GPB + gi) * (8 * NB) + 8 * c + 2 * t) = make_float2(d[0], d[1]);
+      }
+  }
+  __syncthreads();
+
   float* red = reinterpret_cast<float*>(smem + P.red_off);             // [2][rs][mc][32], clusters only
-  float* part = reinterpret_cast<float*>(smem + P.part_off);           // [W][mc][PART_LD]
-  // A finished sum goes out (or to the cluster's sum).
-  const auto emit = [&](int round, int s, int m, int row, float v) {
+  float* part = reinterpret_cast<float*>(smem + P.part_off);           // [W][2][mc][32]
+  // A finished sum goes out (or to the cluster's sum).  One that is not finite is
+  // formed again by its definition.
+  const auto emit = [&](int round, int s, int m, float v) {
     if (!XB) v *= 2097152.0f;
-    const int64_t n = (int64_t)(S0 + round * P.rs + s) * ROWS + row;
-    if (bad[m] && n < a.N)
+    const int64_t n = (int64_t)(S0 + round * P.rs + s) * ROWS + lane;
+    if (!(fabsf(v) <= 3.402823466e38f) && n < a.N)
       v = plain_sum(a, reinterpret_cast<const uint16_t*>(xs + m * P.pitch), (int)n, kb0 * BK, kb0 * BK + klim);
     if (P.ks > 1)
-      red[(((round & 1) * P.rs + s) * mc + m) * 32 + row] = v;
+      red[(((round & 1) * P.rs + s) * mc + m) * 32 + lane] = v;
     else if (n < a.N && !abort_flag)
       store_y(a.y, (int64_t)(m0 + m) * a.ldy + n, a.y_dtype, v);
   };
 
   const uint32_t bits3 = in_register<0x00780078u>(), sixteen = in_register<0x41804180u>();   // bf16 codes
+  // One block (the CTA's b-th of k) of a strip, added to tot.
+  const auto product = [&](const Block<GPB>& B, int b, float (&tot)[2][NB][4]) {
+    const int xo = b * 256, xl = b * l_step;
+    const float* sxp = xsum + b * (GPB * 8 * NB) + 2 * t;
+#pragma unroll
+    for (int gi = 0; gi < GPB; ++gi) {
+      constexpr int KINDS = XB ? 1 : 2;          // fp16 codes have two scales
+      float acc[KINDS][2][NB][4];
+      const float none[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int hh = 0; hh < HPG; ++hh) {
+        const int st = gi * HPG + hh, q = st >> 1, h = st & 1;   // 32 k of the block
+        uint4 xv[NB];
+#pragma unroll
+        for (int c = 0; c < NB; ++c) xv[c] = *reinterpret_cast<const uint4*>(xp[c] + (c < NB - 1 ? xo : xl) + st * 64);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t u = h ? B.w[r][q].y : B.w[r][q].x, v = h ? B.w[r][q].w : B.w[r][q].z;   // rows g, g + 8
+          if (XB) {
+            uint32_t p[4], o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              p[i] = and_or(i ? rot(u, 4 * i) : u, bits3, sixteen);
+              o[i] = and_or(i ? rot(v, 4 * i) : v, bits3, sixteen);
+            }
+#pragma unroll
+            for (int c = 0; c < NB; ++c) {
+              float(&d)[4] = acc[0][r][c];
+              mma16816<XB>(d, hh ? d : none, p[0], o[0], p[2], o[2], xv[c].x, xv[c].y);
+              mma16816<XB>(d, d, p[1], o[1], p[3], o[3], xv[c].z, xv[c].w);
+            }
+          } else {
+            constexpr uint32_t L = 0x00780078u, H = 0x07800780u;
+            const uint32_t u8 = rot(u, 8), v8 = rot(v, 8);
+#pragma unroll
+            for (int c = 0; c < NB; ++c) {
+              float(&d)[4] = acc[0][r][c];
+              float(&e)[4] = acc[KINDS - 1][r][c];
+              mma16816<XB>(d, hh ? d : none, u & L, v & L, u8 & L, v8 & L, xv[c].x, xv[c].y);
+              mma16816<XB>(e, hh ? e : none, u & H, v & H, u8 & H, v8 & H, xv[c].z, xv[c].w);
+            }
+          }
+        }
+      }
+      float2 sx[NB];
+#pragma unroll
+      for (int c = 0; c < NB; ++c) sx[c] = *reinterpret_cast<const float2*>(sxp + gi * (8 * NB) + 8 * c);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint32_t s2 = r ? B.sc[gi].y : B.sc[gi].x;
+        const float s0 = f16_f(s2 & 0xffffu, SB), s1 = SB ? __uint_as_float(s2 & 0xffff0000u) : f16_f(s2 >> 16, SB);
+        const float z0 = zero_f<XB>(B.zp[gi], 2 * r), z1 = zero_f<XB>(B.zp[gi], 2 * r + 1);
+#pragma unroll
+        for (int c = 0; c < NB; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float v = acc[0][r][c][e];
+            if (!XB) v = fmaf(acc[KINDS - 1][r][c][e], 0.0625f, v);
+            v = fmaf(-(e < 2 ? z0 : z1), e & 1 ? sx[c].y : sx[c].x, v);
+            tot[r][c][e] = fmaf(e < 2 ? s0 : s1, v, tot[r][c][e]);
+          }
+      }
+    }
+  };
   int slot = 0, parity = 0;
   for (int round = 0; round < rounds; ++round) {
     const int lo = first_of(round, warp), hi = first_of(round, warp + 1);
-    const int s_lo = (int)((unsigned)lo / (unsigned)kbn);
+    const int s_lo = (int)((unsigned)lo / (unsigned)kbn), F = strips_of(round) * kbn;
     int s = s_lo, blk = lo - s * kbn, f = lo, from = blk;
     float tot[2][NB][4] = {};
-    bool head = true, tail = false;        // the first strip of the range; its last, left unfinished in tot
+    float* mine = part + warp * (2 * mc * ROWS);
+    int place = 0;                         // the first strip of the range, later ones
     while (f < hi) {
       const int cnt = min(P.stage, min(hi - f, kbn - blk));
       if (!__all_sync(~0u, pipe::mbar_wait_fast(&full[warp][slot], parity, &abort_flag, pipe::ERR_TIMEOUT_FULL, &g_w4_error)))
         break;
       const uint8_t* p = ring + slot * P.stage * bb;
-      for (int i = 0; i < cnt; ++i, p += bb) {
-        uint4 w[2][2];
+      Block<GPB> A, B;
+      A.load(p, lane, a.zeros);
+      if (cnt > 1) B.load(p + bb, lane, a.zeros);
+      ++used;
+      __syncwarp();                        // every lane has read the slot: fill it again
+      if (lane == 0 && p_left > 0) issue(slot);
+      if (++slot == P.slots) slot = 0, parity ^= 1;
+      product(A, blk, tot);
+      if (cnt > 1) product(B, blk + 1, tot);
+      f += cnt;
+      blk += cnt;
+      if (blk == kbn || f == hi) {         // the end of the strip, or of the range
+        float* to = mine + place * (mc * ROWS);
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
-          for (int q = 0; q < 2; ++q) w[r][q] = *reinterpret_cast<const uint4*>(p + ((r * 2 + q) * 32 + lane) * 16);
-        const uint8_t* meta = p + CODE_BYTES;
-        uint2 sc[GPB];
-        uint32_t zp[GPB];
+          for (int c = 0; c < NB; ++c)
 #pragma unroll
-        for (int gi = 0; gi < GPB; ++gi) {
-          sc[gi] = *reinterpret_cast<const uint2*>(meta + 2 * (gi * ROWS + g * 4));
-          zp[gi] = a.zeros ? *reinterpret_cast<const uint32_t*>(meta + 2 * GPB * ROWS + gi * ROWS + g * 4) : 0x08080808u;
-        }
-        if (i == cnt - 1) {                // every lane has read the slot: fill it again
-          ++used;
-          __syncwarp();
-          if (lane == 0 && p_left > 0) issue(slot);
-        }
-        const int xo = (blk + i) * 256, xl = (blk + i) * l_step;
-        const float* sxp = xsum + (blk + i) * (GPB * 8 * NB) + 2 * t;
-#pragma unroll
-        for (int gi = 0; gi < GPB; ++gi) {
-          constexpr int KINDS = XB ? 1 : 2;          // fp16 codes have two scales
-          float acc[KINDS][2][NB][4];
-          const float none[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int hh = 0; hh < HPG; ++hh) {
-            const int st = gi * HPG + hh, q = st >> 1, h = st & 1;   // 32 k of the block
-            uint4 xv[NB];
-#pragma unroll
-            for (int c = 0; c < NB; ++c)
-              xv[c] = *reinterpret_cast<const uint4*>(xp[c] + (c < NB - 1 ? xo : xl) + st * 64);
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const uint32_t u = h ? w[r][q].y : w[r][q].x, v = h ? w[r][q].w : w[r][q].z;   // rows g, g + 8
-              if (XB) {
-                uint32_t p[4], o[4];
-#pragma unroll
-                for (int i4 = 0; i4 < 4; ++i4) {
-                  p[i4] = and_or(i4 ? rot(u, 4 * i4) : u, bits3, sixteen);
-                  o[i4] = and_or(i4 ? rot(v, 4 * i4) : v, bits3, sixteen);
-                }
-#pragma unroll
-                for (int c = 0; c < NB; ++c) {
-                  float(&d)[4] = acc[0][r][c];
-                  mma16816<XB>(d, hh ? d : none, p[0], o[0], p[2], o[2], xv[c].x, xv[c].y);
-                  mma16816<XB>(d, d, p[1], o[1], p[3], o[3], xv[c].z, xv[c].w);
-                }
-              } else {
-                constexpr uint32_t L = 0x00780078u, H = 0x07800780u;
-                const uint32_t u8 = rot(u, 8), v8 = rot(v, 8);
-#pragma unroll
-                for (int c = 0; c < NB; ++c) {
-                  float(&d)[4] = acc[0][r][c];
-                  float(&e)[4] = acc[KINDS - 1][r][c];
-                  mma16816<XB>(d, hh ? d : none, u & L, v & L, u8 & L, v8 & L, xv[c].x, xv[c].y);
-                  mma16816<XB>(e, hh ? e : none, u & H, v & H, u8 & H, v8 & H, xv[c].z, xv[c].w);
-                }
-              }
+            for (int e = 0; e < 4; ++e) {
+              const int m = 8 * c + 2 * t + (e & 1);
+              if (m < mc) to[part_at(m, 16 * r + 8 * (e >> 1) + g)] = tot[r][c][e];
+              tot[r][c][e] = 0.0f;
             }
-          }
-          float2 sx[NB];
-#pragma unroll
-          for (int c = 0; c < NB; ++c) sx[c] = *reinterpret_cast<const float2*>(sxp + gi * (8 * NB) + 8 * c);
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const uint32_t s2 = r ? sc[gi].y : sc[gi].x;
-            const float s0 = f16_f(s2 & 0xffffu, SB), s1 = SB ? __uint_as_float(s2 & 0xffff0000u) : f16_f(s2 >> 16, SB);
-            const float z0 = zero_f<XB>(zp[gi], 2 * r), z1 = zero_f<XB>(zp[gi], 2 * r + 1);
-#pragma unroll
-            for (int c = 0; c < NB; ++c)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                float v = acc[0][r][c][e];
-                if (!XB) v = fmaf(acc[KINDS - 1][r][c][e], 0.0625f, v);
-                v = fmaf(-(e < 2 ? z0 : z1), e & 1 ? sx[c].y : sx[c].x, v);
-                tot[r][c][e] = fmaf(e < 2 ? s0 : s1, v, tot[r][c][e]);
-              }
-          }
+        if (from == 0 && blk == kbn) {     // the whole strip
+          __syncwarp();
+#pragma unroll 1
+          for (int m = 0; m < mc; ++m) emit(round, s, m, to[part_at(m, lane)]);
+          __syncwarp();
         }
-      }
-      if (++slot == P.slots) slot = 0, parity ^= 1;
-      f += cnt;
-      blk += cnt;
-      if (blk == kbn || f == hi) {
-        const bool whole = from == 0 && blk == kbn;
-        tail = !whole && !head;
-        if (!tail) {
-#pragma unroll
-          for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int c = 0; c < NB; ++c)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int m = 8 * c + 2 * t + (e & 1), row = 16 * r + 8 * (e >> 1) + g;
-                if (m < mc) {
-                  if (whole)
-                    emit(round, s, m, row, tot[r][c][e]);
-                  else
-                    part[(warp * mc + m) * PART_LD + row] = tot[r][c][e];
-                }
-                tot[r][c][e] = 0.0f;
-              }
-          ++s;
-          blk = from = 0;
-          head = false;
-        }
+        ++s;
+        blk = from = 0;
+        place = 1;
       }
     }
-    const int F = strips_of(round) * kbn;
-    if (lo == hi && lo < F)                  // fewer blocks than warps: nothing to add
-      for (int m = 0; m < mc; ++m) part[(warp * mc + m) * PART_LD + lane] = 0.0f;
+    if (lo == hi && lo < F)                // fewer blocks than warps: nothing to add
+      for (int m = 0; m < mc; ++m) mine[part_at(m, lane)] = 0.0f;
     __syncthreads();
     // Strips that several warps share: the warps w0 .. w0 + nw - 1 whose ranges begin in
-    // the strip share out its columns.  Where the strip itself begins one of the
-    // ranges, its pieces are all in `part`; else its first piece is in the registers of
-    // warp w0 - 1, which finds the sum of the others in w0's place.
+    // the strip share out its columns.  Their pieces are in their first places, and
+    // where the strip begins inside a range, one more in warp w0 - 1's second.
     if (lo < F) {
-      const int st = s_lo, begin = st * kbn, end = begin + kbn;
+      const int begin = s_lo * kbn, end = begin + kbn;
       const int w0 = (int)(((unsigned)begin * W + F - 1) / F), nw = (int)(((unsigned)end * W + F - 1) / F) - w0;
-      const bool begins = first_of(round, w0) == begin, whole = first_of(round, w0 + nw - 1) == begin;
-      if (!whole && (begins || nw > 1))      // one warp had the whole strip, or one other piece is there
+      const bool inside = first_of(round, w0) != begin, whole = first_of(round, w0 + nw - 1) == begin;
+      if (!whole) {                        // else one warp had all of it
+        const float* from0 = part + w0 * (2 * mc * ROWS);
+#pragma unroll 1
         for (int m = warp - w0; m < mc; m += nw) {
-          float v = part[(w0 * mc + m) * PART_LD + lane];
-          for (int q = 1; q < nw; ++q) v += part[((w0 + q) * mc + m) * PART_LD + lane];
-          if (begins)
-            emit(round, st, m, lane, v);
-          else
-            part[(w0 * mc + m) * PART_LD + lane] = v;
+          float v = inside ? from0[part_at(m, lane) - mc * ROWS] : 0.0f;
+          for (int q = 0; q < nw; ++q) v += from0[q * (2 * mc * ROWS) + part_at(m, lane)];
+          emit(round, s_lo, m, v);
         }
-    }
-    __syncthreads();
-    if (tail) {
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int c = 0; c < NB; ++c)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int m = 8 * c + 2 * t + (e & 1), row = 16 * r + 8 * (e >> 1) + g;
-            if (m < mc) emit(round, s, m, row, tot[r][c][e] + part[((warp + 1) * mc + m) * PART_LD + row]);
-          }
+      }
     }
     if (P.ks > 1) {
       // the CTAs of a cluster add theirs, each finishing a share; two buffers, so that the
@@ -509,12 +507,12 @@ static bool lay_out(const GemvArgs4& a, int nb, int ks, int ncl, const DevInfo& 
   const auto up = [](int64_t v) { return (v + 127) & ~(int64_t)127; };
   P->pitch = P->kbs * 256 + 64;
   const int64_t x = up((int64_t)P->pitch * P->cols), xs = up((int64_t)P->kbs * (BK / a.group) * 8 * nb * 4),
-                part = up((int64_t)W * P->cols * PART_LD * 4),
+                part = up((int64_t)W * 2 * P->cols * ROWS * 4),
                 red = ks > 1 ? up((int64_t)2 * rs * P->cols * ROWS * 4) : 0;
   const int64_t left = (int64_t)d.max_smem_optin - 4096 - (x + 256 + xs + part + red);
   const int64_t fit = left / ((int64_t)W * bb);           // blocks a warp's ring can hold
   if (left < 0 || fit < 2) return false;
-  P->stage = fit >= 6 ? 2 : 1;
+  P->stage = fit >= 4 ? 2 : 1;
   P->slots = (int)(fit / P->stage < MAX_SLOTS ? fit / P->stage : MAX_SLOTS);
   P->x_off = (int)up((int64_t)W * P->slots * P->stage * bb);
   P->zero_off = P->x_off + (int)x;

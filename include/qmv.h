@@ -309,6 +309,10 @@ QMV_API int qmv_destroy_pack(qmv_pack *p);
  * Requirement: the packed weights of a matvec must not be written by the
  * kernel launched just before it in the stream (pack once, then run).
  * Works under stream capture (CUDA graphs).  Always returns QMV_OK.
+ * (The verification-step calls below always let their launch overlap the end of
+ * the kernel before, and wait for it before they touch memory; with this on,
+ * qmv_w4_gemv also begins to stream its weights before that wait, under the
+ * same requirement.)
  */
 QMV_API int qmv_set_pdl(int enable);
 
