@@ -11,40 +11,26 @@ constexpr int MAX_NT = 512, MAX_C = 16;
 
 // ----------------------------------------------------------------- softmax --
 
-// What a CTA knows of its part of a row, and two parts joined.
-struct Part {
-  float m, s;      // maximum; sum of exp((x - m) / T)
-  int at, bad;     // first place of the maximum; NaN or +inf seen
-};
-
-__device__ __forceinline__ void join_max(Part& a, const Part& b) {
-  if (b.m > a.m || (b.m == a.m && b.at < a.at)) a.m = b.m, a.at = b.at;
-  a.bad |= b.bad;
-}
-
-// Maximum (and sum, once every part is relative to one maximum) over a CTA.
-__device__ __forceinline__ Part block_max(Part p, Part* red) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    Part q;
-    q.m = __shfl_xor_sync(~0u, p.m, o);
-    q.at = __shfl_xor_sync(~0u, p.at, o);
-    q.bad = __shfl_xor_sync(~0u, p.bad, o);
-    join_max(p, q);
-  }
+// The largest value of a CTA, and the first place of it (asked for by `place`).
+__device__ __forceinline__ void block_max(float& m, int& at, bool place, float* red, int* redi) {
   const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-  if (lane == 0) red[threadIdx.x >> 5] = p;
-  __syncthreads();
-  p = red[lane < nw ? lane : 0];
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    Part q;
-    q.m = __shfl_xor_sync(~0u, p.m, o);
-    q.at = __shfl_xor_sync(~0u, p.at, o);
-    q.bad = __shfl_xor_sync(~0u, p.bad, o);
-    join_max(p, q);
+  for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      const float m2 = __shfl_xor_sync(~0u, m, o);
+      if (place) {
+        const int a2 = __shfl_xor_sync(~0u, at, o);
+        if (m2 > m || (m2 == m && a2 < at)) at = a2;
+      }
+      m = fmaxf(m, m2);
+    }
+    if (pass) break;
+    if (lane == 0) red[threadIdx.x >> 5] = m, redi[threadIdx.x >> 5] = at;
+    __syncthreads();
+    m = red[lane < nw ? lane : 0];
+    at = redi[lane < nw ? lane : 0];
   }
-  return p;
 }
 
 __device__ __forceinline__ float block_sum(float v, float* red) {
@@ -59,13 +45,22 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   return v;
 }
 
+// What a CTA knows of its part of a row.
+struct Part {
+  float m, s;      // maximum; sum of exp((x - m) / T), in the one-hot form of 0 * x (NaN marks the row)
+  int at;          // first place of the maximum
+};
+
 // A cluster of C CTAs a row (C = 1: no cluster).  EPT > 0: a CTA's part of the
 // row stays in registers, EPT elements a thread, so that the row is read once;
 // EPT == 0: a part of any length, read a second and third time (from L2).
+// exp((x - m) / T) is taken as exp2((x - m) * c), c = log2(e) / T.  A row with
+// NaN or +inf has the sum NaN, which reaches every place by itself.
 template <typename X, int EPT>
-__global__ void __launch_bounds__(MAX_NT) softmax_kernel(SoftmaxArgs a, int C, int len) {
-  __shared__ Part red[MAX_NT / 32], mine;
-  __shared__ float reds[MAX_NT / 32];
+__global__ void __launch_bounds__(MAX_NT, 2) softmax_kernel(SoftmaxArgs a, int C, int len) {
+  __shared__ Part mine;
+  __shared__ float redm[MAX_NT / 32], reds[MAX_NT / 32];
+  __shared__ int redi[MAX_NT / 32];
   const int row = blockIdx.x / C, rank = blockIdx.x - row * C, NT = blockDim.x, tid = threadIdx.x;
   const int v0 = min(a.V, rank * len), n = min(a.V - v0, len);     // this CTA's part
   const X* x = (const X*)a.x + (int64_t)row * a.ldx + v0;
@@ -73,84 +68,84 @@ __global__ void __launch_bounds__(MAX_NT) softmax_kernel(SoftmaxArgs a, int C, i
   pdl_begin();
   const float t = a.t ? a.t[row] : a.t0;
   const bool hot = !(t > 0.0f);
-  // 1/T of a subnormal T is infinite; the largest finite factor keeps 0 * it = 0
-  const float it = hot ? 0.0f : fminf(1.0f / t, 3.402823466e38f);
+  // kept finite and above 0, so that 0 * c = 0 and -inf * c = -inf at any T
+  const float c = fminf(fmaxf(1.4426950408889634f / t, 1e-37f), 1e38f);
   constexpr int R = EPT ? EPT : 1;
   float e[R];
-  Part p{-CUDART_INF_F, 0.0f, a.V, 0};
+  Part p{-CUDART_INF_F, 0.0f, a.V};
   if (EPT) {
 #pragma unroll
     for (int j = 0; j < R; ++j) e[j] = j * NT + tid < n ? to_f<X>(x[j * NT + tid]) : -CUDART_INF_F;
 #pragma unroll
-    for (int j = 0; j < R; ++j) {
-      if (e[j] > p.m) p.m = e[j], p.at = v0 + j * NT + tid;
-      p.bad |= !(e[j] < CUDART_INF_F);
+    for (int j = 0; j < R; ++j) p.m = fmaxf(p.m, e[j]);
+    if (hot) {
+#pragma unroll
+      for (int j = R - 1; j >= 0; --j) {
+        if (e[j] == p.m) p.at = v0 + j * NT + tid;
+        if (!(e[j] < CUDART_INF_F)) p.s = CUDART_NAN_F;
+      }
     }
   } else {
     for (int i = tid; i < n; i += NT) {
       const float v = to_f<X>(x[i]);
       if (v > p.m) p.m = v, p.at = v0 + i;
-      p.bad |= !(v < CUDART_INF_F);
+      if (hot && !(v < CUDART_INF_F)) p.s = CUDART_NAN_F;
     }
   }
-  p = block_max(p, red);
+  block_max(p.m, p.at, hot, redm, redi);
   // nothing but -inf so far: any finite maximum will do, every term is 0
   const float m = p.m == -CUDART_INF_F ? 0.0f : p.m;
-  float s = 0.0f;
-  if (EPT) {
+  if (!hot) {
+    if (EPT) {
 #pragma unroll
-    for (int j = 0; j < R; ++j) {
-      e[j] = e[j] == -CUDART_INF_F ? 0.0f : expf((e[j] - m) * it);
-      s += e[j];
-    }
-  } else {
-    for (int i = tid; i < n; i += NT) {
-      const float v = to_f<X>(x[i]);
-      s += v == -CUDART_INF_F ? 0.0f : expf((v - m) * it);
+      for (int j = 0; j < R; ++j) {
+        e[j] = exp2f((e[j] - m) * c);
+        p.s += e[j];
+      }
+    } else {
+      for (int i = tid; i < n; i += NT) p.s += exp2f((to_f<X>(x[i]) - m) * c);
     }
   }
-  p.s = block_sum(s, reds);
+  p.s = block_sum(p.s, reds);
   Part all = p;
   if (C > 1) {
     if (tid == 0) mine = p;
     cluster_arrive();
     cluster_wait();
-    const uint32_t at = cluster_addr(&mine, (tid & 31) < C ? (tid & 31) : 0);
+    const int lane = tid & 31;
+    const uint32_t at = cluster_addr(&mine, lane < C ? lane : 0);
     Part q;
     q.m = __uint_as_float(ld_cluster32(at));
-    q.s = (tid & 31) < C ? __uint_as_float(ld_cluster32(at + 4)) : 0.0f;
+    q.s = __uint_as_float(ld_cluster32(at + 4));
     q.at = (int)ld_cluster32(at + 8);
-    q.bad = (int)ld_cluster32(at + 12);
     cluster_arrive();                        // waited for at the end: the others still read `mine`
     all = q;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
-      Part w;
-      w.m = __shfl_xor_sync(~0u, all.m, o);
-      w.at = __shfl_xor_sync(~0u, all.at, o);
-      w.bad = __shfl_xor_sync(~0u, all.bad, o);
-      join_max(all, w);
+      const float m2 = __shfl_xor_sync(~0u, all.m, o);
+      const int a2 = __shfl_xor_sync(~0u, all.at, o);
+      if (m2 > all.m || (m2 == all.m && a2 < all.at)) all.at = a2;
+      all.m = fmaxf(all.m, m2);
     }
-    float sum = q.m == -CUDART_INF_F ? 0.0f : q.s * expf((q.m - all.m) * it);
+    float sum = lane >= C || q.m == -CUDART_INF_F ? 0.0f : hot ? q.s : q.s * exp2f((q.m - all.m) * c);
+    // a part of NaN alone has the maximum -inf and the sum NaN
+    if (lane < C && isnan(q.s)) sum = q.s;
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
     all.s = sum;
   }
-  // special rows: NaN or +inf anywhere, nothing but -inf, the one-hot form
-  if (all.bad || all.m == -CUDART_INF_F || hot) {
-    for (int i = tid; i < n; i += NT)
-      out[i] = all.bad ? CUDART_NAN_F : hot && v0 + i == all.at ? 1.0f : 0.0f;
+  if (hot || all.m == -CUDART_INF_F) {       // the one-hot form, or nothing but -inf (or NaN)
+    const float rest = isnan(all.s) ? all.s : 0.0f, one = all.m == -CUDART_INF_F ? rest : 1.0f + rest;
+    for (int i = tid; i < n; i += NT) out[i] = v0 + i == all.at ? one : rest;
   } else {
-    const float f = expf((m - all.m) * it) / all.s;   // a part of -inf alone has only zeros
+    // at most 1 over the sum; 0 where this part had only -inf, whose terms are 0
+    const float f = exp2f((p.m - all.m) * c) / all.s;
     if (EPT) {
 #pragma unroll
       for (int j = 0; j < R; ++j)
-        if (j * NT + tid < n) out[j * NT + tid] = p.m == -CUDART_INF_F ? 0.0f : e[j] * f;
+        if (j * NT + tid < n) out[j * NT + tid] = e[j] * f;
     } else {
-      for (int i = tid; i < n; i += NT) {
-        const float v = to_f<X>(x[i]);
-        out[i] = v == -CUDART_INF_F ? 0.0f : expf((v - all.m) * it) / all.s;
-      }
+      for (int i = tid; i < n; i += NT) out[i] = exp2f((to_f<X>(x[i]) - all.m) * c) / all.s;
     }
   }
   if (C > 1) cluster_wait();
@@ -185,11 +180,20 @@ cudaError_t softmax_x(const SoftmaxArgs& a, cudaStream_t s) {
 
 // ------------------------------------------------------------------ verify --
 
-// A weight in whole units of 2^-42, clamped to 0..1; NaN counts as 0.
-__device__ __forceinline__ long long units(float w) {
+// A weight, clamped to 0..1 (NaN counts as 0), in whole units of 2^-42 as hi *
+// 2^21 + lo.  Adding 2^23 while rounding towards 0 leaves the whole part of a
+// number below 2^23 in the mantissa, so hi and lo come from four operations of
+// the floating-point pipe; both are returned on top of the bits of 2^23, which
+// the sums take off at the end (modulo 2^32).
+constexpr uint32_t BIAS = 0x4B000000u;
+__device__ __forceinline__ void units(float w, uint32_t& hi, uint32_t& lo) {
   w = fminf(fmaxf(w, 0.0f), 1.0f);        // fmaxf(NaN, 0) = 0
-  return __float2ll_rz(w * 4398046511104.0f);
+  const float h = __fmaf_rz(w, 2097152.0f, 8388608.0f);
+  const float rem = __fmaf_rn(w, 2097152.0f, -(h - 8388608.0f));   // exact, below 1
+  hi = __float_as_uint(h);
+  lo = __float_as_uint(__fmaf_rz(rem, 2097152.0f, 8388608.0f));
 }
+__device__ __forceinline__ long long whole(uint32_t hi, uint32_t lo) { return ((long long)hi << 21) + lo; }
 
 __device__ __forceinline__ long long warp_sum(long long v) {
 #pragma unroll
@@ -208,32 +212,44 @@ __device__ __forceinline__ long long warp_before(long long v) {
   return s - v;
 }
 
-// A chunk: 256 neighbouring ids, eight a lane (chunk + 32 j + lane), as units.
-// q: the draft's row, or null; hot: the id whose q is 1 where the drafter was sure.
+// A chunk: 256 neighbouring ids, eight a lane (chunk + 32 j + lane).
 constexpr int CHUNK = 256;
-__device__ __forceinline__ void load_chunk(const float* p, const float* q, int hot, int at, int V, long long (&u)[8]) {
-  const int lane = threadIdx.x & 31;
+struct Chunk {
   float x[8], y[8];
+  __device__ __forceinline__ void load(const float* p, const float* q, int at, int V) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int v = at + 32 * j + lane;
-    x[j] = v < V ? p[v] : 0.0f;
-    y[j] = q && v < V ? q[v] : 0.0f;
+    for (int j = 0; j < 8; ++j) {
+      const int v = at + 32 * j + lane;
+      x[j] = v < V ? p[v] : 0.0f;
+      y[j] = q && v < V ? q[v] : 0.0f;
+    }
   }
+  // hot: the id whose q is 1 where the drafter was sure
+  __device__ __forceinline__ float weight(int j, int at, int hot) const {
+    return x[j] - (at + 32 * j + (int)(threadIdx.x & 31) == hot ? 1.0f : y[j]);
+  }
+  __device__ __forceinline__ long long sum(int at, int hot) const {
+    uint32_t h = 0, l = 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int v = at + 32 * j + lane;
-    u[j] = units(x[j] - (v == hot ? 1.0f : y[j]));
+    for (int j = 0; j < 8; ++j) {
+      uint32_t hi, lo;
+      units(weight(j, at, hot), hi, lo);
+      h += hi;
+      l += lo;
+    }
+    // at most 2^21 a weight, 2^29 a chunk
+    return whole(__reduce_add_sync(~0u, h - 8 * BIAS), __reduce_add_sync(~0u, l - 8 * BIAS));
   }
-}
+};
 
 // A cluster of C CTAs a sequence; warps own `per` consecutive chunks each and
 // keep every chunk's sum, so that after the total is known one warp re-reads the
 // one chunk in which the running sum passes the threshold.
-constexpr int MAX_PER = 32;
-static_assert((int64_t)8 * (MAX_NT / 32) * MAX_PER * CHUNK >= 1 << 20, "a chunk sum for every id");
-__global__ void __launch_bounds__(MAX_NT) verify_kernel(VerifyArgs a, int C, int per) {
-  constexpr int NW = MAX_NT / 32;
+constexpr int V_NT = 256, V_NW = V_NT / 32, MAX_PER = 64;
+static_assert((int64_t)8 * V_NW * MAX_PER * CHUNK >= 1 << 20, "a chunk sum for every id");
+__global__ void __launch_bounds__(V_NT, 4) verify_kernel(VerifyArgs a, int C, int per) {
+  constexpr int NW = V_NW;
   __shared__ long long chunk[NW][MAX_PER], wsum[NW], mine[2];
   __shared__ int s_acc;
   const int b = blockIdx.x / C, rank = blockIdx.x - b * C, V = a.V, S = a.S;
@@ -248,7 +264,7 @@ __global__ void __launch_bounds__(MAX_NT) verify_kernel(VerifyArgs a, int C, int
   // the first drafted token that does not stand
   if (threadIdx.x == 0) s_acc = n;
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += MAX_NT) {
+  for (int i = threadIdx.x; i < n; i += V_NT) {
     const int d = draft[i];
     bool ok = d >= 0 && d < V;
     if (ok) {
@@ -267,17 +283,12 @@ __global__ void __launch_bounds__(MAX_NT) verify_kernel(VerifyArgs a, int C, int
   long long total = 0, before = 0, own = 0;
   for (int pass = 0; pass < 2; ++pass) {
     long long w = 0;
-    for (int i = 0; i < per; ++i) {
-      const int at = (first + i) * CHUNK;
-      if (at >= V) {
-        if (lane == 0) chunk[warp][i] = 0;
-        continue;
-      }
-      long long u[8], s = 0;
-      load_chunk(p, q, hot, at, V, u);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s += u[j];
-      s = warp_sum(s);
+    const int last = min(per, max(0, (V + CHUNK - 1) / CHUNK - first));
+#pragma unroll 2
+    for (int i = 0; i < last; ++i) {
+      Chunk c;
+      c.load(p, q, (first + i) * CHUNK, V);
+      const long long s = c.sum((first + i) * CHUNK, hot);
       if (lane == 0) chunk[warp][i] = s;
       w += s;
     }
@@ -302,7 +313,7 @@ __global__ void __launch_bounds__(MAX_NT) verify_kernel(VerifyArgs a, int C, int
   if (C > 1) cluster_arrive();          // waited for at the end: the others still read `mine`
   int* out = a.tokens + (int64_t)b * (S + 1);
   if (rank == 0) {
-    for (int i = threadIdx.x; i <= S; i += MAX_NT)
+    for (int i = threadIdx.x; i <= S; i += V_NT)
       if (i != acc || total == 0) out[i] = i < acc ? draft[i] : -1;
     if (threadIdx.x == 0) a.n_acc[b] = acc;
   }
@@ -318,13 +329,16 @@ __global__ void __launch_bounds__(MAX_NT) verify_kernel(VerifyArgs a, int C, int
       int i = 0;
       while (run + chunk[warp][i] <= t) run += chunk[warp][i++];
       const int at = (first + i) * CHUNK;
-      long long u[8];
-      load_chunk(p, q, hot, at, V, u);
+      Chunk c;
+      c.load(p, q, at, V);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const long long lo = run + warp_before(u[j]);
-        if (t >= lo && t < lo + u[j]) out[acc] = at + 32 * j + lane;
-        run += warp_sum(u[j]);
+        uint32_t hi, lo;
+        units(c.weight(j, at, hot), hi, lo);
+        const long long u = whole(hi - BIAS, lo - BIAS);
+        const long long b0 = run + warp_before(u);
+        if (t >= b0 && t < b0 + u) out[acc] = at + 32 * j + lane;
+        run += warp_sum(u);
       }
     }
   }
@@ -342,13 +356,15 @@ cudaError_t launch_softmax(const SoftmaxArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s) {
-  constexpr int NW = MAX_NT / 32;
   const int chunks = (a.V + CHUNK - 1) / CHUNK;
-  // CTAs a sequence: two chunks a warp, or eight CTAs and more chunks
+  // CTAs a sequence: eight chunks a warp, or eight CTAs and more chunks; with few
+  // sequences as many CTAs as two chunks a warp take, while they still fill no
+  // more than the device
   int C = 1;
-  while (C < 8 && C * NW * 2 < chunks) C *= 2;
-  const int per = (chunks + C * NW - 1) / (C * NW);
-  return launch_step(verify_kernel, dim3((unsigned)a.B * C), MAX_NT, 0, s, C, a, C, per);
+  while (C < 8 && C * V_NW * 8 < chunks) C *= 2;
+  while (C < 8 && C * V_NW * 2 < chunks && (int64_t)a.B * C * 2 <= dev_info().sms) C *= 2;
+  const int per = (chunks + C * V_NW - 1) / (C * V_NW);
+  return launch_step(verify_kernel, dim3((unsigned)a.B * C), V_NT, 0, s, C, a, C, per);
 }
 
 }  // namespace qmv

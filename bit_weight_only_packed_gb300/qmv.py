@@ -461,6 +461,10 @@ _16BIT = (torch.float16, torch.bfloat16)
 _FLOAT = (torch.float32, torch.float16, torch.bfloat16)
 
 
+# looked up once: these calls are short enough for the host's steps to count
+_w4_gemv, _block_norm, _softmax, _verify_draft = (_lib.qmv_w4_gemv, _lib.qmv_block_norm, _lib.qmv_softmax,
+                                                  _lib.qmv_verify_draft)
+_empty = torch.empty
 _current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
@@ -517,7 +521,7 @@ def _place(stream, first, *others):
 def _fresh(shape, dtype, like, stream):
     """A fresh output; one written on another stream than torch's current one is
     recorded there, so the allocator does not hand it out again too early."""
-    t = torch.empty(shape, dtype=dtype, device=like.device)
+    t = _empty(shape, dtype=dtype, device=like.device)
     if stream is not None:
         cur = torch.cuda.current_stream(like.device)
         if _stream(stream) != cur.cuda_stream:
@@ -596,18 +600,24 @@ class W4Pack:
 
 def qmv_w4_gemv(p: W4Pack, x, y=None, y_dtype=QMV_F32, stream=None):
     """y [M, N] = x [M, K] . W^T for a W4Pack; x is fp16 or bf16 ([K] counts as M = 1)."""
+    N, K = p.N, p.K
     M = x.shape[0] if x.dim() == 2 else 1
-    ldx = _rows("x", x, _16BIT, M, p.K)
-    if p.packed is None:
+    ldx = _rows("x", x, _16BIT, M, K)
+    packed = p.packed
+    if packed is None:
         raise ValueError("the pack holds no weights yet")
-    if y_dtype not in _TORCH:
+    ydt = _TORCH.get(y_dtype)
+    if ydt is None:
         raise ValueError(f"y_dtype: unknown value {y_dtype!r}")
-    ldy = p.N if y is None else _rows("y", y, (_TORCH[y_dtype],), M, p.N)
-    st = _place(stream, x, p.packed, y)
     if y is None:
-        y = _fresh((M, p.N), _TORCH[y_dtype], x, stream)
-    _check("qmv_w4_gemv", _lib.qmv_w4_gemv(p.handle, M, x.data_ptr(), ldx, _DTYPE[x.dtype], y.data_ptr(), ldy,
-                                           y_dtype, st))
+        st = _place(stream, x, packed)
+        ldy, y = N, _fresh((M, N), ydt, x, stream)
+    else:
+        ldy = _rows("y", y, (ydt,), M, N)
+        st = _place(stream, x, packed, y)
+    rc = _w4_gemv(p.handle, M, x.data_ptr(), ldx, _DTYPE[x.dtype], y.data_ptr(), ldy, y_dtype, st)
+    if rc:
+        _check("qmv_w4_gemv", rc)
     return y
 
 
@@ -615,10 +625,14 @@ def qmv_block_norm(y, residual, gamma_pre, gamma_post=None, gate=None, residual_
                    gamma_offset=0.0, eps=1e-6, h_out=None, out=None, stream=None):
     """(h, out): h = residual_scale * residual + branch_scale * gate * norm(y), out
     = norm(h); the first norm where gamma_post is given, the gate [D] or [M, D]."""
-    if residual.dim() not in (1, 2):
-        raise ValueError(f"residual: expected a [rows, columns] tensor, got {tuple(residual.shape)}")
+    shape = residual.shape
+    if len(shape) == 2:
+        M, D = shape
+    elif len(shape) == 1:
+        M, D = 1, shape[0]
+    else:
+        raise ValueError(f"residual: expected a [rows, columns] tensor, got {tuple(shape)}")
     dt = residual.dtype
-    M, D = (1, residual.shape[0]) if residual.dim() == 1 else residual.shape
     ldr = _rows("residual", residual, _16BIT, M, D)
     ldy = _rows("y", y, _FLOAT, M, D)
     _vec("gamma_pre", gamma_pre, dt, D)
@@ -637,20 +651,26 @@ def qmv_block_norm(y, residual, gamma_pre, gamma_post=None, gate=None, residual_
         h_out = _fresh((M, D), dt, y, stream)
     if out is None:
         out = _fresh((M, D), dt, y, stream)
-    _check("qmv_block_norm", _lib.qmv_block_norm(
-        M, D, y.data_ptr(), ldy, _DTYPE[y.dtype], residual.data_ptr(), ldr,
-        None if gamma_post is None else gamma_post.data_ptr(), None if gate is None else gate.data_ptr(), ldg,
-        residual_scale, branch_scale, gamma_pre.data_ptr(), gamma_offset, eps, h_out.data_ptr(), ldh,
-        out.data_ptr(), ldo, _DTYPE[dt], st))
+    rc = _block_norm(M, D, y.data_ptr(), ldy, _DTYPE[y.dtype], residual.data_ptr(), ldr,
+                     None if gamma_post is None else gamma_post.data_ptr(),
+                     None if gate is None else gate.data_ptr(), ldg, residual_scale, branch_scale,
+                     gamma_pre.data_ptr(), gamma_offset, eps, h_out.data_ptr(), ldh, out.data_ptr(), ldo,
+                     _DTYPE[dt], st)
+    if rc:
+        _check("qmv_block_norm", rc)
     return h_out, out
 
 
 def qmv_softmax(logits, temperature=1.0, out=None, stream=None):
     """fp32 probabilities [rows, V] of logits at a temperature (a number, or a
     device fp32 tensor [rows]); out may be the fp32 logits themselves."""
-    if logits.dim() not in (1, 2):
-        raise ValueError(f"logits: expected a [rows, columns] tensor, got {tuple(logits.shape)}")
-    rows, V = (1, logits.shape[0]) if logits.dim() == 1 else logits.shape
+    shape = logits.shape
+    if len(shape) == 2:
+        rows, V = shape
+    elif len(shape) == 1:
+        rows, V = 1, shape[0]
+    else:
+        raise ValueError(f"logits: expected a [rows, columns] tensor, got {tuple(shape)}")
     ldl = _rows("logits", logits, _FLOAT, rows, V)
     t, t0 = None, 1.0
     if torch.is_tensor(temperature):
@@ -662,8 +682,10 @@ def qmv_softmax(logits, temperature=1.0, out=None, stream=None):
     st = _place(stream, logits, t, out)
     if out is None:
         out = _fresh((rows, V), torch.float32, logits, stream)
-    _check("qmv_softmax", _lib.qmv_softmax(rows, V, logits.data_ptr(), ldl, _DTYPE[logits.dtype],
-                                           None if t is None else t.data_ptr(), t0, out.data_ptr(), ldo, st))
+    rc = _softmax(rows, V, logits.data_ptr(), ldl, _DTYPE[logits.dtype], None if t is None else t.data_ptr(), t0,
+                  out.data_ptr(), ldo, st)
+    if rc:
+        _check("qmv_softmax", rc)
     return out
 
 
@@ -693,8 +715,9 @@ def qmv_verify_draft(target, draft_probs, draft, u_accept, u_sample, n_draft=Non
         tokens = _fresh((B, S1), torch.int32, target, stream)
     if n_accepted is None:
         n_accepted = _fresh((B,), torch.int32, target, stream)
-    _check("qmv_verify_draft", _lib.qmv_verify_draft(
-        B, S, V, target.data_ptr(), None if draft_probs is None else draft_probs.data_ptr(), draft.data_ptr(),
-        None if n_draft is None else n_draft.data_ptr(), u_accept.data_ptr(), u_sample.data_ptr(),
-        tokens.data_ptr(), n_accepted.data_ptr(), st))
+    rc = _verify_draft(B, S, V, target.data_ptr(), None if draft_probs is None else draft_probs.data_ptr(),
+                       draft.data_ptr(), None if n_draft is None else n_draft.data_ptr(), u_accept.data_ptr(),
+                       u_sample.data_ptr(), tokens.data_ptr(), n_accepted.data_ptr(), st)
+    if rc:
+        _check("qmv_verify_draft", rc)
     return tokens, n_accepted

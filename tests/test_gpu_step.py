@@ -244,9 +244,10 @@ def test_softmax(rows, V, dt, pad):
     o.check("out")
     arg = (x.t.double() - x.t.double().amax(1, keepdim=True)) / t.double()[:, None]
     ref = torch.softmax(arg, 1)
-    # the exponent is rounded three times (difference, 1/T, product), expf is good to
-    # 2 units, the sum of positive terms has at most V / 128 + 64 roundings
-    rel = 3.01 * U24 * arg.abs().clamp(max=200) + (4 + 2 + V / 128 + 64) * U24
+    # the exponent is rounded three times (difference, log2(e) / T, product) and fp32's
+    # log2(e) is off by 1.34e-8 = 0.23 units of 2^-24; exp2f is good to 2 units, the sum
+    # of positive terms has at most V / 128 + 64 roundings
+    rel = 3.25 * U24 * arg.abs().clamp(max=200) + (4 + 2 + V / 128 + 64) * U24
     err = (o.t.double() - ref).abs()
     assert bool((err <= ref * rel + 2.0 ** -126).all())
     if V > 30:
