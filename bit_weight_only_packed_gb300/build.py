@@ -2,7 +2,8 @@
 
 Each .cu file is compiled by its own nvcc process (in parallel), then linked
 into ``bit_weight_only_packed_gb300/_lib/libqmv.so``.  No fast-math: the
-kernels rely on IEEE fp32 rounding.
+kernels rely on IEEE fp32 rounding.  The binding's host module (plain C against
+the running Python's headers) goes beside it as ``qmv_host.so``.
 """
 from __future__ import annotations
 
@@ -11,12 +12,15 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libqmv.so")
+HOST_SRC = os.path.join(CSRC, "host", "qmv_host.c")
+HOST_LIB = os.path.join(OUT_DIR, "qmv_host.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -44,9 +48,24 @@ def _stale(lib: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_host(force: bool = False) -> str:
+    if not force and not _stale(HOST_LIB, [HOST_SRC, os.path.join(ROOT, "include", "qmv.h"), __file__]):
+        return HOST_LIB
+    os.makedirs(OUT_DIR, exist_ok=True)
+    tmp = HOST_LIB + f".tmp{os.getpid()}"
+    r = subprocess.run(["gcc", "-std=c11", "-O2", "-Wall", "-shared", "-fPIC", "-fvisibility=hidden",
+                        "-I", sysconfig.get_paths()["include"], "-I", os.path.join(ROOT, "include"), "-o", tmp,
+                        HOST_SRC], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed on {HOST_SRC}:\n{r.stderr}")
+    os.replace(tmp, HOST_LIB)
+    return HOST_LIB
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [
         os.path.join(ROOT, "include", "qmv.h"), __file__]
+    build_host(force)
     if not force and not extra and not _stale(LIB, deps):
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)

@@ -8,6 +8,8 @@ fallback of any kind).
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -461,12 +463,39 @@ _16BIT = (torch.float16, torch.bfloat16)
 _FLOAT = (torch.float32, torch.float16, torch.bfloat16)
 
 
+
+
+def _load_host():
+    """qmv_host.so (csrc/host/qmv_host.c): the usual form of these calls in C."""
+    path = os.path.join(_HERE, "_lib", "qmv_host.so")
+    if not os.path.exists(path):
+        raise ImportError(f"qmv_host.so is not built ({path}); run "
+                          "`python -c 'import __graft_entry__ as g; g.build()'`")
+    loader = importlib.machinery.ExtensionFileLoader("qmv_host", path)
+    mod = importlib.util.module_from_spec(importlib.util.spec_from_file_location("qmv_host", path, loader=loader))
+    loader.exec_module(mod)
+    addr = lambda f: ctypes.cast(f, _P).value
+    mod.init(torch.Tensor, torch.empty, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream,
+             (torch.float32, torch.float16, torch.bfloat16, torch.int32),
+             (addr(_lib.qmv_w4_gemv), addr(_lib.qmv_block_norm), addr(_lib.qmv_softmax),
+              addr(_lib.qmv_verify_draft)))
+    return mod
+
+
+_host = _load_host()
 # looked up once: these calls are short enough for the host's steps to count
 _w4_gemv, _block_norm, _softmax, _verify_draft = (_lib.qmv_w4_gemv, _lib.qmv_block_norm, _lib.qmv_softmax,
                                                   _lib.qmv_verify_draft)
 _empty = torch.empty
 _current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _done(fn, r):
+    """What a call of _host returned: the outputs, or a failing status to raise."""
+    if type(r) is int:
+        raise QmvError(fn, r)
+    return r
 
 
 def _rows(name, t, dtypes, rows, cols):
@@ -541,11 +570,11 @@ class W4Pack:
         h, nb = _P(), ctypes.c_size_t()
         _check("qmv_w4_create", _lib.qmv_w4_create(ctypes.byref(h), N, K, group, _DTYPE[scale_dtype],
                                                    1 if zeros else 0, ctypes.byref(nb)))
-        self.handle = h
+        self.handle, self._address = h, h.value
         self.N, self.K, self.group, self.G = N, K, group, -(-K // group)
         self.scale_dtype, self.zeros = scale_dtype, bool(zeros)
         self.packed_bytes = nb.value
-        self.packed = None
+        self.packed, self._dev = None, -1       # the packed bytes and their device
 
     def pack_weights(self, codes, scales, zeros=None, stream=None):
         """codes: device uint8 [N, K], 0..15; scales: device fp16/bf16 [N, K/group];
@@ -560,7 +589,7 @@ class W4Pack:
         packed = _fresh((self.packed_bytes,), torch.uint8, codes, stream)
         _check("qmv_w4_pack", _lib.qmv_w4_pack(self.handle, codes.data_ptr(), scales.data_ptr(),
                                                None if zeros is None else zeros.data_ptr(), packed.data_ptr(), st))
-        self.packed = packed
+        self.packed, self._dev = packed, packed.get_device()
         return self
 
     def bind_packed(self, packed):
@@ -568,7 +597,7 @@ class W4Pack:
         _vec("packed", packed, torch.uint8, self.packed_bytes)
         _place(None, packed)
         _check("qmv_w4_bind", _lib.qmv_w4_bind(self.handle, packed.data_ptr()))
-        self.packed = packed
+        self.packed, self._dev = packed, packed.get_device()
         return self
 
     def unpack_codes(self, stream=None):
@@ -589,7 +618,7 @@ class W4Pack:
     def close(self):
         if self.handle is not None and self.handle.value:
             _lib.qmv_w4_destroy(self.handle)
-        self.handle = None
+        self.handle, self._dev = None, -1
 
     def __del__(self):
         try:
@@ -600,6 +629,10 @@ class W4Pack:
 
 def qmv_w4_gemv(p: W4Pack, x, y=None, y_dtype=QMV_F32, stream=None):
     """y [M, N] = x [M, K] . W^T for a W4Pack; x is fp16 or bf16 ([K] counts as M = 1)."""
+    if y is None and stream is None:
+        r = _host.w4_gemv(p._address, p._dev, p.N, p.K, x, y_dtype)
+        if r is not None:
+            return _done("qmv_w4_gemv", r)
     N, K = p.N, p.K
     M = x.shape[0] if x.dim() == 2 else 1
     ldx = _rows("x", x, _16BIT, M, K)
@@ -625,6 +658,10 @@ def qmv_block_norm(y, residual, gamma_pre, gamma_post=None, gate=None, residual_
                    gamma_offset=0.0, eps=1e-6, h_out=None, out=None, stream=None):
     """(h, out): h = residual_scale * residual + branch_scale * gate * norm(y), out
     = norm(h); the first norm where gamma_post is given, the gate [D] or [M, D]."""
+    if h_out is None and out is None and stream is None:
+        r = _host.block_norm(y, residual, gamma_pre, gamma_post, gate, residual_scale, branch_scale, gamma_offset, eps)
+        if r is not None:
+            return _done("qmv_block_norm", r)
     shape = residual.shape
     if len(shape) == 2:
         M, D = shape
@@ -664,6 +701,10 @@ def qmv_block_norm(y, residual, gamma_pre, gamma_post=None, gate=None, residual_
 def qmv_softmax(logits, temperature=1.0, out=None, stream=None):
     """fp32 probabilities [rows, V] of logits at a temperature (a number, or a
     device fp32 tensor [rows]); out may be the fp32 logits themselves."""
+    if out is None and stream is None:
+        r = _host.softmax(logits, temperature)
+        if r is not None:
+            return _done("qmv_softmax", r)
     shape = logits.shape
     if len(shape) == 2:
         rows, V = shape
@@ -694,6 +735,10 @@ def qmv_verify_draft(target, draft_probs, draft, u_accept, u_sample, n_draft=Non
     """(tokens [B, S+1], n_accepted [B]): target fp32 [B, S+1, V], draft_probs
     fp32 [B, S, V] or None (a drafter that is sure of its tokens), draft int32
     [B, S], u_accept fp32 [B, S], u_sample fp32 [B], n_draft int32 [B] or None."""
+    if tokens is None and n_accepted is None and stream is None:
+        r = _host.verify_draft(target, draft_probs, draft, u_accept, u_sample, n_draft)
+        if r is not None:
+            return _done("qmv_verify_draft", r)
     if target.dim() != 3 or target.shape[1] < 1:
         raise ValueError(f"target: expected [B, S+1, V], got {tuple(target.shape)}")
     B, S1, V = target.shape
