@@ -22,104 +22,143 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   return v;
 }
 
-// Eight elements of a row as fp32.  VEC: eight neighbours, aligned to their
-// total size; otherwise every blockDim.x-th one, so that neighbouring threads
-// read neighbouring elements whatever the alignment.
+// Two neighbouring 16-bit elements as fp32 and back (one instruction for the pair).
+template <typename T>
+__device__ __forceinline__ float2 unpack(uint32_t v);
+template <>
+__device__ __forceinline__ float2 unpack<__half>(uint32_t v) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+template <>
+__device__ __forceinline__ float2 unpack<__nv_bfloat16>(uint32_t v) {
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack<__half>(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Eight elements of a row, kept as they are stored.  VEC: eight neighbours,
+// aligned to 16 bytes; otherwise every `step`-th one, so that neighbouring
+// threads read neighbouring elements whatever the alignment.
 template <typename T, bool VEC>
 struct Eight {
-  alignas(16) T v[8];
+  alignas(16) uint32_t w[2 * sizeof(T)];
   __device__ __forceinline__ void load(const T* p, int i0, int step, int D) {
     if (VEC) {
 #pragma unroll
-      for (int q = 0; q < (int)sizeof(v) / 16; ++q)
-        reinterpret_cast<uint4*>(v)[q] = reinterpret_cast<const uint4*>(p + i0)[q];
-    } else {
+      for (int q = 0; q < (int)sizeof(w) / 16; ++q)
+        reinterpret_cast<uint4*>(w)[q] = reinterpret_cast<const uint4*>(p + i0)[q];
+    } else if (sizeof(T) == 4) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (i0 + e * step < D) v[e] = p[i0 + e * step];
+      for (int e = 0; e < 8; ++e) w[e] = i0 + e * step < D ? reinterpret_cast<const uint32_t*>(p)[i0 + e * step] : 0u;
+    } else {
+      const uint16_t* s = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        const uint32_t a = i0 + e * step < D ? s[i0 + e * step] : 0u, b = i0 + (e + 1) * step < D ? s[i0 + (e + 1) * step] : 0u;
+        w[e >> 1] = a | b << 16;
+      }
     }
   }
+  __device__ __forceinline__ float2 pair(int e) const {      // elements e and e + 1
+    if constexpr (sizeof(T) == 4)
+      return make_float2(__uint_as_float(w[e]), __uint_as_float(w[e + 1]));
+    else
+      return unpack<T>(w[e >> 1]);
+  }
+  __device__ __forceinline__ void set(int e, float a, float b) { w[e >> 1] = pack<T>(a, b); }
   __device__ __forceinline__ void store(T* p, int i0, int step, int D) const {
     if (VEC) {
-#pragma unroll
-      for (int q = 0; q < (int)sizeof(v) / 16; ++q)
-        reinterpret_cast<uint4*>(p + i0)[q] = reinterpret_cast<const uint4*>(v)[q];
+      *reinterpret_cast<uint4*>(p + i0) = *reinterpret_cast<const uint4*>(w);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (i0 + e * step < D) p[i0 + e * step] = v[e];
+        if (i0 + e * step < D) reinterpret_cast<uint16_t*>(p)[i0 + e * step] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
     }
   }
 };
 
 // One CTA a row, the row in registers: 8 * P elements a thread, read once.
+// Elements past the row's end are zeros, which add nothing to either sum.
 template <typename Y, typename T, bool VEC, int P>
 __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
   __shared__ float red[2][32];
   const int64_t m = blockIdx.x;
   const int D = a.D, NT = blockDim.x, tid = threadIdx.x;
   const T *gpo = (const T*)a.gamma_post, *gpr = (const T*)a.gamma_pre;
-  int i0[P];
-  bool on[P];                    // VEC: whether these eight are inside the row
+  pdl_begin();
+  Eight<Y, VEC> y[P] = {};
+  Eight<T, VEC> r[P] = {}, gt[P] = {};
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    i0[p] = VEC ? (p * NT + tid) * 8 : p * 8 * NT + tid;
-    on[p] = i0[p] < D;
-  }
-  const int step = NT;
-  pdl_begin();
-  Eight<Y, VEC> y[P];
-  Eight<T, VEC> r[P], gt[P];
-#pragma unroll
-  for (int p = 0; p < P; ++p)
-    if (on[p]) {
-      y[p].load((const Y*)a.y + m * a.ldy, i0[p], step, D);
-      r[p].load((const T*)a.r + m * a.ldr, i0[p], step, D);
-      if (a.gate) gt[p].load((const T*)a.gate + m * a.ldg, i0[p], step, D);
+    const int i0 = VEC ? (p * NT + tid) * 8 : p * 8 * NT + tid;
+    if (i0 < D) {
+      y[p].load((const Y*)a.y + m * a.ldy, i0, NT, D);
+      r[p].load((const T*)a.r + m * a.ldr, i0, NT, D);
+      if (a.gate) gt[p].load((const T*)a.gate + m * a.ldg, i0, NT, D);
     }
-  float inv = 1.0f;
+  }
+  float inv = a.bs;                      // branch scale and first norm as one factor
   if (gpo) {
     float ss = 0.0f;
 #pragma unroll
     for (int p = 0; p < P; ++p)
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (VEC ? on[p] : i0[p] + e * step < D) {
-          const float v = to_f<Y>(y[p].v[e]);
-          ss = fmaf(v, v, ss);
-        }
-    inv = 1.0f / sqrtf(block_sum(ss, red[0]) / (float)D + a.eps);
+      for (int e = 0; e < 8; e += 2) {
+        const float2 v = y[p].pair(e);
+        ss = fmaf(v.x, v.x, fmaf(v.y, v.y, ss));
+      }
+    inv = a.bs / sqrtf(block_sum(ss, red[0]) / (float)D + a.eps);
   }
   float ss = 0.0f;
 #pragma unroll
-  for (int p = 0; p < P; ++p)
-    if (on[p]) {
-      Eight<T, VEC> go;
-      if (gpo) go.load(gpo, i0[p], step, D);
+  for (int p = 0; p < P; ++p) {
+    const int i0 = VEC ? (p * NT + tid) * 8 : p * 8 * NT + tid;
+    if (i0 >= D) continue;
+    Eight<T, VEC> go;
+    if (gpo) go.load(gpo, i0, NT, D);
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (VEC || i0[p] + e * step < D) {
-          float u = to_f<Y>(y[p].v[e]);
-          if (gpo) u = u * inv * (to_f<T>(go.v[e]) + a.goff);
-          if (a.gate) u *= to_f<T>(gt[p].v[e]);
-          const T hv = from_f<T>(fmaf(a.rs, to_f<T>(r[p].v[e]), a.bs * u));
-          r[p].v[e] = hv;
-          const float f = to_f<T>(hv);
-          ss = fmaf(f, f, ss);
-        }
-      if (a.h) r[p].store((T*)a.h + m * a.ldh, i0[p], step, D);
+    for (int e = 0; e < 8; e += 2) {
+      float2 u = y[p].pair(e);
+      u.x *= inv, u.y *= inv;
+      if (gpo) {
+        const float2 g = go.pair(e);
+        u.x *= g.x + a.goff, u.y *= g.y + a.goff;
+      }
+      if (a.gate) {
+        const float2 g = gt[p].pair(e);
+        u.x *= g.x, u.y *= g.y;
+      }
+      const float2 v = r[p].pair(e);
+      r[p].set(e, fmaf(a.rs, v.x, u.x), fmaf(a.rs, v.y, u.y));
+      const float2 h = r[p].pair(e);
+      ss = fmaf(h.x, h.x, fmaf(h.y, h.y, ss));
     }
+    if (a.h) r[p].store((T*)a.h + m * a.ldh, i0, NT, D);
+  }
   const float inv2 = 1.0f / sqrtf(block_sum(ss, red[1]) / (float)D + a.eps);
 #pragma unroll
-  for (int p = 0; p < P; ++p)
-    if (on[p]) {
-      Eight<T, VEC> g;
-      g.load(gpr, i0[p], step, D);
+  for (int p = 0; p < P; ++p) {
+    const int i0 = VEC ? (p * NT + tid) * 8 : p * 8 * NT + tid;
+    if (i0 >= D) continue;
+    Eight<T, VEC> g;
+    g.load(gpr, i0, NT, D);
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (VEC || i0[p] + e * step < D) r[p].v[e] = from_f<T>(to_f<T>(r[p].v[e]) * inv2 * (to_f<T>(g.v[e]) + a.goff));
-      r[p].store((T*)a.out + m * a.ldo, i0[p], step, D);
+    for (int e = 0; e < 8; e += 2) {
+      const float2 h = r[p].pair(e), q = g.pair(e);
+      r[p].set(e, h.x * inv2 * (q.x + a.goff), h.y * inv2 * (q.y + a.goff));
     }
+    r[p].store((T*)a.out + m * a.ldo, i0, NT, D);
+  }
 }
 
 // Rows too long for registers: h waits in shared memory for its own norm.
@@ -172,15 +211,14 @@ cudaError_t run(const NormArgs& a, cudaStream_t s) {
                    ok(a.gate, a.ldg, 2) && ok(a.gamma_pre, 0, 2) && ok(a.h, a.ldh, 2) && ok(a.out, a.ldo, 2);
   const int need = (a.D + 7) / 8;              // threads at eight elements each
   const dim3 grid(a.M);
-  if (need <= 1024) {
-    const int nt = (need + 31) / 32 * 32;
-    return vec ? launch_step(norm_kernel<Y, T, true, 1>, grid, nt, 0, s, 1, a)
-               : launch_step(norm_kernel<Y, T, false, 1>, grid, nt, 0, s, 1, a);
-  }
-  if (need <= 2048 && vec) {
-    const int nt = ((need + 1) / 2 + 31) / 32 * 32;
-    return launch_step(norm_kernel<Y, T, true, 2>, grid, nt, 0, s, 1, a);
-  }
+  const int one = (need + 31) / 32 * 32, two = ((need + 1) / 2 + 31) / 32 * 32;
+  // Few rows: more threads, for the latency of one.  Many rows: twice the elements a
+  // thread, since the sums' steps are shared by them.
+  const bool many = vec && need >= 128 && a.M >= 2 * dev_info().sms;
+  if (need <= 1024 && !many)
+    return vec ? launch_step(norm_kernel<Y, T, true, 1>, grid, one, 0, s, 1, a)
+               : launch_step(norm_kernel<Y, T, false, 1>, grid, one, 0, s, 1, a);
+  if (need <= 2048 && vec) return launch_step(norm_kernel<Y, T, true, 2>, grid, two, 0, s, 1, a);
   static thread_local KernCache c;
   const size_t smem = (size_t)a.D * sizeof(T);
   const cudaError_t e = prep_kernel(norm_long_kernel<Y, T>, c, 1024, smem, nullptr);

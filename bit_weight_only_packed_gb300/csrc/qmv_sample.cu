@@ -45,6 +45,13 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   return v;
 }
 
+// 2^v to 2 units in the last place; results below 2^-126 become 0.
+__device__ __forceinline__ float ex2(float v) {
+  float d;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(v));
+  return d;
+}
+
 // What a CTA knows of its part of a row.
 struct Part {
   float m, s;      // maximum; sum of exp((x - m) / T), in the one-hot form of 0 * x (NaN marks the row)
@@ -56,12 +63,12 @@ struct Part {
 // EPT == 0: a part of any length, read a second and third time (from L2).
 // exp((x - m) / T) is taken as exp2((x - m) * c), c = log2(e) / T.  A row with
 // NaN or +inf has the sum NaN, which reaches every place by itself.
-template <typename X, int EPT>
-__global__ void __launch_bounds__(MAX_NT, 2) softmax_kernel(SoftmaxArgs a, int C, int len) {
+template <typename X, int EPT, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) softmax_kernel(SoftmaxArgs a, int C, int len) {
   __shared__ Part mine;
-  __shared__ float redm[MAX_NT / 32], reds[MAX_NT / 32];
-  __shared__ int redi[MAX_NT / 32];
-  const int row = blockIdx.x / C, rank = blockIdx.x - row * C, NT = blockDim.x, tid = threadIdx.x;
+  __shared__ float redm[NT / 32], reds[NT / 32];
+  __shared__ int redi[NT / 32];
+  const int row = blockIdx.x / C, rank = blockIdx.x - row * C, tid = threadIdx.x;
   const int v0 = min(a.V, rank * len), n = min(a.V - v0, len);     // this CTA's part
   const X* x = (const X*)a.x + (int64_t)row * a.ldx + v0;
   float* out = a.out + (int64_t)row * a.ldo + v0;
@@ -99,26 +106,30 @@ __global__ void __launch_bounds__(MAX_NT, 2) softmax_kernel(SoftmaxArgs a, int C
     if (EPT) {
 #pragma unroll
       for (int j = 0; j < R; ++j) {
-        e[j] = exp2f((e[j] - m) * c);
+        e[j] = ex2((e[j] - m) * c);
         p.s += e[j];
       }
     } else {
-      for (int i = tid; i < n; i += NT) p.s += exp2f((to_f<X>(x[i]) - m) * c);
+      for (int i = tid; i < n; i += NT) p.s += ex2((to_f<X>(x[i]) - m) * c);
     }
   }
   p.s = block_sum(p.s, reds);
   Part all = p;
   if (C > 1) {
-    if (tid == 0) mine = p;
-    cluster_arrive();
-    cluster_wait();
     const int lane = tid & 31;
+    if (tid == 0) mine = p;
+    if (tid < 32) {
+      __syncwarp();
+      cluster_arrive();
+    } else {
+      cluster_arrive_relaxed();
+    }
+    cluster_wait();
     const uint32_t at = cluster_addr(&mine, lane < C ? lane : 0);
     Part q;
     q.m = __uint_as_float(ld_cluster32(at));
     q.s = __uint_as_float(ld_cluster32(at + 4));
     q.at = (int)ld_cluster32(at + 8);
-    cluster_arrive();                        // waited for at the end: the others still read `mine`
     all = q;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
@@ -127,55 +138,54 @@ __global__ void __launch_bounds__(MAX_NT, 2) softmax_kernel(SoftmaxArgs a, int C
       if (m2 > all.m || (m2 == all.m && a2 < all.at)) all.at = a2;
       all.m = fmaxf(all.m, m2);
     }
-    float sum = lane >= C || q.m == -CUDART_INF_F ? 0.0f : hot ? q.s : q.s * exp2f((q.m - all.m) * c);
+    float sum = lane >= C || q.m == -CUDART_INF_F ? 0.0f : hot ? q.s : q.s * ex2((q.m - all.m) * c);
     // a part of NaN alone has the maximum -inf and the sum NaN
     if (lane < C && isnan(q.s)) sum = q.s;
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
     all.s = sum;
+    cluster_arrive_relaxed();                // waited for at the end: the others still read `mine`
   }
   if (hot || all.m == -CUDART_INF_F) {       // the one-hot form, or nothing but -inf (or NaN)
     const float rest = isnan(all.s) ? all.s : 0.0f, one = all.m == -CUDART_INF_F ? rest : 1.0f + rest;
     for (int i = tid; i < n; i += NT) out[i] = v0 + i == all.at ? one : rest;
   } else {
     // at most 1 over the sum; 0 where this part had only -inf, whose terms are 0
-    const float f = exp2f((p.m - all.m) * c) / all.s;
+    const float f = ex2((p.m - all.m) * c) / all.s;
     if (EPT) {
 #pragma unroll
       for (int j = 0; j < R; ++j)
         if (j * NT + tid < n) out[j * NT + tid] = e[j] * f;
     } else {
-      for (int i = tid; i < n; i += NT) out[i] = exp2f((to_f<X>(x[i]) - all.m) * c) / all.s;
+      for (int i = tid; i < n; i += NT) out[i] = ex2((to_f<X>(x[i]) - all.m) * c) / all.s;
     }
   }
   if (C > 1) cluster_wait();
 }
 
-template <typename X, int EPT>
+template <typename X, int EPT, int NT>
 cudaError_t run_softmax(const SoftmaxArgs& a, int C, cudaStream_t s) {
   static thread_local int allowed = -1;
   if (C > 8) {                                // clusters of 16 are opt-in, a function and device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && allowed != dev) {
-      e = cudaFuncSetAttribute(softmax_kernel<X, EPT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      e = cudaFuncSetAttribute(softmax_kernel<X, EPT, NT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       allowed = dev;
     }
     if (e != cudaSuccess) return e;
   }
-  const int len = (a.V + C - 1) / C;
-  int nt = EPT ? (len + EPT - 1) / EPT : MAX_NT;
-  nt = (nt + 31) / 32 * 32;
-  return launch_step(softmax_kernel<X, EPT>, dim3((unsigned)a.rows * C), nt, 0, s, C, a, C, len);
+  return launch_step(softmax_kernel<X, EPT, NT>, dim3((unsigned)a.rows * C), NT, 0, s, C, a, C, (a.V + C - 1) / C);
 }
 
 template <typename X>
 cudaError_t softmax_x(const SoftmaxArgs& a, cudaStream_t s) {
-  if (a.V <= 4096) return run_softmax<X, 8>(a, 1, s);
+  if (a.V <= 1024) return run_softmax<X, 8, 128>(a, 1, s);
+  if (a.V <= 4096) return run_softmax<X, 8, 512>(a, 1, s);
   int C = 1;
   while (C < MAX_C && (int64_t)C * MAX_NT * 32 < a.V) C *= 2;
-  if ((int64_t)C * MAX_NT * 32 >= a.V) return run_softmax<X, 32>(a, C, s);
-  return run_softmax<X, 0>(a, MAX_C, s);
+  if ((int64_t)C * MAX_NT * 32 >= a.V) return run_softmax<X, 32, MAX_NT>(a, C, s);
+  return run_softmax<X, 0, MAX_NT>(a, MAX_C, s);
 }
 
 // ------------------------------------------------------------------ verify --
@@ -246,9 +256,9 @@ struct Chunk {
 // A cluster of C CTAs a sequence; warps own `per` consecutive chunks each and
 // keep every chunk's sum, so that after the total is known one warp re-reads the
 // one chunk in which the running sum passes the threshold.
-constexpr int V_NT = 256, V_NW = V_NT / 32, MAX_PER = 64;
+constexpr int V_NT = 512, V_NW = V_NT / 32, MAX_PER = 32;
 static_assert((int64_t)8 * V_NW * MAX_PER * CHUNK >= 1 << 20, "a chunk sum for every id");
-__global__ void __launch_bounds__(V_NT, 4) verify_kernel(VerifyArgs a, int C, int per) {
+__global__ void __launch_bounds__(V_NT, 2) verify_kernel(VerifyArgs a, int C, int per) {
   constexpr int NW = V_NW;
   __shared__ long long chunk[NW][MAX_PER], wsum[NW], mine[2];
   __shared__ int s_acc;
@@ -284,13 +294,15 @@ __global__ void __launch_bounds__(V_NT, 4) verify_kernel(VerifyArgs a, int C, in
   for (int pass = 0; pass < 2; ++pass) {
     long long w = 0;
     const int last = min(per, max(0, (V + CHUNK - 1) / CHUNK - first));
-#pragma unroll 2
+    Chunk c;
+    if (last > 0) c.load(p, q, first * CHUNK, V);
     for (int i = 0; i < last; ++i) {
-      Chunk c;
-      c.load(p, q, (first + i) * CHUNK, V);
+      Chunk next;                         // on its way while this one is summed
+      if (i + 1 < last) next.load(p, q, (first + i + 1) * CHUNK, V);
       const long long s = c.sum((first + i) * CHUNK, hot);
       if (lane == 0) chunk[warp][i] = s;
       w += s;
+      c = next;
     }
     if (lane == 0) wsum[warp] = w;
     __syncthreads();
@@ -300,7 +312,12 @@ __global__ void __launch_bounds__(V_NT, 4) verify_kernel(VerifyArgs a, int C, in
     if (C > 1) {
       // a slot for each pass: nobody overwrites what another CTA still reads
       if (threadIdx.x == 0) mine[pass] = own;
-      cluster_arrive();
+      if (warp == 0) {
+        __syncwarp();
+        cluster_arrive();
+      } else {
+        cluster_arrive_relaxed();
+      }
       cluster_wait();
       const long long v = lane < C ? ld_cluster64(cluster_addr(&mine[pass], lane)) : 0;
       total = warp_sum(v);
@@ -310,7 +327,7 @@ __global__ void __launch_bounds__(V_NT, 4) verify_kernel(VerifyArgs a, int C, in
     q = nullptr, hot = -1;              // no mass is left: draw from p
     __syncthreads();                    // wsum is written again
   }
-  if (C > 1) cluster_arrive();          // waited for at the end: the others still read `mine`
+  if (C > 1) cluster_arrive_relaxed();  // waited for at the end: the others still read `mine`
   int* out = a.tokens + (int64_t)b * (S + 1);
   if (rank == 0) {
     for (int i = threadIdx.x; i <= S; i += V_NT)
@@ -357,12 +374,21 @@ cudaError_t launch_softmax(const SoftmaxArgs& a, cudaStream_t s) {
 
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s) {
   const int chunks = (a.V + CHUNK - 1) / CHUNK;
-  // CTAs a sequence: eight chunks a warp, or eight CTAs and more chunks; with few
-  // sequences as many CTAs as two chunks a warp take, while they still fill no
-  // more than the device
+  // CTAs a sequence: two chunks a warp or eight CTAs and more chunks; sixteen, which
+  // are opt-in, where the sequences are too few to fill the device with eight
   int C = 1;
-  while (C < 8 && C * V_NW * 8 < chunks) C *= 2;
-  while (C < 8 && C * V_NW * 2 < chunks && (int64_t)a.B * C * 2 <= dev_info().sms) C *= 2;
+  while (C < 8 && C * V_NW * 2 < chunks) C *= 2;
+  if (C == 8 && C * V_NW * 2 < chunks && (int64_t)a.B * 16 <= dev_info().sms) {
+    static thread_local int allowed = -1;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && allowed != dev) {
+      e = cudaFuncSetAttribute(verify_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      allowed = dev;
+    }
+    if (e != cudaSuccess) return e;
+    C = 16;
+  }
   const int per = (chunks + C * V_NW - 1) / (C * V_NW);
   return launch_step(verify_kernel, dim3((unsigned)a.B * C), V_NT, 0, s, C, a, C, per);
 }
