@@ -2,6 +2,8 @@
 // against the target's probabilities (qmv_verify_draft).
 #include <math_constants.h>
 
+#include <type_traits>
+
 #include "qmv_step.cuh"
 
 namespace qmv {
@@ -11,39 +13,11 @@ constexpr int MAX_NT = 512, MAX_C = 16;
 
 // ----------------------------------------------------------------- softmax --
 
-// The largest value of a CTA, and the first place of it (asked for by `place`).
-__device__ __forceinline__ void block_max(float& m, int& at, bool place, float* red, int* redi) {
-  const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-#pragma unroll
-  for (int pass = 0; pass < 2; ++pass) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      const float m2 = __shfl_xor_sync(~0u, m, o);
-      if (place) {
-        const int a2 = __shfl_xor_sync(~0u, at, o);
-        if (m2 > m || (m2 == m && a2 < at)) at = a2;
-      }
-      m = fmaxf(m, m2);
-    }
-    if (pass) break;
-    if (lane == 0) red[threadIdx.x >> 5] = m, redi[threadIdx.x >> 5] = at;
-    __syncthreads();
-    m = red[lane < nw ? lane : 0];
-    at = redi[lane < nw ? lane : 0];
-  }
-}
-
-__device__ __forceinline__ float block_sum(float v, float* red) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-  const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-  if (lane == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = lane < nw ? red[lane] : 0.0f;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-  return v;
-}
+// What a warp, a CTA or a cluster knows of its part of a row.
+struct Part {
+  float m, s;      // maximum; sum of exp((x - m) / T), in the one-hot form of 0 * x (NaN marks the row)
+  int at;          // first place of the maximum (in the one-hot form only)
+};
 
 // 2^v to 2 units in the last place; results below 2^-126 become 0.
 __device__ __forceinline__ float ex2(float v) {
@@ -52,119 +26,208 @@ __device__ __forceinline__ float ex2(float v) {
   return d;
 }
 
-// What a CTA knows of its part of a row.
-struct Part {
-  float m, s;      // maximum; sum of exp((x - m) / T), in the one-hot form of 0 * x (NaN marks the row)
-  int at;          // first place of the maximum
+// The parts of a warp's first W lanes (a power of two) as one, in each of them;
+// parts of nothing but -inf have the sum 0, or NaN where there was one.
+__device__ __forceinline__ Part join(Part p, int W, float c, bool hot) {
+  Part all = p;
+  for (int o = W >> 1; o; o >>= 1) {
+    const float m2 = __shfl_xor_sync(~0u, all.m, o);
+    if (hot) {
+      const int a2 = __shfl_xor_sync(~0u, all.at, o);
+      if (m2 > all.m || (m2 == all.m && a2 < all.at)) all.at = a2;
+    }
+    all.m = fmaxf(all.m, m2);
+  }
+  all.s = hot || p.m == -CUDART_INF_F ? p.s : p.s * ex2((p.m - all.m) * c);
+  for (int o = W >> 1; o; o >>= 1) all.s += __shfl_xor_sync(~0u, all.s, o);
+  return all;
+}
+
+// Four neighbouring elements, aligned to themselves, as they are stored and as fp32.
+template <typename X>
+struct Four {
+  typename std::conditional<sizeof(X) == 4, float4, uint2>::type w;
+  __device__ __forceinline__ void values(float (&v)[4]) const {
+    X h[4];
+    memcpy(h, &w, sizeof(w));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = to_f<X>(h[k]);
+  }
 };
 
 // A cluster of C CTAs a row (C = 1: no cluster).  EPT > 0: a CTA's part of the
-// row stays in registers, EPT elements a thread, so that the row is read once;
-// EPT == 0: a part of any length, read a second and third time (from L2).
-// exp((x - m) / T) is taken as exp2((x - m) * c), c = log2(e) / T.  A row with
+// row stays in registers, EPT elements a thread, so that the row is read once.  A
+// row is taken in fours that are aligned in memory, wherever it begins (an odd V
+// shifts every row; logits and out are shifted alike), `len` of them a CTA; all
+// loads of a thread are on their way before the first value is used.  The fours
+// that stick out of the row at its two ends are two threads' extra ones.
+// EPT == 0: rows of any length and alignment, `len` elements a CTA, read a second
+// and third time (from L2).
+// exp((x - m) / T) is taken as 2^((x - m) * c), c = log2(e) / T.  A row with
 // NaN or +inf has the sum NaN, which reaches every place by itself.
 template <typename X, int EPT, int NT>
 __global__ void __launch_bounds__(NT, 1024 / NT) softmax_kernel(SoftmaxArgs a, int C, int len) {
-  __shared__ Part mine;
-  __shared__ float redm[NT / 32], reds[NT / 32];
-  __shared__ int redi[NT / 32];
-  const int row = blockIdx.x / C, rank = blockIdx.x - row * C, tid = threadIdx.x;
-  const int v0 = min(a.V, rank * len), n = min(a.V - v0, len);     // this CTA's part
-  const X* x = (const X*)a.x + (int64_t)row * a.ldx + v0;
-  float* out = a.out + (int64_t)row * a.ldo + v0;
+  constexpr int NW = NT / 32;
+  __shared__ Part warps[NW], mine;
+  const int row = blockIdx.x / C, rank = blockIdx.x - row * C, tid = threadIdx.x, V = a.V;
+  const X* x = (const X*)a.x + (int64_t)row * a.ldx;
+  float* out = a.out + (int64_t)row * a.ldo;
+  constexpr int R = EPT ? EPT / 4 : 1;
+  // EPT > 0: four f of this CTA holds elements e_of(f) .. + 3; those from `whole0` on,
+  // `wholes` of them, are inside the row
+  const int shift = (int)((uintptr_t)x / sizeof(X) % 4), f0 = rank * len;
+  const auto e_of = [&](int f) { return 4 * (f0 + f) - shift; };
+  const int n = EPT ? max(0, min(len, (V + shift + 3) / 4 - f0)) : max(0, min(len, V - f0));
+  const int whole0 = f0 == 0 && shift ? 1 : 0, wholes = max(0, min(n, (V + shift) / 4 - f0) - whole0);
+  const auto is_whole = [&](int j) { return (unsigned)(j * NT + tid - whole0) < (unsigned)wholes; };
+  // thread 0: the first four, thread 1: the last, where they stick out
+  int extra = -1;
+  if (EPT && tid == 0 && whole0 && n > 0) extra = 0;
+  if (EPT && tid == 1 && whole0 + wholes < n) extra = n - 1;
   pdl_begin();
   const float t = a.t ? a.t[row] : a.t0;
   const bool hot = !(t > 0.0f);
   // kept finite and above 0, so that 0 * c = 0 and -inf * c = -inf at any T
   const float c = fminf(fmaxf(1.4426950408889634f / t, 1e-37f), 1e38f);
-  constexpr int R = EPT ? EPT : 1;
-  float e[R];
-  Part p{-CUDART_INF_F, 0.0f, a.V};
+  float e[R][4], ee[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+  Part p{-CUDART_INF_F, 0.0f, V};
   if (EPT) {
+    Four<X> w[R];
 #pragma unroll
-    for (int j = 0; j < R; ++j) e[j] = j * NT + tid < n ? to_f<X>(x[j * NT + tid]) : -CUDART_INF_F;
+    for (int j = 0; j < R; ++j)
+      if (is_whole(j)) w[j].w = *reinterpret_cast<const decltype(w[j].w)*>(x + e_of(j * NT + tid));
+    if (extra >= 0) {
 #pragma unroll
-    for (int j = 0; j < R; ++j) p.m = fmaxf(p.m, e[j]);
+      for (int k = 0; k < 4; ++k)
+        if ((unsigned)(e_of(extra) + k) < (unsigned)V) ee[k] = to_f<X>(x[e_of(extra) + k]);
+      p.m = fmaxf(fmaxf(ee[0], ee[1]), fmaxf(ee[2], ee[3]));
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      e[j][0] = e[j][1] = e[j][2] = e[j][3] = -CUDART_INF_F;
+      if (is_whole(j)) w[j].values(e[j]);
+      p.m = fmaxf(p.m, fmaxf(fmaxf(e[j][0], e[j][1]), fmaxf(e[j][2], e[j][3])));
+    }
     if (hot) {
+      const auto note = [&](const float (&v)[4], int e0) {
 #pragma unroll
-      for (int j = R - 1; j >= 0; --j) {
-        if (e[j] == p.m) p.at = v0 + j * NT + tid;
-        if (!(e[j] < CUDART_INF_F)) p.s = CUDART_NAN_F;
-      }
+        for (int k = 3; k >= 0; --k) {
+          if (v[k] == p.m) p.at = min(p.at, e0 + k);
+          if (!(v[k] < CUDART_INF_F)) p.s = CUDART_NAN_F;
+        }
+      };
+#pragma unroll
+      for (int j = 0; j < R; ++j)
+        if (is_whole(j)) note(e[j], e_of(j * NT + tid));
+      if (extra >= 0) note(ee, e_of(extra));
     }
   } else {
     for (int i = tid; i < n; i += NT) {
-      const float v = to_f<X>(x[i]);
-      if (v > p.m) p.m = v, p.at = v0 + i;
+      const float v = to_f<X>(x[f0 + i]);
+      if (v > p.m) p.m = v, p.at = f0 + i;
       if (hot && !(v < CUDART_INF_F)) p.s = CUDART_NAN_F;
     }
   }
-  block_max(p.m, p.at, hot, redm, redi);
+  // the warp's maximum; its terms are relative to it
+  {
+    const float own = p.m;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) p.m = fmaxf(p.m, __shfl_xor_sync(~0u, p.m, o));
+    if (hot) {
+      if (own != p.m) p.at = V;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) p.at = min(p.at, __shfl_xor_sync(~0u, p.at, o));
+    }
+  }
   // nothing but -inf so far: any finite maximum will do, every term is 0
   const float m = p.m == -CUDART_INF_F ? 0.0f : p.m;
   if (!hot) {
     if (EPT) {
 #pragma unroll
-      for (int j = 0; j < R; ++j) {
-        e[j] = ex2((e[j] - m) * c);
-        p.s += e[j];
+      for (int j = 0; j < R; ++j)
+        if (j * NT < n) {                      // the same for all threads
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            e[j][k] = ex2((e[j][k] - m) * c);
+            p.s += e[j][k];
+          }
+        }
+      if (extra >= 0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          ee[k] = ex2((ee[k] - m) * c);
+          p.s += ee[k];
+        }
       }
     } else {
-      for (int i = tid; i < n; i += NT) p.s += ex2((to_f<X>(x[i]) - m) * c);
+      for (int i = tid; i < n; i += NT) p.s += ex2((to_f<X>(x[f0 + i]) - m) * c);
     }
   }
-  p.s = block_sum(p.s, reds);
-  Part all = p;
-  if (C > 1) {
-    const int lane = tid & 31;
-    if (tid == 0) mine = p;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) p.s += __shfl_xor_sync(~0u, p.s, o);
+  const int lane = tid & 31;
+  if (lane == 0) warps[tid >> 5] = p;
+  __syncthreads();
+  Part all;
+  if (C == 1) {
+    all = join(warps[lane & (NW - 1)], NW, c, hot);
+  } else {
     if (tid < 32) {
+      const Part q = join(warps[lane & (NW - 1)], NW, c, hot);
+      if (lane == 0) mine = q;
       __syncwarp();
       cluster_arrive();
     } else {
       cluster_arrive_relaxed();
     }
     cluster_wait();
-    const uint32_t at = cluster_addr(&mine, lane < C ? lane : 0);
+    const uint32_t at = cluster_addr(&mine, lane & (C - 1));
     Part q;
     q.m = __uint_as_float(ld_cluster32(at));
     q.s = __uint_as_float(ld_cluster32(at + 4));
-    q.at = (int)ld_cluster32(at + 8);
-    all = q;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      const float m2 = __shfl_xor_sync(~0u, all.m, o);
-      const int a2 = __shfl_xor_sync(~0u, all.at, o);
-      if (m2 > all.m || (m2 == all.m && a2 < all.at)) all.at = a2;
-      all.m = fmaxf(all.m, m2);
-    }
-    float sum = lane >= C || q.m == -CUDART_INF_F ? 0.0f : hot ? q.s : q.s * ex2((q.m - all.m) * c);
-    // a part of NaN alone has the maximum -inf and the sum NaN
-    if (lane < C && isnan(q.s)) sum = q.s;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-    all.s = sum;
+    q.at = hot ? (int)ld_cluster32(at + 8) : V;
+    all = join(q, C, c, hot);
     cluster_arrive_relaxed();                // waited for at the end: the others still read `mine`
   }
-  if (hot || all.m == -CUDART_INF_F) {       // the one-hot form, or nothing but -inf (or NaN)
-    const float rest = isnan(all.s) ? all.s : 0.0f, one = all.m == -CUDART_INF_F ? rest : 1.0f + rest;
-    for (int i = tid; i < n; i += NT) out[i] = v0 + i == all.at ? one : rest;
-  } else {
-    // at most 1 over the sum; 0 where this part had only -inf, whose terms are 0
-    const float f = ex2((p.m - all.m) * c) / all.s;
-    if (EPT) {
+  // special rows, the one-hot form and rows of nothing but -inf (or NaN), have one
+  // value at all.at and another elsewhere; f is at most 1 over the sum, and NaN or
+  // finite where this warp had only -inf, whose terms are 0
+  const bool special = hot || all.m == -CUDART_INF_F;
+  const float rest = isnan(all.s) ? all.s : 0.0f, one = all.m == -CUDART_INF_F ? rest : 1.0f + rest;
+  const float f = p.m == -CUDART_INF_F ? rest : ex2((p.m - all.m) * c) / all.s;
+  if (EPT) {
+    const auto finish = [&](float (&v)[4], int e0) {
 #pragma unroll
-      for (int j = 0; j < R; ++j)
-        if (j * NT + tid < n) out[j * NT + tid] = e[j] * f;
-    } else {
-      for (int i = tid; i < n; i += NT) out[i] = ex2((to_f<X>(x[i]) - all.m) * c) / all.s;
+      for (int k = 0; k < 4; ++k) v[k] = special ? (e0 + k == all.at ? one : rest) : v[k] * f;
+    };
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+      if (is_whole(j)) {
+        const int e0 = e_of(j * NT + tid);
+        if (special) {
+          finish(e[j], e0);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) e[j][k] *= f;
+        }
+        *reinterpret_cast<float4*>(out + e0) = make_float4(e[j][0], e[j][1], e[j][2], e[j][3]);
+      }
+    if (extra >= 0) {
+      const int e0 = e_of(extra);
+      finish(ee, e0);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if ((unsigned)(e0 + k) < (unsigned)V) out[e0 + k] = ee[k];
     }
+  } else {
+    for (int i = tid; i < n; i += NT)
+      out[f0 + i] = special ? (f0 + i == all.at ? one : rest) : ex2((to_f<X>(x[f0 + i]) - all.m) * c) / all.s;
   }
   if (C > 1) cluster_wait();
 }
 
 template <typename X, int EPT, int NT>
-cudaError_t run_softmax(const SoftmaxArgs& a, int C, cudaStream_t s) {
+cudaError_t run_softmax(const SoftmaxArgs& a, int parts, int C, cudaStream_t s) {
   static thread_local int allowed = -1;
   if (C > 8) {                                // clusters of 16 are opt-in, a function and device
     int dev = 0;
@@ -175,17 +238,27 @@ cudaError_t run_softmax(const SoftmaxArgs& a, int C, cudaStream_t s) {
     }
     if (e != cudaSuccess) return e;
   }
-  return launch_step(softmax_kernel<X, EPT, NT>, dim3((unsigned)a.rows * C), NT, 0, s, C, a, C, (a.V + C - 1) / C);
+  return launch_step(softmax_kernel<X, EPT, NT>, dim3((unsigned)a.rows * C), NT, 0, s, C, a, C, (parts + C - 1) / C);
 }
 
 template <typename X>
 cudaError_t softmax_x(const SoftmaxArgs& a, cudaStream_t s) {
-  if (a.V <= 1024) return run_softmax<X, 8, 128>(a, 1, s);
-  if (a.V <= 4096) return run_softmax<X, 8, 512>(a, 1, s);
-  int C = 1;
+  // every row of logits and of out begins at the same place of an aligned four
+  const int sx = (int)((uintptr_t)a.x / sizeof(X) % 4), so = (int)((uintptr_t)a.out / 4 % 4);
+  const bool alike = (a.rows == 1 || a.ldx % 4 == a.ldo % 4) && sx == so;
+  const bool even = (a.rows == 1 || a.ldx % 4 == 0) && sx == 0;
+  const int fours = (int)(((int64_t)a.V + (even ? 0 : 3) + 3) / 4);   // of a row, at most
+  constexpr int PART = MAX_NT * 8;                                    // fours that a CTA holds
+  if (alike && fours <= MAX_C * PART) {
+    if (fours <= 128 * 2) return run_softmax<X, 8, 128>(a, fours, 1, s);
+    if (fours <= MAX_NT * 2) return run_softmax<X, 8, MAX_NT>(a, fours, 1, s);
+    int C = 1;
+    while (C * PART < fours) C *= 2;
+    return run_softmax<X, 32, MAX_NT>(a, fours, C, s);
+  }
+  int C = 1;                                  // 32 elements a thread, or 16 CTAs and more
   while (C < MAX_C && (int64_t)C * MAX_NT * 32 < a.V) C *= 2;
-  if ((int64_t)C * MAX_NT * 32 >= a.V) return run_softmax<X, 32, MAX_NT>(a, C, s);
-  return run_softmax<X, 0, MAX_NT>(a, MAX_C, s);
+  return run_softmax<X, 0, MAX_NT>(a, a.V, C, s);
 }
 
 // ------------------------------------------------------------------ verify --
@@ -222,34 +295,82 @@ __device__ __forceinline__ long long warp_before(long long v) {
   return s - v;
 }
 
-// A chunk: 256 neighbouring ids, eight a lane (chunk + 32 j + lane).
+// A chunk: 256 neighbouring ids, eight a lane.  VEC (rows that begin aligned to 16
+// bytes, V a multiple of 4): two fours, 128 h + 4 lane + k; otherwise 32 j + lane.
 constexpr int CHUNK = 256;
+template <bool VEC>
 struct Chunk {
   float x[8], y[8];
-  __device__ __forceinline__ void load(const float* p, const float* q, int at, int V) {
+  static __device__ __forceinline__ int id(int j) {
     const int lane = threadIdx.x & 31;
+    return VEC ? 128 * (j >> 2) + 4 * lane + (j & 3) : 32 * j + lane;
+  }
+  __device__ __forceinline__ void load(const float* p, const float* q, int at, int V) {
+    if (VEC) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int v = at + 32 * j + lane;
-      x[j] = v < V ? p[v] : 0.0f;
-      y[j] = q && v < V ? q[v] : 0.0f;
+      for (int h = 0; h < 2; ++h) {
+        const int v = at + id(4 * h);
+        float4 a = make_float4(0, 0, 0, 0), b = a;
+        if (v < V) {
+          a = *reinterpret_cast<const float4*>(p + v);
+          if (q) b = *reinterpret_cast<const float4*>(q + v);
+        }
+        x[4 * h] = a.x, x[4 * h + 1] = a.y, x[4 * h + 2] = a.z, x[4 * h + 3] = a.w;
+        y[4 * h] = b.x, y[4 * h + 1] = b.y, y[4 * h + 2] = b.z, y[4 * h + 3] = b.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int v = at + id(j);
+        x[j] = v < V ? p[v] : 0.0f;
+        y[j] = q && v < V ? q[v] : 0.0f;
+      }
     }
   }
-  // hot: the id whose q is 1 where the drafter was sure
-  __device__ __forceinline__ float weight(int j, int at, int hot) const {
-    return x[j] - (at + 32 * j + (int)(threadIdx.x & 31) == hot ? 1.0f : y[j]);
+  // hot: the id whose q is 1 where the drafter was sure, relative to the chunk
+  __device__ __forceinline__ void sure(int hot) {
+    if ((unsigned)hot < (unsigned)CHUNK) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (id(j) == hot) y[j] = 1.0f;
+    }
   }
-  __device__ __forceinline__ long long sum(int at, int hot) const {
+  __device__ __forceinline__ long long sum() const {
     uint32_t h = 0, l = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       uint32_t hi, lo;
-      units(weight(j, at, hot), hi, lo);
+      units(x[j] - y[j], hi, lo);
       h += hi;
       l += lo;
     }
     // at most 2^21 a weight, 2^29 a chunk
     return whole(__reduce_add_sync(~0u, h - 8 * BIAS), __reduce_add_sync(~0u, l - 8 * BIAS));
+  }
+  // The id (relative to the chunk) in which the running sum passes t, from `run`
+  // before the chunk, in the one lane that has it; -1 in the others.
+  __device__ __forceinline__ int find(long long run, long long t) const {
+    int found = -1;
+#pragma unroll
+    for (int g = 0; g < (VEC ? 2 : 8); ++g) {
+      constexpr int N = VEC ? 4 : 1;             // neighbours a lane
+      long long u[N], s = 0;
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        uint32_t hi, lo;
+        units(x[g * N + k] - y[g * N + k], hi, lo);
+        u[k] = whole(hi - BIAS, lo - BIAS);
+        s += u[k];
+      }
+      long long b = run + warp_before(s);
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        if (t >= b && t < b + u[k]) found = id(g * N + k);
+        b += u[k];
+      }
+      run += warp_sum(s);
+    }
+    return found;
   }
 };
 
@@ -258,6 +379,7 @@ struct Chunk {
 // one chunk in which the running sum passes the threshold.
 constexpr int V_NT = 512, V_NW = V_NT / 32, MAX_PER = 32;
 static_assert((int64_t)8 * V_NW * MAX_PER * CHUNK >= 1 << 20, "a chunk sum for every id");
+template <bool VEC>
 __global__ void __launch_bounds__(V_NT, 2) verify_kernel(VerifyArgs a, int C, int per) {
   constexpr int NW = V_NW;
   __shared__ long long chunk[NW][MAX_PER], wsum[NW], mine[2];
@@ -288,18 +410,19 @@ __global__ void __launch_bounds__(V_NT, 2) verify_kernel(VerifyArgs a, int C, in
   const bool refused = acc < n;
   const float* p = p0 + (int64_t)acc * V;
   const float* q = refused && q0 ? q0 + (int64_t)acc * V : nullptr;
-  int hot = refused && !q0 ? draft[acc] : -1;
+  int hot = refused && !q0 ? draft[acc] : -1;           // may lie outside 0 .. V - 1
   const int first = (rank * NW + warp) * per;           // this warp's chunks
   long long total = 0, before = 0, own = 0;
   for (int pass = 0; pass < 2; ++pass) {
     long long w = 0;
     const int last = min(per, max(0, (V + CHUNK - 1) / CHUNK - first));
-    Chunk c;
+    Chunk<VEC> c;
     if (last > 0) c.load(p, q, first * CHUNK, V);
     for (int i = 0; i < last; ++i) {
-      Chunk next;                         // on its way while this one is summed
+      Chunk<VEC> next;                    // on its way while this one is summed
       if (i + 1 < last) next.load(p, q, (first + i + 1) * CHUNK, V);
-      const long long s = c.sum((first + i) * CHUNK, hot);
+      c.sure(hot - (first + i) * CHUNK);
+      const long long s = c.sum();
       if (lane == 0) chunk[warp][i] = s;
       w += s;
       c = next;
@@ -346,17 +469,11 @@ __global__ void __launch_bounds__(V_NT, 2) verify_kernel(VerifyArgs a, int C, in
       int i = 0;
       while (run + chunk[warp][i] <= t) run += chunk[warp][i++];
       const int at = (first + i) * CHUNK;
-      Chunk c;
+      Chunk<VEC> c;
       c.load(p, q, at, V);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        uint32_t hi, lo;
-        units(c.weight(j, at, hot), hi, lo);
-        const long long u = whole(hi - BIAS, lo - BIAS);
-        const long long b0 = run + warp_before(u);
-        if (t >= b0 && t < b0 + u) out[acc] = at + 32 * j + lane;
-        run += warp_sum(u);
-      }
+      c.sure(hot - at);
+      const int id = c.find(run, t);
+      if (id >= 0) out[acc] = at + id;
     }
   }
   if (C > 1) cluster_wait();
@@ -372,7 +489,8 @@ cudaError_t launch_softmax(const SoftmaxArgs& a, cudaStream_t s) {
   }
 }
 
-cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s) {
+template <bool VEC>
+static cudaError_t run_verify(const VerifyArgs& a, cudaStream_t s) {
   const int chunks = (a.V + CHUNK - 1) / CHUNK;
   // CTAs a sequence: two chunks a warp or eight CTAs and more chunks; sixteen, which
   // are opt-in, where the sequences are too few to fill the device with eight
@@ -383,14 +501,19 @@ cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && allowed != dev) {
-      e = cudaFuncSetAttribute(verify_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      e = cudaFuncSetAttribute(verify_kernel<VEC>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       allowed = dev;
     }
     if (e != cudaSuccess) return e;
     C = 16;
   }
   const int per = (chunks + C * V_NW - 1) / (C * V_NW);
-  return launch_step(verify_kernel, dim3((unsigned)a.B * C), V_NT, 0, s, C, a, C, per);
+  return launch_step(verify_kernel<VEC>, dim3((unsigned)a.B * C), V_NT, 0, s, C, a, C, per);
+}
+
+cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s) {
+  const bool vec = a.V % 4 == 0 && (uintptr_t)a.p % 16 == 0 && (uintptr_t)a.q % 16 == 0;
+  return vec ? run_verify<true>(a, s) : run_verify<false>(a, s);
 }
 
 }  // namespace qmv
