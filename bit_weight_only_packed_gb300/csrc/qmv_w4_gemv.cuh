@@ -19,6 +19,8 @@
 // begin and end inside a strip, and only those partial sums are joined, once,
 // at the end.  Every warp keeps a ring of bulk copies of its own in flight.
 #pragma once
+#include <type_traits>
+
 #include "qmv_pipe.cuh"
 #include "qmv_step.cuh"
 
@@ -155,8 +157,7 @@ struct Block {
 #pragma unroll
     for (int gi = 0; gi < GPB; ++gi) {
       sc[gi] = *reinterpret_cast<const uint2*>(meta + gi * (2 * ROWS));
-      zp[gi] = zeros ? *reinterpret_cast<const uint32_t*>(p + CODE_BYTES + 2 * GPB * ROWS + gi * ROWS + (lane >> 2) * 4)
-                     : 0x08080808u;
+      if (zeros) zp[gi] = *reinterpret_cast<const uint32_t*>(p + CODE_BYTES + 2 * GPB * ROWS + gi * ROWS + (lane >> 2) * 4);
     }
   }
 };
@@ -171,7 +172,8 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
   __shared__ uint64_t full[W][MAX_SLOTS];
   __shared__ uint64_t x_full;
   __shared__ int abort_flag;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  // the warp's number from one lane, so that what follows from it is known to be uniform
+  const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int KB = cdiv(a.K, BK), NS = cdiv(a.N, ROWS), bb = block_bytes(GROUP, a.zeros != 0);
   const int m0 = blockIdx.y * P.cols, mc = min(P.cols, a.M - m0);
   const int rank = blockIdx.x & (P.ks - 1), cl = blockIdx.x >> P.ks_log;
@@ -186,9 +188,11 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) abort_flag = 0;
 
-  // Lane 0 keeps the ring full.  A copy is up to `stage` neighbouring blocks of a strip.
+  // The ring is kept full by lane 0; all lanes follow its course.  A copy is up to
+  // `stage` neighbouring blocks of a strip.
   const uint8_t* src = nullptr;
-  int p_round = -1, p_left = 0, p_blk = 0, issued = 0, used = 0;
+  int p_round = -1, p_left = 0, p_blk = 0, issued = 0, landed = 0;
+  bool dead = false;                       // a wait of this lane ran out
   const auto next_round = [&]() {
     while (p_left == 0 && ++p_round < rounds) {
       const int lo = first_of(p_round, warp);
@@ -199,13 +203,15 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
     }
   };
   const auto issue = [&](int s) {
-    const int cnt = min(P.stage, min(p_left, kbn - p_blk));
-    pipe::mbar_arrive_tx(&full[warp][s], cnt * bb);
-    bulk_g2s(ring + s * P.stage * bb, src, cnt * bb, &full[warp][s]);
-    ++issued;
+    const int cnt = min(P.stage, min(p_left, kbn - p_blk)), bytes = cnt * bb;
+    if (lane == 0 && !dead) {
+      pipe::mbar_arrive_tx(&full[warp][s], bytes);
+      bulk_g2s(ring + s * P.stage * bb, src, bytes, &full[warp][s]);
+    }
+    issued += !dead;
     p_left -= cnt;
     p_blk += cnt;
-    src += (int64_t)cnt * bb;
+    src += bytes;
     if (p_blk == kbn) p_blk = 0, src += (int64_t)(KB - kbn) * bb;
     if (p_left == 0) next_round();
   };
@@ -213,10 +219,12 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
     for (int i = 0; i < P.slots; ++i) pipe::mbar_init(&full[warp][i], 1);
     if (warp == 0) pipe::mbar_init(&x_full, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    if (!a.early) asm volatile("griddepcontrol.wait;" ::: "memory");
-    next_round();
-    for (int i = 0; i < P.slots && p_left > 0; ++i) issue(i);
   }
+  if (!a.early) asm volatile("griddepcontrol.wait;" ::: "memory");
+  __syncwarp();
+  next_round();
+  for (int i = 0; i < P.slots && p_left > 0; ++i) issue(i);
+
   // x to shared memory as it is, a row a column, P.pitch bytes apart (64 past a
   // multiple of 128, so that the eight lanes of a 128-byte read touch different banks).
   uint8_t* xs = smem + P.x_off;
@@ -286,7 +294,8 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
 
   const uint32_t bits3 = in_register<0x00780078u>(), sixteen = in_register<0x41804180u>();   // bf16 codes
   // One block (the CTA's b-th of k) of a strip, added to tot.
-  const auto product = [&](const Block<GPB>& B, int b, float (&tot)[2][NB][4]) {
+  const auto product = [&](auto with_zeros, const Block<GPB>& B, int b, float (&tot)[2][NB][4]) {
+    constexpr bool Z = decltype(with_zeros)::value;
     const int xo = b * 256, xl = b * l_step;
     const float* sxp = xsum + b * (GPB * 8 * NB) + 2 * t;
 #pragma unroll
@@ -336,7 +345,7 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
       for (int r = 0; r < 2; ++r) {
         const uint32_t s2 = r ? B.sc[gi].y : B.sc[gi].x;
         const float s0 = f16_f(s2 & 0xffffu, SB), s1 = SB ? __uint_as_float(s2 & 0xffff0000u) : f16_f(s2 >> 16, SB);
-        const float z0 = zero_f<XB>(B.zp[gi], 2 * r), z1 = zero_f<XB>(B.zp[gi], 2 * r + 1);
+        const float z0 = Z ? zero_f<XB>(B.zp[gi], 2 * r) : XB ? 24.0f : 0x1p-18f, z1 = Z ? zero_f<XB>(B.zp[gi], 2 * r + 1) : z0;
 #pragma unroll
         for (int c = 0; c < NB; ++c)
 #pragma unroll
@@ -359,18 +368,24 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
     int place = 0;                         // the first strip of the range, later ones
     while (f < hi) {
       const int cnt = min(P.stage, min(hi - f, kbn - blk));
-      if (!__all_sync(~0u, pipe::mbar_wait_fast(&full[warp][slot], parity, &abort_flag, pipe::ERR_TIMEOUT_FULL, &g_w4_error)))
-        break;
+      // after a wait that ran out nothing is copied or stored any more, but the warp
+      // keeps to its course
+      dead |= !pipe::mbar_wait_fast(&full[warp][slot], parity, &abort_flag, pipe::ERR_TIMEOUT_FULL, &g_w4_error);
+      landed += !dead;
       const uint8_t* p = ring + slot * P.stage * bb;
       Block<GPB> A, B;
       A.load(p, lane, a.zeros);
       if (cnt > 1) B.load(p + bb, lane, a.zeros);
-      ++used;
       __syncwarp();                        // every lane has read the slot: fill it again
-      if (lane == 0 && p_left > 0) issue(slot);
+      if (p_left > 0) issue(slot);
       if (++slot == P.slots) slot = 0, parity ^= 1;
-      product(A, blk, tot);
-      if (cnt > 1) product(B, blk + 1, tot);
+      if (a.zeros) {
+        product(std::true_type(), A, blk, tot);
+        if (cnt > 1) product(std::true_type(), B, blk + 1, tot);
+      } else {
+        product(std::false_type(), A, blk, tot);
+        if (cnt > 1) product(std::false_type(), B, blk + 1, tot);
+      }
       f += cnt;
       blk += cnt;
       if (blk == kbn || f == hi) {         // the end of the strip, or of the range
@@ -435,11 +450,9 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
     }
   }
   // after a wait that ran out: let the copies in flight land before the CTA ends
-  if (lane == 0)
-    for (; used < issued; ++used) {
-      pipe::mbar_drain(&full[warp][slot], parity, &g_w4_error);
-      if (++slot == P.slots) slot = 0, parity ^= 1;
-    }
+  if (lane == 0 && dead)
+    for (; landed < issued; ++landed)
+      pipe::mbar_drain(&full[warp][landed % P.slots], (landed / P.slots) & 1, &g_w4_error);
   if (P.ks > 1) {                          // the others may still read this CTA's sums
     __syncwarp();
     cluster_arrive();
