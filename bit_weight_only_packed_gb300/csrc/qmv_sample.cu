@@ -47,6 +47,11 @@ __device__ __forceinline__ Part join(Part p, int W, float c, bool hot) {
 template <typename X>
 struct Four {
   typename std::conditional<sizeof(X) == 4, float4, uint2>::type w;
+  __device__ __forceinline__ void none() {                   // all -inf
+    constexpr uint32_t P = std::is_same<X, float>::value ? 0xFF800000u : std::is_same<X, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
+    const uint32_t v[4] = {P, P, P, P};
+    memcpy(&w, v, sizeof(w));
+  }
   __device__ __forceinline__ void values(float (&v)[4]) const {
     X h[4];
     memcpy(h, &w, sizeof(w));
@@ -55,58 +60,79 @@ struct Four {
   }
 };
 
-// A cluster of C CTAs a row (C = 1: no cluster).  EPT > 0: a CTA's part of the
-// row stays in registers, EPT elements a thread, so that the row is read once.  A
-// row is taken in fours that are aligned in memory, wherever it begins (an odd V
-// shifts every row; logits and out are shifted alike), `len` of them a CTA; all
-// loads of a thread are on their way before the first value is used.  The fours
-// that stick out of the row at its two ends are two threads' extra ones.
+// A CTA's part of a row (EPT > 0): `wholes` aligned fours inside the row, the first
+// at element e0, and what sticks out of the fours at the row's two ends, elements
+// e1 .. e1 + 3 as far as they are in the row: thread 0's and thread 1's extra four.
+template <typename X>
+struct Place {
+  const X* x;
+  float* out;
+  int e0, wholes, e1;
+  bool extra;
+  __device__ __forceinline__ Place(const SoftmaxArgs& a, int row, int f0, int len) {
+    x = (const X*)a.x + (int64_t)row * a.ldx;
+    out = a.out + (int64_t)row * a.ldo;
+    const int shift = (int)((uintptr_t)x / sizeof(X) % 4);
+    const int n = max(0, min(len, (a.V + shift + 3) / 4 - f0)), skip = f0 == 0 && shift ? 1 : 0;
+    wholes = max(0, min(n, (a.V + shift) / 4 - f0) - skip);
+    e0 = 4 * (f0 + skip) - shift;
+    const bool behind = skip + wholes < n;
+    extra = (threadIdx.x == 0 && skip && n > 0) || (threadIdx.x == 1 && behind);
+    e1 = threadIdx.x == 0 ? -shift : 4 * (f0 + n - 1) - shift;
+  }
+};
+
+// A cluster of C CTAs a row (C = 1: no cluster).  EPT > 0: a CTA's
+// part of the row stays in registers, EPT elements a thread, so that the row is
+// read once.  A row is taken in fours that are aligned in memory, wherever it
+// begins (an odd V shifts every row; logits and out are shifted alike), `len` of
+// them a CTA; all loads of a thread are on their way before the first value is
+// used.
 // EPT == 0: rows of any length and alignment, `len` elements a CTA, read a second
 // and third time (from L2).
 // exp((x - m) / T) is taken as 2^((x - m) * c), c = log2(e) / T.  A row with
 // NaN or +inf has the sum NaN, which reaches every place by itself.
 template <typename X, int EPT, int NT>
 __global__ void __launch_bounds__(NT, 1024 / NT) softmax_kernel(SoftmaxArgs a, int C, int len) {
-  constexpr int NW = NT / 32;
+  constexpr int NW = NT / 32, R = EPT ? EPT / 4 : 1;
   __shared__ Part warps[NW], mine;
-  const int row = blockIdx.x / C, rank = blockIdx.x - row * C, tid = threadIdx.x, V = a.V;
-  const X* x = (const X*)a.x + (int64_t)row * a.ldx;
-  float* out = a.out + (int64_t)row * a.ldo;
-  constexpr int R = EPT ? EPT / 4 : 1;
-  // EPT > 0: four f of this CTA holds elements e_of(f) .. + 3; those from `whole0` on,
-  // `wholes` of them, are inside the row
-  const int shift = (int)((uintptr_t)x / sizeof(X) % 4), f0 = rank * len;
-  const auto e_of = [&](int f) { return 4 * (f0 + f) - shift; };
-  const int n = EPT ? max(0, min(len, (V + shift + 3) / 4 - f0)) : max(0, min(len, V - f0));
-  const int whole0 = f0 == 0 && shift ? 1 : 0, wholes = max(0, min(n, (V + shift) / 4 - f0) - whole0);
-  const auto is_whole = [&](int j) { return (unsigned)(j * NT + tid - whole0) < (unsigned)wholes; };
-  // thread 0: the first four, thread 1: the last, where they stick out
-  int extra = -1;
-  if (EPT && tid == 0 && whole0 && n > 0) extra = 0;
-  if (EPT && tid == 1 && whole0 + wholes < n) extra = n - 1;
+  const int rank = blockIdx.x % C, tid = threadIdx.x, lane = tid & 31, V = a.V, f0 = rank * len;
+  const int row = blockIdx.x / C;
+  const Place<X> at(a, row, f0, len);
+  Four<X> w[R];                                // the row as it is stored
+  X we[4];
   pdl_begin();
+  if (EPT) {
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      w[j].none();
+      if (j * NT + tid < at.wholes) w[j].w = reinterpret_cast<const decltype(w[j].w)*>(at.x + at.e0)[j * NT + tid];
+    }
+    if (at.extra) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if ((unsigned)(at.e1 + k) < (unsigned)V) we[k] = at.x[at.e1 + k];
+    }
+  }
   const float t = a.t ? a.t[row] : a.t0;
   const bool hot = !(t > 0.0f);
   // kept finite and above 0, so that 0 * c = 0 and -inf * c = -inf at any T
   const float c = fminf(fmaxf(1.4426950408889634f / t, 1e-37f), 1e38f);
+  const int n0 = max(0, min(len, V - f0));                 // EPT == 0: elements
   float e[R][4], ee[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
   Part p{-CUDART_INF_F, 0.0f, V};
   if (EPT) {
-    Four<X> w[R];
-#pragma unroll
-    for (int j = 0; j < R; ++j)
-      if (is_whole(j)) w[j].w = *reinterpret_cast<const decltype(w[j].w)*>(x + e_of(j * NT + tid));
-    if (extra >= 0) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if ((unsigned)(e_of(extra) + k) < (unsigned)V) ee[k] = to_f<X>(x[e_of(extra) + k]);
-      p.m = fmaxf(fmaxf(ee[0], ee[1]), fmaxf(ee[2], ee[3]));
-    }
 #pragma unroll
     for (int j = 0; j < R; ++j) {
-      e[j][0] = e[j][1] = e[j][2] = e[j][3] = -CUDART_INF_F;
-      if (is_whole(j)) w[j].values(e[j]);
+      w[j].values(e[j]);
       p.m = fmaxf(p.m, fmaxf(fmaxf(e[j][0], e[j][1]), fmaxf(e[j][2], e[j][3])));
+    }
+    if (at.extra) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if ((unsigned)(at.e1 + k) < (unsigned)V) ee[k] = to_f<X>(we[k]);
+        p.m = fmaxf(p.m, ee[k]);
+      }
     }
     if (hot) {
       const auto note = [&](const float (&v)[4], int e0) {
@@ -118,12 +144,12 @@ __global__ void __launch_bounds__(NT, 1024 / NT) softmax_kernel(SoftmaxArgs a, i
       };
 #pragma unroll
       for (int j = 0; j < R; ++j)
-        if (is_whole(j)) note(e[j], e_of(j * NT + tid));
-      if (extra >= 0) note(ee, e_of(extra));
+        if (j * NT + tid < at.wholes) note(e[j], at.e0 + 4 * (j * NT + tid));
+      if (at.extra) note(ee, at.e1);
     }
   } else {
-    for (int i = tid; i < n; i += NT) {
-      const float v = to_f<X>(x[f0 + i]);
+    for (int i = tid; i < n0; i += NT) {
+      const float v = to_f<X>(at.x[f0 + i]);
       if (v > p.m) p.m = v, p.at = f0 + i;
       if (hot && !(v < CUDART_INF_F)) p.s = CUDART_NAN_F;
     }
@@ -145,14 +171,14 @@ __global__ void __launch_bounds__(NT, 1024 / NT) softmax_kernel(SoftmaxArgs a, i
     if (EPT) {
 #pragma unroll
       for (int j = 0; j < R; ++j)
-        if (j * NT < n) {                      // the same for all threads
+        if (j * NT < at.wholes) {            // the same for all threads
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             e[j][k] = ex2((e[j][k] - m) * c);
             p.s += e[j][k];
           }
         }
-      if (extra >= 0) {
+      if (at.extra) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           ee[k] = ex2((ee[k] - m) * c);
@@ -160,12 +186,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) softmax_kernel(SoftmaxArgs a, i
         }
       }
     } else {
-      for (int i = tid; i < n; i += NT) p.s += ex2((to_f<X>(x[f0 + i]) - m) * c);
+      for (int i = tid; i < n0; i += NT) p.s += ex2((to_f<X>(at.x[f0 + i]) - m) * c);
     }
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) p.s += __shfl_xor_sync(~0u, p.s, o);
-  const int lane = tid & 31;
   if (lane == 0) warps[tid >> 5] = p;
   __syncthreads();
   Part all;
@@ -181,13 +206,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) softmax_kernel(SoftmaxArgs a, i
       cluster_arrive_relaxed();
     }
     cluster_wait();
-    const uint32_t at = cluster_addr(&mine, lane & (C - 1));
+    const uint32_t from = cluster_addr(&mine, lane & (C - 1));
     Part q;
-    q.m = __uint_as_float(ld_cluster32(at));
-    q.s = __uint_as_float(ld_cluster32(at + 4));
-    q.at = hot ? (int)ld_cluster32(at + 8) : V;
+    q.m = __uint_as_float(ld_cluster32(from));
+    q.s = __uint_as_float(ld_cluster32(from + 4));
+    q.at = hot ? (int)ld_cluster32(from + 8) : V;
     all = join(q, C, c, hot);
-    cluster_arrive_relaxed();                // waited for at the end: the others still read `mine`
+    cluster_arrive_relaxed();              // waited for below: the others still read `mine`
   }
   // special rows, the one-hot form and rows of nothing but -inf (or NaN), have one
   // value at all.at and another elsewhere; f is at most 1 over the sum, and NaN or
@@ -196,32 +221,29 @@ __global__ void __launch_bounds__(NT, 1024 / NT) softmax_kernel(SoftmaxArgs a, i
   const float rest = isnan(all.s) ? all.s : 0.0f, one = all.m == -CUDART_INF_F ? rest : 1.0f + rest;
   const float f = p.m == -CUDART_INF_F ? rest : ex2((p.m - all.m) * c) / all.s;
   if (EPT) {
-    const auto finish = [&](float (&v)[4], int e0) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = special ? (e0 + k == all.at ? one : rest) : v[k] * f;
-    };
-#pragma unroll
-    for (int j = 0; j < R; ++j)
-      if (is_whole(j)) {
-        const int e0 = e_of(j * NT + tid);
-        if (special) {
-          finish(e[j], e0);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) e[j][k] *= f;
-        }
-        *reinterpret_cast<float4*>(out + e0) = make_float4(e[j][0], e[j][1], e[j][2], e[j][3]);
+    float4* to = reinterpret_cast<float4*>(at.out + at.e0);
+    const auto value = [&](int el) { return el == all.at ? one : rest; };
+    if (special) {
+      for (int i = tid; i < at.wholes; i += NT) {
+        const int el = at.e0 + 4 * i;
+        to[i] = make_float4(value(el), value(el + 1), value(el + 2), value(el + 3));
       }
-    if (extra >= 0) {
-      const int e0 = e_of(extra);
-      finish(ee, e0);
+    } else {
+#pragma unroll
+      for (int j = 0; j < R; ++j)
+        if (j * NT < at.wholes) {            // the same for all threads
+          const float4 q = make_float4(e[j][0] * f, e[j][1] * f, e[j][2] * f, e[j][3] * f);
+          if (j * NT + tid < at.wholes) to[j * NT + tid] = q;
+        }
+    }
+    if (at.extra) {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if ((unsigned)(e0 + k) < (unsigned)V) out[e0 + k] = ee[k];
+        if ((unsigned)(at.e1 + k) < (unsigned)V) at.out[at.e1 + k] = special ? value(at.e1 + k) : ee[k] * f;
     }
   } else {
-    for (int i = tid; i < n; i += NT)
-      out[f0 + i] = special ? (f0 + i == all.at ? one : rest) : ex2((to_f<X>(x[f0 + i]) - all.m) * c) / all.s;
+    for (int i = tid; i < n0; i += NT)
+      at.out[f0 + i] = special ? (f0 + i == all.at ? one : rest) : ex2((to_f<X>(at.x[f0 + i]) - all.m) * c) / all.s;
   }
   if (C > 1) cluster_wait();
 }
@@ -248,13 +270,12 @@ cudaError_t softmax_x(const SoftmaxArgs& a, cudaStream_t s) {
   const bool alike = (a.rows == 1 || a.ldx % 4 == a.ldo % 4) && sx == so;
   const bool even = (a.rows == 1 || a.ldx % 4 == 0) && sx == 0;
   const int fours = (int)(((int64_t)a.V + (even ? 0 : 3) + 3) / 4);   // of a row, at most
-  constexpr int PART = MAX_NT * 8;                                    // fours that a CTA holds
-  if (alike && fours <= MAX_C * PART) {
+  if (alike) {
     if (fours <= 128 * 2) return run_softmax<X, 8, 128>(a, fours, 1, s);
     if (fours <= MAX_NT * 2) return run_softmax<X, 8, MAX_NT>(a, fours, 1, s);
     int C = 1;
-    while (C * PART < fours) C *= 2;
-    return run_softmax<X, 32, MAX_NT>(a, fours, C, s);
+    while (C < MAX_C && C * MAX_NT * 8 < fours) C *= 2;
+    if (C * MAX_NT * 8 >= fours) return run_softmax<X, 32, MAX_NT>(a, fours, C, s);
   }
   int C = 1;                                  // 32 elements a thread, or 16 CTAs and more
   while (C < MAX_C && (int64_t)C * MAX_NT * 32 < a.V) C *= 2;
