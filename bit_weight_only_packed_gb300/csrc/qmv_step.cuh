@@ -161,14 +161,20 @@ __device__ __forceinline__ uint32_t ld_cluster32(uint32_t a) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
-__device__ __forceinline__ long long ld_cluster64(uint32_t a) {
-  long long v;
-  asm volatile("ld.shared::cluster.s64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
-  return v;
+// Stores to another CTA's shared memory that complete on its mbarrier `bar`.
+__device__ __forceinline__ void st_async128(uint32_t to, uint32_t bar, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+               "r"(a), "r"(b), "r"(c), "r"(d), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void st_async64(uint32_t to, uint32_t bar, long long v) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(to), "l"(v), "r"(bar)
+               : "memory");
 }
 
-// The device error word of the 4-bit matvec (bounded waits).
+// The device error words of the 4-bit matvec and of softmax and verification (bounded waits).
 int read_w4_error(int clear, int* out);
+int read_sample_error(int clear, int* out);
 
 // 16-bit elements as fp32 and back (round to nearest even).
 template <typename T>

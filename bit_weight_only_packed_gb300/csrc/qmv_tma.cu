@@ -553,6 +553,7 @@ int read_tc_error(int clear, int* out);
 int read_chain_error(int clear, int* out);
 int read_mt_error(int clear, int* out);
 int read_w4_error(int clear, int* out);
+int read_sample_error(int clear, int* out);
 
 int read_device_error(int clear, int* out) {
   int t = 0, ch = 0, mt = 0, w4 = 0;
@@ -564,6 +565,9 @@ int read_device_error(int clear, int* out) {
   if (em != 0) return em;
   const int e4 = read_w4_error(clear, &w4);
   if (e4 != 0) return e4;
+  if (w4) t = w4;
+  const int es = read_sample_error(clear, &w4);
+  if (es != 0) return es;
   if (w4) t = w4;
   if (mt) t = mt;
   if (ch) t = ch;
