@@ -2,8 +2,8 @@
 
 Each .cu file is compiled by its own nvcc process (in parallel), then linked
 into ``bit_weight_only_packed_gb300/_lib/libqmv.so``.  No fast-math: the
-kernels rely on IEEE fp32 rounding.  The binding's host module (plain C against
-the running Python's headers) goes beside it as ``qmv_host.so``.
+kernels rely on IEEE fp32 rounding.  The binding's host module (C++ against the
+running torch's and Python's headers) goes beside it as ``qmv_host.so``.
 """
 from __future__ import annotations
 
@@ -19,7 +19,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libqmv.so")
-HOST_SRC = os.path.join(CSRC, "host", "qmv_host.c")
+HOST_SRC = os.path.join(CSRC, "host", "qmv_host.cpp")
 HOST_LIB = os.path.join(OUT_DIR, "qmv_host.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -51,13 +51,21 @@ def _stale(lib: str, deps) -> bool:
 def build_host(force: bool = False) -> str:
     if not force and not _stale(HOST_LIB, [HOST_SRC, os.path.join(ROOT, "include", "qmv.h"), __file__]):
         return HOST_LIB
+    import torch
     os.makedirs(OUT_DIR, exist_ok=True)
+    tdir = os.path.dirname(os.path.abspath(torch.__file__))
+    tlib = os.path.join(tdir, "lib")
+    inc = [os.path.join(tdir, "include"), os.path.join(tdir, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include"),
+           sysconfig.get_paths()["include"]]
     tmp = HOST_LIB + f".tmp{os.getpid()}"
-    r = subprocess.run(["gcc", "-std=c11", "-O2", "-Wall", "-shared", "-fPIC", "-fvisibility=hidden",
-                        "-I", sysconfig.get_paths()["include"], "-I", os.path.join(ROOT, "include"), "-o", tmp,
-                        HOST_SRC], capture_output=True, text=True)
+    r = subprocess.run(["g++", "-std=c++17", "-O2", "-shared", "-fPIC", "-fvisibility=hidden",
+                        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                        *(f for d in inc for f in ("-isystem", d)), "-I", os.path.join(ROOT, "include"), "-o", tmp,
+                        HOST_SRC, "-L", tlib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+                        f"-Wl,-rpath,{tlib}"], capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"gcc failed on {HOST_SRC}:\n{r.stderr}")
+        raise RuntimeError(f"g++ failed on {HOST_SRC}:\n{r.stderr}")
     os.replace(tmp, HOST_LIB)
     return HOST_LIB
 
@@ -65,8 +73,8 @@ def build_host(force: bool = False) -> str:
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [
         os.path.join(ROOT, "include", "qmv.h"), __file__]
-    build_host(force)
     if not force and not extra and not _stale(LIB, deps):
+        build_host()
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
     tmpdir = os.path.join(OUT_DIR, f"obj{os.getpid()}")
@@ -86,7 +94,9 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+        host = ex.submit(build_host, force)
         objs = list(ex.map(compile_one, sources()))
+        host.result()
     tmp_lib = LIB + f".tmp{os.getpid()}"
     link = [cc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp_lib, *objs,
             "-Xlinker", "-rpath,/usr/local/cuda/lib64"]

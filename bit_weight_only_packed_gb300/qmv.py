@@ -466,7 +466,7 @@ _FLOAT = (torch.float32, torch.float16, torch.bfloat16)
 
 
 def _load_host():
-    """qmv_host.so (csrc/host/qmv_host.c): the usual form of these calls in C."""
+    """qmv_host.so (csrc/host/qmv_host.cpp): the usual form of these calls in C++."""
     path = os.path.join(_HERE, "_lib", "qmv_host.so")
     if not os.path.exists(path):
         raise ImportError(f"qmv_host.so is not built ({path}); run "
@@ -475,10 +475,7 @@ def _load_host():
     mod = importlib.util.module_from_spec(importlib.util.spec_from_file_location("qmv_host", path, loader=loader))
     loader.exec_module(mod)
     addr = lambda f: ctypes.cast(f, _P).value
-    mod.init(torch.Tensor, torch.empty, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream,
-             (torch.float32, torch.float16, torch.bfloat16, torch.int32),
-             (addr(_lib.qmv_w4_gemv), addr(_lib.qmv_block_norm), addr(_lib.qmv_softmax),
-              addr(_lib.qmv_verify_draft)))
+    mod.init(addr(_lib.qmv_w4_gemv), addr(_lib.qmv_block_norm), addr(_lib.qmv_softmax), addr(_lib.qmv_verify_draft))
     return mod
 
 
