@@ -114,6 +114,7 @@ struct Plan {
   int vec;                      // x can be read 16 bytes at a time
   int pitch;                    // bytes between the columns of x in shared memory
   int x_off, zero_off, xs_off, part_off, red_off, smem;   // bytes in shared memory; the rings come first
+  int second_off, second_step;  // the second places of the warps
 };
 
 // A sum by its definition: for columns with infinities, NaN or values near
@@ -278,7 +279,12 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
   __syncthreads();
 
   float* red = reinterpret_cast<float*>(smem + P.red_off);             // [2][rs][mc][32], clusters only
-  float* part = reinterpret_cast<float*>(smem + P.part_off);           // [W][2][mc][32]
+  // Where warp w leaves a partial sum [mc][32]: that of the first strip of its range
+  // (place 0), or of a later one (place 1, which may be its own ring, by then read out).
+  const auto place = [&](int w, int second) {
+    return reinterpret_cast<float*>(second ? smem + P.second_off + (size_t)w * P.second_step
+                                           : smem + P.part_off + (size_t)w * (P.cols * ROWS * 4));
+  };
   // A finished sum goes out (or to the cluster's sum).  One that is not finite is
   // formed again by its definition.
   const auto emit = [&](int round, int s, int m, float v) {
@@ -364,8 +370,7 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
     const int s_lo = (int)((unsigned)lo / (unsigned)kbn), F = strips_of(round) * kbn;
     int s = s_lo, blk = lo - s * kbn, f = lo, from = blk;
     float tot[2][NB][4] = {};
-    float* mine = part + warp * (2 * mc * ROWS);
-    int place = 0;                         // the first strip of the range, later ones
+    float* to = place(warp, 0);            // the first strip of the range, later ones
     while (f < hi) {
       const int cnt = min(P.stage, min(hi - f, kbn - blk));
       // after a wait that ran out nothing is copied or stored any more, but the warp
@@ -389,7 +394,6 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
       f += cnt;
       blk += cnt;
       if (blk == kbn || f == hi) {         // the end of the strip, or of the range
-        float* to = mine + place * (mc * ROWS);
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -408,11 +412,11 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
         }
         ++s;
         blk = from = 0;
-        place = 1;
+        to = place(warp, 1);
       }
     }
     if (lo == hi && lo < F)                // fewer blocks than warps: nothing to add
-      for (int m = 0; m < mc; ++m) mine[part_at(m, lane)] = 0.0f;
+      for (int m = 0; m < mc; ++m) to[part_at(m, lane)] = 0.0f;
     __syncthreads();
     // Strips that several warps share: the warps w0 .. w0 + nw - 1 whose ranges begin in
     // the strip share out its columns.  Their pieces are in their first places, and
@@ -422,11 +426,10 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
       const int w0 = (int)(((unsigned)begin * W + F - 1) / F), nw = (int)(((unsigned)end * W + F - 1) / F) - w0;
       const bool inside = first_of(round, w0) != begin, whole = first_of(round, w0 + nw - 1) == begin;
       if (!whole) {                        // else one warp had all of it
-        const float* from0 = part + w0 * (2 * mc * ROWS);
 #pragma unroll 1
         for (int m = warp - w0; m < mc; m += nw) {
-          float v = inside ? from0[part_at(m, lane) - mc * ROWS] : 0.0f;
-          for (int q = 0; q < nw; ++q) v += from0[q * (2 * mc * ROWS) + part_at(m, lane)];
+          float v = inside ? place(w0 - 1, 1)[part_at(m, lane)] : 0.0f;
+          for (int q = 0; q < nw; ++q) v += place(w0 + q, 0)[part_at(m, lane)];
           emit(round, s_lo, m, v);
         }
       }
@@ -519,9 +522,12 @@ static bool lay_out(const GemvArgs4& a, int nb, int ks, int ncl, const DevInfo& 
   P->rs = rs;
   const auto up = [](int64_t v) { return (v + 127) & ~(int64_t)127; };
   P->pitch = P->kbs * 256 + 64;
+  // Only strips that are fewer than warps never lie whole inside a range but at its
+  // beginning; then, and with one round, the second place is used once, at the end.
+  const bool once = rs >= strips && strips <= W;
   const int64_t x = up((int64_t)P->pitch * P->cols), xs = up((int64_t)P->kbs * (BK / a.group) * 8 * nb * 4),
-                part = up((int64_t)W * 2 * P->cols * ROWS * 4),
-                red = ks > 1 ? up((int64_t)2 * rs * P->cols * ROWS * 4) : 0;
+                places = (int64_t)W * P->cols * ROWS * 4, part = up(places * (once ? 1 : 2)),
+                red = ks > 1 ? up((int64_t)(rs < strips ? 2 : 1) * rs * P->cols * ROWS * 4) : 0;
   const int64_t left = (int64_t)d.max_smem_optin - 4096 - (x + 256 + xs + part + red);
   const int64_t fit = left / ((int64_t)W * bb);           // blocks a warp's ring can hold
   if (left < 0 || fit < 2) return false;
@@ -532,6 +538,8 @@ static bool lay_out(const GemvArgs4& a, int nb, int ks, int ncl, const DevInfo& 
   P->xs_off = P->zero_off + 256;
   P->part_off = P->xs_off + (int)xs;
   P->red_off = P->part_off + (int)part;
+  P->second_off = once ? 0 : P->part_off + (int)places;
+  P->second_step = once ? P->slots * P->stage * bb : P->cols * ROWS * 4;
   P->smem = P->red_off + (int)red;
   return true;
 }
@@ -550,8 +558,9 @@ static bool choose(const GemvArgs4& a, Kern kern, int cols, Plan* best) {
     Plan P;
     P.cols = cols;
     const int ncl = clusters_of(kern, warps_of(NB) * 32, ks, d);
+    if (!lay_out(a, NB, ks, ncl, d, &P)) continue;
     const int64_t cost = (int64_t)cdiv(NS, ncl) * cdiv(KB, ks) + (ks > 1 ? CLUSTER_COST : 0);
-    if ((least < 0 || cost < least) && lay_out(a, NB, ks, ncl, d, &P)) least = cost, *best = P;
+    if (least < 0 || cost < least) least = cost, *best = P;
   }
   return least >= 0;
 }
