@@ -120,6 +120,7 @@ int qmv_block_norm(int M, int D, const void* y, int ldy, int y_dtype, const void
   if (ldy < D || ldr < D || ldo < D || (h_out && ldh < D) || (gate && ldg != 0 && ldg < D))
     return QMV_ERR_SHAPE;
   if (h_out == residual && ldh != ldr) return QMV_ERR_SHAPE;
+  if (out == y || out == residual || out == h_out || h_out == y || out == gate) return QMV_ERR_INVALID_ARG;
   if (!aligned(y, dsize(y_dtype)) || !aligned(residual, 2) || !aligned(gamma_post, 2) ||
       !aligned(gate, 2) || !aligned(gamma_pre, 2) || !aligned(h_out, 2) || !aligned(out, 2))
     return QMV_ERR_ALIGNMENT;

@@ -511,7 +511,8 @@ QMV_API int qmv_w4_gemv(const qmv_w4pack *p, int M, const void *x, int ldx, int 
  *   out        device [M][D] of dtype, row stride ldo.
  *   D          1 .. 65536.  eps >= 0.
  * out overlaps nothing; h_out overlaps nothing but residual as above.
- * Errors: INVALID_ARG, SHAPE (a stride below D), UNSUPPORTED (D), ALIGNMENT, CUDA.
+ * Errors: INVALID_ARG (also an output that begins where an input or the other
+ * output does, but for that), SHAPE (a stride below D), UNSUPPORTED (D), ALIGNMENT, CUDA.
  */
 QMV_API int qmv_block_norm(int M, int D, const void *y, int ldy, int y_dtype, const void *residual,
                            int ldr, const void *gamma_post, const void *gate, int ldg,

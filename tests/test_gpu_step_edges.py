@@ -1,0 +1,234 @@
+"""The verification-step operators where they are used together with other work:
+captured first, forked and joined, on several streams, under programmatic launch
+with early weights, through both forms of the binding, at offsets past 32 bits and
+at the ends of their sizes."""
+import subprocess
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+from conftest import ROOT
+from gpu_util import qmv
+from test_gpu_step import BF16, F16, F32, gen, make_w4, ref_verify
+
+pytestmark = pytest.mark.gpu
+
+
+def case(seed=5, M=5, D=512, V=4099):
+    """Inputs of a small step, and a function that runs it: (outputs, ...)."""
+    q = qmv()
+    g = gen(seed)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    up, _, _ = make_w4(1536, D, 128, True, BF16, seed + 1)
+    down, _, _ = make_w4(D, 1536, 64, True, BF16, seed + 2)
+    head, _, _ = make_w4(V, D, 32, False, BF16, seed + 3)
+    y, r = rn(M, D), rn(M, D).to(BF16)
+    g1, g2 = ((1 + 0.1 * rn(D)).to(BF16) for _ in range(2))
+    draft = torch.randint(0, V, (1, M - 1), generator=g, device="cuda", dtype=torch.int32)
+    ua, us = torch.rand(1, M - 1, generator=g, device="cuda") * 1e-3, torch.rand(1, generator=g, device="cuda")
+
+    def run():
+        h, z = q.qmv_block_norm(y, r, g1, gamma_post=g2)
+        a = q.qmv_w4_gemv(up, z, y_dtype=q.QMV_BF16)
+        d = q.qmv_w4_gemv(down, a)
+        h2, z2 = q.qmv_block_norm(d, h, g2, gamma_post=g1)
+        p = q.qmv_softmax(q.qmv_w4_gemv(head, z2), 0.8)
+        return (h2, p, *q.qmv_verify_draft(p.view(1, M, V), None, draft, ua, us))
+
+    return run
+
+
+def same(a, b):
+    return all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+FIRST = """
+import sys; sys.path[:0] = [{root!r}, {root!r} + '/tests']
+import torch
+from test_gpu_step_edges import case, same
+run = case(V=70001)                      # packing and inputs; no operator of the step has run yet
+s = torch.cuda.Stream()
+s.wait_stream(torch.cuda.current_stream())
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph, stream=s):
+    cap = run()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in cap]
+assert same(got, run())
+graph.replay()
+torch.cuda.synchronize()
+assert same(got, cap)
+print('captured first')
+"""
+
+
+def test_first_call_of_a_process_may_be_captured():
+    r = subprocess.run([sys.executable, "-c", FIRST.format(root=ROOT)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
+
+
+def test_fork_and_join_in_a_capture():
+    q = qmv()
+    g = gen(9)
+    x = torch.randn(3, 1024, generator=g, device="cuda").to(F16)
+    one = torch.ones(1024, device="cuda", dtype=F16)
+    pa, _, _ = make_w4(2048, 1024, 64, True, F16, 31)
+    pb, _, _ = make_w4(1024, 2048, 128, True, F16, 32)
+    side = torch.cuda.Stream()
+
+    def run(main):
+        h, z = q.qmv_block_norm(x, x, one)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            b = q.qmv_w4_gemv(pa, z, y_dtype=q.QMV_F16)
+        a = q.qmv_softmax(z, 0.5)
+        main.wait_stream(side)
+        c = q.qmv_w4_gemv(pb, b)
+        return h, a, b, c
+
+    ref = run(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    main = torch.cuda.Stream()
+    main.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        cap = run(main)
+    for _ in range(3):
+        for t in cap:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(cap, ref)
+
+
+def test_two_steps_at_once_on_two_streams():
+    runs = [case(seed=5), case(seed=50)]
+    ref = [r() for r in runs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in runs]
+    for _ in range(10):
+        outs = []
+        for r, s in zip(runs, streams):
+            with torch.cuda.stream(s):
+                outs.append(r())
+        torch.cuda.synchronize()
+        assert all(same(a, b) for a, b in zip(outs, ref))
+
+
+def test_early_weights_under_programmatic_launch():
+    q = qmv()
+    run = case(seed=7)
+    ref = run()
+    torch.cuda.synchronize()
+    q.qmv_set_pdl(True)
+    try:
+        for _ in range(20):
+            out = run()
+        torch.cuda.synchronize()
+    finally:
+        q.qmv_set_pdl(False)
+    assert same(out, ref) and q.qmv_device_error(clear=True) == 0
+
+
+def test_both_forms_of_the_binding_agree():
+    # fresh outputs on the current stream go through the host module; outputs that are
+    # given go through the checks in full
+    q = qmv()
+    g = gen(3)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    p, _, _ = make_w4(515, 640, 64, True, BF16, 3)
+    x = rn(3, 640).to(BF16)
+    for dt, c in ((F32, q.QMV_F32), (F16, q.QMV_F16), (BF16, q.QMV_BF16)):
+        y = q.qmv_w4_gemv(p, x, y_dtype=c)
+        assert y.dtype == dt and torch.equal(y, q.qmv_w4_gemv(p, x, y=torch.empty_like(y), y_dtype=c))
+    gam, gate1, gate2 = rn(640).to(BF16), rn(640).to(BF16), rn(3, 640).to(BF16)
+    for gate in (None, gate1, gate2):
+        for post in (None, gam):
+            a = q.qmv_block_norm(x.float(), x, gam, post, gate, 0.5, 2.0, 1.0, 1e-5)
+            b = q.qmv_block_norm(x.float(), x, gam, post, gate, 0.5, 2.0, 1.0, 1e-5, h_out=torch.empty_like(x))
+            assert same(a, b)
+    for t in (0.7, torch.rand(3, device="cuda")):
+        a = q.qmv_softmax(x, t)
+        assert torch.equal(a, q.qmv_softmax(x, t, out=torch.empty_like(a)))
+    tg = torch.softmax(rn(2, 4, 77), 2)
+    dq, d = torch.softmax(rn(2, 3, 77), 2), torch.randint(0, 77, (2, 3), device="cuda", dtype=torch.int32)
+    ua, us = torch.rand(2, 3, device="cuda"), torch.rand(2, device="cuda")
+    n = torch.tensor([3, 1], device="cuda", dtype=torch.int32)
+    for qq in (None, dq):
+        for nn in (None, n):
+            a = q.qmv_verify_draft(tg, qq, d, ua, us, n_draft=nn)
+            b = q.qmv_verify_draft(tg, qq, d, ua, us, n_draft=nn, tokens=torch.empty_like(a[0]))
+            assert same(a, b)
+    # what the host module leaves to the checks
+    for call in (lambda: q.qmv_w4_gemv(p, x[:, :639]), lambda: q.qmv_block_norm(x, x.float(), gam),
+                 lambda: q.qmv_softmax(x, torch.rand(2, device="cuda")), lambda: q.qmv_softmax(x.cpu()),
+                 lambda: q.qmv_verify_draft(tg, dq[:1], d, ua, us), lambda: q.qmv_block_norm(x, x, gam.cpu())):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(q.QmvError):
+        q.qmv_softmax(x, -1.0)
+    with pytest.raises(q.QmvError):
+        q.qmv_w4_gemv(p, x[:0])
+    p.close()
+    with pytest.raises((q.QmvError, ValueError)):
+        q.qmv_w4_gemv(p, x)
+
+
+def test_w4_many_columns_and_the_longest_rows():
+    q = qmv()
+    for M, N, K, group in ((4096, 40, 256, 128), (40, 64, 131072, 32), (1, 33, 131072, 128)):
+        g = gen(M)
+        codes = torch.randint(0, 16, (N, K), generator=g, device="cuda", dtype=torch.uint8)
+        z = torch.randint(0, 16, (N, K // group), generator=g, device="cuda", dtype=torch.uint8)
+        p = q.W4Pack(N, K, group, F16, True).pack_weights(codes, torch.ones(N, K // group, device="cuda", dtype=F16), z)
+        x = torch.randint(-2, 3, (M, K), generator=g, device="cuda").to(F16)
+        # whole numbers below 2 * 15 * 131072 < 2^24: exact in fp32 in any order
+        w = codes.double() - z.double().repeat_interleave(group, 1)
+        assert torch.equal(q.qmv_w4_gemv(p, x).double(), x.double() @ w.t())
+
+
+def test_offsets_past_32_bits():
+    q = qmv()
+    # packed bytes past 2^32, codes past 2^33
+    N, K = 409600, 21504
+    codes = torch.empty(N, K, dtype=torch.uint8, device="cuda").random_(0, 16)
+    scales = torch.ones(N, K // 128, device="cuda", dtype=F16)
+    p = q.W4Pack(N, K, 128, F16, False).pack_weights(codes, scales)
+    assert p.packed_bytes > 2 ** 32
+    x = torch.randint(-2, 3, (2, K), device="cuda").to(F16)
+    y = q.qmv_w4_gemv(p, x)
+    rows = torch.tensor([0, 1, 199999, N - 33, N - 1], device="cuda")
+    assert torch.equal(y[:, rows].double(), x.double() @ (codes[rows].double() - 8).t())
+    del codes, scales, p, y
+    # rows past 2^31 elements
+    rows, V = 8300, 262144
+    x = torch.empty(rows, V, dtype=F16, device="cuda").normal_()
+    pr = q.qmv_softmax(x)
+    for i in (0, 8191, rows - 1):
+        ref = torch.softmax(x[i].double(), 0)
+        assert float((pr[i].double() - ref).abs().max() / ref.max()) < 1e-5
+    # the same rows as B = 1660 sequences of five positions
+    B = rows // 5
+    d = torch.zeros(B, 4, dtype=torch.int32, device="cuda")
+    ua, us = torch.ones(B, 4, device="cuda") * 0.999, torch.rand(B, device="cuda")
+    n = torch.full((B,), 4, dtype=torch.int32, device="cuda")
+    n[-1] = 0
+    ua[-2] = 0.0
+    tok, acc = q.qmv_verify_draft(pr.view(B, 5, V), None, d, ua, us, n_draft=n)
+    for b in (0, B - 2, B - 1):
+        rt, ra = ref_verify(pr.view(B, 5, V)[b:b + 1].cpu().numpy(), None, d[b:b + 1].cpu().numpy(),
+                            n[b:b + 1].cpu().numpy(), ua[b:b + 1].cpu().numpy(), us[b:b + 1].cpu().numpy())
+        assert np.array_equal(tok[b:b + 1].cpu().numpy(), rt) and int(acc[b]) == ra[0]
+    del x, pr
+    M, D = 540000, 4096
+    y = torch.empty(M, D, dtype=BF16, device="cuda").normal_()
+    one = torch.ones(D, dtype=BF16, device="cuda")
+    h, z = q.qmv_block_norm(y, y, one)
+    for i in (0, 524288, M - 1):
+        assert torch.equal(h[i], (2 * y[i].float()).to(BF16))
+        hs = h[i].double()
+        ref = hs / torch.sqrt(hs.pow(2).mean() + 1e-6)
+        assert bool(((z[i].double() - ref).abs() <= ref.abs() * 2.0 ** -8 * 1.01).all())

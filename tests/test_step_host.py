@@ -74,6 +74,9 @@ def test_block_norm_calls(q):
     for kw in (dict(M=0), dict(D=0), dict(y=None), dict(r=None), dict(gpr=None), dict(out=None), dict(yd=3),
                dict(dt=F32), dict(eps=-1.0), dict(eps=float("nan"))):
         assert call(**kw) == -1, kw
+    # an output on top of an input or of the other output
+    for kw in (dict(out=16), dict(h=48), dict(y=32), dict(gate=48)):
+        assert call(**kw) == -1, kw
     assert call(D=65537, ldy=70000, ldr=70000, ldh=70000, ldo=70000) == -2
     for kw in (dict(ldy=63), dict(ldr=63), dict(ldh=63), dict(ldo=63), dict(gate=16, ldg=63), dict(h=16, ldh=65)):
         assert call(**kw) == -4, kw
