@@ -433,11 +433,14 @@ struct Chunk {
 
 // A cluster of C CTAs a sequence; warps own `per` consecutive chunks each and
 // keep every chunk's sum, so that after the total is known one warp re-reads the
-// one chunk in which the running sum passes the threshold.
-constexpr int V_NT = 512, V_NW = V_NT / 32, MAX_PER = 32;
+// one chunk in which the running sum passes the threshold.  Bound by HBM: one row
+// of p and one of q a sequence; small CTAs, so that all sequences run at once, and
+// loads well ahead (48 sequences over 262144 ids, 100 MB: 22.3 us with 512 threads
+// and one chunk ahead, 19.6 us with 256, 17.1 us with two chunks ahead).
+constexpr int V_NT = 256, V_NW = V_NT / 32, MAX_PER = 64;
 static_assert((int64_t)8 * V_NW * MAX_PER * CHUNK >= 1 << 20, "a chunk sum for every id");
 template <bool VEC>
-__global__ void __launch_bounds__(V_NT, 2) verify_kernel(VerifyArgs a, int C, int per) {
+__global__ void __launch_bounds__(V_NT, 3) verify_kernel(VerifyArgs a, int C, int per) {
   constexpr int NW = V_NW;
   __shared__ long long chunk[NW][MAX_PER], wsum[NW], parts[2][MAX_C];
   __shared__ uint64_t all_here[2];
@@ -476,16 +479,21 @@ __global__ void __launch_bounds__(V_NT, 2) verify_kernel(VerifyArgs a, int C, in
   for (int pass = 0; pass < 2; ++pass) {
     long long w = 0;
     const int last = min(per, max(0, (V + CHUNK - 1) / CHUNK - first));
-    Chunk<VEC> c;
-    if (last > 0) c.load(p, q, first * CHUNK, V);
-    for (int i = 0; i < last; ++i) {
-      Chunk<VEC> next;                    // on its way while this one is summed
-      if (i + 1 < last) next.load(p, q, (first + i + 1) * CHUNK, V);
-      c.sure(hot - (first + i) * CHUNK);
-      const long long s = c.sum();
-      if (lane == 0) chunk[warp][i] = s;
-      w += s;
-      c = next;
+    Chunk<VEC> c[3];                      // two on their way while one is summed
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (j < last) c[j].load(p, q, (first + j) * CHUNK, V);
+    for (int i0 = 0; i0 < last; i0 += 3) {
+#pragma unroll
+      for (int j = 0; j < 3; ++j) {
+        const int i = i0 + j;
+        if (i >= last) break;
+        if (i + 2 < last) c[(j + 2) % 3].load(p, q, (first + i + 2) * CHUNK, V);
+        c[j].sure(hot - (first + i) * CHUNK);
+        const long long s = c[j].sum();
+        if (lane == 0) chunk[warp][i] = s;
+        w += s;
+      }
     }
     if (lane == 0) wsum[warp] = w;
     __syncthreads();
