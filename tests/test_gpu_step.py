@@ -172,7 +172,8 @@ def ref_h(y, r, gpo, gate, rs, bs, off, eps):
 @pytest.mark.parametrize("ydt,dt", [(F32, F16), (F16, F16), (BF16, BF16), (F32, BF16), (F16, BF16)])
 @pytest.mark.parametrize("post,gate", [(True, "none"), (False, "channel"), (True, "token"), (False, "none")])
 @pytest.mark.parametrize("M,D,pad", [(1, 1, 0), (3, 7, 2), (1, 2048, 0), (5, 64, 8), (4, 1000, 0), (2, 4099, 5), (7, 5376, 0),
-                                     (2, 16384, 16), (300, 256, 0), (1, 65536, 0), (2, 40000, 0), (33, 8192, 8)])
+                                     (2, 16384, 16), (300, 256, 0), (1, 65536, 0), (2, 40000, 0), (33, 8192, 8),
+                                     (320, 1024, 0), (310, 4096, 8), (305, 5384, 0), (400, 8192, 8), (340, 1001, 0)])
 def test_block_norm(M, D, pad, post, gate, ydt, dt):
     g = gen(M * 7 + D)
     rn = lambda *s: torch.randn(*s, generator=g, device="cuda")

@@ -179,7 +179,9 @@ def test_both_forms_of_the_binding_agree():
 
 def test_w4_many_columns_and_the_longest_rows():
     q = qmv()
-    for M, N, K, group in ((4096, 40, 256, 128), (40, 64, 131072, 32), (1, 33, 131072, 128)):
+    # the last two: clusters along k that meet several times over many strips
+    for M, N, K, group in ((4096, 40, 256, 128), (40, 64, 131072, 32), (1, 33, 131072, 128),
+                           (32, 8192, 16384, 128), (13, 12000, 24576, 64)):
         g = gen(M)
         codes = torch.randint(0, 16, (N, K), generator=g, device="cuda", dtype=torch.uint8)
         z = torch.randint(0, 16, (N, K // group), generator=g, device="cuda", dtype=torch.uint8)
@@ -188,6 +190,24 @@ def test_w4_many_columns_and_the_longest_rows():
         # whole numbers below 2 * 15 * 131072 < 2^24: exact in fp32 in any order
         w = codes.double() - z.double().repeat_interleave(group, 1)
         assert torch.equal(q.qmv_w4_gemv(p, x).double(), x.double() @ w.t())
+
+
+@pytest.mark.parametrize("V", [33, 1000, 4099, 70001])
+@pytest.mark.parametrize("dt", [F32, F16])
+def test_softmax_rows_and_results_shifted_differently(V, dt):
+    q = qmv()
+    x = torch.randn(7, V + 3, generator=gen(V), device="cuda").to(dt)
+    x[2, 1:] = -torch.inf
+    t = torch.tensor([0.5, 0.0, 1.0, 2.0, 0.1, 1.0, 0.0], device="cuda")
+    ref = q.qmv_softmax(x[:, 1:V + 1].contiguous(), t)
+    for lead, ld in ((0, V), (1, V + 2), (3, V + 5)):
+        out = torch.full((7, ld + lead), -7.0, device="cuda")
+        v = out[:, lead:lead + V]
+        assert q.qmv_softmax(x[:, 1:V + 1], t, out=v) is v
+        # other paths sum in other orders: V / 128 + 70 roundings each, as elsewhere
+        assert bool(((v - ref).abs() <= ref * 2 * (V / 128 + 70) * 2.0 ** -24 + 2.0 ** -126).all())
+        rest = torch.cat([out[:, :lead], out[:, lead + V:]], 1)
+        assert bool((rest == -7.0).all())
 
 
 def test_offsets_past_32_bits():
@@ -231,4 +251,5 @@ def test_offsets_past_32_bits():
         assert torch.equal(h[i], (2 * y[i].float()).to(BF16))
         hs = h[i].double()
         ref = hs / torch.sqrt(hs.pow(2).mean() + 1e-6)
+        # one rounding to bf16, and less than a hundredth of it for the fp32 steps before
         assert bool(((z[i].double() - ref).abs() <= ref.abs() * 2.0 ** -8 * 1.01).all())
