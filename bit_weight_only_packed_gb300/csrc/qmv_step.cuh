@@ -58,9 +58,9 @@ cudaError_t launch_w4_pack(const qmv_w4pack& p, const uint8_t* codes, const uint
                            const uint8_t* zeros, uint8_t* packed, cudaStream_t s);
 cudaError_t launch_w4_unpack(const qmv_w4pack& p, uint8_t* codes, cudaStream_t s);
 cudaError_t launch_w4_gemv(const GemvArgs4& a, cudaStream_t s);
-template <int GROUP, bool XB>
+template <int GROUP, bool SB>
 cudaError_t launch_group(const GemvArgs4& a, cudaStream_t s);
-template <int GROUP, bool XB>
+template <int GROUP, bool SB>
 cudaError_t read_error(int clear, int* out);
 
 }  // namespace w4

@@ -8,8 +8,7 @@
 // moves between lanes.  Inside a 32-bit word the pairs (k, k + 1) lie at the
 // same bits of the two halves: (0, 1) at bit 3, (4, 5) at 7, (2, 3) at 11 and
 // (6, 7) at 15, wrapping around.  One mask, after a rotation of the word, yields
-// a pair in place for the matvec's operand: bit 3 is where bf16 wants a code
-// under the exponent of 16, and bits 3 and 7 are both where fp16 reads one
+// a pair in place for the matvec's operand: fp16 reads a code at bit 3 or 7
 // evenly spaced.
 #include "qmv_step.cuh"
 
@@ -104,9 +103,9 @@ cudaError_t launch_w4_unpack(const qmv_w4pack& p, uint8_t* codes, cudaStream_t s
 }
 
 cudaError_t launch_w4_gemv(const GemvArgs4& a, cudaStream_t s) {
-  if (a.group == 32) return a.x_bf16 ? launch_group<32, true>(a, s) : launch_group<32, false>(a, s);
-  if (a.group == 64) return a.x_bf16 ? launch_group<64, true>(a, s) : launch_group<64, false>(a, s);
-  return a.x_bf16 ? launch_group<128, true>(a, s) : launch_group<128, false>(a, s);
+  if (a.group == 32) return a.scale_bf16 ? launch_group<32, true>(a, s) : launch_group<32, false>(a, s);
+  if (a.group == 64) return a.scale_bf16 ? launch_group<64, true>(a, s) : launch_group<64, false>(a, s);
+  return a.scale_bf16 ? launch_group<128, true>(a, s) : launch_group<128, false>(a, s);
 }
 
 }  // namespace w4

@@ -1,4 +1,4 @@
-// qmv_w4_g128_bf16.cu -- the 4-bit matvec for groups of 128 and x in bf16.
+// qmv_w4_g128_bf16.cu -- the 4-bit matvec for groups of 128 with scales in bf16.
 #include "qmv_w4_gemv.cuh"
 
 namespace qmv {

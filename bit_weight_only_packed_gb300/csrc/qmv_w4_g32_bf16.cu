@@ -1,4 +1,4 @@
-// qmv_w4_g32_bf16.cu -- the 4-bit matvec for groups of 32 and x in bf16.
+// qmv_w4_g32_bf16.cu -- the 4-bit matvec for groups of 32 with scales in bf16.
 #include "qmv_w4_gemv.cuh"
 
 namespace qmv {

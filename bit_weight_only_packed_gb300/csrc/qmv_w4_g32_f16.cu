@@ -1,4 +1,4 @@
-// qmv_w4_g32_f16.cu -- the 4-bit matvec for groups of 32 and x in fp16.
+// qmv_w4_g32_f16.cu -- the 4-bit matvec for groups of 32 with scales in fp16.
 #include "qmv_w4_gemv.cuh"
 
 namespace qmv {

@@ -1,4 +1,4 @@
-// qmv_w4_g64_f16.cu -- the 4-bit matvec for groups of 64 and x in fp16.
+// qmv_w4_g64_f16.cu -- the 4-bit matvec for groups of 64 with scales in fp16.
 #include "qmv_w4_gemv.cuh"
 
 namespace qmv {

@@ -1,15 +1,18 @@
 // qmv_w4_gemv.cuh -- the matvec of the 4-bit weights packed by qmv_w4.cu:
 //   y[m][n] = sum_g s[n][g] * (sum_{k in g} x[m][k] * q[n][k] - z[n][g] * sum_{k in g} x[m][k]).
-// One translation unit a group size and type of x includes it.
+// One translation unit a group size and type of scales includes it.
 //
 // The products run on m16n8k16 tensor instructions with the weights as the
-// 16-row operand and x as it is, so all products are exact and sums fp32.
-//   fp16: the numbers below 2^-13 are evenly spaced, so a masked code in the low
-//   11 bits of a half is, read as fp16, the code times 2^-21 (at bit 3) or 2^-17
-//   (at bit 7): the operand without any arithmetic, four masks and one rotation
-//   for eight codes.  The two kinds have sums of their own.
-//   bf16: a code at bit 3 under the exponent of 16 reads 16 + q: four masks and
-//   three rotations; the 16 comes off with the zero point.
+// 16-row operand, in fp16: products are exact and sums fp32.  The fp16 numbers
+// below 2^-13 are evenly spaced, so a masked code in the low 11 bits of a half is,
+// read as fp16, the code times 2^-21 (at bit 3) or 2^-17 (at bit 7): the operand
+// without any arithmetic, four masks and one rotation for eight codes.  The two
+// kinds have sums of their own.  x in bf16 becomes fp16 once a CTA, each column
+// scaled by a power of two that puts its largest value at 2^14: what falls off is
+// below 2^-39 of that.  (Decoding to bf16 instead, where a code at bit 3 under the
+// exponent of 16 is 16 + q, takes four masks and three rotations, all on a pipe of
+// half rate: 25.4 us against 24.0 us for 43008x5376 and one token, 57.9 against 56.2
+// for 262144x2048 in groups of 32 and five.)
 // The zero point comes off a group's sum as z * sum(x), as the library's fast
 // form does for its offset; the sums of x are formed once a CTA.
 //
@@ -47,34 +50,13 @@ __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t by
 }
 
 // D = A . B + C on 16 rows x 8 columns x 16 k.
-template <bool XB>
-__device__ __forceinline__ void mma16816(float (&d)[4], const float* c, uint32_t a0, uint32_t a1,
-                                         uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  if (XB)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%10,%11,%12,%13};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%10,%11,%12,%13};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
-}
-
-// (v & mask) | bits in one instruction; both constants from registers.
-__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) {
-  uint32_t d;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(v), "r"(mask), "r"(bits));
-  return d;
-}
-template <uint32_t V>
-__device__ __forceinline__ uint32_t in_register() {
-  uint32_t d;
-  asm("mov.b32 %0, %1;" : "=r"(d) : "n"(V));
-  return d;
+__device__ __forceinline__ void mma16816(float (&d)[4], const float* c, uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
 __device__ __forceinline__ uint32_t rot(uint32_t v, int n) { return __funnelshift_r(v, v, n); }
@@ -83,14 +65,17 @@ __device__ __forceinline__ float f16_f(uint32_t bits16, int bf16) {
   return bf16 ? __uint_as_float(bits16 << 16) : __half2float(__ushort_as_half((unsigned short)bits16));
 }
 
-// The zero point in byte i of v on the scale of a group's sum: placed in the
-// mantissa of 4, whose last bit is 2^-21 (fp16), or of 2^23 (bf16: 16 + z).
-template <bool XB>
+// The zero point in byte i of v on the scale of a group's sum, 2^-21: placed in the
+// mantissa of 4, whose last bit that is.
 __device__ __forceinline__ float zero_f(uint32_t v, int i) {
-  const uint32_t sel = 0x7650u | (uint32_t)i;
-  return XB ? __uint_as_float(__byte_perm(v, 0x4B000000u, sel)) - 8388592.0f
-            : __uint_as_float(__byte_perm(v, 0x40800000u, sel)) - 4.0f;
+  return __uint_as_float(__byte_perm(v, 0x40800000u, 0x7650u | (uint32_t)i)) - 4.0f;
 }
+
+// The power of two that scales a bf16 column, from the bits of its largest
+// magnitude (141 minus the exponent field puts that at 2^14), kept where it and its
+// inverse are normal.
+__device__ __forceinline__ int column_exp(uint32_t top) { return min(141 - (int)(top >> 7), 126); }
+__device__ __forceinline__ float pow2_f(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
 __device__ __forceinline__ void store_y(void* y, int64_t at, int dtype, float v) {
   if (dtype == QMV_F32)
@@ -117,10 +102,10 @@ struct Plan {
   int second_off, second_step;  // the second places of the warps
 };
 
-// A sum by its definition: for columns with infinities, NaN or values near
-// the end of fp32's range, where x * q and z * sum(x) apart would give another
-// answer.  x: the column in shared memory, from k0 on.
-static __device__ __noinline__ float plain_sum(const GemvArgs4& a, const uint16_t* x, int n, int k0, int k1) {
+// A sum by its definition: for results that are not finite, where x * q and z *
+// sum(x) apart may give another answer.
+static __device__ __noinline__ float plain_sum(const GemvArgs4& a, int m, int n, int k0, int k1) {
+  const uint16_t* x = (const uint16_t*)a.x + (int64_t)m * a.ldx;
   const int KB = cdiv(a.K, BK), bb = block_bytes(a.group, a.zeros != 0), gpb = BK / a.group;
   const int row = n & 31, r = row >> 4, hi = (row >> 3) & 1;
   float v = 0.0f, sum = 0.0f, s = 0.0f;
@@ -137,7 +122,7 @@ static __device__ __noinline__ float plain_sum(const GemvArgs4& a, const uint16_
     }
     const int j = (k >> 6) & 1, h = (k >> 5) & 1, lane = (row & 7) * 4 + ((k >> 3) & 3);
     const uint32_t w = reinterpret_cast<const uint32_t*>(b)[((r * 2 + j) * 32 + lane) * 4 + hi * 2 + h];
-    sum = fmaf(f16_f(x[k - k0], a.x_bf16), (float)((int)(rot(w, shift_of(k & 7)) & 15u) - z), sum);
+    sum = fmaf(f16_f(x[k], a.x_bf16), (float)((int)(rot(w, shift_of(k & 7)) & 15u) - z), sum);
   }
   return v + sum * s;
 }
@@ -163,8 +148,8 @@ struct Block {
   }
 };
 
-// XB, SB: x and the scales are bf16 (fp16 otherwise).
-template <int GROUP, int NB, bool XB, bool SB>
+// SB: the scales are bf16 (fp16 otherwise).
+template <int GROUP, int NB, bool SB>
 __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
     gemv_kernel(const __grid_constant__ GemvArgs4 a, const __grid_constant__ Plan P) {
   constexpr int W = warps_of(NB), NT = W * 32;
@@ -172,6 +157,7 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[W][MAX_SLOTS];
   __shared__ uint64_t x_full;
+  __shared__ uint32_t colmax[8 * NB];
   __shared__ int abort_flag;
   // the warp's number from one lane, so that what follows from it is known to be uniform
   const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -188,6 +174,7 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
   uint8_t* ring = smem + (size_t)warp * P.slots * P.stage * bb;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) abort_flag = 0;
+  if (tid < 8 * NB) colmax[tid] = 0;
 
   // The ring is kept full by lane 0; all lanes follow its course.  A copy is up to
   // `stage` neighbouring blocks of a strip.
@@ -250,6 +237,43 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
   if (P.vec && !pipe::mbar_wait_fast(&x_full, 0, &abort_flag, pipe::ERR_TIMEOUT_TFULL, &g_w4_error))
     pipe::mbar_drain(&x_full, 0, &g_w4_error);           // nothing is stored after a wait that ran out
 
+  if (a.x_bf16) {
+    // to fp16, in place: 16 lanes take a block of a column, eight values a lane, once
+    // for the columns' largest magnitudes and once to scale by them
+    const auto each = [&](auto f) {
+      for (int b = 2 * warp + (lane >> 4), m = 0;; b += 2 * W) {
+        while (b >= kbn && m < mc) b -= kbn, ++m;
+        if (__all_sync(~0u, m >= mc)) break;
+        f(m, reinterpret_cast<uint4*>(xs + m * P.pitch + b * 256) + (lane & 15));
+      }
+    };
+    each([&](int m, const uint4* p) {
+      uint32_t top = 0;
+      if (m < mc) {
+        const uint4 v = *p;
+        constexpr uint32_t ABS = 0x7fff7fffu;
+        const uint32_t t2 = __vmaxu2(__vmaxu2(v.x & ABS, v.y & ABS), __vmaxu2(v.z & ABS, v.w & ABS));
+        top = max(t2 & 0xffffu, t2 >> 16);
+      }
+#pragma unroll
+      for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
+      if ((lane & 15) == 0 && m < mc) atomicMax(&colmax[m], top);
+    });
+    __syncthreads();
+    each([&](int m, uint4* p) {
+      if (m >= mc) return;
+      const float f = pow2_f(column_exp(colmax[m]));
+      uint4 v = *p;
+      const auto two = [&](uint32_t& w) {
+        const __half2 h = __floats2half2_rn(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f);
+        w = *reinterpret_cast<const uint32_t*>(&h);
+      };
+      two(v.x), two(v.y), two(v.z), two(v.w);
+      *p = v;
+    });
+    __syncthreads();
+  }
+
   // Where a lane reads x; lanes past the last column read zeros.
   const bool in_last = 8 * (NB - 1) + g < mc;
   const uint8_t* xp[NB];
@@ -261,7 +285,7 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
   // The sums of x over each group, by the same instructions with ones for weights.
   float* xsum = reinterpret_cast<float*>(smem + P.xs_off);             // [group][8 * NB]
   for (int b = warp; b < kbn; b += W) {
-    constexpr uint32_t ONE = XB ? 0x3F803F80u : 0x3C003C00u;
+    constexpr uint32_t ONE = 0x3C003C00u;
 #pragma unroll
     for (int c = 0; c < NB; ++c)
 #pragma unroll
@@ -270,8 +294,8 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
 #pragma unroll
         for (int hh = 0; hh < HPG; ++hh) {
           const uint4 v = *reinterpret_cast<const uint4*>(xp[c] + b * (c < NB - 1 ? 256 : l_step) + (gi * HPG + hh) * 64);
-          mma16816<XB>(d, d, ONE, ONE, ONE, ONE, v.x, v.y);
-          mma16816<XB>(d, d, ONE, ONE, ONE, ONE, v.z, v.w);
+          mma16816(d, d, ONE, ONE, ONE, ONE, v.x, v.y);
+          mma16816(d, d, ONE, ONE, ONE, ONE, v.z, v.w);
         }
         if (g == 0) *reinterpret_cast<float2*>(xsum + (b * GPB + gi) * (8 * NB) + 8 * c + 2 * t) = make_float2(d[0], d[1]);
       }
@@ -288,17 +312,17 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
   // A finished sum goes out (or to the cluster's sum).  One that is not finite is
   // formed again by its definition.
   const auto emit = [&](int round, int s, int m, float v) {
-    if (!XB) v *= 2097152.0f;
+    v *= 2097152.0f;
+    if (a.x_bf16) v *= pow2_f(-column_exp(colmax[m]));
     const int64_t n = (int64_t)(S0 + round * P.rs + s) * ROWS + lane;
     if (!(fabsf(v) <= 3.402823466e38f) && n < a.N)
-      v = plain_sum(a, reinterpret_cast<const uint16_t*>(xs + m * P.pitch), (int)n, kb0 * BK, kb0 * BK + klim);
+      v = plain_sum(a, m0 + m, (int)n, kb0 * BK, kb0 * BK + klim);
     if (P.ks > 1)
       red[(((round & 1) * P.rs + s) * mc + m) * 32 + lane] = v;
     else if (n < a.N && !abort_flag)
       store_y(a.y, (int64_t)(m0 + m) * a.ldy + n, a.y_dtype, v);
   };
 
-  const uint32_t bits3 = in_register<0x00780078u>(), sixteen = in_register<0x41804180u>();   // bf16 codes
   // One block (the CTA's b-th of k) of a strip, added to tot.
   const auto product = [&](auto with_zeros, const Block<GPB>& B, int b, float (&tot)[2][NB][4]) {
     constexpr bool Z = decltype(with_zeros)::value;
@@ -306,8 +330,7 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
     const float* sxp = xsum + b * (GPB * 8 * NB) + 2 * t;
 #pragma unroll
     for (int gi = 0; gi < GPB; ++gi) {
-      constexpr int KINDS = XB ? 1 : 2;          // fp16 codes have two scales
-      float acc[KINDS][2][NB][4];
+      float low[2][NB][4], high[2][NB][4];       // codes times 2^-21 and 2^-17
       const float none[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int hh = 0; hh < HPG; ++hh) {
@@ -318,29 +341,12 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const uint32_t u = h ? B.w[r][q].y : B.w[r][q].x, v = h ? B.w[r][q].w : B.w[r][q].z;   // rows g, g + 8
-          if (XB) {
-            uint32_t p[4], o[4];
+          constexpr uint32_t L = 0x00780078u, H = 0x07800780u;
+          const uint32_t u8 = rot(u, 8), v8 = rot(v, 8);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              p[i] = and_or(i ? rot(u, 4 * i) : u, bits3, sixteen);
-              o[i] = and_or(i ? rot(v, 4 * i) : v, bits3, sixteen);
-            }
-#pragma unroll
-            for (int c = 0; c < NB; ++c) {
-              float(&d)[4] = acc[0][r][c];
-              mma16816<XB>(d, hh ? d : none, p[0], o[0], p[2], o[2], xv[c].x, xv[c].y);
-              mma16816<XB>(d, d, p[1], o[1], p[3], o[3], xv[c].z, xv[c].w);
-            }
-          } else {
-            constexpr uint32_t L = 0x00780078u, H = 0x07800780u;
-            const uint32_t u8 = rot(u, 8), v8 = rot(v, 8);
-#pragma unroll
-            for (int c = 0; c < NB; ++c) {
-              float(&d)[4] = acc[0][r][c];
-              float(&e)[4] = acc[KINDS - 1][r][c];
-              mma16816<XB>(d, hh ? d : none, u & L, v & L, u8 & L, v8 & L, xv[c].x, xv[c].y);
-              mma16816<XB>(e, hh ? e : none, u & H, v & H, u8 & H, v8 & H, xv[c].z, xv[c].w);
-            }
+          for (int c = 0; c < NB; ++c) {
+            mma16816(low[r][c], hh ? low[r][c] : none, u & L, v & L, u8 & L, v8 & L, xv[c].x, xv[c].y);
+            mma16816(high[r][c], hh ? high[r][c] : none, u & H, v & H, u8 & H, v8 & H, xv[c].z, xv[c].w);
           }
         }
       }
@@ -351,13 +357,12 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
       for (int r = 0; r < 2; ++r) {
         const uint32_t s2 = r ? B.sc[gi].y : B.sc[gi].x;
         const float s0 = f16_f(s2 & 0xffffu, SB), s1 = SB ? __uint_as_float(s2 & 0xffff0000u) : f16_f(s2 >> 16, SB);
-        const float z0 = Z ? zero_f<XB>(B.zp[gi], 2 * r) : XB ? 24.0f : 0x1p-18f, z1 = Z ? zero_f<XB>(B.zp[gi], 2 * r + 1) : z0;
+        const float z0 = Z ? zero_f(B.zp[gi], 2 * r) : 0x1p-18f, z1 = Z ? zero_f(B.zp[gi], 2 * r + 1) : z0;
 #pragma unroll
         for (int c = 0; c < NB; ++c)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float v = acc[0][r][c][e];
-            if (!XB) v = fmaf(acc[KINDS - 1][r][c][e], 0.0625f, v);
+            float v = fmaf(high[r][c][e], 0.0625f, low[r][c][e]);
             v = fmaf(-(e < 2 ? z0 : z1), e & 1 ? sx[c].y : sx[c].x, v);
             tot[r][c][e] = fmaf(e < 2 ? s0 : s1, v, tot[r][c][e]);
           }
@@ -565,9 +570,9 @@ static bool choose(const GemvArgs4& a, Kern kern, int cols, Plan* best) {
   return least >= 0;
 }
 
-template <int GROUP, int NB, bool XB, bool SB>
+template <int GROUP, int NB, bool SB>
 static cudaError_t run(const GemvArgs4& a, int cols, cudaStream_t s, bool* fits) {
-  const auto kern = gemv_kernel<GROUP, NB, XB, SB>;
+  const auto kern = gemv_kernel<GROUP, NB, SB>;
   Plan P;
   *fits = choose<NB>(a, kern, cols, &P);
   if (!*fits) return cudaSuccess;
@@ -579,29 +584,24 @@ static cudaError_t run(const GemvArgs4& a, int cols, cudaStream_t s, bool* fits)
 }
 
 // Columns in as few launch rows as fit, filled evenly.
-template <int GROUP, bool XB, bool SB>
-static cudaError_t run_m(const GemvArgs4& a, cudaStream_t s) {
+template <int GROUP, bool SB>
+cudaError_t launch_group(const GemvArgs4& a, cudaStream_t s) {
   for (int top = 8 * NBMAX; top >= 1; top = top > 8 ? top - 8 : top / 2) {
     const int cols = cdiv(a.M, cdiv(a.M, top));
     bool fits = false;
     cudaError_t e;
     switch (cdiv(cols, 8)) {
-      case 1: e = run<GROUP, 1, XB, SB>(a, cols, s, &fits); break;
-      case 2: e = run<GROUP, 2, XB, SB>(a, cols, s, &fits); break;
-      case 3: e = run<GROUP, 3, XB, SB>(a, cols, s, &fits); break;
-      default: e = run<GROUP, 4, XB, SB>(a, cols, s, &fits); break;
+      case 1: e = run<GROUP, 1, SB>(a, cols, s, &fits); break;
+      case 2: e = run<GROUP, 2, SB>(a, cols, s, &fits); break;
+      case 3: e = run<GROUP, 3, SB>(a, cols, s, &fits); break;
+      default: e = run<GROUP, 4, SB>(a, cols, s, &fits); break;
     }
     if (fits || e != cudaSuccess) return e;
   }
   return cudaErrorInvalidConfiguration;    // not reached: one column of MAX_K fits
 }
 
-template <int GROUP, bool XB>
-cudaError_t launch_group(const GemvArgs4& a, cudaStream_t s) {
-  return a.scale_bf16 ? run_m<GROUP, XB, true>(a, s) : run_m<GROUP, XB, false>(a, s);
-}
-
-template <int GROUP, bool XB>
+template <int GROUP, bool SB>
 cudaError_t read_error(int clear, int* out) {
   cudaError_t e = cudaMemcpyFromSymbol(out, g_w4_error, sizeof(int));
   if (e == cudaSuccess && clear && *out) {

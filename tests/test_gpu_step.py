@@ -112,6 +112,29 @@ def test_w4_general(M, N, K, group, xdt, sdt, ydt):
     assert bool((err <= tol).all()), float((err / tol).max())
 
 
+def test_w4_bf16_magnitudes():
+    # columns of very different scales, one with a single large value among small
+    # ones, one of zeros, one of the smallest normal numbers
+    N, K = 130, 2048
+    p, _, w = make_w4(N, K, 64, True, BF16, 23)
+    x = torch.randn(7, K, generator=gen(4), device="cuda")
+    x = x * torch.tensor([2.0 ** -100, 2.0 ** -20, 1.0, 2.0 ** 60, 1e-3, 0.0, 2.0 ** -125], device="cuda")[:, None]
+    x[4, 77] = 1e4
+    x = x.to(BF16)
+    y = qmv().qmv_w4_gemv(p, x)
+    ref = x.double() @ w.t()
+    A, top = x.double().abs() @ w.abs().t(), x.double().abs().amax(1, keepdim=True)
+    # x * q and z * sum(x) apart: (q + z) / |q - z| larger than the sum of magnitudes;
+    # q + z is at most 30 and s is A's; and each value off by 2^-39 of its column's largest
+    # (2^-21 in the last column, where the scaling stops at 2^126)
+    B = x.double().abs().sum(1, keepdim=True) * 30 * 0.02
+    off = top * w.abs().sum(1) * torch.tensor([2.0 ** -39] * 6 + [2.0 ** -21], device="cuda")[:, None]
+    tol = (A + B) * (17 * 4 + K / 64 + 32) * 2.0 ** -23 + off + 2.0 ** -149
+    assert bool(((y.double() - ref).abs() <= tol).all())
+    rel = (y.double() - ref).norm(dim=1) / ref.norm(dim=1).clamp(min=1e-300)
+    assert float(rel[[0, 1, 2, 3]].max()) < 1e-6 and not bool(y[5].any())
+
+
 @pytest.mark.parametrize("shift", [1, 2, 4])
 def test_w4_x_at_any_element(shift):
     # x and y not aligned to 16 bytes, odd strides
