@@ -46,25 +46,58 @@ __device__ __forceinline__ uint32_t pack<__nv_bfloat16>(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Eight elements of a row, kept as they are stored.  VEC: eight neighbours,
-// aligned to 16 bytes; otherwise every `step`-th one, so that neighbouring
-// threads read neighbouring elements whatever the alignment.
-template <typename T, bool VEC>
+// How a thread takes its eights of a row:
+//   ALIGNED  eight neighbours, 16-byte aligned everywhere;
+//   SHIFTED  the same, but every row begins `shift` elements past such an alignment (an
+//            odd D shifts every row; all [M][D] tensors alike), so that its first and
+//            last eight may stick out of it, and the vectors [D] lie another way;
+//   APART    every NT-th element, whatever the alignments.
+enum Mode { ALIGNED, SHIFTED, APART };
+
+// Eight 16-bit elements from p on, whatever p's alignment: the two aligned 16-byte words
+// that hold them, moved into place; both are the caller's to read.  Against eight loads
+// (3000 rows of 5381): 40.2 for 44.1 us in bf16, 39.4 for 49.9 with y in fp32 (1333 of 12001:
+// 43.3 for 48.7, but 48.4 for 45.7); where one warp takes a row, whose
+// ends then go both ways, it costs (160000 x 99: 106 for 93 us).
+__device__ __forceinline__ void load_across(const uint16_t* p, uint32_t* w) {
+  const uint32_t off = (uint32_t)(uintptr_t)p & 15;            // the same in a whole row
+  const uint4* q = reinterpret_cast<const uint4*>((uintptr_t)p - off);
+  const uint4 lo = q[0], hi = q[1];
+  uint32_t v[7] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z};
+  if (off & 8) v[0] = v[2], v[1] = v[3], v[2] = v[4], v[3] = v[5], v[4] = v[6], v[5] = hi.w;
+  if (off & 4) v[0] = v[1], v[1] = v[2], v[2] = v[3], v[3] = v[4], v[4] = v[5];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(v[k], v[k + 1], (off & 2) * 8);
+}
+
+// Eight elements of a row from i0 on, kept as they are stored; those outside the
+// row are zeros.
+template <typename T, Mode MODE>
 struct Eight {
   alignas(16) uint32_t w[2 * sizeof(T)];
-  __device__ __forceinline__ void load(const T* p, int i0, int step, int D) {
-    if (VEC) {
+  // whole: all eight are inside the row.  vector: a [D] vector, aligned as it is, by
+  // load_across where that pays.
+  __device__ __forceinline__ void load(const T* p, int i0, int step, int D, bool whole, bool vector, bool across) {
+    if (MODE == ALIGNED || (MODE == SHIFTED && whole && !vector)) {
 #pragma unroll
       for (int q = 0; q < (int)sizeof(w) / 16; ++q)
         reinterpret_cast<uint4*>(w)[q] = reinterpret_cast<const uint4*>(p + i0)[q];
     } else if (sizeof(T) == 4) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = i0 + e * step < D ? reinterpret_cast<const uint32_t*>(p)[i0 + e * step] : 0u;
+      for (int e = 0; e < 8; ++e) {
+        const int i = i0 + e * step;
+        w[e] = (unsigned)i < (unsigned)D ? reinterpret_cast<const uint32_t*>(p)[i] : 0u;
+      }
     } else {
       const uint16_t* s = reinterpret_cast<const uint16_t*>(p);
+      if (MODE == SHIFTED && vector && across && i0 >= 8 && i0 + 16 <= D) {     // both words inside
+        load_across(s + i0, w);
+        return;
+      }
 #pragma unroll
       for (int e = 0; e < 8; e += 2) {
-        const uint32_t a = i0 + e * step < D ? s[i0 + e * step] : 0u, b = i0 + (e + 1) * step < D ? s[i0 + (e + 1) * step] : 0u;
+        const int i = i0 + e * step, j = i + step;
+        const uint32_t a = whole || (unsigned)i < (unsigned)D ? s[i] : 0u, b = whole || (unsigned)j < (unsigned)D ? s[j] : 0u;
         w[e >> 1] = a | b << 16;
       }
     }
@@ -76,39 +109,45 @@ struct Eight {
       return unpack<T>(w[e >> 1]);
   }
   __device__ __forceinline__ void set(int e, float a, float b) { w[e >> 1] = pack<T>(a, b); }
-  __device__ __forceinline__ void store(T* p, int i0, int step, int D) const {
-    if (VEC) {
+  __device__ __forceinline__ void store(T* p, int i0, int step, int D, bool whole) const {
+    if (MODE == ALIGNED || (MODE == SHIFTED && whole)) {
       *reinterpret_cast<uint4*>(p + i0) = *reinterpret_cast<const uint4*>(w);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (i0 + e * step < D) reinterpret_cast<uint16_t*>(p)[i0 + e * step] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+        if ((unsigned)(i0 + e * step) < (unsigned)D)
+          reinterpret_cast<uint16_t*>(p)[i0 + e * step] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
     }
   }
 };
 
-// One CTA a row, the row in registers: 8 * P elements a thread, read once.
-// Elements past the row's end are zeros, which add nothing to either sum.
-// MAXT: the most threads of a launch; below 1024 the registers are held to what
-// 1536 threads (1280 with fp32 y) a streaming multiprocessor leave.
-template <typename Y, typename T, bool VEC, int P, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT < 1024 ? (sizeof(Y) == 4 ? 1280 : 1536) / MAXT : 1) norm_kernel(NormArgs a) {
-  __shared__ float red[2][32];
-  const int64_t m = blockIdx.x;
-  const int D = a.D, NT = blockDim.x, tid = threadIdx.x;
+// One row by NT threads, in registers: 8 * P elements a thread, read once.  Elements
+// past the row's ends are zeros, which add nothing to either sum.
+template <typename Y, typename T, Mode MODE, int P, bool WARP, typename Sum>
+__device__ __forceinline__ void norm_row(const NormArgs& a, int64_t m, int tid, int NT, const Sum& sum) {
+  const int D = a.D, step = MODE == APART ? NT : 1;
   const T *gpo = (const T*)a.gamma_post, *gpr = (const T*)a.gamma_pre;
-  pdl_begin();
-  Eight<Y, VEC> y[P] = {};
-  Eight<T, VEC> r[P] = {}, gt[P] = {};
+  const T *rr = (const T*)a.r + m * a.ldr, *gg = (const T*)a.gate + m * a.ldg;
+  const Y* yy = (const Y*)a.y + m * a.ldy;
+  const bool per_row = a.ldg != 0;            // a gate of one row [D] is a vector
+  const int shift = MODE == SHIFTED ? (int)((uintptr_t)rr / sizeof(T) % 8) : 0;
+  int i0[P];
+  bool on[P], whole[P];
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    const int i0 = VEC ? (p * NT + tid) * 8 : p * 8 * NT + tid;
-    if (i0 < D) {
-      y[p].load((const Y*)a.y + m * a.ldy, i0, NT, D);
-      r[p].load((const T*)a.r + m * a.ldr, i0, NT, D);
-      if (a.gate) gt[p].load((const T*)a.gate + m * a.ldg, i0, NT, D);
-    }
+    i0[p] = MODE == APART ? p * 8 * NT + tid : (p * NT + tid) * 8 - shift;
+    on[p] = i0[p] < D;
+    whole[p] = MODE == SHIFTED && i0[p] >= 0 && i0[p] + 8 <= D;
   }
+  Eight<Y, MODE> y[P] = {};
+  Eight<T, MODE> r[P] = {}, gt[P] = {};
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+    if (on[p]) {
+      y[p].load(yy, i0[p], step, D, whole[p], false, false);
+      r[p].load(rr, i0[p], step, D, whole[p], false, false);
+      if (a.gate) gt[p].load(gg, i0[p], step, D, whole[p], !per_row, !WARP);
+    }
   float inv = a.bs;                      // branch scale and first norm as one factor
   if (gpo) {
     float ss = 0.0f;
@@ -119,15 +158,14 @@ __global__ void __launch_bounds__(MAXT, MAXT < 1024 ? (sizeof(Y) == 4 ? 1280 : 1
         const float2 v = y[p].pair(e);
         ss = fmaf(v.x, v.x, fmaf(v.y, v.y, ss));
       }
-    inv = a.bs / sqrtf(block_sum(ss, red[0]) / (float)D + a.eps);
+    inv = a.bs / sqrtf(sum(ss, 0) / (float)D + a.eps);
   }
   float ss = 0.0f;
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    const int i0 = VEC ? (p * NT + tid) * 8 : p * 8 * NT + tid;
-    if (i0 >= D) continue;
-    Eight<T, VEC> go;
-    if (gpo) go.load(gpo, i0, NT, D);
+    if (!on[p]) continue;
+    Eight<T, MODE> go;
+    if (gpo) go.load(gpo, i0[p], step, D, whole[p], true, !WARP);
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
       float2 u = y[p].pair(e);
@@ -145,22 +183,45 @@ __global__ void __launch_bounds__(MAXT, MAXT < 1024 ? (sizeof(Y) == 4 ? 1280 : 1
       const float2 h = r[p].pair(e);
       ss = fmaf(h.x, h.x, fmaf(h.y, h.y, ss));
     }
-    if (a.h) r[p].store((T*)a.h + m * a.ldh, i0, NT, D);
+    if (a.h) r[p].store((T*)a.h + m * a.ldh, i0[p], step, D, whole[p]);
   }
-  const float inv2 = 1.0f / sqrtf(block_sum(ss, red[1]) / (float)D + a.eps);
+  const float inv2 = 1.0f / sqrtf(sum(ss, 1) / (float)D + a.eps);
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    const int i0 = VEC ? (p * NT + tid) * 8 : p * 8 * NT + tid;
-    if (i0 >= D) continue;
-    Eight<T, VEC> g;
-    g.load(gpr, i0, NT, D);
+    if (!on[p]) continue;
+    Eight<T, MODE> g;
+    g.load(gpr, i0[p], step, D, whole[p], true, !WARP);
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
       const float2 h = r[p].pair(e), q = g.pair(e);
       r[p].set(e, h.x * inv2 * (q.x + a.goff), h.y * inv2 * (q.y + a.goff));
     }
-    r[p].store((T*)a.out + m * a.ldo, i0, NT, D);
+    r[p].store((T*)a.out + m * a.ldo, i0[p], step, D, whole[p]);
   }
+}
+
+// One CTA a row.  MAXT: the most threads of a launch; below 1024 the registers are
+// held to what 1536 threads (1280 with fp32 y) a streaming multiprocessor leave.
+template <typename Y, typename T, Mode MODE, int P, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT < 1024 ? (sizeof(Y) == 4 && MAXT < 768 ? 1280 : 1536) / MAXT : 1)
+    norm_kernel(NormArgs a) {
+  __shared__ float red[2][32];
+  pdl_begin();
+  norm_row<Y, T, MODE, P, false>(a, blockIdx.x, threadIdx.x, blockDim.x, [&](float v, int i) { return block_sum(v, red[i]); });
+}
+
+// One warp a row, eight rows a CTA: short rows, many of them.
+constexpr int ROWS_A_CTA = 8;
+template <typename Y, typename T, Mode MODE, int P>
+__global__ void __launch_bounds__(32 * ROWS_A_CTA) norm_warp_kernel(NormArgs a) {
+  const int64_t m = (int64_t)blockIdx.x * ROWS_A_CTA + (threadIdx.x >> 5);
+  pdl_begin();
+  if (m >= a.M) return;
+  norm_row<Y, T, MODE, P, true>(a, m, threadIdx.x & 31, 32, [](float v, int) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    return v;
+  });
 }
 
 // Rows too long for registers: h waits in shared memory for its own norm.
@@ -204,32 +265,54 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(NormArgs a) {
   }
 }
 
-template <typename Y, typename T>
-cudaError_t run(const NormArgs& a, cudaStream_t s) {
-  const auto ok = [&](const void* p, int ld, size_t size) {
-    return (uintptr_t)p % 16 == 0 && ((size_t)ld * size) % 16 == 0;
-  };
-  const bool vec = a.D % 8 == 0 && ok(a.y, a.ldy, sizeof(Y)) && ok(a.r, a.ldr, 2) && ok(a.gamma_post, 0, 2) &&
-                   ok(a.gate, a.ldg, 2) && ok(a.gamma_pre, 0, 2) && ok(a.h, a.ldh, 2) && ok(a.out, a.ldo, 2);
-  const int need = (a.D + 7) / 8;              // threads at eight elements each
-  const dim3 grid(a.M);
+// Few rows: more threads, for the latency of one.  Many rows: twice the elements a
+// thread, since the sums' steps are shared by them, and more rows at once (4096 rows
+// of 4096 in bf16 with a gate: 33.0 us at eight elements a thread, 30.5 us at sixteen,
+// 28.8 us with six rows a streaming multiprocessor); short ones a warp each (160000 rows
+// of 64 to 99: 162 us at a CTA a row, 53 aligned and 93 shifted at a warp).  Rows that
+// begin unaligned, all alike, still go by eights (3000 x 5381: 58 us at APART, 40 at
+// SHIFTED, 29 for 5376 aligned; 1333 x 12001: 81, 43 and 31).
+template <typename Y, typename T, Mode MODE>
+cudaError_t run_mode(const NormArgs& a, cudaStream_t s) {
+  const int need = (a.D + (MODE == SHIFTED ? 14 : 7)) / 8;      // threads at eight elements each
+  const dim3 grid(a.M), warps((a.M + ROWS_A_CTA - 1) / ROWS_A_CTA);
+  const bool many = a.M >= 2 * dev_info().sms;
+  if (many && need <= 32) return launch_step(norm_warp_kernel<Y, T, MODE, 1>, warps, 32 * ROWS_A_CTA, 0, s, 1, a);
+  if (many && need <= 64) return launch_step(norm_warp_kernel<Y, T, MODE, 2>, warps, 32 * ROWS_A_CTA, 0, s, 1, a);
+  if (many && need <= 128) return launch_step(norm_warp_kernel<Y, T, MODE, 4>, warps, 32 * ROWS_A_CTA, 0, s, 1, a);
   const int one = (need + 31) / 32 * 32, two = ((need + 1) / 2 + 31) / 32 * 32;
-  // Few rows: more threads, for the latency of one.  Many rows: twice the elements a
-  // thread, since the sums' steps are shared by them, and more rows at once (4096 rows
-  // of 4096 in bf16 with a gate: 33.0 us at eight elements a thread, 30.5 us at
-  // sixteen, 28.8 us with six rows a streaming multiprocessor).
-  const bool many = vec && need >= 128 && a.M >= 2 * dev_info().sms;
-  if (many && two <= 256) return launch_step(norm_kernel<Y, T, true, 2, 256>, grid, two, 0, s, 1, a);
-  if (many && two <= 512) return launch_step(norm_kernel<Y, T, true, 2, 512>, grid, two, 0, s, 1, a);
-  if (need <= 1024)
-    return vec ? launch_step(norm_kernel<Y, T, true, 1, 1024>, grid, one, 0, s, 1, a)
-               : launch_step(norm_kernel<Y, T, false, 1, 1024>, grid, one, 0, s, 1, a);
-  if (need <= 2048 && vec) return launch_step(norm_kernel<Y, T, true, 2, 1024>, grid, two, 0, s, 1, a);
+  if (MODE != APART) {
+    if (many && two <= 256) return launch_step(norm_kernel<Y, T, MODE, 2, 256>, grid, two, 0, s, 1, a);
+    if (many && two <= 512) return launch_step(norm_kernel<Y, T, MODE, 2, 512>, grid, two, 0, s, 1, a);
+    if (many && two <= 768) return launch_step(norm_kernel<Y, T, MODE, 2, 768>, grid, two, 0, s, 1, a);
+  }
+  if (one <= 1024) return launch_step(norm_kernel<Y, T, MODE, 1, 1024>, grid, one, 0, s, 1, a);
+  if (MODE != APART && two <= 1024) return launch_step(norm_kernel<Y, T, MODE, 2, 1024>, grid, two, 0, s, 1, a);
   static thread_local KernCache c;
   const size_t smem = (size_t)a.D * sizeof(T);
   const cudaError_t e = prep_kernel(norm_long_kernel<Y, T>, c, 1024, smem, nullptr);
   if (e != cudaSuccess) return e;
   return launch_step(norm_long_kernel<Y, T>, grid, 1024, smem, s, 1, a);
+}
+
+template <typename Y, typename T>
+cudaError_t run(const NormArgs& a, cudaStream_t s) {
+  // every row of y, residual, gate, h and out begins at the same element of an aligned
+  // eight; ALIGNED where that is its first
+  const auto shift = [](const void* p, size_t size) { return (uintptr_t)p % (8 * size) / size; };
+  const auto like = [&](const void* p, int ld, size_t size) {
+    return !p || (shift(p, size) == shift(a.r, 2) && (a.M == 1 || ld % 8 == a.ldr % 8));
+  };
+  // fp32 rows need 16 of their 32 bytes aligned only, so a shift of four is none
+  const bool y_like = like(a.y, a.ldy, sizeof(Y)) ||
+                      (sizeof(Y) == 4 && shift(a.r, 2) == 0 && (uintptr_t)a.y % 16 == 0 && (a.M == 1 || a.ldy % 8 == a.ldr % 8));
+  const bool gate_like = a.ldg == 0 || like(a.gate, a.ldg, 2);      // one row [D] is read like a vector
+  const bool alike = y_like && gate_like && like(a.h, a.ldh, 2) && like(a.out, a.ldo, 2);
+  if (!alike) return run_mode<Y, T, APART>(a, s);
+  const bool vectors = (uintptr_t)a.gamma_post % 16 == 0 && (uintptr_t)a.gamma_pre % 16 == 0 &&
+                       (a.ldg != 0 || (uintptr_t)a.gate % 16 == 0);
+  if (a.D % 8 == 0 && shift(a.r, 2) == 0 && (a.M == 1 || a.ldr % 8 == 0) && vectors) return run_mode<Y, T, ALIGNED>(a, s);
+  return run_mode<Y, T, SHIFTED>(a, s);
 }
 
 template <typename T>

@@ -196,7 +196,9 @@ def ref_h(y, r, gpo, gate, rs, bs, off, eps):
 @pytest.mark.parametrize("post,gate", [(True, "none"), (False, "channel"), (True, "token"), (False, "none")])
 @pytest.mark.parametrize("M,D,pad", [(1, 1, 0), (3, 7, 2), (1, 2048, 0), (5, 64, 8), (4, 1000, 0), (2, 4099, 5), (7, 5376, 0),
                                      (2, 16384, 16), (300, 256, 0), (1, 65536, 0), (2, 40000, 0), (33, 8192, 8),
-                                     (320, 1024, 0), (310, 4096, 8), (305, 5384, 0), (400, 8192, 8), (340, 1001, 0)])
+                                     (320, 1024, 0), (310, 4096, 8), (305, 5384, 0), (400, 8192, 8), (340, 1001, 0),
+                                     (400, 64, 0), (999, 99, 0), (310, 515, 3), (320, 512, 8), (330, 1009, 16), (305, 5381, 0), (306, 4099, 1),
+                                     (304, 12001, 0), (311, 8191, 0), (3, 12001, 0), (2, 16383, 0), (5, 5381, 0)])
 def test_block_norm(M, D, pad, post, gate, ydt, dt):
     g = gen(M * 7 + D)
     rn = lambda *s: torch.randn(*s, generator=g, device="cuda")

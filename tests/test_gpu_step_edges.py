@@ -11,7 +11,7 @@ import torch
 
 from conftest import ROOT
 from gpu_util import qmv
-from test_gpu_step import BF16, F16, F32, gen, make_w4, ref_verify
+from test_gpu_step import BF16, F16, F32, gen, make_w4, ref_h, ref_verify
 
 pytestmark = pytest.mark.gpu
 
@@ -208,6 +208,46 @@ def test_softmax_rows_and_results_shifted_differently(V, dt):
         assert bool(((v - ref).abs() <= ref * 2 * (V / 128 + 70) * 2.0 ** -24 + 2.0 ** -126).all())
         rest = torch.cat([out[:, :lead], out[:, lead + V:]], 1)
         assert bool((rest == -7.0).all())
+
+
+@pytest.mark.parametrize("M", [3, 320])
+@pytest.mark.parametrize("D", [96, 1003, 4100])
+def test_norm_tensors_shifted_differently(M, D):
+    # y, residual, gate and the results begin at elements and have strides of their own;
+    # every placement gives what contiguous tensors give, up to the order of the sums
+    q = qmv()
+    g = gen(D)
+
+    def view(t, lead, pad):
+        out = torch.full((M * (D + pad) + lead + 8,), 9.0, device="cuda", dtype=t.dtype)
+        v = out[lead:].as_strided((M, D), (D + pad, 1))
+        v.copy_(t)
+        return v
+
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    y, r, gate = rn(M, D), rn(M, D).to(BF16), torch.sigmoid(rn(M, D)).to(BF16)
+    g1, g2 = ((1 + 0.1 * rn(D)).to(BF16) for _ in range(2))
+    ref = q.qmv_block_norm(y, r, g1, g2, gate)
+    # Two orders of the sums. Each form's fp32 h is off by at most (D / 64 + 48) 2^-24 of the
+    # magnitudes added in it, then rounded to bf16 by 2^-8 of itself: off_h. With z = h gamma / rms,
+    # |dz| <= |dh| gamma / rms + |z| d(rms) / rms, where d(rms) <= rms(dh), to which come the
+    # norm's own sum, twice, and a rounding of z on each side. 1.02 covers the second-order terms,
+    # each below (2^-7)^2 times a few
+    sums = 2 * (D / 64 + 48) * 2.0 ** -24
+    mag = ref_h(y, r, g2, gate, 1.0, 1.0, 0.0, 1e-6)[1].float()
+    h0, z0 = ref[0].float(), ref[1].float().abs()
+    off_h = mag * sums + h0.abs() * 2.0 ** -7
+    rms = torch.sqrt(h0.pow(2).mean(1, keepdim=True) + 1e-6)
+    drms = off_h.pow(2).mean(1, keepdim=True).sqrt() / rms
+    off = (off_h, 1.02 * (off_h * g1.float().abs() / rms + z0 * (drms + sums + 2.0 ** -7)))
+    for lead, pad in ((0, 8), (3, 8), (4, 0), (1, 5)):
+        for same_too in (True, False):
+            l2, p2 = (lead, pad) if same_too else (lead + 1, pad + 3)
+            h, z = view(r, l2, p2), view(r, lead, pad)
+            vec = view(g1.expand(M, D).contiguous(), lead, pad)[0] if same_too else g1
+            out = q.qmv_block_norm(view(y, lead, pad), view(r, lead, pad), vec, g2, view(gate, lead, pad), h_out=h, out=z)
+            for a, b, o in zip(out, ref, off):
+                assert bool(((a.float() - b.float()).abs() <= o).all())
 
 
 def test_offsets_past_32_bits():
