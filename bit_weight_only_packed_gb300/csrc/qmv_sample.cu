@@ -473,7 +473,9 @@ __global__ void __launch_bounds__(V_NT, 3) verify_kernel(VerifyArgs a, int C, in
   const bool refused = acc < n;
   const float* p = p0 + (int64_t)acc * V;
   const float* q = refused && q0 ? q0 + (int64_t)acc * V : nullptr;
-  int hot = refused && !q0 ? draft[acc] : -1;           // may lie outside 0 .. V - 1
+  int hot = refused && !q0 ? draft[acc] : -1;
+  if (hot >= V) hot = -1;
+  hot = max(hot, -1);
   const int first = (rank * NW + warp) * per;           // this warp's chunks
   long long total = 0, before = 0, own = 0;
   for (int pass = 0; pass < 2; ++pass) {
