@@ -425,7 +425,10 @@ QMV_API int qmv_chain_destroy(qmv_chain *c);
  * take row strides (ld*, in elements, at least the row's length), fp16 and
  * bf16, and pointers aligned to their element; the conventions at the top of
  * this file hold for the rest.  They keep no device state and need no
- * workspace, so calls may overlap on several streams.
+ * workspace, so calls may overlap on several streams.  An output that shares
+ * memory with an input or another output is refused (INVALID_ARG) but where a call
+ * allows it; rows of one stride may lie between each other's, as two halves of a
+ * wider tensor do.
  */
 
 /*
@@ -481,12 +484,13 @@ QMV_API int qmv_w4_destroy(qmv_w4pack *p);
  * qmv_w4_gemv -- y[m][n] = sum_g s[n][g] * sum_{k in g} x[m][k] * (q[n][k] - z[n][g])
  * for M columns, computed as s * (sum(x * q) - z * sum(x)) a group, with exact
  * products and fp32 sums in a fixed order and one rounding to y's type at the
- * end.  Infinities and NaN of x act as the definition has them.  Repeated calls
+ * end.  x in bf16 is first taken to within 2^-39 of its column's largest magnitude.
+ * Infinities and NaN of x act as the definition has them.  Repeated calls
  * give the same bits.
  *   M        1 .. 4096.
  *   x        device [M][K] of x_dtype (QMV_F16 or QMV_BF16, any mix with the
  *            scales' type), row stride ldx.
- *   y        device [M][N] of y_dtype, row stride ldy; must not overlap x.
+ *   y        device [M][N] of y_dtype, row stride ldy.
  * Errors: INVALID_ARG, SHAPE (ldx < K or ldy < N), ALIGNMENT, CUDA.
  */
 QMV_API int qmv_w4_gemv(const qmv_w4pack *p, int M, const void *x, int ldx, int x_dtype, void *y,
@@ -511,8 +515,7 @@ QMV_API int qmv_w4_gemv(const qmv_w4pack *p, int M, const void *x, int ldx, int 
  *   out        device [M][D] of dtype, row stride ldo.
  *   D          1 .. 65536.  eps >= 0.
  * out overlaps nothing; h_out overlaps nothing but residual as above.
- * Errors: INVALID_ARG (also an output that begins where an input or the other
- * output does, but for that), SHAPE (a stride below D), UNSUPPORTED (D), ALIGNMENT, CUDA.
+ * Errors: INVALID_ARG, SHAPE (a stride below D), UNSUPPORTED (D), ALIGNMENT, CUDA.
  */
 QMV_API int qmv_block_norm(int M, int D, const void *y, int ldy, int y_dtype, const void *residual,
                            int ldr, const void *gamma_post, const void *gate, int ldg,

@@ -293,3 +293,22 @@ def test_offsets_past_32_bits():
         ref = hs / torch.sqrt(hs.pow(2).mean() + 1e-6)
         # one rounding to bf16, and less than a hundredth of it for the fp32 steps before
         assert bool(((z[i].double() - ref).abs() <= ref.abs() * 2.0 ** -8 * 1.01).all())
+
+
+@pytest.mark.parametrize("M", [1, 2, 5])
+def test_halves_of_one_tensor(M):
+    # rows that lie between each other's share no memory
+    q = qmv()
+    D, g = 192, gen(M)
+    y, r = torch.randn(M, D, generator=g, device="cuda"), torch.randn(M, D, generator=g, device="cuda").to(F16)
+    g1 = torch.ones(D, device="cuda", dtype=F16)
+    both = torch.zeros(M, 2 * D, device="cuda", dtype=F16)
+    h, z = q.qmv_block_norm(y, r, g1)
+    q.qmv_block_norm(y, r, g1, h_out=both[:, :D], out=both[:, D:])
+    assert torch.equal(both[:, :D], h) and torch.equal(both[:, D:], z)
+    wide = torch.zeros(M, 2 * D, device="cuda")
+    wide[:, D:] = y
+    q.qmv_softmax(wide[:, D:], out=wide[:, :D])
+    assert torch.equal(wide[:, :D], q.qmv_softmax(y)) and torch.equal(wide[:, D:], y)
+    with pytest.raises(q.QmvError):
+        q.qmv_softmax(wide[:, 1:D + 1], out=wide[:, :D])

@@ -153,3 +153,53 @@ def test_binding_refuses_before_any_call(q):
     for call, msg in cases:
         with pytest.raises(ValueError, match=msg):
             call()
+
+
+def test_outputs_on_top_of_inputs(q):
+    # every call here is in order but for an output that shares memory with an input or
+    # the other output; addresses that nothing reads
+    lib, M, D, at = q.lib(), 2, 64, 1 << 20
+    far = [at + 65536 * i for i in range(12)]
+    p = q.W4Pack(64, 256, 128)
+    assert lib.qmv_w4_bind(p.handle, far[0]) == 0
+    nb = p.packed_bytes
+    row = 2 * 256 * 2                                    # bytes of x, M = 2
+    for x, y in ((far[1], far[1]), (far[1], far[1] + row - 2), (far[1] + 254, far[1]), (far[1], far[0] + nb - 4)):
+        assert lib.qmv_w4_gemv(p.handle, 2, x, 256, F16, y, 64, F16, None) == -1, (x, y)
+    # columns that cross the next row's, and strides that differ
+    assert lib.qmv_w4_gemv(p.handle, 2, far[1], 320, F16, far[1] + 2 * 257, 320, F16, None) == -1
+    assert lib.qmv_w4_gemv(p.handle, 2, far[1], 320, F16, far[1] + 2 * 256, 321, F16, None) == -1
+    assert lib.qmv_w4_unpack(p.handle, far[0] + nb - 1, None) == -1
+    for codes, scales, zeros in ((far[2] + 2048, far[3], far[4]), (far[1], far[2], far[4]), (far[1], far[3], far[2] + 64)):
+        assert lib.qmv_w4_pack(p.handle, codes, scales, zeros, far[2], None) == -1
+
+    def norm(y=far[0], r=far[1], gpo=far[2], gate=far[3], ldg=D, gpr=far[4], h=far[5], out=far[6], ldo=D):
+        return lib.qmv_block_norm(M, D, y, D, F16, r, D, gpo, gate, ldg, 1.0, 1.0, gpr, 0.0, 1e-6, h, D, out, ldo,
+                                  F16, None)
+
+    n = 2 * M * D
+    for base in (far[0], far[1], far[2], far[3], far[4]):
+        last = base + (n if base in (far[0], far[1], far[3]) else 2 * D) - 2
+        for o in (base, last, base - n + 2):
+            assert norm(out=o) == -1, (base, o)
+            if (base, o) != (far[1], far[1]):            # h_out may be the residual itself
+                assert norm(h=o) == -1, (base, o)
+    assert norm(out=far[5] + 2) == -1
+    assert norm(out=far[3] + 2 * D - 2, ldg=0) == -1
+    assert norm(out=far[0] + 2, ldo=D + 1) == -1
+
+    def softmax(x=far[0], dt=F32, t=far[1], out=far[2], ldo=D):
+        return lib.qmv_softmax(M, D, x, D, dt, t, 1.0, out, ldo, None)
+
+    for o in (far[0] + 4, far[0] + 4 * M * D - 4, far[0] - 4 * M * D + 4, far[1], far[1] + 4):
+        assert softmax(out=o) == -1, o
+    assert softmax(dt=F16, out=far[0] + 2 * M * D - 4) == -1
+
+    B, S, V = 2, 3, 64
+    args = dict(p=far[0], dq=far[1], d=far[2], n=far[3], ua=far[4], us=far[5], tok=far[6], na=far[7])
+    sizes = dict(p=B * (S + 1) * V, dq=B * S * V, d=B * S, n=B, ua=B * S, us=B)
+    verify = lambda **kw: lib.qmv_verify_draft(B, S, V, *{**args, **kw}.values(), None)
+    for name, size in sizes.items():
+        for o in (args[name], args[name] + 4 * size - 4):
+            assert verify(tok=o) == -1 and verify(na=o) == -1, name
+    assert verify(na=far[6] + 4 * (B * (S + 1) - 1)) == -1
