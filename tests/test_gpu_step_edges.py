@@ -312,3 +312,53 @@ def test_halves_of_one_tensor(M):
     assert torch.equal(wide[:, :D], q.qmv_softmax(y)) and torch.equal(wide[:, D:], y)
     with pytest.raises(q.QmvError):
         q.qmv_softmax(wide[:, 1:D + 1], out=wide[:, :D])
+
+
+@pytest.mark.parametrize("dt", [F32, F16, BF16])
+@pytest.mark.parametrize("rows,V", [(304, 4097), (311, 5003), (400, 20003), (700, 9001), (305, 27001), (333, 50257), (304, 56001)])
+def test_softmax_many_rows(rows, V, dt):
+    # rows enough that a streaming multiprocessor takes several; special ones among them, and
+    # rows that begin at any element
+    q = qmv()
+    inf, nan = float("inf"), float("nan")
+    lead, pad = V % 3, V % 5
+    buf = torch.full((rows * (V + pad) + 16,), 5.0, device="cuda", dtype=dt)
+    x = buf[lead:].as_strided((rows, V), (V + pad, 1))
+    x.copy_(torch.randn(rows, V, generator=gen(V), device="cuda") * 4)
+    t = 0.25 + torch.rand(rows, generator=gen(rows), device="cuda")
+    x[:, 3:9] = -inf
+    x[1] = -inf
+    x[160, V - 1] = nan
+    x[161, 0] = inf
+    x[162, :V - 1] = -inf
+    x[163, 9:] = -inf
+    t[[164, 165, 166, 167]] = torch.tensor([0.0, -1.0, nan, inf], device="cuda")
+    x[164:167, V - 2:] = 60.0
+    x[165, 0] = 60.0
+    x[303] = torch.finfo(dt).min
+    out = torch.full((rows * (V + pad) + 16,), -7.0, device="cuda")
+    o = out[lead:].as_strided((rows, V), (V + pad, 1))
+    q.qmv_softmax(x, t, out=o)
+    plain = torch.ones(rows, dtype=torch.bool, device="cuda")
+    plain[[1, 160, 161, 162, 164, 165, 166, 167, 303]] = False
+    arg = (x[plain].double() - x[plain].double().amax(1, keepdim=True)) / t[plain].double()[:, None]
+    ref = torch.softmax(arg, 1)
+    # as for few rows: the exponent's roundings, exp2 and the sum's
+    rel = 3.25 * 2.0 ** -24 * arg.abs().clamp(max=200) + (4 + 2 + V / 128 + 64) * 2.0 ** -24
+    assert bool(((o[plain].double() - ref).abs() <= ref * rel + 2.0 ** -126).all())
+    assert not bool(o[1].any())
+    assert bool(torch.isnan(o[160]).all()) and bool(torch.isnan(o[161]).all())
+    assert float(o[162, V - 1]) == 1.0 and float(o[162].sum()) == 1.0
+    for row, at in ((164, V - 2), (165, 0), (166, V - 2)):
+        assert float(o[row, at]) == 1.0 and float(o[row].sum()) == 1.0
+    assert not bool(o[167, 3:9].any()) and bool((o[167, 9:] == o[167, 0]).all())
+    assert bool((o[303] == o[303, 0]).all()) and abs(float(o[303, 0]) * V - 1) < 1e-4
+    gaps = torch.ones_like(out, dtype=torch.bool)
+    gaps[lead:].as_strided((rows, V), (V + pad, 1)).fill_(False)
+    assert bool((out[gaps] == -7.0).all())
+    again = torch.empty_like(o.contiguous())
+    q.qmv_softmax(x.contiguous(), t, out=again)
+    if dt == F32:
+        assert torch.equal(q.qmv_softmax(x, t, out=x).nan_to_num(9.0), o.nan_to_num(9.0))      # in place
+    assert torch.equal(again.isnan(), o.isnan())
+    assert bool(((again[plain].double() - ref).abs() <= ref * rel + 2.0 ** -126).all())
