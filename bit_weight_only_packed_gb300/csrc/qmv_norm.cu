@@ -2,6 +2,8 @@
 // scale (qmv_block_norm):
 //   u = gate * (y / sqrt(mean y^2 + eps) * g_post),  h = round(a r + b u),
 //   z = round(h / sqrt(mean h^2 + eps) * g_pre).
+#include <algorithm>
+
 #include "qmv_step.cuh"
 
 namespace qmv {
@@ -48,17 +50,17 @@ __device__ __forceinline__ uint32_t pack<__nv_bfloat16>(float a, float b) {
 
 // How a thread takes its eights of a row:
 //   ALIGNED  eight neighbours, 16-byte aligned everywhere;
-//   SHIFTED  the same, but every row begins `shift` elements past such an alignment (an
-//            odd D shifts every row; all [M][D] tensors alike), so that its first and
-//            last eight may stick out of it, and the vectors [D] lie another way;
+//   SHIFTED  the same, but every row begins somewhere past such an alignment (an odd D
+//            shifts every row; all [M][D] tensors alike).  The elements before its first
+//            aligned eight and after its last, at most seven each, go one to a thread
+//            of the first sixteen; the vectors [D] lie another way;
 //   APART    every NT-th element, whatever the alignments.
 enum Mode { ALIGNED, SHIFTED, APART };
 
 // Eight 16-bit elements from p on, whatever p's alignment: the two aligned 16-byte words
-// that hold them, moved into place; both are the caller's to read.  Against eight loads
-// (3000 rows of 5381): 40.2 for 44.1 us in bf16, 39.4 for 49.9 with y in fp32 (1333 of 12001:
-// 43.3 for 48.7, but 48.4 for 45.7); where one warp takes a row, whose
-// ends then go both ways, it costs (160000 x 99: 106 for 93 us).
+// that hold them, moved into place; both are the caller's to read.  Against eight loads, for
+// 3000 rows of 5381: 40.2 for 44.1 us in bf16, 39.4 for 49.9 with y in fp32; where one warp
+// takes a row, which then goes both ways, it costs (160000 x 99: 106 for 93 us).
 __device__ __forceinline__ void load_across(const uint16_t* p, uint32_t* w) {
   const uint32_t off = (uint32_t)(uintptr_t)p & 15;            // the same in a whole row
   const uint4* q = reinterpret_cast<const uint4*>((uintptr_t)p - off);
@@ -75,10 +77,9 @@ __device__ __forceinline__ void load_across(const uint16_t* p, uint32_t* w) {
 template <typename T, Mode MODE>
 struct Eight {
   alignas(16) uint32_t w[2 * sizeof(T)];
-  // whole: all eight are inside the row.  vector: a [D] vector, aligned as it is, by
-  // load_across where that pays.
-  __device__ __forceinline__ void load(const T* p, int i0, int step, int D, bool whole, bool vector, bool across) {
-    if (MODE == ALIGNED || (MODE == SHIFTED && whole && !vector)) {
+  // vector: a [D] vector, aligned as it is, by load_across where that pays.
+  __device__ __forceinline__ void load(const T* p, int i0, int step, int D, bool vector, bool across) {
+    if (MODE == ALIGNED || (MODE == SHIFTED && !vector)) {
 #pragma unroll
       for (int q = 0; q < (int)sizeof(w) / 16; ++q)
         reinterpret_cast<uint4*>(w)[q] = reinterpret_cast<const uint4*>(p + i0)[q];
@@ -86,7 +87,7 @@ struct Eight {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int i = i0 + e * step;
-        w[e] = (unsigned)i < (unsigned)D ? reinterpret_cast<const uint32_t*>(p)[i] : 0u;
+        w[e] = i < D ? reinterpret_cast<const uint32_t*>(p)[i] : 0u;
       }
     } else {
       const uint16_t* s = reinterpret_cast<const uint16_t*>(p);
@@ -97,7 +98,7 @@ struct Eight {
 #pragma unroll
       for (int e = 0; e < 8; e += 2) {
         const int i = i0 + e * step, j = i + step;
-        const uint32_t a = whole || (unsigned)i < (unsigned)D ? s[i] : 0u, b = whole || (unsigned)j < (unsigned)D ? s[j] : 0u;
+        const uint32_t a = MODE == SHIFTED || i < D ? s[i] : 0u, b = MODE == SHIFTED || j < D ? s[j] : 0u;
         w[e >> 1] = a | b << 16;
       }
     }
@@ -109,20 +110,20 @@ struct Eight {
       return unpack<T>(w[e >> 1]);
   }
   __device__ __forceinline__ void set(int e, float a, float b) { w[e >> 1] = pack<T>(a, b); }
-  __device__ __forceinline__ void store(T* p, int i0, int step, int D, bool whole) const {
-    if (MODE == ALIGNED || (MODE == SHIFTED && whole)) {
+  __device__ __forceinline__ void store(T* p, int i0, int step, int D) const {
+    if (MODE != APART) {
       *reinterpret_cast<uint4*>(p + i0) = *reinterpret_cast<const uint4*>(w);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if ((unsigned)(i0 + e * step) < (unsigned)D)
+        if (i0 + e * step < D)
           reinterpret_cast<uint16_t*>(p)[i0 + e * step] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
     }
   }
 };
 
 // One row by NT threads, in registers: 8 * P elements a thread, read once.  Elements
-// past the row's ends are zeros, which add nothing to either sum.
+// past the row's end are zeros, which add nothing to either sum.
 template <typename Y, typename T, Mode MODE, int P, bool WARP, typename Sum>
 __device__ __forceinline__ void norm_row(const NormArgs& a, int64_t m, int tid, int NT, const Sum& sum) {
   const int D = a.D, step = MODE == APART ? NT : 1;
@@ -130,27 +131,35 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, int64_t m, int tid, 
   const T *rr = (const T*)a.r + m * a.ldr, *gg = (const T*)a.gate + m * a.ldg;
   const Y* yy = (const Y*)a.y + m * a.ldy;
   const bool per_row = a.ldg != 0;            // a gate of one row [D] is a vector
-  const int shift = MODE == SHIFTED ? (int)((uintptr_t)rr / sizeof(T) % 8) : 0;
+  // SHIFTED: the first aligned eight, what follows the last, and this thread's element of
+  // the row's ends (-1: none)
+  const int lead = MODE == SHIFTED ? min((int)(-(uintptr_t)rr / sizeof(T) % 8), D) : 0, behind = lead + (D - lead) / 8 * 8;
+  int end = -1;
+  if (MODE == SHIFTED) {
+    if (tid < lead) end = tid;
+    if (tid >= 8 && tid < 8 + D - behind) end = behind + tid - 8;
+  }
   int i0[P];
-  bool on[P], whole[P];
+  bool on[P];
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    i0[p] = MODE == APART ? p * 8 * NT + tid : (p * NT + tid) * 8 - shift;
-    on[p] = i0[p] < D;
-    whole[p] = MODE == SHIFTED && i0[p] >= 0 && i0[p] + 8 <= D;
+    i0[p] = MODE == APART ? p * 8 * NT + tid : lead + (p * NT + tid) * 8;
+    on[p] = i0[p] < (MODE == SHIFTED ? behind : D);
   }
   Eight<Y, MODE> y[P] = {};
   Eight<T, MODE> r[P] = {}, gt[P] = {};
 #pragma unroll
   for (int p = 0; p < P; ++p)
     if (on[p]) {
-      y[p].load(yy, i0[p], step, D, whole[p], false, false);
-      r[p].load(rr, i0[p], step, D, whole[p], false, false);
-      if (a.gate) gt[p].load(gg, i0[p], step, D, whole[p], !per_row, !WARP);
+      y[p].load(yy, i0[p], step, D, false, false);
+      r[p].load(rr, i0[p], step, D, false, false);
+      if (a.gate) gt[p].load(gg, i0[p], step, D, !per_row, !WARP);
     }
+  float ye = 0.0f, he = 0.0f;
+  if (MODE == SHIFTED && end >= 0) ye = to_f<Y>(yy[end]), he = to_f<T>(rr[end]);
   float inv = a.bs;                      // branch scale and first norm as one factor
   if (gpo) {
-    float ss = 0.0f;
+    float ss = ye * ye;
 #pragma unroll
     for (int p = 0; p < P; ++p)
 #pragma unroll
@@ -161,11 +170,20 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, int64_t m, int tid, 
     inv = a.bs / sqrtf(sum(ss, 0) / (float)D + a.eps);
   }
   float ss = 0.0f;
+  if (MODE == SHIFTED && end >= 0) {
+    float u = ye * inv;
+    if (gpo) u *= to_f<T>(gpo[end]) + a.goff;
+    if (a.gate) u *= to_f<T>(gg[end]);
+    const T h = from_f<T>(fmaf(a.rs, he, u));
+    he = to_f<T>(h);
+    ss = he * he;
+    if (a.h) ((T*)a.h + m * a.ldh)[end] = h;
+  }
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     if (!on[p]) continue;
     Eight<T, MODE> go;
-    if (gpo) go.load(gpo, i0[p], step, D, whole[p], true, !WARP);
+    if (gpo) go.load(gpo, i0[p], step, D, true, !WARP);
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
       float2 u = y[p].pair(e);
@@ -183,20 +201,21 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, int64_t m, int tid, 
       const float2 h = r[p].pair(e);
       ss = fmaf(h.x, h.x, fmaf(h.y, h.y, ss));
     }
-    if (a.h) r[p].store((T*)a.h + m * a.ldh, i0[p], step, D, whole[p]);
+    if (a.h) r[p].store((T*)a.h + m * a.ldh, i0[p], step, D);
   }
   const float inv2 = 1.0f / sqrtf(sum(ss, 1) / (float)D + a.eps);
+  if (MODE == SHIFTED && end >= 0) ((T*)a.out + m * a.ldo)[end] = from_f<T>(he * inv2 * (to_f<T>(gpr[end]) + a.goff));
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     if (!on[p]) continue;
     Eight<T, MODE> g;
-    g.load(gpr, i0[p], step, D, whole[p], true, !WARP);
+    g.load(gpr, i0[p], step, D, true, !WARP);
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
       const float2 h = r[p].pair(e), q = g.pair(e);
       r[p].set(e, h.x * inv2 * (q.x + a.goff), h.y * inv2 * (q.y + a.goff));
     }
-    r[p].store((T*)a.out + m * a.ldo, i0[p], step, D, whole[p]);
+    r[p].store((T*)a.out + m * a.ldo, i0[p], step, D);
   }
 }
 
@@ -270,11 +289,13 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(NormArgs a) {
 // of 4096 in bf16 with a gate: 33.0 us at eight elements a thread, 30.5 us at sixteen,
 // 28.8 us with six rows a streaming multiprocessor); short ones a warp each (160000 rows
 // of 64 to 99: 162 us at a CTA a row, 53 aligned and 93 shifted at a warp).  Rows that
-// begin unaligned, all alike, still go by eights (3000 x 5381: 58 us at APART, 40 at
-// SHIFTED, 29 for 5376 aligned; 1333 x 12001: 81, 43 and 31).
+// begin unaligned, all alike, still go by eights (in bf16, 3000 x 5381: 58 us at APART,
+// 40 with ends in the first and last eight, 36 with an element a thread, 29 for 5376
+// aligned; 1333 x 12001: 81, 43, 38 and 31).  A launch's registers follow its threads:
+// fp32 y, 3000 x 5376, 36.6 us bound for 512, 30.5 for 384.
 template <typename Y, typename T, Mode MODE>
 cudaError_t run_mode(const NormArgs& a, cudaStream_t s) {
-  const int need = (a.D + (MODE == SHIFTED ? 14 : 7)) / 8;      // threads at eight elements each
+  const int need = MODE == SHIFTED ? std::max(a.D / 8, 1) : (a.D + 7) / 8;      // threads at eight elements each
   const dim3 grid(a.M), warps((a.M + ROWS_A_CTA - 1) / ROWS_A_CTA);
   const bool many = a.M >= 2 * dev_info().sms;
   if (many && need <= 32) return launch_step(norm_warp_kernel<Y, T, MODE, 1>, warps, 32 * ROWS_A_CTA, 0, s, 1, a);
@@ -283,6 +304,7 @@ cudaError_t run_mode(const NormArgs& a, cudaStream_t s) {
   const int one = (need + 31) / 32 * 32, two = ((need + 1) / 2 + 31) / 32 * 32;
   if (MODE != APART) {
     if (many && two <= 256) return launch_step(norm_kernel<Y, T, MODE, 2, 256>, grid, two, 0, s, 1, a);
+    if (many && two <= 384) return launch_step(norm_kernel<Y, T, MODE, 2, 384>, grid, two, 0, s, 1, a);
     if (many && two <= 512) return launch_step(norm_kernel<Y, T, MODE, 2, 512>, grid, two, 0, s, 1, a);
     if (many && two <= 768) return launch_step(norm_kernel<Y, T, MODE, 2, 768>, grid, two, 0, s, 1, a);
   }
