@@ -607,19 +607,9 @@ int qmv_chain_run(qmv_chain* c, void* stream) {
   }
   if (lock.owns_lock()) lock.unlock();
   const ChainLayout L = chain_layout(c->max_K);
-  static thread_local int set_dev = -1;
-  static thread_local int set_smem = 0;
-  int dev = 0;
-  e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return record_cuda_error(e);
-  if (dev != set_dev || L.smem > set_smem) {
-    e = cudaFuncSetAttribute(gemv_chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L.smem);
-    if (e != cudaSuccess) return record_cuda_error(e);
-    set_dev = dev;
-    set_smem = L.smem;
-  }
+  static thread_local KernCache cache;
   int occ = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, gemv_chain_kernel, CH_THREADS, L.smem);
+  e = prep_kernel(gemv_chain_kernel, cache, CH_THREADS, (size_t)L.smem, &occ);
   if (e != cudaSuccess) return record_cuda_error(e);
   if (occ < 1) return QMV_ERR_UNSUPPORTED;
   // the barrier words start at zero every run

@@ -102,12 +102,24 @@ int launch_tile(const GemvArgs& a, int bits, cudaStream_t s, cudaError_t* err);
 int launch_mtile(const GemvArgs& a, int bits, cudaStream_t s, cudaError_t* err);
 
 
-// Per-kernel launch facts, cached per device: the dynamic shared-memory limit
-// set so far and the occupancy for one (threads, smem) shape.  This keeps the
-// host cost of a call to a few lookups after the first call.
+// Lets kernel k be launched with all the shared memory the device has for it; *limit
+// receives those bytes.  The limit belongs to the process, not to a thread or a call: every
+// caller sets the same one, so that none lowers what another was allowed.
+template <typename Kern>
+inline cudaError_t allow_smem(Kern k, int* limit) {
+  cudaFuncAttributes f;
+  cudaError_t e = cudaFuncGetAttributes(&f, k);
+  if (e != cudaSuccess) return e;
+  *limit = dev_info().max_smem_optin - (int)f.sharedSizeBytes;
+  return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, *limit);
+}
+
+// Per-kernel launch facts, cached per host thread and device: the dynamic
+// shared-memory limit and the occupancy for one (threads, smem) shape.  This keeps
+// the host cost of a call to a few lookups after the first call.
 struct KernCache {
   int dev = -1;
-  size_t smem_set = 48 * 1024;
+  int smem_limit = 0;         // 0: not raised yet
   int occ_threads = -1;
   size_t occ_smem = 0;
   int occ = 0;
@@ -122,11 +134,13 @@ inline cudaError_t prep_kernel(Kern k, KernCache& c, int threads, size_t smem, i
     c = KernCache();
     c.dev = dev;
   }
-  if (smem > c.smem_set) {
-    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (!c.smem_limit) {
+    int limit = 0;
+    e = allow_smem(k, &limit);
     if (e != cudaSuccess) return e;
-    c.smem_set = smem;
+    c.smem_limit = limit;
   }
+  if (smem > (size_t)c.smem_limit) return cudaErrorInvalidValue;
   if (occ) {
     if (c.occ_threads != threads || c.occ_smem != smem) {
       e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&c.occ, k, threads, smem);

@@ -701,7 +701,8 @@ int run_mt(const GemvArgs& a, cudaStream_t s, cudaError_t* err) {
     // the fused residual add + RMSNorm runs in the table kernel
     const size_t nsm = ((size_t)MC * (a.K / 32) + MC) * sizeof(float);
     auto tk = mt_table_kernel<BITS, FOLD, MC, true>;
-    if (nsm > 16 * 1024) e = cudaFuncSetAttribute(tk, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)nsm);
+    static thread_local KernCache table;
+    e = prep_kernel(tk, table, MT_TB_THREADS * MC, nsm, nullptr);
     if (e == cudaSuccess)
       e = mt_launch(tk, dim3(P.NSEG, P.CC), MT_TB_THREADS * MC, nsm, s, a.x, a.r, a.gamma, a.eps, a.h_out, a.M, a.K,
                     P.NSEG, reinterpret_cast<unsigned char*>(a.ws));

@@ -333,37 +333,21 @@ static size_t tma_smem(const TmaPlan& P, int /*K*/) {
 template <int BITS, bool PERROW, bool FUSED, bool EXACT, int U, int MAXT>
 static int run_tma(const GemvArgs& a, const TmaPlan& P, cudaStream_t s, cudaError_t* err,
                    int* occ_only = nullptr) {
-  static thread_local int cached_dev = -1;
-  static thread_local size_t smem_set = 0;
-  static thread_local int occ_cache = 0;
-  static thread_local size_t occ_smem = 0;
-  static thread_local int occ_threads = 0;
+  static thread_local KernCache cache;
   auto kern = gemv_tma_kernel<BITS, PERROW, FUSED, EXACT, U, MAXT>;
   const size_t smem = tma_smem(P, a.K);
   const DevInfo& d = dev_info();
   if (smem > (size_t)d.max_smem_optin) return QMV_ERR_UNSUPPORTED;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) { *err = e; return QMV_ERR_CUDA; }
-  if (dev != cached_dev) { cached_dev = dev; smem_set = 0; occ_smem = 0; occ_threads = 0; }
-  if (smem > smem_set) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) { *err = e; return QMV_ERR_CUDA; }
-    smem_set = smem;
-  }
   const int threads = 64 + P.Tc;
-  if (occ_smem != smem || occ_threads != threads) {
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ_cache, kern, threads, smem);
-    if (e != cudaSuccess) { *err = e; return QMV_ERR_CUDA; }
-    occ_smem = smem;
-    occ_threads = threads;
-  }
+  int occ = 0;
+  cudaError_t e = prep_kernel(kern, cache, threads, smem, &occ);
+  if (e != cudaSuccess) { *err = e; return QMV_ERR_CUDA; }
   if (occ_only) {
-    *occ_only = occ_cache;
+    *occ_only = occ;
     return QMV_OK;
   }
-  if (occ_cache < 1) return QMV_ERR_UNSUPPORTED;
-  int grid = d.sms * occ_cache;
+  if (occ < 1) return QMV_ERR_UNSUPPORTED;
+  int grid = d.sms * occ;
   if (grid > P.ngroups) grid = P.ngroups;
   CUtensorMap tmc, tms;
   if (!tensor_maps(a, BITS, P, &tmc, &tms)) return QMV_ERR_UNSUPPORTED;

@@ -494,8 +494,8 @@ static int clusters_of(Kern kern, int threads, int ks, const DevInfo& d) {
     cfg.dynamicSmemBytes = smem;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+    int n = 0, limit = 0;
+    if (allow_smem(kern, &limit) != cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
       cudaGetLastError();
       n = d.sms / ks;
