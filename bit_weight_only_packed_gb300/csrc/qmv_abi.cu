@@ -9,8 +9,11 @@ namespace {
 
 thread_local int g_last_cuda_error = 0;
 
+// The error is the caller's now (qmv_last_cuda_error): the runtime's own note of it is
+// taken back, or the next library of the thread to ask would report it as its own.
 int cuda_fail(cudaError_t e) {
   g_last_cuda_error = (int)e;
+  cudaGetLastError();
   return QMV_ERR_CUDA;
 }
 
