@@ -50,12 +50,14 @@ constexpr int MAX_NT = 512, MAX_C = 16;
 
 // ----------------------------------------------------------------- softmax --
 
-// What a warp, a CTA or a cluster knows of its part of a row.
-struct Part {
+// What a warp, a CTA or a cluster knows of its part of a row: 16 bytes, stored whole
+// into another CTA's shared memory.
+struct alignas(16) Part {
   float m, s;      // maximum; sum of exp((x - m) / T), in the one-hot form of 0 * x (NaN marks the row)
   int at;          // first place of the maximum (in the one-hot form only)
-  int unused;      // 16 bytes, the size of one store
+  int unused;
 };
+static_assert(sizeof(Part) == 16 && alignof(Part) == 16, "one 16-byte store");
 
 // 2^v to 2 units in the last place; results below 2^-126 become 0.
 __device__ __forceinline__ float ex2(float v) {
