@@ -116,6 +116,42 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+# Calls on a stream of their own (stream=): torch hands freed memory out again in the
+# order of the stream that it was allocated on, so a fresh tensor comes from the memory of
+# the stream that writes it (memory of the current stream may still be written there by work
+# queued earlier), and tensors that a torch stream reads are recorded on it.  With a raw
+# stream handle the caller keeps the inputs alive until the work is done: the handle may no
+# longer exist when they are freed.
+
+def _other(stream, device):
+    """The stream as torch's, if it is not torch's current one of the device."""
+    if stream is None or device.type != "cuda" or _stream(stream) == torch.cuda.current_stream(device).cuda_stream:
+        return None
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(stream), device=device)
+
+
+def _fresh(shape, dtype, device, stream):
+    """A fresh tensor for work on a stream; it may then be used on the current one too."""
+    s = _other(stream, device)
+    if s is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    cur = torch.cuda.current_stream(device)
+    with torch.cuda.stream(s):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(cur)
+    return t
+
+
+def _record(stream, *tensors):
+    """The tensors that work on another torch stream uses keep their memory until it is done."""
+    if isinstance(stream, torch.cuda.Stream):
+        for t in tensors:
+            if t is not None and t.is_cuda and _other(stream, t.device) is not None:
+                t.record_stream(stream)
+
+
 def _dptr(t):
     if t is None:
         return None
@@ -195,9 +231,9 @@ class Pack:
 
     def pack_weights(self, codes: torch.Tensor, scales: torch.Tensor, stream=None, device=None):
         """codes: device int8 [N, K] signed codes; scales: device fp16 [N, K/group]."""
-        dev = codes.device if device is None else device
-        self.words = torch.empty(self.codes_bytes // 4, dtype=torch.int32, device=dev)
-        self.scales = torch.empty(self.scales_bytes // 2, dtype=torch.float16, device=dev)
+        dev = codes.device if device is None else torch.device(device)
+        self.words = _fresh(self.codes_bytes // 4, torch.int32, dev, stream)
+        self.scales = _fresh(self.scales_bytes // 2, torch.float16, dev, stream)
         qmv_pack_weights(self, codes, scales, self.words, self.scales, stream)
         return self
 
@@ -223,14 +259,15 @@ def qmv_pack_weights(p: Pack, codes, scales, d_codes, d_scales, stream=None):
     _need("scales", scales, torch.float16, p.N * G)
     _need_bytes("d_codes", d_codes, p.codes_bytes)
     _need_bytes("d_scales", d_scales, p.scales_bytes)
+    _record(stream, codes, scales, d_codes, d_scales)
     _check("qmv_pack_weights", _lib.qmv_pack_weights(
         p.handle, _dptr(codes), _dptr(scales), _dptr(d_codes), _dptr(d_scales), _stream(stream)))
 
 
-def _out(y, M, N, y_dtype, like):
+def _out(y, M, N, y_dtype, like, stream):
     if y is None:
         dt = torch.float16 if y_dtype == QMV_F16 else torch.float32
-        y = torch.empty((M, N), dtype=dt, device=like.device)
+        y = _fresh((M, N), dt, like.device, stream)
     return y
 
 
@@ -247,20 +284,12 @@ def workspace(p: Pack, M: int, y_dtype=QMV_F32, mode=QMV_FAST, fused=False, devi
 
 def _ws(p, M, y_dtype, mode, fused, ws, like, stream=None):
     """The caller's workspace, checked, or (when none is given) a fresh torch
-    allocation of the size the call needs: (pointer, bytes, tensor).  A fresh
-    one used on another stream than torch's current one is recorded on that
-    stream, so the allocator does not hand it out again before the call ends."""
+    allocation of the size the call needs: (pointer, bytes, tensor)."""
     n = qmv_workspace_bytes(p, M, y_dtype, mode, fused)
     if ws is None:
         if n == 0:
             return None, 0, None
-        ws = torch.empty(n, dtype=torch.uint8, device=like.device)
-        if stream is not None:
-            cur = torch.cuda.current_stream(like.device)
-            if _stream(stream) != cur.cuda_stream:
-                ts = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(
-                    int(stream), device=like.device)
-                ws.record_stream(ts)
+        ws = _fresh(n, torch.uint8, like.device, stream)
     _need_bytes("workspace", ws, n)
     return _dptr(ws), ws.numel() * ws.element_size(), ws
 
@@ -269,8 +298,9 @@ def qmv_gemv(p: Pack, x, y=None, y_dtype=QMV_F32, mode=QMV_FAST, stream=None, M=
     M = x.shape[0] if (M is None and x.dim() == 2) else (M or 1)
     _need("x", x, torch.float16, M * p.K)
     _need("y", y, _YDT.get(y_dtype), M * p.N)
-    y = _out(y, M, p.N, y_dtype, x)
+    y = _out(y, M, p.N, y_dtype, x, stream)
     wp, wb, _keep = _ws(p, M, y_dtype, mode, False, workspace, x, stream)
+    _record(stream, p.words, p.scales, x, y, _keep)
     _check("qmv_gemv", _lib.qmv_gemv(p.handle, M, p.N, p.K, p.bits, p.group, _dptr(x), _dptr(y),
                                      y_dtype, mode, wp, wb, _stream(stream)))
     return y
@@ -280,8 +310,9 @@ def qmv_chunk_gemm(p: Pack, x, y=None, y_dtype=QMV_F32, mode=QMV_FAST, stream=No
     M = x.shape[0]
     _need("x", x, torch.float16, M * p.K)
     _need("y", y, _YDT.get(y_dtype), M * p.N)
-    y = _out(y, M, p.N, y_dtype, x)
+    y = _out(y, M, p.N, y_dtype, x, stream)
     wp, wb, _keep = _ws(p, M, y_dtype, mode, False, workspace, x, stream)
+    _record(stream, p.words, p.scales, x, y, _keep)
     _check("qmv_chunk_gemm", _lib.qmv_chunk_gemm(p.handle, M, _dptr(x), _dptr(y), y_dtype, mode,
                                                  wp, wb, _stream(stream)))
     return y
@@ -295,8 +326,9 @@ def qmv_fused_rmsnorm_gemv(p: Pack, x, residual, gamma, eps=1e-6, h_out=None, y=
     _need("gamma", gamma, torch.float16, p.K)
     _need("h_out", h_out, torch.float16, M * p.K)
     _need("y", y, _YDT.get(y_dtype), M * p.N)
-    y = _out(y, M, p.N, y_dtype, x)
+    y = _out(y, M, p.N, y_dtype, x, stream)
     wp, wb, _keep = _ws(p, M, y_dtype, mode, True, workspace, x, stream)
+    _record(stream, p.words, p.scales, x, residual, gamma, h_out, y, _keep)
     _check("qmv_fused_rmsnorm_gemv", _lib.qmv_fused_rmsnorm_gemv(
         p.handle, M, _dptr(x), _dptr(residual), _dptr(gamma), float(eps), _dptr(h_out), _dptr(y),
         y_dtype, mode, wp, wb, _stream(stream)))
@@ -310,7 +342,8 @@ def qmv_gemv_gather(p: Pack, rows_per_expert: int, expert_ids, x, y=None, y_dtyp
     _need("expert_ids", expert_ids, torch.int32, n)
     _need("x", x, torch.float16, p.K)
     _need("y", y, _YDT.get(y_dtype), n * rows_per_expert)
-    y = _out(y, 1, n * rows_per_expert, y_dtype, x)
+    y = _out(y, 1, n * rows_per_expert, y_dtype, x, stream)
+    _record(stream, p.words, p.scales, expert_ids, x, y)
     _check("qmv_gemv_gather", _lib.qmv_gemv_gather(p.handle, rows_per_expert, _dptr(expert_ids), n,
                                                    _dptr(x), _dptr(y), y_dtype, mode, _stream(stream)))
     return y
@@ -334,9 +367,10 @@ def qmv_gemv_argmax(p: Pack, x, workspace, residual=None, gamma=None, eps=1e-6, 
     _need("value", value, torch.float32, 1)
     _need_bytes("workspace", workspace, _lib.qmv_argmax_workspace_bytes())
     if index is None:
-        index = torch.empty(1, dtype=torch.int32, device=x.device)
+        index = _fresh(1, torch.int32, x.device, stream)
     if value is None:
-        value = torch.empty(1, dtype=torch.float32, device=x.device)
+        value = _fresh(1, torch.float32, x.device, stream)
+    _record(stream, p.words, p.scales, x, workspace, residual, gamma, h_out, y, index, value)
     _check("qmv_gemv_argmax", _lib.qmv_gemv_argmax(
         p.handle, _dptr(x), _dptr(residual), _dptr(gamma), float(eps), _dptr(h_out), _dptr(y), y_dtype,
         mode, _dptr(index), _dptr(value), _dptr(workspace), _stream(stream)))
@@ -345,8 +379,9 @@ def qmv_gemv_argmax(p: Pack, x, workspace, residual=None, gamma=None, eps=1e-6, 
 
 def qmv_unpack_codes(p: Pack, out=None, stream=None):
     if out is None:
-        out = torch.empty((p.N, p.K), dtype=torch.int8, device=p.words.device)
+        out = _fresh((p.N, p.K), torch.int8, p.words.device, stream)
     _need("out", out, torch.int8, p.N * p.K)
+    _record(stream, p.words, out)
     _check("qmv_unpack_codes", _lib.qmv_unpack_codes(p.handle, _dptr(out), _stream(stream)))
     return out
 
@@ -483,7 +518,6 @@ _host = _load_host()
 # looked up once: these calls are short enough for the host's steps to count
 _w4_gemv, _block_norm, _softmax, _verify_draft = (_lib.qmv_w4_gemv, _lib.qmv_block_norm, _lib.qmv_softmax,
                                                   _lib.qmv_verify_draft)
-_empty = torch.empty
 _current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
@@ -541,19 +575,9 @@ def _place(stream, first, *others):
     for t in others:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"tensors are on {first.device} and {t.device}")
-    return _raw_stream(dev) if stream is None else _stream(stream)
-
-
-def _fresh(shape, dtype, like, stream):
-    """A fresh output; one written on another stream than torch's current one is
-    recorded there, so the allocator does not hand it out again too early."""
-    t = _empty(shape, dtype=dtype, device=like.device)
     if stream is not None:
-        cur = torch.cuda.current_stream(like.device)
-        if _stream(stream) != cur.cuda_stream:
-            t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
-                            torch.cuda.ExternalStream(int(stream), device=like.device))
-    return t
+        _record(stream, first, *others)
+    return _raw_stream(dev) if stream is None else _stream(stream)
 
 
 class W4Pack:
@@ -583,7 +607,7 @@ class W4Pack:
         if zeros is not None:
             _vec("zeros", zeros, torch.uint8, self.N * self.G)
         st = _place(stream, codes, scales, zeros)
-        packed = _fresh((self.packed_bytes,), torch.uint8, codes, stream)
+        packed = _fresh((self.packed_bytes,), torch.uint8, codes.device, stream)
         _check("qmv_w4_pack", _lib.qmv_w4_pack(self.handle, codes.data_ptr(), scales.data_ptr(),
                                                None if zeros is None else zeros.data_ptr(), packed.data_ptr(), st))
         self.packed, self._dev = packed, packed.get_device()
@@ -601,7 +625,7 @@ class W4Pack:
         if self.packed is None:
             raise ValueError("the pack holds no weights yet")
         st = _place(stream, self.packed)
-        out = _fresh((self.N, self.K), torch.uint8, self.packed, stream)
+        out = _fresh((self.N, self.K), torch.uint8, self.packed.device, stream)
         _check("qmv_w4_unpack", _lib.qmv_w4_unpack(self.handle, out.data_ptr(), st))
         return out
 
@@ -641,7 +665,7 @@ def qmv_w4_gemv(p: W4Pack, x, y=None, y_dtype=QMV_F32, stream=None):
         raise ValueError(f"y_dtype: unknown value {y_dtype!r}")
     if y is None:
         st = _place(stream, x, packed)
-        ldy, y = N, _fresh((M, N), ydt, x, stream)
+        ldy, y = N, _fresh((M, N), ydt, x.device, stream)
     else:
         ldy = _rows("y", y, (ydt,), M, N)
         st = _place(stream, x, packed, y)
@@ -682,9 +706,9 @@ def qmv_block_norm(y, residual, gamma_pre, gamma_post=None, gate=None, residual_
     ldo = D if out is None else _rows("out", out, (dt,), M, D)
     st = _place(stream, y, residual, gamma_pre, gamma_post, gate, h_out, out)
     if h_out is None:
-        h_out = _fresh((M, D), dt, y, stream)
+        h_out = _fresh((M, D), dt, y.device, stream)
     if out is None:
-        out = _fresh((M, D), dt, y, stream)
+        out = _fresh((M, D), dt, y.device, stream)
     rc = _block_norm(M, D, y.data_ptr(), ldy, _DTYPE[y.dtype], residual.data_ptr(), ldr,
                      None if gamma_post is None else gamma_post.data_ptr(),
                      None if gate is None else gate.data_ptr(), ldg, residual_scale, branch_scale,
@@ -719,7 +743,7 @@ def qmv_softmax(logits, temperature=1.0, out=None, stream=None):
     ldo = V if out is None else _rows("out", out, (torch.float32,), rows, V)
     st = _place(stream, logits, t, out)
     if out is None:
-        out = _fresh((rows, V), torch.float32, logits, stream)
+        out = _fresh((rows, V), torch.float32, logits.device, stream)
     rc = _softmax(rows, V, logits.data_ptr(), ldl, _DTYPE[logits.dtype], None if t is None else t.data_ptr(), t0,
                   out.data_ptr(), ldo, st)
     if rc:
@@ -754,9 +778,9 @@ def qmv_verify_draft(target, draft_probs, draft, u_accept, u_sample, n_draft=Non
         _vec("n_accepted", n_accepted, torch.int32, B)
     st = _place(stream, target, draft_probs, draft, u_accept, u_sample, n_draft, tokens, n_accepted)
     if tokens is None:
-        tokens = _fresh((B, S1), torch.int32, target, stream)
+        tokens = _fresh((B, S1), torch.int32, target.device, stream)
     if n_accepted is None:
-        n_accepted = _fresh((B,), torch.int32, target, stream)
+        n_accepted = _fresh((B,), torch.int32, target.device, stream)
     rc = _verify_draft(B, S, V, target.data_ptr(), None if draft_probs is None else draft_probs.data_ptr(),
                        draft.data_ptr(), None if n_draft is None else n_draft.data_ptr(), u_accept.data_ptr(),
                        u_sample.data_ptr(), tokens.data_ptr(), n_accepted.data_ptr(), st)
