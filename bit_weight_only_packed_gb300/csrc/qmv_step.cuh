@@ -107,7 +107,10 @@ cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s);
 // A launch on s in clusters of `cluster` CTAs along x, as a programmatic
 // dependent of the kernel before it: its CTAs may start while that one still
 // drains, and every kernel launched here waits for it (griddepcontrol.wait)
-// before it touches global memory, so that only the launch itself overlaps.
+// before it touches global memory, so that only the launch itself overlaps.  (The
+// matvec with early weights reads those before it waits.)  Each lets its own dependents
+// start after that wait and not before, so what runs early runs ahead of one kernel
+// only: all before that one have ended, and what they wrote can be read.
 // (43008x5376 for one token, call after call: 28.7 us without, 25.8 us with.)
 template <typename... P, typename... A>
 inline cudaError_t launch_step(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, int cluster,
@@ -134,10 +137,10 @@ inline cudaError_t launch_step(void (*kern)(P...), dim3 grid, int threads, size_
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-// Lets the next kernel of the stream start, and waits for the one before.
+// Waits for the kernel before, then lets the next one of the stream start.
 __device__ __forceinline__ void pdl_begin() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // Clusters: a barrier of all their threads, and a CTA's shared memory as the others see it.

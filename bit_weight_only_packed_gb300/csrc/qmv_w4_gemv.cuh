@@ -172,7 +172,6 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
   const auto strips_of = [&](int r) { return min(P.rs, S1 - S0 - r * P.rs); };
   const auto first_of = [&](int r, int w) { return (int)((unsigned)(strips_of(r) * kbn) * (unsigned)w / W); };
   uint8_t* ring = smem + (size_t)warp * P.slots * P.stage * bb;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) abort_flag = 0;
   if (tid < 8 * NB) colmax[tid] = 0;
 
@@ -219,7 +218,7 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
   const uint16_t* xg = (const uint16_t*)a.x + (int64_t)m0 * a.ldx + (int64_t)kb0 * BK;
   const int klim = min(kbn * BK, a.K - kb0 * BK);
   if (tid < 16) reinterpret_cast<uint4*>(smem + P.zero_off)[tid] = make_uint4(0, 0, 0, 0);
-  asm volatile("griddepcontrol.wait;" ::: "memory");     // x may come from the kernel before
+  pdl_begin();                             // x may come from the kernel before
   if (P.vec) {
     if (warp == 0) {
       if (lane == 0) pipe::mbar_arrive_tx(&x_full, mc * klim * 2);

@@ -307,12 +307,14 @@ QMV_API int qmv_destroy_pack(qmv_pack *p);
  * between the dependent matvecs of a decode layer ([A19] "What moved the
  * needle", dispatch-count item: the per-dispatch tax between kernels).
  * Requirement: the packed weights of a matvec must not be written by the
- * kernel launched just before it in the stream (pack once, then run).
+ * kernel launched just before it in the stream (pack once, then run), nor by the
+ * kernel before a run of M = 1 matvecs or M-column tiles launched with this on,
+ * since those let the next one start before they have waited themselves.
  * Works under stream capture (CUDA graphs).  Always returns QMV_OK.
  * (The verification-step calls below always let their launch overlap the end of
- * the kernel before, and wait for it before they touch memory; with this on,
- * qmv_w4_gemv also begins to stream its weights before that wait, under the
- * same requirement.)
+ * the kernel before, and wait for it before they touch memory and before they let
+ * the next one start; with this on, qmv_w4_gemv also begins to stream its weights
+ * before that wait, under the same requirement.)
  */
 QMV_API int qmv_set_pdl(int enable);
 

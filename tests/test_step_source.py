@@ -17,3 +17,15 @@ def test_what_the_ctas_of_a_cluster_store_to_each_other_is_aligned():
     assert "static_assert(sizeof(Part) == 16 && alignof(Part) == 16" in text
     # the other exchange is 8 bytes of an array of 8-byte numbers
     assert re.search(r"long long [^;]*parts\[2\]\[MAX_C\]", text)
+
+
+def test_dependents_start_after_the_wait():
+    # A matvec with early weights reads them ahead of its own wait. It may do so because the
+    # kernel before it let it start only after all kernels before that one had ended; one that
+    # lets its dependents start first would let them read weights that are still being written.
+    texts = {n: source(n) for n in ("qmv_step.cuh", "qmv_norm.cu", "qmv_sample.cu", "qmv_w4_gemv.cuh", "qmv_w4.cu")}
+    assert texts["qmv_step.cuh"].index("griddepcontrol.wait;\"") < texts["qmv_step.cuh"].index("griddepcontrol.launch_dependents;\"")
+    assert sum(t.count("griddepcontrol.launch_dependents;") for t in texts.values()) == 1
+    # every kernel goes through it: the softmaxes, the verification, the norms, the matvec
+    for name, kernels in (("qmv_norm.cu", 3), ("qmv_sample.cu", 3), ("qmv_w4_gemv.cuh", 1)):
+        assert texts[name].count("pdl_begin();") == kernels, name
