@@ -27,9 +27,9 @@ namespace {
 // have come.  The one barrier that this needs (no store before the others have set
 // theirs up) is arrived at when a kernel begins and waited for only here, so it
 // costs nothing; and a CTA may end as soon as it has what it waited for, since
-// only then does nobody store to it any more.  (Five rows of 262144, sixteen CTAs a
-// row: 7.8 us, against 9.4 us with a cluster barrier before and after reading the
-// others' shared memory.)
+// only then does nobody store to it any more.  One whose wait ran out goes through
+// exchange_leave first.  (Five rows of 262144, sixteen CTAs a row: 7.8 us, against
+// 9.4 us with a cluster barrier before and after reading the others' shared memory.)
 __device__ __forceinline__ void exchange_begin(uint64_t* bar, int bars, uint32_t bytes) {
   if (threadIdx.x == 0) {
     for (int i = 0; i < bars; ++i) {
@@ -44,6 +44,16 @@ __device__ __forceinline__ void exchange_begin(uint64_t* bar, int bars, uint32_t
   } else {
     cluster_arrive_relaxed();
   }
+}
+
+// The end of a warp whose wait ran out: the others may still store to this CTA, so it
+// stays until each of them has ended or come here too (each has stored by then, and its
+// own wait is bounded), and until what they sent has landed.
+__device__ __noinline__ void exchange_leave(uint64_t* bar, int bars) {
+  __syncwarp();
+  cluster_arrive();
+  cluster_wait();
+  for (int i = 0; i < bars; ++i) pipe::mbar_drain(bar + i, 0, &g_sample_error);
 }
 
 constexpr int MAX_NT = 512, MAX_C = 16;
@@ -250,7 +260,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) softmax_kernel(SoftmaxArgs a, i
         st_async128(cluster_addr(&parts[rank], lane), cluster_addr(&all_here, lane), __float_as_uint(q.m),
                     __float_as_uint(q.s), (uint32_t)q.at, 0u);
     }
-    if (!pipe::mbar_wait_fast(&all_here, 0, &abort_flag, pipe::ERR_TIMEOUT_FULL, &g_sample_error)) return;
+    const bool came = pipe::mbar_wait_fast(&all_here, 0, &abort_flag, pipe::ERR_TIMEOUT_FULL, &g_sample_error);
+    if (!__all_sync(~0u, came)) return exchange_leave(&all_here, 1);
     all = join(parts[lane & (C - 1)], C, c, hot);
   }
   // special rows, the one-hot form and rows of nothing but -inf (or NaN), have one
@@ -678,7 +689,7 @@ __global__ void __launch_bounds__(V_NT, 3) verify_kernel(VerifyArgs a, int C, in
         if (!came) s_dead = 1;
       }
       __syncthreads();
-      if (s_dead) return;                 // the same for all threads
+      if (s_dead) return exchange_leave(all_here, 2);       // the same for all threads
       const long long v = lane < C ? parts[pass][lane] : 0;
       total = warp_sum(v);
       before = __shfl_sync(~0u, warp_before(v), rank);

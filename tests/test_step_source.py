@@ -29,3 +29,25 @@ def test_dependents_start_after_the_wait():
     # every kernel goes through it: the softmaxes, the verification, the norms, the matvec
     for name, kernels in (("qmv_norm.cu", 3), ("qmv_sample.cu", 3), ("qmv_w4_gemv.cuh", 1)):
         assert texts[name].count("pdl_begin();") == kernels, name
+
+
+def test_a_cta_whose_wait_ran_out_stays_until_nobody_stores_to_it():
+    # The CTAs of a cluster store to each other's shared memory; one that ended after a wait that
+    # ran out, while another has yet to store, would be stored to after its end.
+    text = source("qmv_sample.cu")
+    leave = re.search(r"void exchange_leave\(.*?\n\}", text, re.S).group(0)
+    assert leave.index("cluster_arrive();") < leave.index("cluster_wait();") < leave.index("mbar_drain(")
+    kernels = re.findall(r"\n__global__ .*?\n\}\n", text, re.S)
+    waits = 0
+    for k in kernels:
+        if "exchange_begin(" not in k:
+            continue
+        # between the wait for the others' values and the next use of them
+        for m in re.finditer(r"mbar_wait_fast\(&all_here", k):
+            after = k[m.start():m.start() + 600]
+            assert re.search(r"return exchange_leave\(", after), after
+            waits += 1
+        # no other way out once the exchange has begun
+        body = k[k.index("exchange_begin("):]
+        assert not re.search(r"\breturn;", body)
+    assert waits == 2
