@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(NormArgs a) {
 template <typename Y, typename T, Mode MODE>
 cudaError_t run_mode(const NormArgs& a, cudaStream_t s) {
   const int need = MODE == SHIFTED ? std::max(a.D / 8, 1) : (a.D + 7) / 8;      // threads at eight elements each
-  const dim3 grid(a.M), warps((a.M + ROWS_A_CTA - 1) / ROWS_A_CTA);
+  const dim3 grid(a.M), warps((a.M - 1) / ROWS_A_CTA + 1);
   const bool many = a.M >= 2 * dev_info().sms;
   if (many && need <= 32) return launch_step(norm_warp_kernel<Y, T, MODE, 1>, warps, 32 * ROWS_A_CTA, 0, s, 1, a);
   if (many && need <= 64) return launch_step(norm_warp_kernel<Y, T, MODE, 2>, warps, 32 * ROWS_A_CTA, 0, s, 1, a);

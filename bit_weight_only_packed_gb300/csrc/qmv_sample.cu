@@ -119,9 +119,10 @@ struct Place {
   float* out;
   int e0, wholes, e1;
   bool extra;
-  __device__ __forceinline__ Place(const SoftmaxArgs& a, int row, int f0, int len) {
+  __device__ __forceinline__ Place(const SoftmaxArgs& a, int row, int f0, int len, bool fours) {
     x = (const X*)a.x + (int64_t)row * a.ldx;
     out = a.out + (int64_t)row * a.ldo;
+    if (!fours) return;
     const int shift = (int)((uintptr_t)x / sizeof(X) % 4);
     const int n = max(0, min(len, (a.V + shift + 3) / 4 - f0)), skip = f0 == 0 && shift ? 1 : 0;
     wholes = max(0, min(n, (a.V + shift) / 4 - f0) - skip);
@@ -150,7 +151,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) softmax_kernel(SoftmaxArgs a, i
   __shared__ int abort_flag;
   const int rank = blockIdx.x % C, tid = threadIdx.x, lane = tid & 31, V = a.V, f0 = rank * len;
   const int row = blockIdx.x / C;
-  const Place<X> at(a, row, f0, len);
+  const Place<X> at(a, row, f0, len, EPT > 0);
   if (C > 1) {
     if (tid == 0) abort_flag = 0;
     exchange_begin(&all_here, 1, C * sizeof(Part));
@@ -309,7 +310,7 @@ cudaError_t run_softmax(const SoftmaxArgs& a, int parts, int C, cudaStream_t s) 
     }
     if (e != cudaSuccess) return e;
   }
-  return launch_step(softmax_kernel<X, EPT, NT>, dim3((unsigned)a.rows * C), NT, 0, s, C, a, C, (parts + C - 1) / C);
+  return launch_step(softmax_kernel<X, EPT, NT>, dim3((unsigned)a.rows * C), NT, 0, s, C, a, C, (parts - 1) / C + 1);
 }
 
 // Many rows that fit twice into a CTA's shared memory: a CTA a streaming multiprocessor
