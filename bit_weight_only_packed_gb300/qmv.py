@@ -755,7 +755,8 @@ def qmv_verify_draft(target, draft_probs, draft, u_accept, u_sample, n_draft=Non
                      stream=None):
     """(tokens [B, S+1], n_accepted [B]): target fp32 [B, S+1, V], draft_probs
     fp32 [B, S, V] or None (a drafter that is sure of its tokens), draft int32
-    [B, S], u_accept fp32 [B, S], u_sample fp32 [B], n_draft int32 [B] or None."""
+    [B, S], u_accept fp32 [B, S], u_sample fp32 [B], n_draft int32 [B] or None.
+    draft and u_accept may be None where S is 0."""
     if tokens is None and n_accepted is None and stream is None:
         r = _host.verify_draft(target, draft_probs, draft, u_accept, u_sample, n_draft)
         if r is not None:
@@ -767,8 +768,11 @@ def qmv_verify_draft(target, draft_probs, draft, u_accept, u_sample, n_draft=Non
     _vec("target", target, torch.float32, B * S1 * V)
     if draft_probs is not None:
         _vec("draft_probs", draft_probs, torch.float32, B * S * V)
-    _vec("draft", draft, torch.int32, B * S)
-    _vec("u_accept", u_accept, torch.float32, B * S)
+    for name, t, dtype in (("draft", draft, torch.int32), ("u_accept", u_accept, torch.float32)):
+        if t is not None:
+            _vec(name, t, dtype, B * S)
+        elif S:
+            raise ValueError(f"{name}: needed for {S} drafted tokens")
     _vec("u_sample", u_sample, torch.float32, B)
     if n_draft is not None:
         _vec("n_draft", n_draft, torch.int32, B)
@@ -782,8 +786,8 @@ def qmv_verify_draft(target, draft_probs, draft, u_accept, u_sample, n_draft=Non
     if n_accepted is None:
         n_accepted = _fresh((B,), torch.int32, target.device, stream)
     rc = _verify_draft(B, S, V, target.data_ptr(), None if draft_probs is None else draft_probs.data_ptr(),
-                       draft.data_ptr(), None if n_draft is None else n_draft.data_ptr(), u_accept.data_ptr(),
-                       u_sample.data_ptr(), tokens.data_ptr(), n_accepted.data_ptr(), st)
+                       None if draft is None else draft.data_ptr(), None if n_draft is None else n_draft.data_ptr(),
+                       None if u_accept is None else u_accept.data_ptr(), u_sample.data_ptr(), tokens.data_ptr(), n_accepted.data_ptr(), st)
     if rc:
         _check("qmv_verify_draft", rc)
     return tokens, n_accepted
