@@ -3,7 +3,8 @@
 Each .cu file is compiled by its own nvcc process (in parallel), then linked
 into ``bit_weight_only_packed_gb300/_lib/libqmv.so``.  No fast-math: the
 kernels rely on IEEE fp32 rounding.  The binding's host module (C++ against the
-running torch's and Python's headers) goes beside it as ``qmv_host.so``.
+running torch's and Python's headers) goes beside it as ``qmv_host.so``, with a note
+of what it was built for; the library does without it where it cannot be built.
 """
 from __future__ import annotations
 
@@ -12,7 +13,9 @@ import glob
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -48,8 +51,23 @@ def _stale(lib: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def host_abi() -> str:
+    """What the host module's code depends on beside its sources."""
+    import torch
+    return f"torch {torch.__version__}, {sys.implementation.cache_tag}"
+
+
+def _host_built_for() -> str:
+    try:
+        with open(HOST_LIB + ".for") as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
 def build_host(force: bool = False) -> str:
-    if not force and not _stale(HOST_LIB, [HOST_SRC, os.path.join(ROOT, "include", "qmv.h"), __file__]):
+    if not force and _host_built_for() == host_abi() and not _stale(
+            HOST_LIB, [HOST_SRC, os.path.join(ROOT, "include", "qmv.h"), __file__]):
         return HOST_LIB
     import torch
     os.makedirs(OUT_DIR, exist_ok=True)
@@ -66,15 +84,27 @@ def build_host(force: bool = False) -> str:
                         f"-Wl,-rpath,{tlib}"], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {HOST_SRC}:\n{r.stderr}")
+    if os.path.exists(HOST_LIB + ".for"):       # no note while the module changes
+        os.remove(HOST_LIB + ".for")
     os.replace(tmp, HOST_LIB)
+    with open(HOST_LIB + ".for", "w") as f:
+        f.write(host_abi())
     return HOST_LIB
+
+
+def _try_host(force: bool = False):
+    """The library's calls all work without the host module, so a failure is only told."""
+    try:
+        build_host(force)
+    except (OSError, RuntimeError, AttributeError, ImportError) as e:
+        warnings.warn(f"qmv_host.so could not be built: {e}")
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [
         os.path.join(ROOT, "include", "qmv.h"), __file__]
     if not force and not extra and not _stale(LIB, deps):
-        build_host()
+        _try_host()
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
     tmpdir = os.path.join(OUT_DIR, f"obj{os.getpid()}")
@@ -94,7 +124,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
-        host = ex.submit(build_host, force)
+        host = ex.submit(_try_host, force)
         objs = list(ex.map(compile_one, sources()))
         host.result()
     tmp_lib = LIB + f".tmp{os.getpid()}"

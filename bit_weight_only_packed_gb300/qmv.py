@@ -11,6 +11,7 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import warnings
 
 import torch
 
@@ -498,17 +499,34 @@ _16BIT = (torch.float16, torch.bfloat16)
 _FLOAT = (torch.float32, torch.float16, torch.bfloat16)
 
 
+class _NoHost:
+    """In the place of qmv_host.so where it cannot be used: leaves every call to the Python form."""
+
+    @staticmethod
+    def leave(*args):
+        return None
+
+    w4_gemv = block_norm = softmax = verify_draft = leave
 
 
 def _load_host():
-    """qmv_host.so (csrc/host/qmv_host.cpp): the usual form of these calls in C++."""
+    """qmv_host.so (csrc/host/qmv_host.cpp): the usual form of these calls in C++.  It holds
+    to the headers of the torch and Python that it was built with; without one for those
+    that are running, the Python form takes every call, with more host time."""
     path = os.path.join(_HERE, "_lib", "qmv_host.so")
-    if not os.path.exists(path):
-        raise ImportError(f"qmv_host.so is not built ({path}); run "
-                          "`python -c 'import __graft_entry__ as g; g.build()'`")
-    loader = importlib.machinery.ExtensionFileLoader("qmv_host", path)
-    mod = importlib.util.module_from_spec(importlib.util.spec_from_file_location("qmv_host", path, loader=loader))
-    loader.exec_module(mod)
+    try:
+        from .build import host_abi
+        with open(path + ".for") as f:
+            built_for = f.read()
+        if built_for != host_abi():
+            raise ImportError(f"it was built for {built_for}, this is {host_abi()}")
+        loader = importlib.machinery.ExtensionFileLoader("qmv_host", path)
+        mod = importlib.util.module_from_spec(importlib.util.spec_from_file_location("qmv_host", path, loader=loader))
+        loader.exec_module(mod)
+    except (OSError, ImportError) as e:
+        warnings.warn(f"qmv_host.so is not used ({e}): the verification-step calls take more host time; "
+                      "build it with `python -c 'import __graft_entry__ as g; g.build()'`")
+        return _NoHost()
     addr = lambda f: ctypes.cast(f, _P).value
     mod.init(addr(_lib.qmv_w4_gemv), addr(_lib.qmv_block_norm), addr(_lib.qmv_softmax), addr(_lib.qmv_verify_draft))
     return mod
