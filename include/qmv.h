@@ -564,7 +564,8 @@ QMV_API int qmv_softmax(int rows, int V, const void *logits, int ldl, int dtype,
  *   n_accepted  device int32 [B]: drafted tokens that stand.
  * S may be 0 (draft, draft_probs and u_accept are then not read and may be NULL).
  *   B 1 .. 65535, S 0 .. 1024, V 1 .. 2^20.
- * NaN in p or q counts as 0 in the draw and refuses its token.
+ * NaN in p or q refuses its token; in the draw an id whose weight is NaN (p, or where
+ * max(p - q, 0) is drawn from, p or q) counts 0.
  * Errors: INVALID_ARG, UNSUPPORTED (sizes), ALIGNMENT (4 bytes), CUDA.
  */
 QMV_API int qmv_verify_draft(int B, int S, int V, const float *target, const float *draft_probs,
