@@ -525,6 +525,12 @@ static int chain_add(qmv_chain* c, const qmv_pack* p, const void* x, const void*
   if (!chain_plan(a.N, a.K, p->bits, a.perrow != 0, dev_info().sms, &o.P)) return QMV_ERR_UNSUPPORTED;
   const int max_K = c->max_K > a.K ? c->max_K : a.K;
   if (chain_layout(max_K).smem > dev_info().max_smem_optin) return QMV_ERR_UNSUPPORTED;
+  // tensor maps are made in the device's context, which a host thread has only after a call
+  // that needs it
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaSetDevice(dev);
+  if (e != cudaSuccess) return record_cuda_error(e);
   if (!encode_pack_maps(a, o.P, &o.tm_codes, &o.tm_scales)) return QMV_ERR_UNSUPPORTED;
   o.bits = p->bits;
   o.exact = (mode == QMV_EXACT) ? 1 : 0;
