@@ -73,7 +73,8 @@ __device__ __forceinline__ float zero_f(uint32_t v, int i) {
 
 // The power of two that scales a bf16 column, from the bits of its largest
 // magnitude (141 minus the exponent field puts that at 2^14), kept where it and its
-// inverse are normal.
+// inverse are normal: a column below 2^-112 is scaled by 2^126 only, which leaves
+// multiples of 2^-7, so that fp16 still holds all of it.
 __device__ __forceinline__ int column_exp(uint32_t top) { return min(141 - (int)(top >> 7), 126); }
 __device__ __forceinline__ float pow2_f(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
     for (int m = 0; m < mc; ++m) reinterpret_cast<uint16_t*>(xs + m * P.pitch)[klim + tid] = 0;
   __syncthreads();
   if (P.vec && !pipe::mbar_wait_fast(&x_full, 0, &abort_flag, pipe::ERR_TIMEOUT_TFULL, &g_w4_error))
-    pipe::mbar_drain(&x_full, 0, &g_w4_error);           // nothing is stored after a wait that ran out
+    pipe::mbar_drain(&x_full, 0, &g_w4_error);           // this CTA stores nothing after a wait that ran out
 
   if (a.x_bf16) {
     // to fp16, in place: 16 lanes take a block of a column, eight values a lane, once
@@ -377,8 +378,9 @@ __global__ void __launch_bounds__(warps_of(NB) * 32, 1)
     float* to = place(warp, 0);            // the first strip of the range, later ones
     while (f < hi) {
       const int cnt = min(P.stage, min(hi - f, kbn - blk));
-      // after a wait that ran out nothing is copied or stored any more, but the warp
-      // keeps to its course
+      // after a wait that ran out this CTA copies and stores nothing any more, but the warp
+      // keeps to its course; with a cluster along k the others still add and store what it
+      // had by then (the device error word says that results are incomplete)
       dead |= !pipe::mbar_wait_fast(&full[warp][slot], parity, &abort_flag, pipe::ERR_TIMEOUT_FULL, &g_w4_error);
       landed += !dead;
       const uint8_t* p = ring + slot * P.stage * bb;

@@ -487,8 +487,9 @@ QMV_API int qmv_w4_destroy(qmv_w4pack *p);
  * for M columns, computed as s * (sum(x * q) - z * sum(x)) a group, with exact
  * products and fp32 sums in a fixed order and one rounding to y's type at the
  * end.  x in bf16 is first taken to within 2^-39 of its column's largest magnitude.
- * Infinities and NaN of x act as the definition has them.  Repeated calls
- * give the same bits.
+ * Infinities and NaN of x act as the definition has them: each result that is
+ * not finite is formed again from it, which takes far longer (43008 x 5376, one
+ * column: 1.1 ms instead of 24 us).  Repeated calls give the same bits.
  *   M        1 .. 4096.
  *   x        device [M][K] of x_dtype (QMV_F16 or QMV_BF16, any mix with the
  *            scales' type), row stride ldx.
@@ -536,6 +537,9 @@ QMV_API int qmv_block_norm(int M, int D, const void *y, int ldy, int y_dtype, co
  *           same pointer, ldo == ldl).
  * A logit of -inf gets 0; a row of nothing but -inf gets all zeros.  A row that
  * holds NaN or +inf gives NaN in every place.
+ * All steps are fp32: a probability is off by at most 2^-24 * (70 + V / 128 +
+ * 3.25 |x - max| / T) of itself, and what is below 2^-126 may be 0.  T acts as it
+ * is from 2^-125 to 1e37 and as those beyond.
  * Errors: INVALID_ARG (also temperature < 0 or NaN), SHAPE, ALIGNMENT, CUDA.
  */
 QMV_API int qmv_softmax(int rows, int V, const void *logits, int ldl, int dtype,
