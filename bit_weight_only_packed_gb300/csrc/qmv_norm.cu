@@ -302,14 +302,16 @@ cudaError_t run_mode(const NormArgs& a, cudaStream_t s) {
   if (many && need <= 64) return launch_step(norm_warp_kernel<Y, T, MODE, 2>, warps, 32 * ROWS_A_CTA, 0, s, 1, a);
   if (many && need <= 128) return launch_step(norm_warp_kernel<Y, T, MODE, 4>, warps, 32 * ROWS_A_CTA, 0, s, 1, a);
   const int one = (need + 31) / 32 * 32, two = ((need + 1) / 2 + 31) / 32 * 32;
-  if (MODE != APART) {
+  if constexpr (MODE != APART) {
     if (many && two <= 256) return launch_step(norm_kernel<Y, T, MODE, 2, 256>, grid, two, 0, s, 1, a);
     if (many && two <= 384) return launch_step(norm_kernel<Y, T, MODE, 2, 384>, grid, two, 0, s, 1, a);
     if (many && two <= 512) return launch_step(norm_kernel<Y, T, MODE, 2, 512>, grid, two, 0, s, 1, a);
     if (many && two <= 768) return launch_step(norm_kernel<Y, T, MODE, 2, 768>, grid, two, 0, s, 1, a);
   }
   if (one <= 1024) return launch_step(norm_kernel<Y, T, MODE, 1, 1024>, grid, one, 0, s, 1, a);
-  if (MODE != APART && two <= 1024) return launch_step(norm_kernel<Y, T, MODE, 2, 1024>, grid, two, 0, s, 1, a);
+  if constexpr (MODE != APART) {
+    if (two <= 1024) return launch_step(norm_kernel<Y, T, MODE, 2, 1024>, grid, two, 0, s, 1, a);
+  }
   static thread_local KernCache c;
   const size_t smem = (size_t)a.D * sizeof(T);
   const cudaError_t e = prep_kernel(norm_long_kernel<Y, T>, c, 1024, smem, nullptr);
