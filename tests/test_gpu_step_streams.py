@@ -134,3 +134,32 @@ def test_streams_of_their_own_in_a_capture():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(cap, ref)
+
+
+def test_steps_on_several_host_threads_at_once():
+    import threading
+
+    from test_gpu_step_edges import case, same
+    runs = [case(seed=5 + 45 * i, M=3 + i, V=(4099, 70001, 515)[i]) for i in range(3)]
+    ref = [r() for r in runs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def body(i):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(30):
+                    out = runs[i]()
+                    s.synchronize()
+                    if not same(out, ref[i]):
+                        wrong.append(i)
+        except Exception as e:
+            wrong.append(e)
+
+    threads = [threading.Thread(target=body, args=(i,)) for i in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
