@@ -2,40 +2,17 @@
 // include/qmv.h: argument checks on the host and dispatch to the kernels.
 #include <new>
 
+#include "qmv_span.cuh"
 #include "qmv_step.cuh"
+
+using namespace qmv::span_of;
 
 namespace {
 
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 bool pack_ok(const qmv_w4pack* p) { return p && p->magic == QMV_W4_MAGIC; }
 bool dtype16(int d) { return d == QMV_F16 || d == QMV_BF16; }
 bool dtype_ok(int d) { return d == QMV_F32 || dtype16(d); }
 size_t dsize(int d) { return d == QMV_F32 ? 4 : 2; }
-
-// The bytes that a call reads or writes at one pointer: rows of `width`, `ld` apart.
-struct Span {
-  const void* p;
-  int64_t rows, ld, width;
-};
-Span span(const void* p, int64_t rows, int64_t ld, int64_t cols, size_t size) {
-  return {p, rows, ld * (int64_t)size, cols * (int64_t)size};
-}
-Span flat(const void* p, int64_t n, size_t size) { return span(p, 1, n, n, size); }
-
-// Whether two spans share a byte.  Rows of one stride may lie between each other's
-// (two halves of a wider tensor); ranges that cross with different strides are taken
-// to share one.
-bool meet(const Span& a, const Span& b) {
-  if (!a.p || !b.p) return false;
-  const Span &lo = (uintptr_t)a.p <= (uintptr_t)b.p ? a : b, &hi = &lo == &a ? b : a;
-  const uint64_t d = (uintptr_t)hi.p - (uintptr_t)lo.p;
-  if (d >= (uint64_t)((lo.rows - 1) * lo.ld + lo.width)) return false;
-  if (lo.rows > 1 && hi.rows > 1 && lo.ld != hi.ld) return true;
-  const uint64_t ld = lo.rows > 1 ? lo.ld : hi.rows > 1 ? hi.ld : 1;
-  return d % ld < (uint64_t)lo.width || d % ld + hi.width > ld;
-}
-template <typename... S>
-bool meets(const Span& out, const S&... others) { return (meet(out, others) || ...); }
 
 int done(cudaError_t e) { return e == cudaSuccess ? QMV_OK : qmv::record_cuda_error(e); }
 

@@ -28,6 +28,8 @@
 //   * Every mbarrier wait is bounded; on timeout the kernel records an error
 //     code in the device error word, stops issuing, lets its own copies land
 //     and returns.
+#include <initializer_list>
+
 #include "qmv_pipe.cuh"
 
 namespace qmv {
@@ -538,6 +540,8 @@ int read_chain_error(int clear, int* out);
 int read_mt_error(int clear, int* out);
 int read_w4_error(int clear, int* out);
 int read_sample_error(int clear, int* out);
+int read_experts_error(int clear, int* out);
+int read_draw_error(int clear, int* out);
 
 int read_device_error(int clear, int* out) {
   int t = 0, ch = 0, mt = 0, w4 = 0;
@@ -550,9 +554,11 @@ int read_device_error(int clear, int* out) {
   const int e4 = read_w4_error(clear, &w4);
   if (e4 != 0) return e4;
   if (w4) t = w4;
-  const int es = read_sample_error(clear, &w4);
-  if (es != 0) return es;
-  if (w4) t = w4;
+  for (const auto read : {read_sample_error, read_experts_error, read_draw_error}) {
+    const int es = read(clear, &w4);
+    if (es != 0) return es;
+    if (w4) t = w4;
+  }
   if (mt) t = mt;
   if (ch) t = ch;
   int v = 0;

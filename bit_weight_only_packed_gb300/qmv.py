@@ -28,10 +28,15 @@ QMV_ERR_TIMEOUT = -6
 QMV_ERR_WORKSPACE = -7
 QMV_F32, QMV_F16, QMV_BF16 = 0, 1, 2
 QMV_FAST, QMV_EXACT = 0, 1
+QMV_ROPE_HALF, QMV_ROPE_INTERLEAVED = 0, 1
+QMV_SCALE_NONE, QMV_SCALE_LINEAR, QMV_SCALE_NTK, QMV_SCALE_YARN = 0, 1, 2, 3
+QMV_SCORE_SOFTMAX, QMV_SCORE_SIGMOID = 0, 1
+QMV_ACT_NONE, QMV_ACT_SILU, QMV_ACT_GELU = 0, 1, 2
 QMV_PACK_HEADER_BYTES, QMV_PACK_VERSION = 64, 1
 
 # every entry point declared in include/qmv.h, with its ctypes signature
 _P, _I, _F, _SZP = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.POINTER(ctypes.c_size_t)
+_D = ctypes.c_double
 SIGNATURES = {
     "qmv_create_pack": (_I, [ctypes.POINTER(_P), _I, _I, _I, _I, _SZP, _SZP]),
     "qmv_pack_weights": (_I, [_P, _P, _P, _P, _P, _P]),
@@ -73,6 +78,13 @@ SIGNATURES = {
                             _P]),
     "qmv_softmax": (_I, [_I, _I, _P, _I, _I, _P, _F, _P, _I, _P]),
     "qmv_verify_draft": (_I, [_I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "qmv_rope_inv_freq": (_I, [_I, _D, _I, _D, _D, _D, _D, _P, _P]),
+    "qmv_rope_turns": (_I, [_I, _P, _P]),
+    "qmv_qk_norm_rope": (_I, [_I, _I, _I, _I, _P, _I, _I, _P, _P, _I, _I, _F, _P, _P, _F, _F, _P, _I, _P, _I, _I, _P]),
+    "qmv_route": (_I, [_I, _I, _I, _P, _I, _I, _I, _P, _I, _I, _I, _I, _F, _P, _P, _P]),
+    "qmv_w4_experts_workspace_bytes": (ctypes.c_size_t, [_P, _I, _I, _I]),
+    "qmv_w4_experts": (_I, [_P, _I, _I, _I, _P, _P, _P, _I, _I, _I, _I, _P, _I, _I, _P, ctypes.c_size_t, _P]),
+    "qmv_sample": (_I, [_I, _I, _P, _I, _I, _P, _F, _P, _I, _P, _F, _P, _F, _P, _P, _P]),
 }
 
 
@@ -809,3 +821,224 @@ def qmv_verify_draft(target, draft_probs, draft, u_accept, u_sample, n_draft=Non
     if rc:
         _check("qmv_verify_draft", rc)
     return tokens, n_accepted
+
+
+# ------------------------------------------------------- decode-step calls --
+# What a decode step does around its matvecs; tensors as for the calls above.
+
+def _matrix(name, t):
+    """(rows, columns) of a [rows, columns] tensor; [columns] is one row."""
+    if t.dim() == 2:
+        return t.shape
+    if t.dim() == 1:
+        return 1, t.shape[0]
+    raise ValueError(f"{name}: expected a [rows, columns] tensor, got {tuple(t.shape)}")
+
+
+def _heads(name, t, dt, M, n, D):
+    """Row stride of a [M, n, D] or [M, n * D] tensor."""
+    if t.dim() == 3:
+        if t.shape != (M, n, D):
+            raise ValueError(f"{name}: expected [{M}, {n}, {D}], got {tuple(t.shape)}")
+        if D > 1 and t.stride(2) != 1 or n > 1 and t.stride(1) != D:
+            raise ValueError(f"{name}: the heads of a row must be contiguous")
+        t = t.as_strided((M, n * D), (t.stride(0), 1))
+    return _rows(name, t, (dt,), M, n * D)
+
+
+class Rope:
+    """The frequencies of a position rotation over the first `rot` elements of a head, and
+    their turns on the device.  inv_freq: frequencies of one's own (rot / 2 numbers,
+    radians a position) in place of base and scaling; amplitude: what turned elements are
+    multiplied by (by default what the scaling has)."""
+
+    def __init__(self, rot: int, base: float = 10000.0, layout=QMV_ROPE_HALF, scaling=QMV_SCALE_NONE, factor: float = 1.0,
+                 original_length: float = 8192.0, beta_fast: float = 32.0, beta_slow: float = 1.0, inv_freq=None,
+                 amplitude=None, device=None):
+        if layout not in (QMV_ROPE_HALF, QMV_ROPE_INTERLEAVED):
+            raise ValueError(f"layout: unknown value {layout!r}")
+        if rot < 2 or rot > 1024 or rot % 2:
+            raise ValueError(f"rot: expected an even number from 2 to 1024, got {rot}")
+        n, amp = rot // 2, ctypes.c_float(1.0)
+        w, turns = (ctypes.c_double * n)(), (ctypes.c_int64 * n)()
+        if inv_freq is None:
+            _check("qmv_rope_inv_freq", _lib.qmv_rope_inv_freq(rot, base, scaling, factor, original_length, beta_fast,
+                                                               beta_slow, w, ctypes.byref(amp)))
+        else:
+            given = [float(v) for v in inv_freq]
+            if len(given) != n:
+                raise ValueError(f"inv_freq: needs {n} numbers, has {len(given)}")
+            w[:] = given
+        _check("qmv_rope_turns", _lib.qmv_rope_turns(n, w, turns))
+        self.rot, self.layout = rot, layout
+        self.inv_freq = list(w)
+        self.amplitude = amp.value if amplitude is None else float(amplitude)
+        self.turns = torch.tensor(list(turns), dtype=torch.int64, device=device or "cuda")
+
+
+def qmv_qk_norm_rope(qkv, n_q, n_k, head_dim, rope=None, positions=None, gamma_q=None, gamma_k=None, gamma_offset=0.0,
+                     eps=1e-6, y_dtype=None, q=None, k=None, stream=None):
+    """(q [M, n_q, D], k [M, n_k, D]): the query and key heads at the front of each row of qkv
+    [M, ..], normed where their gamma [D] is given and turned by a Rope at int32
+    positions [M] (rope None: not turned).  y_dtype QMV_F16 or QMV_BF16, by default that
+    of q, k, qkv or a gamma, else QMV_F16; q and k may be views of qkv itself.  None for no heads."""
+    M, C = _matrix("qkv", qkv)
+    D = head_dim
+    if n_q < 0 or n_k < 0 or D < 1 or C < (n_q + n_k) * D:
+        raise ValueError(f"qkv: {tuple(qkv.shape)} does not hold {n_q} + {n_k} heads of {D}")
+    if y_dtype is None:
+        given = [t.dtype for t in (q, k, qkv, gamma_q, gamma_k) if t is not None and t.dtype in _16BIT]
+        dt = given[0] if given else torch.float16
+    else:
+        dt = _TORCH.get(y_dtype)
+        if dt not in _16BIT:
+            raise ValueError(f"y_dtype: expected QMV_F16 or QMV_BF16, got {y_dtype!r}")
+    ld = _rows("qkv", qkv, _FLOAT, M, C)
+    if (rope is None) != (positions is None):
+        raise ValueError("positions: given exactly when there is a rope")
+    turns = None
+    if rope is not None:
+        turns = rope.turns
+        _vec("positions", positions, torch.int32, M)
+        if rope.rot > D:
+            raise ValueError(f"rope: turns {rope.rot} elements of heads of {D}")
+    for name, t in (("gamma_q", gamma_q), ("gamma_k", gamma_k)):
+        if t is not None:
+            _vec(name, t, dt, D)
+    for name, t, n in (("q", q, n_q), ("k", k, n_k)):
+        if t is not None and n == 0:
+            raise ValueError(f"{name}: there are no such heads")
+    ldq = n_q * D if q is None else _heads("q", q, dt, M, n_q, D)
+    ldk = n_k * D if k is None else _heads("k", k, dt, M, n_k, D)
+    st = _place(stream, qkv, positions, turns, gamma_q, gamma_k, q, k)
+    if q is None and n_q:
+        q = _fresh((M, n_q, D), dt, qkv.device, stream)
+    if k is None and n_k:
+        k = _fresh((M, n_k, D), dt, qkv.device, stream)
+    ptr = lambda t: None if t is None else t.data_ptr()
+    rot, layout, amp = (0, QMV_ROPE_HALF, 1.0) if rope is None else (rope.rot, rope.layout, rope.amplitude)
+    rc = _lib.qmv_qk_norm_rope(M, n_q, n_k, D, qkv.data_ptr(), ld, _DTYPE[qkv.dtype], ptr(positions), ptr(turns), rot, layout,
+                               amp, ptr(gamma_q), ptr(gamma_k), gamma_offset, eps, ptr(q), ldq, ptr(k), ldk, _DTYPE[dt], st)
+    if rc:
+        _check("qmv_qk_norm_rope", rc)
+    return q, k
+
+
+def qmv_route(logits, top_k, score=QMV_SCORE_SOFTMAX, bias=None, groups=1, group_k=1, group_top=1, renormalise=True,
+              scale=1.0, ids=None, weights=None, stream=None):
+    """(ids int32 [M, top_k], weights fp32 [M, top_k]): the experts of each token and their
+    weights, from router logits [M, E]; bias fp32 [E] counts for the choice alone."""
+    M, E = _matrix("logits", logits)
+    ldl = _rows("logits", logits, _FLOAT, M, E)
+    if bias is not None:
+        _vec("bias", bias, torch.float32, E)
+    if ids is not None:
+        _vec("ids", ids, torch.int32, M * top_k)
+    if weights is not None:
+        _vec("weights", weights, torch.float32, M * top_k)
+    st = _place(stream, logits, bias, ids, weights)
+    if ids is None:
+        ids = _fresh((M, max(top_k, 0)), torch.int32, logits.device, stream)
+    if weights is None:
+        weights = _fresh((M, max(top_k, 0)), torch.float32, logits.device, stream)
+    rc = _lib.qmv_route(M, E, top_k, logits.data_ptr(), ldl, _DTYPE[logits.dtype], score,
+                        None if bias is None else bias.data_ptr(), groups, group_k, group_top, 1 if renormalise else 0, scale,
+                        ids.data_ptr(), weights.data_ptr(), st)
+    if rc:
+        _check("qmv_route", rc)
+    return ids, weights
+
+
+def qmv_w4_experts_workspace_bytes(p: W4Pack, rows_per_expert: int, M: int, T: int) -> int:
+    """Device scratch bytes that qmv_w4_experts needs for up to M tokens of T experts (0 for none)."""
+    return int(_lib.qmv_w4_experts_workspace_bytes(p.handle, rows_per_expert, M, T))
+
+
+def qmv_w4_experts_workspace(p: W4Pack, rows_per_expert: int, M: int, T: int, device=None):
+    """A workspace tensor for such calls (None when they need none)."""
+    n = qmv_w4_experts_workspace_bytes(p, rows_per_expert, M, T)
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda") if n else None
+
+
+def qmv_w4_experts(p: W4Pack, rows_per_expert, ids, x, weights=None, act=QMV_ACT_NONE, y=None, y_dtype=QMV_F32,
+                   workspace=None, stream=None):
+    """Products of the experts ids int32 [M, T] with x: y [M, T, R], or summed by weights fp32
+    [M, T] y [M, R].  x is [M, K], or [M, T, K] for a row a pair; with act its rows
+    are gate and up, 2 K wide."""
+    if ids.dim() != 2:
+        raise ValueError(f"ids: expected [tokens, experts], got {tuple(ids.shape)}")
+    M, T = ids.shape
+    R, K = rows_per_expert, p.K
+    _vec("ids", ids, torch.int32, M * T)
+    if weights is not None:
+        _vec("weights", weights, torch.float32, M * T)
+    if p.packed is None:
+        raise ValueError("the pack holds no weights yet")
+    width = K if act == QMV_ACT_NONE else 2 * K
+    per_pair = x.dim() == 3
+    if per_pair:
+        ldx = _heads_rows("x", x, _16BIT, M, T, width)
+    else:
+        ldx = _rows("x", x, _16BIT, M, width)
+    ydt = _TORCH.get(y_dtype)
+    if ydt is None:
+        raise ValueError(f"y_dtype: unknown value {y_dtype!r}")
+    ldy = R
+    if y is not None:
+        ldy = _rows("y", y, (ydt,), M, R) if weights is not None else _heads_rows("y", y, (ydt,), M, T, R)
+    n = qmv_w4_experts_workspace_bytes(p, R, M, T)
+    if workspace is not None:
+        _need_bytes("workspace", workspace, n)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace: expected a contiguous tensor")
+    st = _place(stream, x, p.packed, ids, weights, y, workspace)
+    if y is None:
+        y = _fresh((M, T, R) if weights is None else (M, R), ydt, x.device, stream)
+    if workspace is None and n:
+        workspace = _fresh((n,), torch.uint8, x.device, stream)
+    rc = _lib.qmv_w4_experts(p.handle, R, M, T, ids.data_ptr(), None if weights is None else weights.data_ptr(), x.data_ptr(),
+                             ldx, 1 if per_pair else 0, _DTYPE[x.dtype], act, y.data_ptr(), ldy, y_dtype,
+                             None if workspace is None else workspace.data_ptr(),
+                             0 if workspace is None else workspace.numel() * workspace.element_size(), st)
+    if rc:
+        _check("qmv_w4_experts", rc)
+    return y
+
+
+def _heads_rows(name, t, dtypes, M, T, C):
+    """Row stride of a [M, T, C] tensor whose M * T rows are evenly apart."""
+    if t.dim() != 3 or t.shape != (M, T, C):
+        raise ValueError(f"{name}: expected [{M}, {T}, {C}], got {tuple(t.shape)}")
+    step = t.stride(1) if T > 1 else t.stride(0) if M > 1 else C
+    if M > 1 and T > 1 and t.stride(0) != T * step or C > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: rows must be contiguous and evenly apart")
+    return _rows(name, t.as_strided((M * T, C), (step, 1)), dtypes, M * T, C)
+
+
+def qmv_sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tokens=None, stream=None):
+    """int32 tokens [rows]: one a row of logits [rows, V], from random numbers u fp32 [rows]
+    in [0, 1).  The settings are numbers, or device tensors [rows] (top_k int32, the
+    others fp32); top_k 0, top_p 1 and min_p 0 cut nothing off, temperature 0 takes the largest."""
+    rows, V = _matrix("logits", logits)
+    ldl = _rows("logits", logits, _FLOAT, rows, V)
+    _vec("u", u, torch.float32, rows)
+    at, num = [], []
+    for name, v, dtype in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
+                           ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
+        if torch.is_tensor(v):
+            _vec(name, v, dtype, rows)
+            at.append(v.data_ptr())
+            num.append(0)
+        else:
+            at.append(None)
+            num.append(v)
+    if tokens is not None:
+        _vec("tokens", tokens, torch.int32, rows)
+    st = _place(stream, logits, u, *(v for v in (temperature, top_k, top_p, min_p) if torch.is_tensor(v)), tokens)
+    if tokens is None:
+        tokens = _fresh((rows,), torch.int32, logits.device, stream)
+    rc = _lib.qmv_sample(rows, V, logits.data_ptr(), ldl, _DTYPE[logits.dtype], at[0], float(num[0]), at[1], int(num[1]), at[2],
+                         float(num[2]), at[3], float(num[3]), u.data_ptr(), tokens.data_ptr(), st)
+    if rc:
+        _check("qmv_sample", rc)
+    return tokens

@@ -89,8 +89,9 @@ typedef enum {
     QMV_ERR_WORKSPACE = -7      /* the call needs a larger workspace (qmv_workspace_bytes) */
 } qmv_status;
 
-/* element types; QMV_BF16 is taken by the verification-step calls only (the
- * qmv_w4_*, qmv_block_norm, qmv_softmax and qmv_verify_draft entry points) */
+/* element types; QMV_BF16 is taken by the verification-step calls (the
+ * qmv_w4_*, qmv_block_norm, qmv_softmax and qmv_verify_draft entry points) and the
+ * decode-step calls after them */
 typedef enum { QMV_F32 = 0, QMV_F16 = 1, QMV_BF16 = 2 } qmv_dtype;
 typedef enum { QMV_FAST = 0, QMV_EXACT = 1 } qmv_mode;    /* accumulation mode */
 
@@ -575,6 +576,160 @@ QMV_API int qmv_softmax(int rows, int V, const void *logits, int ldl, int dtype,
 QMV_API int qmv_verify_draft(int B, int S, int V, const float *target, const float *draft_probs,
                              const int *draft, const int *n_draft, const float *u_accept,
                              const float *u_sample, int *tokens, int *n_accepted, void *stream);
+
+/*
+ * What a decode step does around its matvecs: the heads of the fused q/k/v matvec are
+ * normed and rotated, tokens are routed to experts and multiplied with their weights,
+ * and the next token is drawn from the logits.  As the verification-step calls above,
+ * these take row strides, fp16 and bf16, and pointers aligned to their element, refuse
+ * an output that shares memory with an input or another output but where a call allows
+ * it (INVALID_ARG), keep no device state, and may overlap on several streams.
+ */
+typedef enum { QMV_ROPE_HALF = 0, QMV_ROPE_INTERLEAVED = 1 } qmv_rope_layout;
+typedef enum { QMV_SCALE_NONE = 0, QMV_SCALE_LINEAR = 1, QMV_SCALE_NTK = 2, QMV_SCALE_YARN = 3 } qmv_rope_scaling;
+typedef enum { QMV_SCORE_SOFTMAX = 0, QMV_SCORE_SIGMOID = 1 } qmv_score;
+typedef enum { QMV_ACT_NONE = 0, QMV_ACT_SILU = 1, QMV_ACT_GELU = 2 } qmv_act;
+
+/*
+ * qmv_rope_inv_freq -- the angle a position of each of rot / 2 pairs, in radians:
+ *   QMV_SCALE_NONE    w_i = base^(-2 i / rot)
+ *   QMV_SCALE_LINEAR  w_i / factor
+ *   QMV_SCALE_NTK     w_i of the base base * factor^(rot / (rot - 2))
+ *   QMV_SCALE_YARN    w_i / factor * r_i + w_i * (1 - r_i), with the ramp r_i = (i - lo) / (hi - lo)
+ *                     kept in 0..1 between lo, the pair that turns beta_fast times in
+ *                     original_length positions (rounded down), and hi, the one that turns
+ *                     beta_slow times (rounded up); *amplitude = 0.1 ln(factor) + 1 for
+ *                     factor > 1.
+ *   rot        even, 2 .. 1024 (above 2 for QMV_SCALE_NTK).   base > 1, factor > 0.
+ *   inv_freq   host double [rot / 2];  amplitude (nullable) receives 1 where not stated.
+ * Errors: INVALID_ARG (also original_length or a beta that is not above 0 for YARN),
+ * SHAPE (rot).  Host only.
+ */
+QMV_API int qmv_rope_inv_freq(int rot, double base, int scaling, double factor, double original_length,
+                              double beta_fast, double beta_slow, double *inv_freq, float *amplitude);
+
+/*
+ * qmv_rope_turns -- frequencies as qmv_qk_norm_rope takes them: turns a position, without
+ * the whole ones, in units of 2^-64 (host int64 [n], for the caller to copy to the device).
+ * A position times this, modulo 2^64, is its angle: exact however far the position, up to
+ * the frequency's own 53 bits.  Any finite frequencies will do.
+ * Errors: INVALID_ARG (NULL, n < 1, a frequency that is not finite).  Host only.
+ */
+QMV_API int qmv_rope_turns(int n, const double *inv_freq, int64_t *turns);
+
+/*
+ * qmv_qk_norm_rope -- norms of query and key heads and their position rotation, for M
+ * rows as a fused q/k/v matvec leaves them: n_q query heads of D, then n_k key heads, then
+ * anything (values), which is not read.  For each head
+ *   u = x;  with its gamma: u = x / sqrt(mean(x^2) + eps) * (gamma + gamma_offset);
+ *   pairs (a, b) of the first rot elements become amplitude * (a cos t - b sin t,
+ *   b cos t + a sin t), t = position * frequency; the others stay u.
+ * QMV_ROPE_HALF pairs element i with i + rot / 2, QMV_ROPE_INTERLEAVED 2 i with 2 i + 1.
+ * Steps are fp32 with one rounding to dtype; cosines and sines are within 2^-21.
+ *   qkv        device [M][(n_q + n_k) * D, at least] of x_dtype (QMV_F32, QMV_F16 or QMV_BF16),
+ *              row stride ld.
+ *   positions  device int32 [M] (negative ones turn back); NULL exactly when rot is 0.
+ *   turns      device int64 [rot / 2] from qmv_rope_turns, 8-byte aligned; NULL exactly when rot is 0.
+ *   gamma_q, gamma_k  nullable device [D] of dtype.
+ *   q, k       device [M][n_q * D] and [M][n_k * D] of dtype (QMV_F16 or QMV_BF16), row strides
+ *              ldq, ldk; q is NULL exactly when n_q is 0, k when n_k is 0.  Either may be its
+ *              own place in qkv (same pointer, stride and type).
+ *   M >= 1; n_q, n_k 0 .. 4096, not both 0; D 1 .. 1024; rot even, 0 .. D; eps >= 0.
+ * Errors: INVALID_ARG, SHAPE (a stride below its row, rot), UNSUPPORTED (sizes), ALIGNMENT, CUDA.
+ */
+QMV_API int qmv_qk_norm_rope(int M, int n_q, int n_k, int D, const void *qkv, int ld, int x_dtype,
+                             const int *positions, const int64_t *turns, int rot, int layout,
+                             float amplitude, const void *gamma_q, const void *gamma_k,
+                             float gamma_offset, float eps, void *q, int ldq, void *k, int ldk,
+                             int dtype, void *stream);
+
+/*
+ * qmv_route -- the T experts of each of M tokens and their weights, from router logits:
+ *   s[e] = softmax or sigmoid of the row;  r[e] = s[e] + bias[e] (s[e] without bias);
+ *   with groups > 1 (of E / groups neighbouring experts): a group counts the sum of its
+ *   group_top largest r, and only the experts of the best group_k groups remain;
+ *   ids = the T largest r, the largest first;  weights = s of those, over their sum where
+ *   renormalise is not 0 (0 where that sum is 0), times scale.
+ * Equal ones go to the lowest index.  r is compared as 64-bit arithmetic would have it: where
+ * fp32 cannot tell two apart they are formed again in 64 bits; without bias the
+ * logits themselves are compared.  Weights are fp32, within 2^-20 of themselves.
+ * An expert whose logit or bias is NaN or -inf is never chosen (nor counted in a
+ * group, as -inf); places that are left over hold id -1 and weight 0.  Logits of +inf
+ * share a softmax evenly.
+ *   logits   device [M][E] of dtype (QMV_F32, QMV_F16 or QMV_BF16), row stride ldl.
+ *   bias     nullable device fp32 [E].
+ *   ids      device int32 [M][T], as qmv_w4_experts and (a row at a time) qmv_gemv_gather take them.
+ *   weights  device fp32 [M][T].
+ *   M >= 1; E 1 .. 1024; T 1 .. 64; groups 1 .. 32 divides E; group_k 1 .. groups; group_top 1 or 2;
+ *   T <= group_k * E / groups, group_top <= E / groups.
+ * Errors: INVALID_ARG (also score), SHAPE (counts that do not go together, ldl), UNSUPPORTED
+ * (E, T or groups above their limits), ALIGNMENT, CUDA.
+ */
+QMV_API int qmv_route(int M, int E, int T, const void *logits, int ldl, int dtype, int score,
+                      const float *bias, int groups, int group_k, int group_top, int renormalise,
+                      float scale, int *ids, float *weights, void *stream);
+
+/*
+ * qmv_w4_experts -- products of 4-bit expert weights with the tokens routed to them.  The
+ * pack holds E = N / rows_per_expert experts of R = rows_per_expert rows, stacked; for token m
+ * and its j-th expert e = ids[m][j]
+ *   y[m][j] = W_e . x(m, j)       (weights NULL), or   y[m] = sum_j weights[m][j] * (W_e . x(m, j)),
+ * with x(m, j) row m of x (per_pair 0) or its row m * T + j (per_pair not 0); with act that
+ * row is [2 K], gate then up, and x(m, j) = act(gate) * up, formed in fp32 and rounded to
+ * x_dtype, as an activation of its own would leave it: QMV_ACT_SILU g / (1 + exp(-g)),
+ * QMV_ACT_GELU g / 2 * (1 + tanh(sqrt(2 / pi) * (g + 0.044715 g^3))).
+ * Exact products, fp32 sums in a fixed order, one rounding to y's type; x in bf16 as in
+ * qmv_w4_gemv.  Repeated calls give the same bits.  Infinities and NaN of x act as the
+ * definition has them, in their own row.
+ *   rows_per_expert  divides the pack's N and is a multiple of 32.
+ *   ids      device int32 [M][T]; may come from the kernel just before.  An id outside [0, E)
+ *            has the product 0; but for -1 it sets the device error word (8).
+ *   weights  nullable device fp32 [M][T].
+ *   x        device, M or M * T rows of K (2 K with act) of x_dtype (QMV_F16 or QMV_BF16), row stride ldx.
+ *   y        device [M][T][R], or [M][R] with weights, of y_dtype, row stride ldy (of M * T or M rows of R).
+ *   d_workspace, workspace_bytes  caller scratch, 256-byte aligned, at least
+ *            qmv_w4_experts_workspace_bytes(p, rows_per_expert, M, T) bytes; its contents on entry
+ *            do not matter; calls that share a workspace must not overlap.
+ *   M 1 .. 4096; T 1 .. 64; M * T <= 32768; E <= 1024; K <= 16384.
+ * Errors: INVALID_ARG, SHAPE (rows_per_expert, strides), UNSUPPORTED (sizes), ALIGNMENT, WORKSPACE, CUDA.
+ */
+QMV_API size_t qmv_w4_experts_workspace_bytes(const qmv_w4pack *p, int rows_per_expert, int M, int T);
+QMV_API int qmv_w4_experts(const qmv_w4pack *p, int rows_per_expert, int M, int T, const int *ids,
+                           const float *weights, const void *x, int ldx, int per_pair, int x_dtype,
+                           int act, void *y, int ldy, int y_dtype, void *d_workspace,
+                           size_t workspace_bytes, void *stream);
+
+/*
+ * qmv_sample -- one token a row of logits, from given random numbers.  In a row, with T its
+ * temperature and top its largest logit, the weight of id v is in whole units of 2^-42
+ *   w[v] = floor(2^42 * 2^-z),  z = min((top - x[v]) * c, 64),  c = log2(e) / T,
+ * each step one fp32 operation: with n = z rounded to a whole number (ties to even) and
+ * f = n - z, 2^-z is 2^-n * P(f), P the polynomial with the coefficients 1,
+ * 0.6931471824645996, 0.2402234971523285, 0.055503811687231064, 0.00966636836528778,
+ * 0.0013381302123889327 (from f^0 on) in fused multiply-adds, the highest first: within 2^-21
+ * of 2^f.  Sums of whole numbers do not depend on their order, so a row gives the same token
+ * on every run.  In the order of logits, the largest first, equal ones by id:
+ *   top-k  the first k stay (k = 0: all);
+ *   top-p  of those the fewest first ones stay whose sum is at least floor(P * S / 2^31), S the sum
+ *          of what top-k left, P = floor(2^31 * top_p); the first one in any case (top_p >= 1: all);
+ *   min-p  of those stay the ones with w >= floor(2^42 * min_p) (min_p = 0: all).
+ * The token is the lowest id, among those that stay, whose running sum in the order of ids
+ * is above floor(U * W / 2^31), W the whole sum and U = floor(2^31 * u).
+ * T = 0 gives the row's first maximum.  NaN and -inf are never drawn; a row of nothing else
+ * gives -1.  +inf is drawn evenly among its like.
+ *   logits  device [rows][V] of dtype (QMV_F32, QMV_F16 or QMV_BF16), row stride ldl.
+ *   d_temperature, d_top_k, d_top_p, d_min_p  nullable device [rows] (int32 for top_k, fp32
+ *           otherwise): a row's own setting; NULL takes the number beside it for all.
+ *           Their values act as the nearest allowed ones, NaN as 0 (top_p: as 1).
+ *   u       device fp32 [rows] in [0, 1).
+ *   tokens  device int32 [rows].
+ *   rows >= 1; V 1 .. 2^20; temperature >= 0, top_k >= 0, top_p and min_p 0 .. 1.
+ * Errors: INVALID_ARG, SHAPE (ldl), UNSUPPORTED (V), ALIGNMENT, CUDA.
+ */
+QMV_API int qmv_sample(int rows, int V, const void *logits, int ldl, int dtype,
+                       const float *d_temperature, float temperature, const int *d_top_k, int top_k,
+                       const float *d_top_p, float top_p, const float *d_min_p, float min_p,
+                       const float *u, int *tokens, void *stream);
 
 #ifdef __cplusplus
 }
