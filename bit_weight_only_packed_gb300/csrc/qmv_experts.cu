@@ -1,18 +1,35 @@
-// qmv_experts.cu -- products of 4-bit expert weights with the tokens routed to them
-// (qmv_w4_experts), on the packed layout of qmv_w4.cu.
-#include "qmv_pipe.cuh"
-#include "qmv_token.cuh"
+// qmv_experts.cu -- around the experts' products (qmv_experts.cuh): the pairs of token and expert in
+// the order of experts, x in fp16 with the activation in front of it, and the weighted sum
+// behind them.
+#include "qmv_experts.cuh"
 
 namespace qmv {
+namespace w4 {
+
+extern template cudaError_t run_experts<32>(const ExpertsArgs&, const ExpertsPlan&, cudaStream_t);
+extern template cudaError_t run_experts<64>(const ExpertsArgs&, const ExpertsPlan&, cudaStream_t);
+extern template cudaError_t run_experts<128>(const ExpertsArgs&, const ExpertsPlan&, cudaStream_t);
+extern template cudaError_t read_x_error<32>(int, int*);
+extern template cudaError_t read_x_error<64>(int, int*);
+extern template cudaError_t read_x_error<128>(int, int*);
+
+}  // namespace w4
 
 static __device__ int g_experts_error = 0;
 
 int read_experts_error(int clear, int* out) {
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_experts_error, sizeof(int));
-  if (e == cudaSuccess && clear && *out) {
+  int v[4] = {};
+  cudaError_t (*const read[])(int, int*) = {w4::read_x_error<32>, w4::read_x_error<64>, w4::read_x_error<128>};
+  for (int i = 0; i < 3; ++i) {
+    const cudaError_t e = read[i](clear, &v[i]);
+    if (e != cudaSuccess) return (int)e;
+  }
+  cudaError_t e = cudaMemcpyFromSymbol(&v[3], g_experts_error, sizeof(int));
+  if (e == cudaSuccess && clear && v[3]) {
     const int z = 0;
     e = cudaMemcpyToSymbol(g_experts_error, &z, sizeof(int));
   }
+  *out = v[0] ? v[0] : v[1] ? v[1] : v[2] ? v[2] : v[3];
   return (int)e;
 }
 
@@ -20,78 +37,208 @@ namespace {
 
 using namespace w4;
 
-__device__ __forceinline__ float f16_of(uint32_t bits16, int bf16) {
-  return bf16 ? __uint_as_float(bits16 << 16) : __half2float(__ushort_as_half((unsigned short)bits16));
-}
+constexpr int PREP_NT = 512, PREP_W = PREP_NT / 32;
 
-// act(gate) * up, rounded to x's type.
-__device__ __forceinline__ float gated(float g, float u, int act, int bf16) {
-  float v;
-  if (act == QMV_ACT_SILU) {
-    v = g / (1.0f + expf(-g)) * u;
-  } else {
-    const float t = 0.7978845608028654f * (g + 0.044715f * g * g * g);
-    v = 0.5f * g * (1.0f + tanhf(t)) * u;
+// The pairs in the order of their experts, pairs of one expert as they came, and the tasks.  A warp
+// counts a contiguous part of the pairs in counters of its own, [warp][expert], which then
+// become the places where it puts them.
+__device__ void sort_pairs(const ExpertsArgs& a, int cols, int* head, int* order, Task* tasks, int* counts) {
+  __shared__ int sums[PREP_W], t_sums[PREP_W], totals[2];
+  const int P = a.M * a.T, E1 = a.E + 1, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int i = tid; i < PREP_W * E1; i += PREP_NT) counts[i] = 0;
+  __syncthreads();
+  const int per = cdiv(cdiv(P, PREP_W), 32) * 32, p0 = min(P, warp * per), p1 = min(P, p0 + per);
+  const auto expert_of = [&](int p) {
+    const int e = a.ids[p];
+    return (unsigned)e < (unsigned)a.E ? e : a.E;          // those without one come last
+  };
+  for (int p = p0 + lane; p < p1; p += 32) {
+    const int e = a.ids[p];
+    if (e < -1 || e >= a.E) atomicCAS(&g_experts_error, 0, pipe::ERR_BAD_EXPERT);
+    atomicAdd(&counts[warp * E1 + expert_of(p)], 1);
   }
-  return bf16 ? __bfloat162float(__float2bfloat16_rn(v)) : __half2float(__float2half_rn(v));
-}
-
-// One thread a result row.
-__global__ void __launch_bounds__(128) experts_kernel(ExpertsArgs a) {
-  pdl_begin();
-  const int r = blockIdx.x * 128 + threadIdx.x;
-  if (r >= a.R) return;
-  const int KB = cdiv(a.K, BK), bb = block_bytes(a.group, a.zeros != 0), gpb = BK / a.group;
-  for (int out = blockIdx.y; out < (a.weights ? a.M : a.M * a.T); out += gridDim.y) {
-    float y = 0.0f;
-    const int first = a.weights ? out * a.T : out, last = a.weights ? first + a.T : out + 1;
-    for (int p = first; p < last; ++p) {
-      const int e = a.ids[p];
-      if ((unsigned)e >= (unsigned)a.E) {
-        if (e != -1) atomicCAS(&g_experts_error, 0, pipe::ERR_BAD_EXPERT);
-        continue;
+  __syncthreads();
+  // running sums over the experts, of pairs and of tasks; E1 <= 1025: three experts a thread
+  int n[3], tn[3], all = 0, t_all = 0;
+#pragma unroll
+  for (int j = 0; j < 3; ++j) {
+    const int e = tid * 3 + j;
+    n[j] = 0;
+    if (e < E1)
+      for (int w = 0; w < PREP_W; ++w) n[j] += counts[w * E1 + e];
+    tn[j] = e < a.E ? cdiv(n[j], cols) : 0;
+    all += n[j];
+    t_all += tn[j];
+  }
+  int run = all, t_run = t_all;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(~0u, run, o), tv = __shfl_up_sync(~0u, t_run, o);
+    if (lane >= o) run += v, t_run += tv;
+  }
+  if (lane == 31) sums[warp] = run, t_sums[warp] = t_run;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) run += sums[w], t_run += t_sums[w];
+  run -= all, t_run -= t_all;
+#pragma unroll
+  for (int j = 0; j < 3; ++j) {
+    const int e = tid * 3 + j;
+    if (e < a.E)
+      for (int i = 0; i < tn[j]; ++i) tasks[t_run + i] = Task{e, run + i * cols, min(cols, n[j] - i * cols), 0};
+    if (e == a.E) totals[0] = t_run, totals[1] = run;
+    t_run += tn[j];
+    if (e < E1)
+      for (int w = 0, at = run; w < PREP_W; ++w) {
+        const int c = counts[w * E1 + e];
+        counts[w * E1 + e] = at;
+        at += c;
       }
-      const uint16_t* x = (const uint16_t*)a.x + (int64_t)(a.per_pair ? p : p / a.T) * a.ldx;
-      const int n = e * a.R + r, row = n & 31, half = row >> 4, hi = (row >> 3) & 1;
-      float v = 0.0f, sum = 0.0f, s = 0.0f;
-      int z = 8;
-      for (int k = 0; k < a.K; ++k) {
-        const uint8_t* b = a.packed + ((int64_t)(n >> 5) * KB + (k >> 7)) * bb;
-        if (k % a.group == 0) {
-          v += sum * s;
-          sum = 0.0f;
-          const uint8_t* meta = b + CODE_BYTES;
-          const int at = (k & 127) / a.group * ROWS + meta_slot(row);
-          s = f16_of(reinterpret_cast<const uint16_t*>(meta)[at], a.scale_bf16);
-          if (a.zeros) z = meta[2 * gpb * ROWS + at];
-        }
-        const int j = (k >> 6) & 1, h = (k >> 5) & 1, lane = (row & 7) * 4 + ((k >> 3) & 3);
-        const uint32_t w = reinterpret_cast<const uint32_t*>(b)[((half * 2 + j) * 32 + lane) * 4 + hi * 2 + h];
-        const int shift = shift_of(k & 7), code = (int)(__funnelshift_r(w, w, shift) & 15u);
-        float xv = f16_of(x[k], a.x_bf16);
-        if (a.act != QMV_ACT_NONE) xv = gated(xv, f16_of(x[a.K + k], a.x_bf16), a.act, a.x_bf16);
-        sum = fmaf(xv, (float)(code - z), sum);
-      }
-      v += sum * s;
-      y += a.weights ? a.weights[p] * v : v;
+    run += n[j];
+  }
+  __syncthreads();
+  if (tid == 0) head[0] = totals[0], head[1] = totals[1];
+  for (int b = p0; b < p1; b += 32) {
+    const int p = b + lane, e = p < p1 ? expert_of(p) : -1;
+    const unsigned same = __match_any_sync(~0u, e);
+    const int before = __popc(same & ((1u << lane) - 1));
+    int at = 0;
+    if (p < p1) {
+      at = counts[warp * E1 + e];
+      order[at + before] = p;
     }
-    const int64_t at = (int64_t)out * a.ldy + r;
-    if (a.y_dtype == QMV_F32)
-      ((float*)a.y)[at] = y;
-    else if (a.y_dtype == QMV_F16)
-      ((__half*)a.y)[at] = __float2half_rn(y);
-    else
-      ((__nv_bfloat16*)a.y)[at] = __float2bfloat16_rn(y);
+    __syncwarp();
+    if (p < p1 && before == 0) counts[warp * E1 + e] = at + __popc(same);
+    __syncwarp();
   }
+}
+
+// CTA 0 sorts the pairs; each of the others makes a row of x: the activation, then fp16, for bf16
+// scaled by a power of two that puts the row's largest value at 2^14 (as the 4-bit matvec does).
+__global__ void __launch_bounds__(PREP_NT) prepare_kernel(ExpertsArgs a, int cols, int* head, int* order, Task* tasks,
+                                                          int* exps, uint16_t* xh, int64_t ldxh) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ uint32_t s_top;
+  if (threadIdx.x == 0) s_top = 0;
+  __syncthreads();
+  pdl_begin();
+  if (blockIdx.x == 0) return sort_pairs(a, cols, head, order, tasks, reinterpret_cast<int*>(smem));
+  const int row = blockIdx.x - 1;
+  const uint16_t* x = (const uint16_t*)a.x + (int64_t)row * a.ldx;
+  uint16_t* v = reinterpret_cast<uint16_t*>(smem);
+  uint32_t top = 0;
+  for (int k = threadIdx.x; k < a.K; k += PREP_NT) {
+    uint32_t b = x[k];
+    if (a.act != QMV_ACT_NONE) b = gated_bits(f16_f(b, a.x_bf16), f16_f(x[a.K + k], a.x_bf16), a.act, a.x_bf16);
+    v[k] = (uint16_t)b;
+    top = max(top, b & 0x7fffu);
+  }
+  if (!a.x_bf16) {
+    for (int k = threadIdx.x; k < a.K; k += PREP_NT) xh[row * ldxh + k] = v[k];
+    return;
+  }
+  top = __reduce_max_sync(~0u, top);
+  if ((threadIdx.x & 31) == 0) atomicMax(&s_top, top);
+  __syncthreads();
+  const int e = column_exp(s_top);
+  const float f = pow2_f(e);
+  if (threadIdx.x == 0) exps[row] = e;
+  for (int k = threadIdx.x; k < a.K; k += PREP_NT)
+    xh[row * ldxh + k] = __half_as_ushort(__float2half_rn(__uint_as_float((uint32_t)v[k] << 16) * f));
+}
+
+// y[m] = sum_j weights[m][j] * part[m][j], in the order of j.
+__global__ void __launch_bounds__(128) combine_kernel(ExpertsArgs a, const float* part) {
+  pdl_begin();
+  const int r = (blockIdx.x * 128 + threadIdx.x) * 4;
+  if (r >= a.R) return;
+  for (int m = blockIdx.y; m < a.M; m += gridDim.y) {
+    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int j = 0; j < a.T; ++j) {
+      const int p = m * a.T + j;
+      if ((unsigned)a.ids[p] >= (unsigned)a.E) continue;
+      const float w = a.weights[p];
+      const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)p * a.R + r);
+      y.x = fmaf(w, v.x, y.x), y.y = fmaf(w, v.y, y.y), y.z = fmaf(w, v.z, y.z), y.w = fmaf(w, v.w, y.w);
+    }
+    const int64_t at = (int64_t)m * a.ldy + r;
+    store_y(a.y, at, a.y_dtype, y.x), store_y(a.y, at + 1, a.y_dtype, y.y);
+    store_y(a.y, at + 2, a.y_dtype, y.z), store_y(a.y, at + 3, a.y_dtype, y.w);
+  }
+}
+
+// Where things lie in the workspace.
+struct Places {
+  size_t head, order, tasks, exps, x, part, bytes;
+  Places(int K, int R, int M, int T) {
+    const auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
+    const size_t P = (size_t)M * T;
+    head = 0;
+    order = 256;
+    tasks = order + up(P * 4);
+    exps = tasks + up(P * sizeof(Task));
+    x = exps + up(P * 4);
+    part = x + up(P * K * 2);
+    bytes = part + up(P * R * 4);
+  }
+};
+
+// The shared memory of the products with up to `cols` tokens a task, or false where it does not fit.
+bool lay_out(const ExpertsArgs& a, int cols, ExpertsPlan* P) {
+  const int bb = block_bytes(a.group, a.zeros != 0);
+  const auto up = [](int64_t v) { return (v + 127) & ~(int64_t)127; };
+  P->KB = cdiv(a.K, BK);
+  P->strips = a.R / ROWS;
+  P->cols = cols;
+  P->pitch = P->KB * 256 + 64;
+  P->x_size = (int)up((int64_t)P->pitch * cols);
+  P->xs_size = (int)up((int64_t)P->KB * (BK / a.group) * X_COLS * 4);
+  const int64_t part = (int64_t)X_W * 2 * cols * ROWS * 4;
+  const int64_t left = (int64_t)dev_info().max_smem_optin - 4096 - (2 * P->x_size + 256 + 2 * P->xs_size + part);
+  const int64_t fit = left / ((int64_t)X_W * bb);         // blocks a warp's ring can hold
+  if (left < 0 || fit < 2) return false;
+  P->stage = fit >= 4 ? 2 : 1;
+  P->slots = (int)(fit / P->stage < X_SLOTS ? fit / P->stage : X_SLOTS);
+  P->x_off = (int)up((int64_t)X_W * P->slots * P->stage * bb);
+  P->zero_off = P->x_off + 2 * P->x_size;
+  P->xs_off = P->zero_off + 256;
+  P->part_off = P->xs_off + 2 * P->xs_size;
+  P->smem = P->part_off + (int)part;
+  return true;
 }
 
 }  // namespace
 
-size_t experts_workspace(int K, int group, int R, int M, int T, int E) { return 0; }
+size_t experts_workspace(int K, int R, int M, int T) { return Places(K, R, M, T).bytes; }
 
 cudaError_t launch_experts(const ExpertsArgs& a, cudaStream_t s) {
-  const int outs = a.weights ? a.M : a.M * a.T;
-  return launch_step(experts_kernel, dim3((a.R + 127) / 128, outs < 65535 ? outs : 65535), 128, 0, s, 1, a);
+  ExpertsPlan P;
+  int cols = X_COLS;
+  while (!lay_out(a, cols, &P))
+    if ((cols /= 2) == 0) return cudaErrorInvalidConfiguration;       // not reached: one column of EXPERTS_MAX_K fits
+  const Places at(a.K, a.R, a.M, a.T);
+  uint8_t* ws = (uint8_t*)a.ws;
+  P.head = (int*)(ws + at.head);
+  P.order = (int*)(ws + at.order);
+  P.tasks = (Task*)(ws + at.tasks);
+  P.exps = (int*)(ws + at.exps);
+  P.part = a.weights ? (float*)(ws + at.part) : nullptr;
+  // x as it is where the copies can take it
+  const bool as_is = !a.x_bf16 && a.act == QMV_ACT_NONE && (uintptr_t)a.x % 16 == 0 && a.ldx % 8 == 0;
+  uint16_t* xh = (uint16_t*)(ws + at.x);
+  P.x = as_is ? (const uint16_t*)a.x : xh;
+  P.ldx = as_is ? a.ldx : a.K;
+  const int rows = as_is ? 0 : a.per_pair ? a.M * a.T : a.M;
+  const size_t sort = (size_t)PREP_W * (a.E + 1) * 4, smem = sort > (size_t)a.K * 2 ? sort : (size_t)a.K * 2;
+  static thread_local KernCache c;
+  cudaError_t e = prep_kernel(prepare_kernel, c, PREP_NT, smem, nullptr);
+  if (e == cudaSuccess)
+    e = launch_step(prepare_kernel, dim3(1 + rows), PREP_NT, smem, s, 1, a, cols, (int*)(ws + at.head), (int*)(ws + at.order),
+                    (Task*)(ws + at.tasks), (int*)(ws + at.exps), xh, (int64_t)a.K);
+  if (e != cudaSuccess) return e;
+  e = a.group == 32 ? run_experts<32>(a, P, s) : a.group == 64 ? run_experts<64>(a, P, s) : run_experts<128>(a, P, s);
+  if (e != cudaSuccess || !a.weights) return e;
+  return launch_step(combine_kernel, dim3(cdiv(a.R, 512), a.M), 128, 0, s, 1, a, (const float*)P.part);
 }
 
 }  // namespace qmv

@@ -47,10 +47,11 @@ struct ExpertsArgs {
   void* y;
   int ldy, y_dtype;
   void* ws;
-  int early;                  // the weights may be read before the kernel before has ended
 };
-constexpr int EXPERTS_MAX_K = 16384, EXPERTS_MAX_PAIRS = 32768, EXPERTS_MAX_E = 1024;
-size_t experts_workspace(int K, int group, int R, int M, int T, int E);
+// One column of the longest row fits twice beside the rings; strips of all tasks are counted in int.
+constexpr int EXPERTS_MAX_K = 16384, EXPERTS_MAX_PAIRS = 32768, EXPERTS_MAX_E = 1024, EXPERTS_MAX_R = 1 << 20;
+static_assert((int64_t)EXPERTS_MAX_PAIRS * (EXPERTS_MAX_R / 32) <= (int64_t)1 << 30, "strips");
+size_t experts_workspace(int K, int R, int M, int T);
 cudaError_t launch_experts(const ExpertsArgs& a, cudaStream_t s);
 // The device error word of the experts' products (bounded waits, ids out of range).
 int read_experts_error(int clear, int* out);

@@ -21,7 +21,7 @@ int experts_of(const qmv_w4pack* p, int R) {
 
 bool experts_fit(const qmv_w4pack* p, int E, int M, int T) {
   return M <= 4096 && T <= 64 && (int64_t)M * T <= qmv::EXPERTS_MAX_PAIRS && E <= qmv::EXPERTS_MAX_E &&
-         p->K <= qmv::EXPERTS_MAX_K;
+         p->K <= qmv::EXPERTS_MAX_K && p->N / E <= qmv::EXPERTS_MAX_R;
 }
 
 }  // namespace
@@ -123,7 +123,7 @@ size_t qmv_w4_experts_workspace_bytes(const qmv_w4pack* p, int rows_per_expert, 
   if (!p || p->magic != QMV_W4_MAGIC || M < 1 || T < 1) return 0;
   const int E = experts_of(p, rows_per_expert);
   if (!E || !experts_fit(p, E, M, T)) return 0;
-  return qmv::experts_workspace(p->K, p->group, rows_per_expert, M, T, E);
+  return qmv::experts_workspace(p->K, rows_per_expert, M, T);
 }
 
 int qmv_w4_experts(const qmv_w4pack* p, int rows_per_expert, int M, int T, const int* ids, const float* weights,
@@ -140,14 +140,14 @@ int qmv_w4_experts(const qmv_w4pack* p, int rows_per_expert, int M, int T, const
       (d_workspace && !aligned(d_workspace, 256)))
     return QMV_ERR_ALIGNMENT;
   const int64_t pairs = (int64_t)M * T;
-  const size_t need = qmv::experts_workspace(p->K, p->group, R, M, T, E);
+  const size_t need = qmv::experts_workspace(p->K, R, M, T);
   if (need && (!d_workspace || workspace_bytes < need)) return QMV_ERR_WORKSPACE;
   const Span in = span(x, per_pair ? pairs : M, ldx, width, 2), i = flat(ids, pairs, 4), w = flat(weights, pairs, 4),
              packed = flat(p->d_packed, p->bytes, 1), out = span(y, weights ? M : pairs, ldy, R, dsize(y_dtype)),
              ws = flat(need ? d_workspace : nullptr, need, 1);
   if (meets(out, in, i, w, packed, ws) || meets(ws, in, i, w, packed)) return QMV_ERR_INVALID_ARG;
   qmv::ExpertsArgs a{p->d_packed, p->K, p->scale_bf16, p->group, p->zeros, E, R, M, T, ids, weights, x, ldx, per_pair != 0,
-                     x_dtype == QMV_BF16, act, y, ldy, y_dtype, d_workspace, qmv::pdl_enabled()};
+                     x_dtype == QMV_BF16, act, y, ldy, y_dtype, d_workspace};
   return done(qmv::launch_experts(a, (cudaStream_t)stream));
 }
 

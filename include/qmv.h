@@ -690,7 +690,7 @@ QMV_API int qmv_route(int M, int E, int T, const void *logits, int ldl, int dtyp
  *   d_workspace, workspace_bytes  caller scratch, 256-byte aligned, at least
  *            qmv_w4_experts_workspace_bytes(p, rows_per_expert, M, T) bytes; its contents on entry
  *            do not matter; calls that share a workspace must not overlap.
- *   M 1 .. 4096; T 1 .. 64; M * T <= 32768; E <= 1024; K <= 16384.
+ *   M 1 .. 4096; T 1 .. 64; M * T <= 32768; E <= 1024; K <= 16384; R <= 2^20.
  * Errors: INVALID_ARG, SHAPE (rows_per_expert, strides), UNSUPPORTED (sizes), ALIGNMENT, WORKSPACE, CUDA.
  */
 QMV_API size_t qmv_w4_experts_workspace_bytes(const qmv_w4pack *p, int rows_per_expert, int M, int T);
