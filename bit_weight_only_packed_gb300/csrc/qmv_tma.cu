@@ -541,7 +541,6 @@ int read_mt_error(int clear, int* out);
 int read_w4_error(int clear, int* out);
 int read_sample_error(int clear, int* out);
 int read_experts_error(int clear, int* out);
-int read_draw_error(int clear, int* out);
 
 int read_device_error(int clear, int* out) {
   int t = 0, ch = 0, mt = 0, w4 = 0;
@@ -554,7 +553,7 @@ int read_device_error(int clear, int* out) {
   const int e4 = read_w4_error(clear, &w4);
   if (e4 != 0) return e4;
   if (w4) t = w4;
-  for (const auto read : {read_sample_error, read_experts_error, read_draw_error}) {
+  for (const auto read : {read_sample_error, read_experts_error}) {
     const int es = read(clear, &w4);
     if (es != 0) return es;
     if (w4) t = w4;

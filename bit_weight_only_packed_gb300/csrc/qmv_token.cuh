@@ -72,6 +72,5 @@ struct DrawArgs {
   int* tokens;
 };
 cudaError_t launch_draw(const DrawArgs& a, cudaStream_t s);
-int read_draw_error(int clear, int* out);
 
 }  // namespace qmv

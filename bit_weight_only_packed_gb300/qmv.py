@@ -518,7 +518,7 @@ class _NoHost:
     def leave(*args):
         return None
 
-    w4_gemv = block_norm = softmax = verify_draft = leave
+    w4_gemv = block_norm = softmax = verify_draft = qk_norm_rope = route = w4_experts = sample = leave
 
 
 def _load_host():
@@ -540,7 +540,9 @@ def _load_host():
                       "build it with `python -c 'import __graft_entry__ as g; g.build()'`")
         return _NoHost()
     addr = lambda f: ctypes.cast(f, _P).value
-    mod.init(addr(_lib.qmv_w4_gemv), addr(_lib.qmv_block_norm), addr(_lib.qmv_softmax), addr(_lib.qmv_verify_draft))
+    mod.init(*(addr(f) for f in (_lib.qmv_w4_gemv, _lib.qmv_block_norm, _lib.qmv_softmax, _lib.qmv_verify_draft,
+                                 _lib.qmv_qk_norm_rope, _lib.qmv_route, _lib.qmv_w4_experts,
+                                 _lib.qmv_w4_experts_workspace_bytes, _lib.qmv_sample)))
     return mod
 
 
@@ -874,6 +876,10 @@ class Rope:
         self.inv_freq = list(w)
         self.amplitude = amp.value if amplitude is None else float(amplitude)
         self.turns = torch.tensor(list(turns), dtype=torch.int64, device=device or "cuda")
+        self._args = (self.turns, rot, layout, self.amplitude)
+
+
+_NO_ROPE = (None, 0, QMV_ROPE_HALF, 1.0)
 
 
 def qmv_qk_norm_rope(qkv, n_q, n_k, head_dim, rope=None, positions=None, gamma_q=None, gamma_k=None, gamma_offset=0.0,
@@ -882,6 +888,11 @@ def qmv_qk_norm_rope(qkv, n_q, n_k, head_dim, rope=None, positions=None, gamma_q
     [M, ..], normed where their gamma [D] is given and turned by a Rope at int32
     positions [M] (rope None: not turned).  y_dtype QMV_F16 or QMV_BF16, by default that
     of q, k, qkv or a gamma, else QMV_F16; q and k may be views of qkv itself.  None for no heads."""
+    if q is None and k is None and stream is None:
+        r = _host.qk_norm_rope(qkv, n_q, n_k, head_dim, *(rope._args if rope is not None else _NO_ROPE), positions, gamma_q,
+                               gamma_k, gamma_offset, eps, y_dtype)
+        if r is not None:
+            return _done("qmv_qk_norm_rope", r)
     M, C = _matrix("qkv", qkv)
     D = head_dim
     if n_q < 0 or n_k < 0 or D < 1 or C < (n_q + n_k) * D:
@@ -896,9 +907,8 @@ def qmv_qk_norm_rope(qkv, n_q, n_k, head_dim, rope=None, positions=None, gamma_q
     ld = _rows("qkv", qkv, _FLOAT, M, C)
     if (rope is None) != (positions is None):
         raise ValueError("positions: given exactly when there is a rope")
-    turns = None
+    turns, rot, layout, amp = _NO_ROPE if rope is None else rope._args
     if rope is not None:
-        turns = rope.turns
         _vec("positions", positions, torch.int32, M)
         if rope.rot > D:
             raise ValueError(f"rope: turns {rope.rot} elements of heads of {D}")
@@ -916,7 +926,6 @@ def qmv_qk_norm_rope(qkv, n_q, n_k, head_dim, rope=None, positions=None, gamma_q
     if k is None and n_k:
         k = _fresh((M, n_k, D), dt, qkv.device, stream)
     ptr = lambda t: None if t is None else t.data_ptr()
-    rot, layout, amp = (0, QMV_ROPE_HALF, 1.0) if rope is None else (rope.rot, rope.layout, rope.amplitude)
     rc = _lib.qmv_qk_norm_rope(M, n_q, n_k, D, qkv.data_ptr(), ld, _DTYPE[qkv.dtype], ptr(positions), ptr(turns), rot, layout,
                                amp, ptr(gamma_q), ptr(gamma_k), gamma_offset, eps, ptr(q), ldq, ptr(k), ldk, _DTYPE[dt], st)
     if rc:
@@ -928,6 +937,10 @@ def qmv_route(logits, top_k, score=QMV_SCORE_SOFTMAX, bias=None, groups=1, group
               scale=1.0, ids=None, weights=None, stream=None):
     """(ids int32 [M, top_k], weights fp32 [M, top_k]): the experts of each token and their
     weights, from router logits [M, E]; bias fp32 [E] counts for the choice alone."""
+    if ids is None and weights is None and stream is None:
+        r = _host.route(logits, top_k, score, bias, groups, group_k, group_top, renormalise, scale)
+        if r is not None:
+            return _done("qmv_route", r)
     M, E = _matrix("logits", logits)
     ldl = _rows("logits", logits, _FLOAT, M, E)
     if bias is not None:
@@ -965,6 +978,10 @@ def qmv_w4_experts(p: W4Pack, rows_per_expert, ids, x, weights=None, act=QMV_ACT
     """Products of the experts ids int32 [M, T] with x: y [M, T, R], or summed by weights fp32
     [M, T] y [M, R].  x is [M, K], or [M, T, K] for a row a pair; with act its rows
     are gate and up, 2 K wide."""
+    if y is None and stream is None:
+        r = _host.w4_experts(p._address, p._dev, p.K, rows_per_expert, ids, x, weights, act, y_dtype, workspace)
+        if r is not None:
+            return _done("qmv_w4_experts", r)
     if ids.dim() != 2:
         raise ValueError(f"ids: expected [tokens, experts], got {tuple(ids.shape)}")
     M, T = ids.shape
@@ -1019,6 +1036,10 @@ def qmv_sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tokens
     """int32 tokens [rows]: one a row of logits [rows, V], from random numbers u fp32 [rows]
     in [0, 1).  The settings are numbers, or device tensors [rows] (top_k int32, the
     others fp32); top_k 0, top_p 1 and min_p 0 cut nothing off, temperature 0 takes the largest."""
+    if tokens is None and stream is None:
+        r = _host.sample(logits, u, temperature, top_k, top_p, min_p)
+        if r is not None:
+            return _done("qmv_sample", r)
     rows, V = _matrix("logits", logits)
     ldl = _rows("logits", logits, _FLOAT, rows, V)
     _vec("u", u, torch.float32, rows)
