@@ -1,7 +1,7 @@
 // qmv_draw.cu -- one token a row of logits, from given random numbers (qmv_sample).
 //
-// A cluster of CTAs takes a row and keeps it in registers, so that HBM is read once; its CTAs
-// tell each other what they know of their parts through their shared memories.  Weights
+// A cluster of CTAs takes a row; they tell each other what they know of their parts through
+// their shared memories.  Weights
 // are whole numbers, so neither the split nor the order of sums shows in the result.  What
 // stays is always the first so many ids of an order (logit, the largest first, then id), so
 // every cut is one place of it, a 64-bit number made of both (`Place`).
@@ -16,6 +16,8 @@
 //          threshold falls into finds the id.
 #include <math_constants.h>
 
+#include <type_traits>
+
 #include "qmv_token.cuh"
 
 namespace qmv {
@@ -28,7 +30,7 @@ constexpr int NT = 512, NW = NT / 32, MAX_C = 16;
 constexpr int SUB_LOG = 8, SH = 23 - SUB_LOG, BINS = 43 << SUB_LOG;      // bins of weights from 2^-42 to 1
 constexpr uint32_t E_MIN = (127u - 42u) << 23;                           // 2^-42, a weight of 1
 constexpr int MAX_CAND = 2048, MAX_FEW = 1024;
-constexpr int PER_BIN = (BINS + NT - 1) / NT;
+constexpr int OCTAVES = 43;
 
 // fp32 as a whole number of the same order; -inf (and NaN), which is never drawn, is 0.
 __device__ __forceinline__ uint32_t ordered(float v) {
@@ -41,9 +43,12 @@ __device__ __forceinline__ float unordered(uint32_t k) {
 }
 __device__ __forceinline__ Place place_of(float x, int id) { return (u64)ordered(x) << 32 | (uint32_t)~id; }
 
-// 2^-z of qmv.h, its weight being floor(2^42 e).
+// z of qmv.h, and e = 2^-z, the weight being floor(2^42 e).
+__device__ __forceinline__ float z_of(float x, float top, float c) {
+  return x == top ? 0.0f : fminf(__fmul_rn(__fsub_rn(top, x), c), 64.0f);
+}
 __device__ __forceinline__ float exp_of(float x, float top, float c) {
-  const float z = x == top ? 0.0f : fminf(__fmul_rn(__fsub_rn(top, x), c), 64.0f);
+  const float z = z_of(x, top, c);
   const float t = z + 12582912.0f, f = (t - 12582912.0f) - z;            // n = z rounded, in t's last bits
   float p = 0.0013381302123889327f;
   p = fmaf(p, f, 0.00966636836528778f);
@@ -88,24 +93,24 @@ __device__ __forceinline__ u64 warp_before(u64 v) {
 __device__ __forceinline__ void st_cluster64(uint32_t a, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
+__device__ __forceinline__ void st_cluster32(uint32_t a, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
 __device__ __forceinline__ u64 ld_cluster64(uint32_t a) {
   u64 v;
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
   return v;
 }
-__device__ __forceinline__ uint4 ld_cluster128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-  return v;
-}
-
 struct Shared {
   u64 red[2][NW];                // sums of warps
   u64 told[2][MAX_C][3];         // what the CTAs of the cluster tell each other
+  u64 octaves[MAX_C][OCTAVES];   // and of the octaves of weights: ids, and sums of their bins
+  uint32_t ends[2 << SUB_LOG];   // the bins of the two octaves that hold a range's ends
+  uint32_t start[NT];            // where buckets begin
   u64 cut;
   uint32_t sub[256];
   uint32_t top, bound, n;
-  int i0, i1, last;
+  int o[2], i[2];                // the octaves, and the bins that end the range
 };
 
 // A CTA's sum of v, in all threads, and what the threads before this one have of it.
@@ -120,46 +125,82 @@ __device__ __forceinline__ u64 block_sum(Shared& S, u64 v, u64* before) {
   return __shfl_sync(~0u, b + p, NW - 1);
 }
 
-// The first n of `list` (up to MAX_CAND) in falling order; n2, a power of two from n on, is filled up with 0.
-__device__ void sort_down(u64* list, int n, int n2) {
-  for (int i = n + threadIdx.x; i < n2; i += NT) list[i] = 0;
-  for (int size = 2; size <= n2; size *= 2)
-    for (int step = size / 2; step; step /= 2) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < n2 / 2; i += NT) {
-        const int a = 2 * i - (i & (step - 1)), b = a + step;
-        const u64 u = list[a], v = list[b];
-        if ((u < v) == ((a & size) == 0)) list[a] = v, list[b] = u;
-      }
+// The least of a CTA's values, in all threads.
+__device__ __forceinline__ uint32_t block_min(Shared& S, uint32_t v) {
+  v = __reduce_min_sync(~0u, v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) S.sub[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return __reduce_min_sync(~0u, S.sub[threadIdx.x % NW]);
+}
+
+// n keys that all differ, up to four a thread, in falling order to `sorted`: into NT buckets by a
+// number that falls as the key rises, within one by comparing all of its keys.  (2048
+// keys: 1.5 us, against 18 us for a sorting network.)
+__device__ __noinline__ void sort_down(Shared& S, const u64 (&key)[4], const float (&number)[4], int n, u64* spread, u64* sorted) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t least = 0x7f800000u, most = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (tid + i * NT < n) least = min(least, __float_as_uint(number[i])), most = max(most, __float_as_uint(number[i]));
+  S.start[tid] = 0;
+  const float from = __uint_as_float(block_min(S, least)), range = __uint_as_float(~block_min(S, ~most)) - from;
+  const float scale = range > 0.0f ? fminf((NT - 1) / range, 1e30f) : 0.0f;
+  int bucket[4], slot[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (tid + i * NT < n) {
+      bucket[i] = min(NT - 1, (int)((number[i] - from) * scale));
+      slot[i] = atomicAdd(&S.start[bucket[i]], 1u);
+    }
+  __syncthreads();
+  const int count = S.start[tid];
+  int run = count;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(~0u, run, o);
+    if (lane >= o) run += t;
+  }
+  if (lane == 31) S.sub[warp] = run;
+  __syncthreads();
+  const int w = lane < warp ? S.sub[lane] : 0;             // at most 16 warps
+  S.start[tid] = run - count + __reduce_add_sync(~0u, w);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (tid + i * NT < n) spread[S.start[bucket[i]] + slot[i]] = key[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (tid + i * NT < n) {
+      const int at = S.start[bucket[i]], end = bucket[i] + 1 < NT ? S.start[bucket[i] + 1] : n;
+      int to = at;
+      for (int j = at; j < end; ++j) to += spread[j] > key[i];
+      sorted[to] = key[i];
     }
   __syncthreads();
 }
 
-// The edges of bin b in whole weights: those in it are at least edge(b) and at most edge(b + 1).
-__device__ __forceinline__ u64 edge(int b) {
-  const int o = b >> SUB_LOG;
-  const u64 v = (u64)((1 << SUB_LOG) + (b & ((1 << SUB_LOG) - 1))) << (42 - SUB_LOG);
-  return o <= 42 ? v >> (42 - o) : v << (o - 42);
-}
-
-// EPT > 0: a thread's part of the row stays in registers, EPT elements in fours that are
-// aligned in memory wherever the row begins; EPT == 0: rows of any length, `fours` a thread, read
-// again for each pass.  In either form a warp has neighbouring ids, 128 at a time.
-template <typename X, int EPT>
+// C CTAs a row, each with an even share: a warp has neighbouring ids, 128 * fours, a thread fours of
+// them, aligned in memory wherever the row begins.  Every pass reads them again, from L2.  (Kept on the
+// streaming multiprocessor, in shared memory or in registers, 128 rows of 262144 need clusters of
+// sixteen with 64 KB a CTA, so that eight rows are worked on at once, and each takes its 14 meetings:
+// 557 us.)
+template <typename X>
 __global__ void __launch_bounds__(NT, 2) draw_kernel(DrawArgs a, int C, int fours) {
   extern __shared__ __align__(16) uint32_t dyn[];
-  uint32_t *hist = dyn, *all_hist = dyn + BINS;
-  u64 *list = reinterpret_cast<u64*>(hist), *cand = list + MAX_CAND;     // once hist has been added up
+  uint32_t* hist = dyn;
+  u64 *list = reinterpret_cast<u64*>(dyn), *cand = list + MAX_CAND;      // once hist has been read
+  static_assert(2 * MAX_CAND * 8 <= BINS * 4, "they fit there");
   __shared__ Shared S;
-  constexpr int R = EPT ? EPT / 4 : 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = blockIdx.x % C, row = blockIdx.x / C, V = a.V;
   if (tid == 0) S.n = 0, S.top = 0;
   __syncthreads();
   if (C > 1) cluster_arrive();
   const X* x = (const X*)a.x + (int64_t)row * a.ldx;
-  const int shift = (int)((uintptr_t)x / sizeof(X) % 4), rows4 = EPT ? R : fours;
-  const int first = ((rank * NW + warp) * rows4) * 128 + lane * 4 - shift;   // the first four's first id
+  const int shift = (int)((uintptr_t)x / sizeof(X) % 4);
+  const int first = ((rank * NW + warp) * fours) * 128 + lane * 4 - shift;   // the first four's first id
   pdl_begin();
   // four ids, -inf where there are none
   const auto fetch = [&](int j, float (&v)[4]) {
@@ -182,24 +223,25 @@ __global__ void __launch_bounds__(NT, 2) draw_kernel(DrawArgs a, int C, int four
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = isnan(v[k]) ? -CUDART_INF_F : v[k];
   };
-  float v[R][4];                 // logits, later 2^-z
-  if (EPT) {
+  // f(j, the four logits) for all of a thread's; AHEAD of them are on their way while one is worked on
+  const auto each = [&](auto ahead, auto f) {
+    constexpr int AHEAD = decltype(ahead)::value;
+    float v[AHEAD][4];
 #pragma unroll
-    for (int j = 0; j < R; ++j) fetch(j, v[j]);
-  }
-  // f(j, the four logits), f(j, the four of v): the same while v holds logits
-  const auto each_logit = [&](auto f) {
-    if (EPT) {
+    for (int q = 0; q < AHEAD; ++q)
+      if (q < fours) fetch(q, v[q]);
+#pragma unroll 1
+    for (int j = 0; j < fours; j += AHEAD) {
 #pragma unroll
-      for (int j = 0; j < R; ++j) f(j, v[j]);
-    } else {
-      for (int j = 0; j < fours; ++j) {
-        float w[4];
-        fetch(j, w);
-        f(j, w);
-      }
+      for (int q = 0; q < AHEAD; ++q)
+        if (j + q < fours) {
+          f(j + q, v[q]);
+          if (j + q + AHEAD < fours) fetch(j + q + AHEAD, v[q]);
+        }
     }
   };
+  constexpr std::integral_constant<int, 4> ahead;
+  constexpr std::integral_constant<int, 1> one_by_one;
   const float t = a.t ? a.t[row] : a.t0, tp = a.p ? a.p[row] : a.p0, mp = a.m ? a.m[row] : a.m0;
   const int k = a.k ? a.k[row] : a.k0;
   const bool greedy = !(t > 0.0f), k_on = k > 0 && k < V, p_on = tp < 1.0f;
@@ -235,10 +277,7 @@ __global__ void __launch_bounds__(NT, 2) draw_kernel(DrawArgs a, int C, int four
   const bool short_row = C == 1 && V <= MAX_CAND;
   bool few = !greedy && (short_row || (k_on && k <= MAX_FEW && per <= 128));
   float most = -CUDART_INF_F;
-  each_logit([&](int, const float(&w)[4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) most = fmaxf(most, w[i]);
-  });
+  each(ahead, [&](int, const float(&w)[4]) { most = fmaxf(fmaxf(most, fmaxf(w[0], w[1])), fmaxf(w[2], w[3])); });
   const uint32_t key = ordered(most), warp_top = __reduce_max_sync(~0u, key);
   if (lane == 0) atomicMax(&S.top, warp_top);
   uint32_t bound = 0;
@@ -275,7 +314,7 @@ __global__ void __launch_bounds__(NT, 2) draw_kernel(DrawArgs a, int C, int four
   const float largest = unordered(top);
   if (greedy) {
     int at = V;
-    each_logit([&](int j, const float(&w)[4]) {
+    each(ahead, [&](int j, const float(&w)[4]) {
 #pragma unroll
       for (int i = 3; i >= 0; --i)
         if (w[i] == largest) at = min(at, first + j * 128 + i);
@@ -291,16 +330,15 @@ __global__ void __launch_bounds__(NT, 2) draw_kernel(DrawArgs a, int C, int four
     return;
   }
 
-  // The CTAs' lists, one after another, to the first CTA's `cand`; they hold n in all.
+  // The CTAs' lists, one after another, to the first CTA's `cand`: a warp a list.
   const auto gather = [&](const u64(*told)[3]) {
-    int at = 0;
-    for (int r = 0; r < C; ++r) {
-      const int m = (int)told[r][2];
-      const uint32_t from = cluster_addr(list, r);
-      for (int i = tid; i < m; i += NT) cand[at + i] = ld_cluster64(from + i * 8);
-      at += m;
+    const int mine = lane < C ? (int)told[lane][2] : 0;
+    const int at = __reduce_add_sync(~0u, lane < warp ? mine : 0), m = __shfl_sync(~0u, mine, warp);
+    if (warp < C) {
+      const uint32_t from = cluster_addr(list, warp);
+      for (int i = lane; i < m; i += 32) cand[at + i] = ld_cluster64(from + i * 8);
     }
-    return at;
+    __syncthreads();
   };
   const auto listed = [&](const u64(*told)[3], bool* fits) {
     int n = 0;
@@ -314,58 +352,71 @@ __global__ void __launch_bounds__(NT, 2) draw_kernel(DrawArgs a, int C, int four
     if (at < MAX_CAND) list[at] = p;
   };
 
-  if (few) {
-    each_logit([&](int j, const float(&w)[4]) {
+  // The candidates that the first CTA has gathered, in falling order: those neighbouring
+  // places 4 * tid .. are in p afterwards, 0 behind the last.
+  Place p[4];
+  float z[4];
+  const auto in_order = [&](int n) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t o = ordered(w[i]);
-        if (o && o >= bound) note((u64)o << 32 | (uint32_t)~(first + j * 128 + i));
-      }
+    for (int i = 0; i < 4; ++i)
+      if (tid + i * NT < n) p[i] = cand[tid + i * NT], z[i] = z_of(unordered((uint32_t)(p[i] >> 32)), largest, c);
+    sort_down(S, p, z, n, list, cand);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = 4 * tid + i < n ? cand[4 * tid + i] : 0;
+  };
+  const auto weight_of = [&](Place p) { return weight(exp_of(unordered((uint32_t)(p >> 32)), largest, c)); };
+
+  if (few) {
+    const float reach = bound ? unordered(bound) : -CUDART_INF_F;
+    each(ahead, [&](int j, const float(&w)[4]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)          // from 2^-43 on nothing weighs anything
+        if (w[i] >= reach && z_of(w[i], largest, c) < 43.0f) note(place_of(w[i], first + j * 128 + i));
     });
     __syncthreads();
     const auto told = tell(0, 0, S.n);
     bool fits;
-    const int n = listed(told, &fits);
+    int n = listed(told, &fits);
     if (fits) {
       if (rank == 0) {
         gather(told);
-        int n2 = 32;
-        while (n2 < n) n2 *= 2;
-        __syncthreads();
-        sort_down(cand, n, n2);
-        // a thread takes four neighbours of the order
+        in_order(n);
         u64 w[4], sum = 0, before;
-        const int k1 = k_on ? min(k, n) : n;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int at = tid * 4 + i;
-          w[i] = at < k1 ? weight(exp_of(unordered((uint32_t)(cand[at] >> 32)), largest, c)) : 0;
+          w[i] = 4 * tid + i < (k_on ? min(k, n) : n) ? weight_of(p[i]) : 0;
           sum += w[i];
         }
-        const u64 need = p_on ? share(block_sum(S, sum, &before), P) : ~0ull;
-        if (!p_on) before = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int at = tid * 4 + i;
-          const u64 p = at < n2 ? cand[at] : 0;
-          if (at < n2)                     // in the order of ids, with what is needed for the weight
-            cand[at] = at < k1 && (before < need || at == 0) && w[i] >= least ? (p << 32 | p >> 32) : 0;
-          before += w[i];
-        }
+        sum = block_sum(S, sum, &before);
+        const u64 need = p_on ? max(share(sum, P), (u64)1) : ~0ull;
+        if (tid == 0) S.n = 0;
         __syncthreads();
-        sort_down(cand, n2, n2);           // ~id falls as the id rises
+        // what stays, by id
         sum = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int at = tid * 4 + i;
-          const u64 p = at < n2 ? cand[at] : 0;
-          w[i] = p ? weight(exp_of(unordered((uint32_t)p), largest, c)) : 0;
-          sum += w[i];
+          const bool in = before < need && w[i] >= max(least, (u64)1);
+          before += w[i];
+          if (in) cand[atomicAdd(&S.n, 1u)] = p[i] << 32 | p[i] >> 32, sum += w[i];
         }
-        const u64 total = block_sum(S, sum, &before), at = share(total, U);
+        sum = block_sum(S, sum, &before);
+        n = S.n;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (tid + i * NT < n) p[i] = cand[tid + i * NT], z[i] = (float)~(uint32_t)(p[i] >> 32);
+        sort_down(S, p, z, n, list, cand);
+        u64 own = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (before <= at && at < before + w[i]) a.tokens[row] = (int)~(uint32_t)(cand[tid * 4 + i] >> 32);
+          p[i] = 4 * tid + i < n ? cand[4 * tid + i] : 0;
+          w[i] = p[i] ? weight_of(p[i] << 32) : 0;
+          own += w[i];
+        }
+        block_sum(S, own, &before);
+        const u64 at = share(sum, U);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (before <= at && at < before + w[i]) a.tokens[row] = (int)~(uint32_t)(p[i] >> 32);
           before += w[i];
         }
       }
@@ -373,301 +424,310 @@ __global__ void __launch_bounds__(NT, 2) draw_kernel(DrawArgs a, int C, int four
       return;
     }
     meet();
-    if (tid == 0) S.n = 0;
   }
 
-  // Weights in place of logits.
-  const bool cutting = k_on || p_on;
-  if (EPT) {
-#pragma unroll
-    for (int j = 0; j < R; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[j][i] = exp_of(v[j][i], largest, c);
-  }
-  const auto each = [&](auto f) {
-    if (EPT) {
-#pragma unroll
-      for (int j = 0; j < R; ++j) f(j, v[j]);
-    } else {
-      for (int j = 0; j < fours; ++j) {
-        float w[4];
-        fetch(j, w);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = exp_of(w[i], largest, c);
-        f(j, w);
-      }
-    }
-  };
-  const auto logit = [&](int id) { return to_f<X>(x[id]); };
-
-  // What stays so far: weights from `sure` on, and those from `maybe` on whose place is `cut` or before.
+  // What stays so far: weights from `sure` on, and of those from `maybe` on the ones whose place is
+  // `cut` or before.
   uint32_t sure = 0, maybe = 0;
   Place cut = 0;
-  const auto stays = [&](float e, int id) {
+  const auto e_of = [&](float x) { return exp_of(x, largest, c); };
+  const auto stays = [&](float e, float x, int id) {
     const uint32_t b = __float_as_uint(e);
-    return b >= sure || (b >= maybe && place_of(logit(id), id) >= cut);
+    return b >= sure || (b >= maybe && place_of(x, id) >= cut);
   };
-  const auto sum_of = [&](u64 least) {
-    u64 sum = 0;
-    each([&](int j, const float(&e)[4]) {
-      uint32_t hi = 0, lo = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (stays(e[i], first + j * 128 + i)) {
-          if (least == 0) {
-            add_weight(e[i], hi, lo);
-          } else {
-            const u64 w = weight(e[i]);
-            sum += w >= least ? w : 0;
-          }
-        }
-      sum += ((u64)hi << 21) + lo;
-    });
-    return sum;
-  };
-
-  if (cutting) {
-    sure = maybe = E_MIN;                  // the others weigh nothing
+  if (k_on || p_on) sure = maybe = E_MIN;  // the others weigh nothing, and may lie outside the row
+  bool summed = false;                     // the sums of the warps are known already
+  for (int stage = 0; stage < 2; ++stage) {
+    // stage 0 counts ids up to k, stage 1 weights up to top_p of what is left
+    if (stage == 0 ? !k_on : !p_on) continue;
     for (int i = tid; i < BINS / 4; i += NT) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
+    if (tid == 0) S.n = 0;
     __syncthreads();
-    u64 sum = 0, before;
-    each([&](int, const float(&e)[4]) {
+    u64 whole = 0, before;
+    each(ahead, [&](int j, const float(&x)[4]) {
       uint32_t hi = 0, lo = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t b = __float_as_uint(e[i]);
-        if (b >= E_MIN) {
-          atomicAdd(&hist[(b - E_MIN) >> SH], 1u);
-          add_weight(e[i], hi, lo);
+        const float e = e_of(x[i]);
+        if (stays(e, x[i], first + j * 128 + i)) {
+          atomicAdd(&hist[(__float_as_uint(e) - E_MIN) >> SH], 1u);
+          if (stage == 1) add_weight(e, hi, lo);
         }
       }
-      sum += ((u64)hi << 21) + lo;
+      whole += ((u64)hi << 21) + lo;
     });
-    sum = block_sum(S, sum, &before);
-    u64 whole = 0;
+    whole = block_sum(S, whole, &before);
+    // each octave's ids, and the sum of their bins' lower edges (256 .. 511), to all CTAs
+    for (int o = warp; o < OCTAVES; o += NW) {
+      const uint4* h = reinterpret_cast<const uint4*>(hist + (o << SUB_LOG)) + lane * 2;
+      const uint4 u = h[0], w = h[1];
+      const uint32_t ids = u.x + u.y + u.z + u.w + w.x + w.y + w.z + w.w, e = (1 << SUB_LOG) + lane * 8;
+      const uint32_t all = __reduce_add_sync(~0u, ids);
+      const uint32_t edges = __reduce_add_sync(~0u, ids * e + u.y + 2 * u.z + 3 * u.w + 4 * w.x + 5 * w.y + 6 * w.z + 7 * w.w);
+      if (lane < C) st_cluster64(cluster_addr(&S.octaves[rank][o], lane), (u64)all << 32 | edges);
+    }
+    const auto told_whole = tell(whole, 0, 0);
+    whole = 0;
+    for (int r = 0; r < C; ++r) whole += told_whole[r][0];
+    u64 need = stage == 0 ? (u64)k : max(share(whole, P), (u64)1);
+    // The bins that may hold the cut.  The sum down to a bin lies between those of the bins' edges, from
+    // the top as from the bottom, the whole sum being known.  Warp 0 looks for the first bin
+    // down to which it may reach `need`, warp 1 for the last one above which it may not have yet:
+    // for their octaves first.
+    struct Bounds {
+      u64 most, least;
+    };
+    const auto bounds = [&](u64 ids, u64 edges, int o) {
+      if (stage == 0) return Bounds{ids, ids};
+      if (o == OCTAVES - 1) return Bounds{ids << 42, ids << 42};         // the largest logits alone
+      if (o < SUB_LOG) return Bounds{ids << (o + 1), 0};
+      return Bounds{(edges + ids) << (o - SUB_LOG), edges << (o - SUB_LOG)};
+    };
+    const bool far = warp == 1;
+    u64 most_all = 0, least_all = 0, most0 = 0, least0 = 0, sum = 0;
+    const auto there = [&](u64 m, u64 l, u64 m1, u64 l1) {               // sums above and down to here
+      return far ? max(l, sum + m > most_all ? sum + m - most_all : 0) < need : min(m1, sum - least_all + l1) >= need;
+    };
+    if (warp < 2) {
+      Bounds v[2];                         // two octaves a lane, the largest weights first
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int o = OCTAVES - 1 - (2 * lane + i);
+        u64 ids = 0, edges = 0;
+        if (o >= 0)
+          for (int r = 0; r < C; ++r) ids += S.octaves[r][o] >> 32, edges += (uint32_t)S.octaves[r][o];
+        v[i] = bounds(ids, edges, max(o, 0));
+      }
+      u64 most = warp_before(v[0].most + v[1].most), least = warp_before(v[0].least + v[1].least);
+      most_all = __shfl_sync(~0u, most + v[0].most + v[1].most, 31);
+      least_all = __shfl_sync(~0u, least + v[0].least + v[1].least, 31);
+      sum = stage == 0 ? most_all : whole;
+      int mine = -1;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const u64 m1 = most + v[i].most, l1 = least + v[i].least;
+        if (2 * lane + i < OCTAVES && (far || mine < 0) && there(most, least, m1, l1)) mine = 2 * lane + i, most0 = most, least0 = least;
+        most = m1, least = l1;
+      }
+      const uint32_t who = __ballot_sync(~0u, mine >= 0);
+      const int from = (far ? 31 - __clz(who) : __ffs(who) - 1) & 31;
+      mine = __shfl_sync(~0u, mine, from);
+      most0 = __shfl_sync(~0u, most0, from), least0 = __shfl_sync(~0u, least0, from);
+      // stage 0: where no more than k weigh anything, all of those stay
+      if (lane == 0) S.o[warp] = stage == 0 && sum <= need ? -1 : OCTAVES - 1 - max(mine, 0);
+    }
+    __syncthreads();
+    const int o0 = S.o[0], o1 = S.o[1];
+    if (o0 < 0) {
+      meet();                              // S.octaves has been read
+      continue;
+    }
     {
-      const auto told = tell(sum, 0, 0);   // and hist is complete in all CTAs
-      for (int r = 0; r < C; ++r) whole += told[r][0];
+      // the bins of those two octaves: C threads a bin add it up, and tell one CTA each
+      const int b = rank * (NT / C) + tid / C, r = tid & (C - 1);
+      static_assert(NT == 2 << SUB_LOG, "a bin a thread of each CTA");
+      const uint32_t* h = hist + ((b >> SUB_LOG ? o1 : o0) << SUB_LOG) + (b & ((1 << SUB_LOG) - 1));
+      uint32_t n = ld_cluster32(cluster_addr(h, r));
+      for (int o = C >> 1; o; o >>= 1) n += __shfl_xor_sync(~0u, n, o);
+      st_cluster32(cluster_addr(&S.ends[b], r), n);
+      meet();
     }
-    // each CTA adds up its share of the bins and tells the others
-    const int q = BINS / 4 / C;            // fours of bins
-    static_assert(BINS / 4 % MAX_C == 0, "shares are whole");
-    for (int i = tid; i < q; i += NT) {
-      uint4 s = make_uint4(0, 0, 0, 0);
-      for (int r = 0; r < C; ++r) {
-        const uint4 o = ld_cluster128(cluster_addr(reinterpret_cast<uint4*>(hist) + rank * q + i, (rank + r) % C));
-        s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w;
+    if (warp < 2) {
+      Bounds v[8];                         // eight bins a lane, the largest weights first
+      const int o = far ? o1 : o0, b = (31 - lane) * 8;
+      u64 m8 = 0, l8 = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const u64 n = S.ends[(warp << SUB_LOG) + b + i];
+        v[i] = bounds(n, n * ((1 << SUB_LOG) + b + i), o);
+        m8 += v[i].most, l8 += v[i].least;
       }
-      for (int r = 0; r < C; ++r) {
-        const uint32_t to = cluster_addr(reinterpret_cast<uint4*>(all_hist) + rank * q + i, (rank + r) % C);
-        asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(s.x), "r"(s.y), "r"(s.z), "r"(s.w) : "memory");
+      u64 most = most0 + warp_before(m8), least = least0 + warp_before(l8);
+      int bin = -1;
+#pragma unroll
+      for (int i = 7; i >= 0; --i) {
+        const u64 m1 = most + v[i].most, l1 = least + v[i].least;
+        if ((far || bin < 0) && there(most, least, m1, l1)) bin = b + i;
+        most = m1, least = l1;
       }
+      const uint32_t hit = __ballot_sync(~0u, bin >= 0);
+      bin = __shfl_sync(~0u, bin, (far ? 31 - __clz(hit) : __ffs(hit) - 1) & 31);
+      if (lane == 0) S.i[warp] = (o << SUB_LOG) + bin;
     }
-    meet();
-    int k0 = 0, k1 = BINS - 1;             // bins, from the largest weights on, in which top-k's cut may lie
-    for (int stage = 0; stage < 2; ++stage) {
-      // stage 0 counts ids up to k, stage 1 weights up to top_p of what is left
-      if (stage == 0 ? !k_on : !p_on) continue;
-      u64 need = (u64)k;
-      if (stage == 1) {
-        if (cut) {
-          u64 b;
-          const u64 s = block_sum(S, sum_of(0), &b);
-          const auto told = tell(s, 0, 0);
-          whole = 0;
-          for (int r = 0; r < C; ++r) whole += told[r][0];
-        }
-        need = max(share(whole, P), (u64)1);
+    __syncthreads();
+    // one more on either side, since the order within 2^-20 of a weight is that of logits alone
+    const int b_hi = min(BINS - 1, S.i[0] + 1), b_lo = max(0, S.i[1] - 1);
+    const uint32_t above = E_MIN + ((uint32_t)(b_hi + 1) << SH), from = E_MIN + ((uint32_t)b_lo << SH);
+    // what lies above them, exactly; those among them go to the list
+    uint32_t count = 0;
+    u64 over = 0;
+    each(ahead, [&](int j, const float(&x)[4]) {
+      uint32_t hi = 0, lo = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float e = e_of(x[i]);
+        const uint32_t b = __float_as_uint(e);
+        const int id = first + j * 128 + i;
+        if (b < from || !stays(e, x[i], id)) continue;
+        if (b < above)
+          note(place_of(x[i], id));
+        else if (stage == 0)
+          ++count;
+        else
+          add_weight(e, hi, lo);
       }
-      // the bins that may hold the cut: the sum up to each lies between `low` and `high`
-      u64 low = 0, high = 0;
-      const auto bin = [&](int i, u64* lo, u64* hi) {
-        const int b = BINS - 1 - i;
-        const u64 n = i < BINS && (!cut || i <= k1) ? all_hist[b] : 0;
-        *hi = stage == 0 ? n : n * (b == 42 << SUB_LOG ? edge(b) : edge(b + 1));
-        *lo = cut && i >= k0 ? 0 : stage == 0 ? n : n * edge(b);
-      };
-#pragma unroll 1
-      for (int i = tid * PER_BIN; i < (tid + 1) * PER_BIN; ++i) {
-        u64 lo, hi;
-        bin(i, &lo, &hi);
-        low += lo, high += hi;
-      }
-      if (tid == 0) S.i0 = BINS - 1, S.i1 = 0, S.n = 0;
-      block_sum(S, low, &low);
-      const u64 most_of_all = block_sum(S, high, &high);
-      if (stage == 0 && most_of_all <= need) continue;       // what weighs anything all stays
-#pragma unroll 1
-      for (int i = tid * PER_BIN; i < min(BINS, (tid + 1) * PER_BIN); ++i) {
-        u64 lo, hi;
-        bin(i, &lo, &hi);
-        high += hi;
-        if (high >= need && high - hi < need) atomicMin(&S.i0, i);
-        if (low < need && hi) atomicMax(&S.i1, i);
-        low += lo;
-      }
-      __syncthreads();
-      // one more on either side, since the order within 2^-20 of a weight is that of logits alone
-      int i0 = max(0, S.i0 - 1), i1 = min(BINS - 1, S.i1 + 1);
-      if (cut) i0 = min(i0, k0), i1 = min(i1, k1);
-      const uint32_t was_maybe = maybe;
-      const Place was_cut = cut;
-      const uint32_t above = E_MIN + ((uint32_t)(BINS - i0) << SH), from = E_MIN + ((uint32_t)(BINS - 1 - i1) << SH);
-      // what lies above them, exactly, and their ids
-      const auto in_band = [&](uint32_t b) { return b < above && b >= from; };
-      u64 over = 0;
-      uint32_t count = 0;
-      each([&](int j, const float(&e)[4]) {
-        uint32_t hi = 0, lo = 0;
+      over += ((u64)hi << 21) + lo;
+    });
+    // f(place) for each of those among them
+    const auto band = [&](auto f) {
+      each(one_by_one, [&](int j, const float(&x)[4]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t b = __float_as_uint(e[i]);
-          if (b >= above) {
-            ++count;
-            add_weight(e[i], hi, lo);
-          } else if (b >= from && b >= was_maybe) {
-            const int id = first + j * 128 + i;
-            const Place p = place_of(logit(id), id);
-            if (p >= was_cut) note(p);
-          }
+          const float e = e_of(x[i]);
+          const uint32_t b = __float_as_uint(e);
+          const int id = first + j * 128 + i;
+          if (b >= from && b < above && stays(e, x[i], id)) f(place_of(x[i], id));
         }
-        over += ((u64)hi << 21) + lo;
       });
-      over = block_sum(S, stage == 0 ? (u64)count : over, &before);
-      const auto told = tell(over, 0, S.n);
-      over = 0;
-      for (int r = 0; r < C; ++r) over += told[r][0];
-      bool fits;
-      const int n = listed(told, &fits);
-      if (fits) {
-        if (rank == 0) {
-          gather(told);
-          int n2 = 32;
-          while (n2 < n) n2 *= 2;
-          if (tid == 0) S.last = 0;
-          __syncthreads();
-          sort_down(cand, n, n2);
-          u64 w[4], s = 0, run;
+    };
+    const u64 warp_over = warp_sum(over);
+    over = block_sum(S, stage == 0 ? (u64)count : over, &before);
+    const auto told = tell(over, 0, S.n);
+    over = 0;
+    for (int r = 0; r < C; ++r) over += told[r][0];
+    bool fits;
+    const int n = listed(told, &fits);
+    if (fits) {
+      if (rank == 0) {
+        gather(told);
+        in_order(n);
+        u64 w[4], own = 0, run;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int at = tid * 4 + i;
-            w[i] = at >= n ? 0 : stage == 0 ? 1 : weight(exp_of(unordered((uint32_t)(cand[at] >> 32)), largest, c));
-            s += w[i];
-          }
-          block_sum(S, s, &run);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int at = tid * 4 + i;
-            if (at < n && over + run < need) atomicMax(&S.last, at);
-            run += w[i];
-          }
-          __syncthreads();
-          if (tid < C) st_cluster64(cluster_addr(&S.cut, tid), cand[S.last]);
+        for (int i = 0; i < 4; ++i) {
+          w[i] = !p[i] ? 0 : stage == 0 ? 1 : weight_of(p[i]);
+          own += w[i];
         }
-        meet();
-      } else {
-        // more than fit, as ties make them: halves of their logits, each time between the
-        // smallest and the largest that are left
-        uint32_t k_lo = ~0u, k_hi = 0;
-        const auto band = [&](auto f) {
-          each([&](int j, const float(&e)[4]) {
+        block_sum(S, own, &run);
+        run += over;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t b = __float_as_uint(e[i]);
-              if (!in_band(b) || b < was_maybe) continue;
-              const int id = first + j * 128 + i;
-              const Place p = place_of(logit(id), id);
-              if (p >= was_cut) f((uint32_t)(p >> 32), e[i], j, i);
-            }
-          });
-        };
-        const auto least_of = [&](uint32_t v) {
-          v = __reduce_min_sync(~0u, v);
-          __syncthreads();
-          if (lane == 0) S.sub[warp] = v;
-          __syncthreads();
-          return __reduce_min_sync(~0u, S.sub[lane % NW]);
-        };
-        const auto agree = [&](u64 sum, uint32_t lo, uint32_t hi, u64* all, uint32_t* all_lo, uint32_t* all_hi) {
-          u64 b;
-          sum = block_sum(S, sum, &b);
-          lo = least_of(lo);
-          hi = ~least_of(~hi);
-          const auto told = tell(sum, lo, hi);
-          *all = 0;
-          *all_lo = ~0u, *all_hi = 0;
-          for (int r = 0; r < C; ++r) {
-            *all += told[r][0];
-            *all_lo = min(*all_lo, (uint32_t)told[r][1]);
-            *all_hi = max(*all_hi, (uint32_t)told[r][2]);
-          }
-        };
-        u64 s;
-        band([&](uint32_t o, float, int, int) { k_lo = min(k_lo, o), k_hi = max(k_hi, o); });
-        agree(0, k_lo, k_hi, &s, &k_lo, &k_hi);
-        while (k_lo < k_hi) {
-          const uint32_t mid = k_lo + (k_hi - k_lo) / 2;
-          u64 up = 0;
-          uint32_t up_lo = ~0u, down_hi = 0;
-          band([&](uint32_t o, float e, int, int) {
-            if (o > mid && o <= k_hi) up += stage == 0 ? 1 : weight(e), up_lo = min(up_lo, o);
-            if (o <= mid && o >= k_lo) down_hi = max(down_hi, o);
-          });
-          agree(up, up_lo, down_hi, &s, &up_lo, &down_hi);
-          if (over + s >= need)
-            k_lo = up_lo;
-          else
-            over += s, k_hi = down_hi;
+        for (int i = 0; i < 4; ++i) {
+          if (run < need && need <= run + w[i])
+            for (int r = 0; r < C; ++r) st_cluster64(cluster_addr(&S.cut, r), p[i]);
+          run += w[i];
         }
-        // equal logits: the first so many by id
-        const u64 one = stage == 0 ? 1 : weight(exp_of(unordered(k_lo), largest, c));
-        u64 wanted = (need - over + one - 1) / one, mine = 0;
-        band([&](uint32_t o, float, int, int) { mine += o == k_lo; });
-        const u64 warp_ties = warp_sum(mine);
-        __syncthreads();
-        if (lane == 0) S.red[1][warp] = warp_ties;
-        const u64 ties = block_sum(S, mine, &before);
-        const auto told = tell(ties, 0, 0);
-        u64 run = 0;
-        for (int r = 0; r < rank; ++r) run += told[r][0];
-        for (int w = 0; w < warp; ++w) run += S.red[1][w];
-        if (run < wanted && wanted <= run + warp_ties) {
-          // the warp with the last of them, 128 ids at a time
-          each([&](int j, const float(&e)[4]) {
-            u64 n = 0;
-            bool tie[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t b = __float_as_uint(e[i]);
-              const int id = first + j * 128 + i;
-              tie[i] = in_band(b) && b >= was_maybe && ordered(logit(id)) == k_lo && place_of(logit(id), id) >= was_cut;
-              n += tie[i];
-            }
-            u64 at = run + warp_before(n);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              at += tie[i];
-              if (tie[i] && at == wanted)
-                for (int r = 0; r < C; ++r) st_cluster64(cluster_addr(&S.cut, r), (u64)k_lo << 32 | (uint32_t)~(first + j * 128 + i));
-            }
-            run += warp_sum(n);
-          });
-        }
-        meet();
       }
-      cut = S.cut;
-      sure = above, maybe = from;
-      k0 = i0, k1 = i1;
-      meet();                              // before anything here is written again
+      meet();
+    } else {
+      // More than fit, as ties make them: halves of their logits, each time between the smallest and
+      // the largest that are left.
+      uint32_t k_lo = ~0u, k_hi = 0;
+      const auto size_of = [&](Place p) { return stage == 0 ? (u64)1 : weight_of(p); };
+      const auto agree = [&](u64 v, uint32_t lo, uint32_t hi, u64* all, uint32_t* all_lo, uint32_t* all_hi) {
+        u64 b;
+        v = block_sum(S, v, &b);
+        lo = block_min(S, lo);
+        hi = ~block_min(S, ~hi);
+        const auto told = tell(v, lo, hi);
+        *all = 0;
+        *all_lo = ~0u, *all_hi = 0;
+        for (int r = 0; r < C; ++r) {
+          *all += told[r][0];
+          *all_lo = min(*all_lo, (uint32_t)told[r][1]);
+          *all_hi = max(*all_hi, (uint32_t)told[r][2]);
+        }
+      };
+      u64 v;
+      band([&](Place p) { k_lo = min(k_lo, (uint32_t)(p >> 32)), k_hi = max(k_hi, (uint32_t)(p >> 32)); });
+      agree(0, k_lo, k_hi, &v, &k_lo, &k_hi);
+      while (k_lo < k_hi) {
+        const uint32_t mid = k_lo + (k_hi - k_lo) / 2;
+        u64 up = 0;
+        uint32_t up_lo = ~0u, down_hi = 0;
+        band([&](Place p) {
+          const uint32_t o = (uint32_t)(p >> 32);
+          if (o > mid && o <= k_hi) up += size_of(p), up_lo = min(up_lo, o);
+          if (o <= mid && o >= k_lo) down_hi = max(down_hi, o);
+        });
+        agree(up, up_lo, down_hi, &v, &up_lo, &down_hi);
+        if (over + v >= need)
+          k_lo = up_lo;
+        else
+          over += v, k_hi = down_hi;
+      }
+      // equal logits: the first so many by id
+      const u64 one = size_of((Place)k_lo << 32), wanted = (need - over + one - 1) / one;
+      u64 mine = 0;
+      band([&](Place p) { mine += p >> 32 == k_lo; });
+      const u64 warp_ties = warp_sum(mine);
+      __syncthreads();
+      if (lane == 0) S.red[1][warp] = warp_ties;
+      const u64 cta = block_sum(S, mine, &before);
+      const auto told = tell(cta, 0, 0);
+      u64 run = 0;
+      for (int r = 0; r < rank; ++r) run += told[r][0];
+      for (int w = 0; w < warp; ++w) run += S.red[1][w];
+      if (run < wanted && wanted <= run + warp_ties) {
+        // the warp with the last of them, 128 ids at a time
+        each(one_by_one, [&](int j, const float(&x)[4]) {
+          u64 n = 0;
+          bool tie[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float e = e_of(x[i]);
+            tie[i] = ordered(x[i]) == k_lo && stays(e, x[i], first + j * 128 + i);
+            n += tie[i];
+          }
+          u64 at = run + warp_before(n);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            at += tie[i];
+            if (tie[i] && at == wanted)
+              for (int r = 0; r < C; ++r) st_cluster64(cluster_addr(&S.cut, r), place_of(unordered(k_lo), first + j * 128 + i));
+          }
+          run += warp_sum(n);
+        });
+      }
+      meet();
     }
+    cut = S.cut;
+    // Sums of warps: what lies above, known already, and what of the list stays; unless min-p takes off more.
+    summed = stage == 1 && fits && least <= weight(__uint_as_float(from));
+    if (summed) {
+      __syncthreads();
+      if (lane == 0) S.red[1][warp] = warp_over;
+      __syncthreads();
+      // the first CTA's own list has been sorted away: it looks through all
+      const u64* of = rank == 0 ? cand : list;
+      const int m = rank == 0 ? n : (int)told[rank][2], id0 = rank * NW * fours * 128 - shift;
+      for (int i = tid; i < m; i += NT) {
+        const int w = ((int)~(uint32_t)of[i] - id0) / (fours * 128);
+        if (of[i] >= cut && w < NW) atomicAdd(&S.red[1][w], weight_of(of[i]));
+      }
+      __syncthreads();
+    }
+    sure = max(sure, above), maybe = from;                 // what top-k has cut off stays so
+    meet();                                // before anything here is written again
   }
 
   // What stays, all of it; then the id at the threshold.
-  const u64 own = sum_of(least), warp_own = warp_sum(own);
-  u64 before;
-  __syncthreads();
-  if (lane == 0) S.red[1][warp] = warp_own;
-  const u64 cta = block_sum(S, own, &before);
+  const auto weight_if = [&](float x, int id) {
+    const float e = e_of(x);
+    const u64 w = stays(e, x, id) ? weight(e) : 0;
+    return w >= least ? w : 0;
+  };
+  if (!summed) {
+    u64 own = 0;
+    each(ahead, [&](int j, const float(&x)[4]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) own += weight_if(x[i], first + j * 128 + i);
+    });
+    own = warp_sum(own);
+    __syncthreads();
+    if (lane == 0) S.red[1][warp] = own;
+    __syncthreads();
+  }
+  const u64 warp_own = S.red[1][warp];
+  u64 cta = warp_sum(lane < NW ? S.red[1][lane] : 0);
   u64 total = 0, run = 0;
   {
     const auto told = tell(cta, 0, 0);
@@ -680,13 +740,12 @@ __global__ void __launch_bounds__(NT, 2) draw_kernel(DrawArgs a, int C, int four
   for (int w = 0; w < warp; ++w) run += S.red[1][w];
   if (run > at || at >= run + warp_own) return;
   bool found = false;
-  each([&](int j, const float(&e)[4]) {
+  each(one_by_one, [&](int j, const float(&x)[4]) {
     if (found) return;
     u64 w[4], n = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      w[i] = stays(e[i], first + j * 128 + i) ? weight(e[i]) : 0;
-      w[i] = w[i] >= least ? w[i] : 0;
+      w[i] = weight_if(x[i], first + j * 128 + i);
       n += w[i];
     }
     const u64 all = warp_sum(n);
@@ -703,32 +762,29 @@ __global__ void __launch_bounds__(NT, 2) draw_kernel(DrawArgs a, int C, int four
   });
 }
 
-template <typename X, int EPT>
+template <typename X>
 cudaError_t run(const DrawArgs& a, int C, int fours, cudaStream_t s) {
   static thread_local KernCache cache;
   static thread_local int allowed = -1;
-  constexpr int SMEM = 2 * BINS * 4;
-  cudaError_t e = prep_kernel(draw_kernel<X, EPT>, cache, NT, SMEM, nullptr);
+  constexpr int SMEM = BINS * 4;
+  cudaError_t e = prep_kernel(draw_kernel<X>, cache, NT, SMEM, nullptr);
   if (e == cudaSuccess && C > 8 && allowed != cache.dev) {  // clusters of 16 are opt-in, a function and device
-    e = cudaFuncSetAttribute(draw_kernel<X, EPT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    e = cudaFuncSetAttribute(draw_kernel<X>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     allowed = cache.dev;
   }
   if (e != cudaSuccess) return e;
-  return launch_step(draw_kernel<X, EPT>, dim3((unsigned)a.rows * C), NT, SMEM, s, C, a, C, fours);
+  return launch_step(draw_kernel<X>, dim3((unsigned)a.rows * C), NT, SMEM, s, C, a, C, fours);
 }
 
-// CTAs a row: as few as hold it, or more where rows are few.
+// CTAs a row: so many that each thread has two fours, but no more than run at once.
 template <typename X>
 cudaError_t typed(const DrawArgs& a, cudaStream_t s) {
-  const int64_t elements = (int64_t)a.V + 3;               // wherever the row begins
-  const int slots = 2 * dev_info().sms;
+  const bool even = (a.rows == 1 || a.ldx % 4 == 0) && (uintptr_t)a.x % (4 * sizeof(X)) == 0;
+  const int elements = a.V + (even ? 0 : 3);               // wherever the row begins
+  const auto fours = [&](int C) { return (elements + C * NT * 4 - 1) / (C * NT * 4); };
   int C = 1;
-  while (C < MAX_C && (int64_t)C * NT * 32 < elements) C *= 2;
-  if ((int64_t)C * NT * 32 < elements) return run<X, 0>(a, C, (int)((elements + (int64_t)C * NT * 4 - 1) / ((int64_t)C * NT * 4)), s);
-  int C8 = C;
-  while (C8 < MAX_C && (int64_t)C8 * NT * 8 < elements) C8 *= 2;
-  if ((int64_t)C8 * NT * 8 >= elements && (int64_t)C8 * a.rows <= slots) return run<X, 8>(a, C8, 2, s);
-  return run<X, 32>(a, C, 8, s);
+  while (C < MAX_C && fours(C) > 2 && (int64_t)C * 2 * a.rows <= 2 * dev_info().sms) C *= 2;
+  return run<X>(a, C, fours(C), s);
 }
 
 }  // namespace
