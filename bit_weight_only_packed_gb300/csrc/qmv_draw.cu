@@ -43,10 +43,9 @@ __device__ __forceinline__ float unordered(uint32_t k) {
 }
 __device__ __forceinline__ Place place_of(float x, int id) { return (u64)ordered(x) << 32 | (uint32_t)~id; }
 
-// z of qmv.h, and e = 2^-z, the weight being floor(2^42 e).
-__device__ __forceinline__ float z_of(float x, float top, float c) {
-  return x == top ? 0.0f : fminf(__fmul_rn(__fsub_rn(top, x), c), 64.0f);
-}
+// z of qmv.h, and e = 2^-z, the weight being floor(2^42 e).  top is finite; NaN and -inf have z = 64,
+// whatever c is, and weigh nothing.
+__device__ __forceinline__ float z_of(float x, float top, float c) { return fminf(__fmul_rn(__fsub_rn(top, x), c), 64.0f); }
 __device__ __forceinline__ float exp_of(float x, float top, float c) {
   const float z = z_of(x, top, c);
   const float t = z + 12582912.0f, f = (t - 12582912.0f) - z;            // n = z rounded, in t's last bits
@@ -58,16 +57,24 @@ __device__ __forceinline__ float exp_of(float x, float top, float c) {
   p = fmaf(p, f, 1.0f);
   return __uint_as_float(__float_as_uint(p) - (__float_as_uint(t) << 23));
 }
-// floor(2^42 e) = hi 2^21 + lo, each cut off by the rounding of a sum with 2^23.
-__device__ __forceinline__ void add_weight(float e, uint32_t& hi, uint32_t& lo) {
-  const float t = __fmaf_rz(e, 2097152.0f, 8388608.0f), r = fmaf(e, 2097152.0f, 8388608.0f - t);
-  hi += __float_as_uint(t) & 0x7fffffu;
-  lo += __float_as_uint(__fmaf_rz(r, 2097152.0f, 8388608.0f)) & 0x7fffffu;
-}
-__device__ __forceinline__ u64 weight(float e) {
+// Sums of weights: floor(2^42 e) = hi 2^21 + lo, each cut off by the rounding of a sum with 2^23, whose
+// other bits come off at the end.
+struct Weights {
   uint32_t hi = 0, lo = 0;
-  add_weight(e, hi, lo);
-  return ((u64)hi << 21) + lo;
+  __device__ __forceinline__ void add(float e) {
+    const float t = __fmaf_rz(e, 2097152.0f, 8388608.0f), r = fmaf(e, 2097152.0f, 8388608.0f - t);
+    hi += __float_as_uint(t);
+    lo += __float_as_uint(__fmaf_rz(r, 2097152.0f, 8388608.0f));
+  }
+  // of so many, at most 1024
+  __device__ __forceinline__ u64 sum(int n) const {
+    return ((u64)(hi - n * 0x4B000000u) << 21) + (lo - n * 0x4B000000u);
+  }
+};
+__device__ __forceinline__ u64 weight(float e) {
+  Weights w;
+  w.add(e);
+  return w.sum(1);
 }
 
 // floor(total * u / 2^31)
@@ -202,6 +209,7 @@ __global__ void __launch_bounds__(NT, 2) draw_kernel(DrawArgs a, int C, int four
   const int shift = (int)((uintptr_t)x / sizeof(X) % 4);
   const int first = ((rank * NW + warp) * fours) * 128 + lane * 4 - shift;   // the first four's first id
   pdl_begin();
+  bool infinite = false;         // +inf is among them: from where that is known, 0 in its place and -inf in all others'
   // four ids, -inf where there are none
   const auto fetch = [&](int j, float (&v)[4]) {
     const int id = first + j * 128;
@@ -220,8 +228,10 @@ __global__ void __launch_bounds__(NT, 2) draw_kernel(DrawArgs a, int C, int four
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] = (unsigned)(id + k) < (unsigned)V ? to_f<X>(x[id + k]) : -CUDART_INF_F;
     }
+    if (infinite) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = isnan(v[k]) ? -CUDART_INF_F : v[k];
+      for (int k = 0; k < 4; ++k) v[k] = v[k] == CUDART_INF_F ? 0.0f : -CUDART_INF_F;
+    }
   };
   // f(j, the four logits) for all of a thread's; AHEAD of them are on their way while one is worked on
   const auto each = [&](auto ahead, auto f) {
@@ -240,7 +250,8 @@ __global__ void __launch_bounds__(NT, 2) draw_kernel(DrawArgs a, int C, int four
         }
     }
   };
-  constexpr std::integral_constant<int, 4> ahead;
+  constexpr std::integral_constant<int, 4> ahead;          // where little is done with them
+  constexpr std::integral_constant<int, 2> two_ahead;
   constexpr std::integral_constant<int, 1> one_by_one;
   const float t = a.t ? a.t[row] : a.t0, tp = a.p ? a.p[row] : a.p0, mp = a.m ? a.m[row] : a.m0;
   const int k = a.k ? a.k[row] : a.k0;
@@ -311,7 +322,7 @@ __global__ void __launch_bounds__(NT, 2) draw_kernel(DrawArgs a, int C, int four
     if (rank == 0 && tid == 0) a.tokens[row] = -1;
     return;
   }
-  const float largest = unordered(top);
+  float largest = unordered(top);
   if (greedy) {
     int at = V;
     each(ahead, [&](int j, const float(&w)[4]) {
@@ -329,6 +340,8 @@ __global__ void __launch_bounds__(NT, 2) draw_kernel(DrawArgs a, int C, int four
     if (rank == 0 && tid == 0) a.tokens[row] = (int)b;
     return;
   }
+
+  if (largest == CUDART_INF_F) infinite = true, largest = 0.0f;
 
   // The CTAs' lists, one after another, to the first CTA's `cand`: a warp a list.
   const auto gather = [&](const u64(*told)[3]) {
@@ -367,7 +380,7 @@ __global__ void __launch_bounds__(NT, 2) draw_kernel(DrawArgs a, int C, int four
   const auto weight_of = [&](Place p) { return weight(exp_of(unordered((uint32_t)(p >> 32)), largest, c)); };
 
   if (few) {
-    const float reach = bound ? unordered(bound) : -CUDART_INF_F;
+    const float reach = infinite ? 0.0f : bound ? unordered(bound) : -CUDART_INF_F;
     each(ahead, [&](int j, const float(&w)[4]) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)          // from 2^-43 on nothing weighs anything
@@ -431,9 +444,18 @@ __global__ void __launch_bounds__(NT, 2) draw_kernel(DrawArgs a, int C, int four
   uint32_t sure = 0, maybe = 0;
   Place cut = 0;
   const auto e_of = [&](float x) { return exp_of(x, largest, c); };
-  const auto stays = [&](float e, float x, int id) {
-    const uint32_t b = __float_as_uint(e);
-    return b >= sure || (b >= maybe && place_of(x, id) >= cut);
+  // e of four neighbours, 0 for those that do not stay
+  const auto left_of = [&](const float(&x)[4], int j, float(&e)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e[i] = e_of(x[i]);
+    if (sure > E_MIN) {                    // else those weigh nothing
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t b = __float_as_uint(e[i]);
+        const int id = first + j * 128 + i;
+        if (b < sure && !(b >= maybe && place_of(x[i], id) >= cut)) e[i] = 0.0f;
+      }
+    }
   };
   if (k_on || p_on) sure = maybe = E_MIN;  // the others weigh nothing, and may lie outside the row
   bool summed = false;                     // the sums of the warps are known already
@@ -444,17 +466,16 @@ __global__ void __launch_bounds__(NT, 2) draw_kernel(DrawArgs a, int C, int four
     if (tid == 0) S.n = 0;
     __syncthreads();
     u64 whole = 0, before;
-    each(ahead, [&](int j, const float(&x)[4]) {
-      uint32_t hi = 0, lo = 0;
+    each(two_ahead, [&](int j, const float(&x)[4]) {
+      float e[4];
+      left_of(x, j, e);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float e = e_of(x[i]);
-        if (stays(e, x[i], first + j * 128 + i)) {
-          atomicAdd(&hist[(__float_as_uint(e) - E_MIN) >> SH], 1u);
-          if (stage == 1) add_weight(e, hi, lo);
-        }
-      }
-      whole += ((u64)hi << 21) + lo;
+      for (int i = 0; i < 4; ++i)
+        if (__float_as_uint(e[i]) >= E_MIN) atomicAdd(&hist[(__float_as_uint(e[i]) - E_MIN) >> SH], 1u);
+      Weights w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w.add(e[i]);
+      whole += w.sum(4);
     });
     whole = block_sum(S, whole, &before);
     // each octave's ids, and the sum of their bins' lower edges (256 .. 511), to all CTAs
@@ -561,32 +582,34 @@ __global__ void __launch_bounds__(NT, 2) draw_kernel(DrawArgs a, int C, int four
     // what lies above them, exactly; those among them go to the list
     uint32_t count = 0;
     u64 over = 0;
-    each(ahead, [&](int j, const float(&x)[4]) {
-      uint32_t hi = 0, lo = 0;
+    each(two_ahead, [&](int j, const float(&x)[4]) {
+      float e[4];
+      left_of(x, j, e);
+      Weights w;
+      uint32_t among = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float e = e_of(x[i]);
-        const uint32_t b = __float_as_uint(e);
-        const int id = first + j * 128 + i;
-        if (b < from || !stays(e, x[i], id)) continue;
-        if (b < above)
-          note(place_of(x[i], id));
-        else if (stage == 0)
-          ++count;
-        else
-          add_weight(e, hi, lo);
+        const uint32_t b = __float_as_uint(e[i]);
+        w.add(b >= above ? e[i] : 0.0f);
+        if (stage == 0) count += b >= above;
+        if (b - from < above - from) among |= 1u << i;
       }
-      over += ((u64)hi << 21) + lo;
+      over += w.sum(4);
+      if (among) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (among >> i & 1) note(place_of(x[i], first + j * 128 + i));
+      }
     });
     // f(place) for each of those among them
     const auto band = [&](auto f) {
       each(one_by_one, [&](int j, const float(&x)[4]) {
+        float e[4];
+        left_of(x, j, e);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float e = e_of(x[i]);
-          const uint32_t b = __float_as_uint(e);
-          const int id = first + j * 128 + i;
-          if (b >= from && b < above && stays(e, x[i], id)) f(place_of(x[i], id));
+          const uint32_t b = __float_as_uint(e[i]);
+          if (b >= from && b < above) f(place_of(x[i], first + j * 128 + i));
         }
       });
     };
@@ -669,12 +692,13 @@ __global__ void __launch_bounds__(NT, 2) draw_kernel(DrawArgs a, int C, int four
       if (run < wanted && wanted <= run + warp_ties) {
         // the warp with the last of them, 128 ids at a time
         each(one_by_one, [&](int j, const float(&x)[4]) {
+          float e[4];
+          left_of(x, j, e);
           u64 n = 0;
           bool tie[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float e = e_of(x[i]);
-            tie[i] = ordered(x[i]) == k_lo && stays(e, x[i], first + j * 128 + i);
+            tie[i] = ordered(x[i]) == k_lo && __float_as_uint(e[i]) >= E_MIN;
             n += tie[i];
           }
           u64 at = run + warp_before(n);
@@ -710,16 +734,17 @@ __global__ void __launch_bounds__(NT, 2) draw_kernel(DrawArgs a, int C, int four
   }
 
   // What stays, all of it; then the id at the threshold.
-  const auto weight_if = [&](float x, int id) {
-    const float e = e_of(x);
-    const u64 w = stays(e, x, id) ? weight(e) : 0;
-    return w >= least ? w : 0;
-  };
+  // (w >= least where 2^42 e is)
+  const float e_least = __double2float_ru((double)least * 0x1p-42);
   if (!summed) {
     u64 own = 0;
-    each(ahead, [&](int j, const float(&x)[4]) {
+    each(two_ahead, [&](int j, const float(&x)[4]) {
+      float e[4];
+      left_of(x, j, e);
+      Weights w;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) own += weight_if(x[i], first + j * 128 + i);
+      for (int i = 0; i < 4; ++i) w.add(e[i] >= e_least ? e[i] : 0.0f);
+      own += w.sum(4);
     });
     own = warp_sum(own);
     __syncthreads();
@@ -742,10 +767,12 @@ __global__ void __launch_bounds__(NT, 2) draw_kernel(DrawArgs a, int C, int four
   bool found = false;
   each(one_by_one, [&](int j, const float(&x)[4]) {
     if (found) return;
+    float e[4];
+    left_of(x, j, e);
     u64 w[4], n = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      w[i] = weight_if(x[i], first + j * 128 + i);
+      w[i] = e[i] >= e_least ? weight(e[i]) : 0;
       n += w[i];
     }
     const u64 all = warp_sum(n);
