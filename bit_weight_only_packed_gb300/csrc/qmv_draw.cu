@@ -210,43 +210,40 @@ __global__ void __launch_bounds__(NT, 2) draw_kernel(DrawArgs a, int C, int four
   const int first = ((rank * NW + warp) * fours) * 128 + lane * 4 - shift;   // the first four's first id
   pdl_begin();
   bool infinite = false;         // +inf is among them: from where that is known, 0 in its place and -inf in all others'
-  // four ids, -inf where there are none
-  const auto fetch = [&](int j, float (&v)[4]) {
-    const int id = first + j * 128;
-    if (id >= 0 && id + 4 <= V) {
-      X h[4];
-      if (sizeof(X) == 4) {
-        const float4 w = *reinterpret_cast<const float4*>(x + id);
-        memcpy(h, &w, sizeof(h));
-      } else {
-        const uint2 w = *reinterpret_cast<const uint2*>(x + id);
-        memcpy(h, &w, sizeof(h));
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = to_f<X>(h[k]);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = (unsigned)(id + k) < (unsigned)V ? to_f<X>(x[id + k]) : -CUDART_INF_F;
-    }
-    if (infinite) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = v[k] == CUDART_INF_F ? 0.0f : -CUDART_INF_F;
-    }
-  };
-  // f(j, the four logits) for all of a thread's; AHEAD of them are on their way while one is worked on
+  typedef typename std::conditional<sizeof(X) == 4, uint4, uint2>::type Raw;
+  // f(j, four logits, -inf where there are none) for all of a thread's fours; AHEAD of them are on their
+  // way, as they are stored, while one is worked on.  Fours that stick out of the row are read an element
+  // at a time when their turn comes.
   const auto each = [&](auto ahead, auto f) {
     constexpr int AHEAD = decltype(ahead)::value;
-    float v[AHEAD][4];
+    const auto whole = [&](int j) { return (unsigned)(first + j * 128) <= (unsigned)(V - 4) && V >= 4 && j < fours; };
+    Raw raw[AHEAD];
 #pragma unroll
-    for (int q = 0; q < AHEAD; ++q)
-      if (q < fours) fetch(q, v[q]);
+    for (int q = 0; q < AHEAD; ++q) {
+      memset(&raw[q], 0, sizeof(Raw));
+      if (whole(q)) raw[q] = *reinterpret_cast<const Raw*>(x + first + q * 128);
+    }
 #pragma unroll 1
     for (int j = 0; j < fours; j += AHEAD) {
 #pragma unroll
       for (int q = 0; q < AHEAD; ++q)
         if (j + q < fours) {
-          f(j + q, v[q]);
-          if (j + q + AHEAD < fours) fetch(j + q + AHEAD, v[q]);
+          const int id = first + (j + q) * 128;
+          float v[4];
+          X h[4];
+          memcpy(h, &raw[q], sizeof(Raw));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = to_f<X>(h[i]);
+          if (whole(j + q + AHEAD)) raw[q] = *reinterpret_cast<const Raw*>(x + id + AHEAD * 128);
+          if (!whole(j + q)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = (unsigned)(id + i) < (unsigned)V ? to_f<X>(x[id + i]) : -CUDART_INF_F;
+          }
+          if (infinite) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = v[i] == CUDART_INF_F ? 0.0f : -CUDART_INF_F;
+          }
+          f(j + q, v);
         }
     }
   };
