@@ -211,40 +211,42 @@ __global__ void __launch_bounds__(NT, 2) draw_kernel(DrawArgs a, int C, int four
   pdl_begin();
   bool infinite = false;         // +inf is among them: from where that is known, 0 in its place and -inf in all others'
   typedef typename std::conditional<sizeof(X) == 4, uint4, uint2>::type Raw;
+  // the first and the last four that lie whole in the row, if any
+  const int low = (4 - shift) & 3, high = V - 4 >= low ? low + (V - 4 - low) / 4 * 4 : -1;
   // f(j, four logits, -inf where there are none) for all of a thread's fours; AHEAD of them are on their
-  // way, as they are stored, while one is worked on.  Fours that stick out of the row are read an element
-  // at a time when their turn comes.
+  // way, as they are stored, while one is worked on.  Each load is made, from a place inside the row: one
+  // under a condition waits for those before it (the largest logits of 128 rows of 262144, a CTA
+  // each: 65 us so, whatever AHEAD is, against 28).  Fours that stick out of the row are read
+  // an element at a time when their turn comes.
   const auto each = [&](auto ahead, auto f) {
     constexpr int AHEAD = decltype(ahead)::value;
-    const auto whole = [&](int j) { return (unsigned)(first + j * 128) <= (unsigned)(V - 4) && V >= 4 && j < fours; };
+    const auto load = [&](int j) { return *reinterpret_cast<const Raw*>(x + min(max(first + j * 128, low), high)); };
     Raw raw[AHEAD];
+    if (high >= 0) {
 #pragma unroll
-    for (int q = 0; q < AHEAD; ++q) {
-      memset(&raw[q], 0, sizeof(Raw));
-      if (whole(q)) raw[q] = *reinterpret_cast<const Raw*>(x + first + q * 128);
+      for (int q = 0; q < AHEAD; ++q) raw[q] = load(q);
     }
 #pragma unroll 1
     for (int j = 0; j < fours; j += AHEAD) {
 #pragma unroll
-      for (int q = 0; q < AHEAD; ++q)
-        if (j + q < fours) {
-          const int id = first + (j + q) * 128;
-          float v[4];
-          X h[4];
-          memcpy(h, &raw[q], sizeof(Raw));
+      for (int q = 0; q < AHEAD; ++q) {
+        const int id = first + (j + q) * 128;
+        float v[4];
+        X h[4];
+        memcpy(h, &raw[q], sizeof(Raw));
+        if (high >= 0) raw[q] = load(j + q + AHEAD);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = to_f<X>(h[i]);
-          if (whole(j + q + AHEAD)) raw[q] = *reinterpret_cast<const Raw*>(x + id + AHEAD * 128);
-          if (!whole(j + q)) {
+        for (int i = 0; i < 4; ++i) v[i] = to_f<X>(h[i]);
+        if (id < low || id > high) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = (unsigned)(id + i) < (unsigned)V ? to_f<X>(x[id + i]) : -CUDART_INF_F;
-          }
-          if (infinite) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = v[i] == CUDART_INF_F ? 0.0f : -CUDART_INF_F;
-          }
-          f(j + q, v);
+          for (int i = 0; i < 4; ++i) v[i] = (unsigned)(id + i) < (unsigned)V ? to_f<X>(x[id + i]) : -CUDART_INF_F;
         }
+        if (infinite) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = v[i] == CUDART_INF_F ? 0.0f : -CUDART_INF_F;
+        }
+        if (j + q < fours) f(j + q, v);
+      }
     }
   };
   constexpr std::integral_constant<int, 4> ahead;          // where little is done with them
