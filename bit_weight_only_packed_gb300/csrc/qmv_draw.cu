@@ -802,14 +802,17 @@ cudaError_t run(const DrawArgs& a, int C, int fours, cudaStream_t s) {
   return launch_step(draw_kernel<X>, dim3((unsigned)a.rows * C), NT, SMEM, s, C, a, C, fours);
 }
 
-// CTAs a row: so many that each thread has two fours, but no more than run at once.
+// CTAs a row: so many that each thread has two fours, but no more than run at once, or twice as many
+// while a thread has more than 16 (128 rows of 262144: 205 us with two CTAs a row, 186 with four, 210 with
+// eight; 32 rows: 75, 60 and 103 with four, eight and sixteen; 512 rows of 32000: 101 and 134 with one and two).
 template <typename X>
 cudaError_t typed(const DrawArgs& a, cudaStream_t s) {
   const bool even = (a.rows == 1 || a.ldx % 4 == 0) && (uintptr_t)a.x % (4 * sizeof(X)) == 0;
   const int elements = a.V + (even ? 0 : 3);               // wherever the row begins
   const auto fours = [&](int C) { return (elements + C * NT * 4 - 1) / (C * NT * 4); };
   int C = 1;
-  while (C < MAX_C && fours(C) > 2 && (int64_t)C * 2 * a.rows <= 2 * dev_info().sms) C *= 2;
+  const int64_t at_once = 2 * dev_info().sms;
+  while (C < MAX_C && (fours(C) > 2 && C * 2 * (int64_t)a.rows <= at_once || fours(C) > 16 && C * (int64_t)a.rows <= at_once)) C *= 2;
   return run<X>(a, C, fours(C), s);
 }
 

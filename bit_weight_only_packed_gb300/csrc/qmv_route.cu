@@ -1,13 +1,19 @@
 // qmv_route.cu -- the experts of each token and their weights (qmv_route).
 //
 // A warp takes a token and its lanes N neighbouring experts each, all in registers.  A group's
-// worth comes through shared memory (any number of groups of any size); the T largest
-// ranks are taken one after another, each with one maximum over the warp.
+// worth comes by exchanges within the warp where its experts are whole lanes', otherwise through shared
+// memory.  The lanes' largest ranks, sorted, give a bound that T + 1 experts reach; the few that
+// reach it, one a lane, are sorted into the answer.  Where T is large, or ties make them more than 32,
+// experts are taken one after another, each with a maximum over the warp.
+//
+// Bound by instructions (16384 tokens of 256 experts: 62 us with a maximum over the warp an expert
+// and conditional loads, 36 with the sort, 43 % of that the tail of tokens ranked again in 64 bits).
 //
 // Ranks are compared as exact arithmetic has them.  Without a bias they follow the
 // logits, which are compared themselves.  Otherwise fp32 ranks decide where neighbours in
-// the order are further apart than their errors add up to; a token where they are not is
-// ranked again in 64 bits (about one in a thousand of 256 experts).
+// the order are further apart than their errors add up to.  Where they are not (about one token in a
+// thousand of 256 experts) the choice of groups, or the order of the few, is formed again in 64
+// bits, or all of it where a softmax needs that.
 #include <math_constants.h>
 
 #include "qmv_token.cuh"
@@ -15,7 +21,15 @@
 namespace qmv {
 namespace {
 
+typedef unsigned long long u64;
 constexpr int WARPS = 4, MAX_E = 1024;
+constexpr int MAX_SORTED = 24;     // picks by sorting: some more than T have to fit in 32
+
+// One of the experts that may be chosen.
+struct alignas(16) Few {
+  float rank, x, b;
+  int e;
+};
 
 // fp32 as a whole number of the same order (NaN does not occur).
 __device__ __forceinline__ uint32_t ordered(float v) {
@@ -24,6 +38,33 @@ __device__ __forceinline__ uint32_t ordered(float v) {
 }
 __device__ __forceinline__ float unordered(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
+// Keys of a warp's first n lanes in falling order, equal ones by `who`; the others' come last.
+template <typename K>
+__device__ __forceinline__ void sort_lanes(K& key, uint32_t& who, int n, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 32; size *= 2) {
+    if (size == 32 && n <= 16) break;                                    // the others are behind those anyway
+#pragma unroll
+    for (int step = size / 2; step; step /= 2) {
+      const K k = __shfl_xor_sync(~0u, key, step);
+      const uint32_t w = __shfl_xor_sync(~0u, who, step);
+      const bool theirs = k > key || (k == key && w < who);              // comes first
+      if ((((lane & size) == 0) == ((lane & step) == 0)) == theirs) key = k, who = w;
+    }
+  }
+}
+// The lanes' values in falling order.
+__device__ __forceinline__ float sort_lanes(float v, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+    for (int step = size / 2; step; step /= 2) {
+      const float o = __shfl_xor_sync(~0u, v, step);
+      v = ((lane & size) == 0) == ((lane & step) == 0) ? fmaxf(v, o) : fminf(v, o);
+    }
+  return v;
 }
 
 __device__ __forceinline__ float warp_max(float v) { return unordered(__reduce_max_sync(~0u, ordered(v))); }
@@ -39,24 +80,42 @@ __device__ __forceinline__ F warp_total(F v) {
   return v;
 }
 
-// What a score may be off by in fp32: a sigmoid by an ulp of its exponential (1 at most) and two
-// roundings; a softmax, relative to itself, by |x - max| 2^-24 (times p: 2^-25 at most), two
-// ulps, the sum of 32 partial sums of up to 32 terms, and two roundings.
-template <typename F>
-__device__ __forceinline__ F score_error(int score) {
-  return sizeof(F) == 8 ? (F)0 : score == QMV_SCORE_SIGMOID ? (F)0x1p-22 : (F)0x1p-19;
+// e^v, v <= 88, and a / b for b from 1 on; in fp32 by the exponential and reciprocal instructions: off
+// by |v| 2^-23 + 2^-22 and 2^-22 of themselves.  (The weights of those that are chosen are formed from
+// their logits again, with expf.)
+__device__ __forceinline__ double exp_of(double v) { return exp(v); }
+__device__ __forceinline__ double over(double a, double b) { return a / b; }
+__device__ __forceinline__ float exp_of(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v * 1.4426950408889634f));
+  return r;
+}
+__device__ __forceinline__ float over(float a, float b) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(b));
+  return a * r;
 }
 
-// Scores of a lane's N experts, exps in F.  x: logits, those that cannot be chosen -inf.
+// What a score may be off by in fp32.  A sigmoid 1 / (1 + e): e's error counts s (1 - s) times, and
+// x s (1 - s) is below 1/4, so 2^-25 + 2^-24; the sum 2^-24, the reciprocal 2^-23, the product 2^-24.  A
+// softmax, relative to itself: (x - max) 2^-22 (times p: below 2^-23), 2^-22, the sum of 32 sums of up
+// to 32 such terms, 2^-22.
+template <typename F>
+__device__ __forceinline__ F score_error(int score) {
+  return sizeof(F) == 8 ? (F)0 : score == QMV_SCORE_SIGMOID ? (F)0x1p-21 : (F)0x1p-18;
+}
+
+template <typename F>
+__device__ __forceinline__ F sigmoid(F x) { return over((F)1, (F)1 + exp_of(-x)); }
+
+// Scores of a lane's N experts.  x: logits, those that cannot be chosen -inf.  Returns the largest logit,
+// and in *whole the sum of exp(x - that) (softmax).
 template <typename F, int N>
-__device__ __forceinline__ void scores(const float (&x)[N], int score, F (&s)[N]) {
+__device__ __forceinline__ float scores(const float (&x)[N], int score, F (&s)[N], F* whole) {
   if (score == QMV_SCORE_SIGMOID) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const F e = exp(-fabs((F)x[i]));
-      s[i] = (x[i] >= 0.0f ? (F)1 : e) / ((F)1 + e);
-    }
-    return;
+    for (int i = 0; i < N; ++i) s[i] = sigmoid((F)x[i]);
+    return 0.0f;
   }
   float top = -CUDART_INF_F;
 #pragma unroll
@@ -65,36 +124,54 @@ __device__ __forceinline__ void scores(const float (&x)[N], int score, F (&s)[N]
   F sum = 0;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
+    // expf in the sum, whose error is all weights'
     s[i] = x[i] == -CUDART_INF_F ? (F)0 : x[i] == top ? (F)1 : exp((F)x[i] - (F)top);
     sum += s[i];
   }
-  sum = warp_total(sum);
+  *whole = sum = warp_total(sum);
 #pragma unroll
-  for (int i = 0; i < N; ++i) s[i] = sum > 0 ? s[i] / sum : (F)0;
+  for (int i = 0; i < N; ++i) s[i] = sum > 0 ? over(s[i], sum) : (F)0;
+  return top;
 }
 
-// The choice of one token with scores in F: lane t % 32 receives pick t (place t / 32) with its
-// score.  Returns whether F could tell all that it had to; rank: a warp's [E] in shared memory.
+__device__ __forceinline__ int group_of(const RouteArgs& a, int e) {
+  return a.per == 1 ? e : (int)__umulhi((uint32_t)e, a.per_inv);
+}
+
+// What choose_groups() knows of lane g's group g, and between which worths fp32 cannot tell.
+template <typename F>
+struct Groups {
+  F worth, reach, low, high;
+  bool sure;
+};
+
+// The groups that remain, a bit each.  r: ranks, or logits without a bias; top: as scores() gives it;
+// rank: a warp's [E] in shared memory.
 template <typename F, int N>
-__device__ __forceinline__ bool choose(const RouteArgs& a, const float (&x)[N], const float (&b)[N], int lane, F* rank,
-                                       int (&id)[2], float (&w)[2]) {
+__device__ __forceinline__ uint32_t choose_groups(const RouteArgs& a, const F (&r)[N], float top, int lane, F* rank, Groups<F>* known) {
   const F none = (F)(-CUDART_INF_F);
-  const int e0 = lane * N;
-  F s[N], r[N];
-  scores<F, N>(x, a.score, s);
-  const F err = score_error<F>(a.score);
-  bool sure = true;
-  uint32_t left = ~0u;                               // one bit a group
-  if (a.groups > 1) {
-    const int per = a.E / a.groups;
+  const int per = a.per, lanes = per / N, e0 = lane * N;
+  F one = none, two = none;                          // lane g: the largest of group g
+  if (per % N == 0 && (lanes & (lanes - 1)) == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      two = fmax(two, fmin(one, r[i]));
+      one = fmax(one, r[i]);
+    }
+    for (int o = 1; o < lanes; o <<= 1) {
+      const F v = __shfl_xor_sync(~0u, one, o), v2 = __shfl_xor_sync(~0u, two, o);
+      two = fmax(fmax(two, v2), fmin(one, v));
+      one = fmax(one, v);
+    }
+    one = __shfl_sync(~0u, one, (lane * lanes) & 31), two = __shfl_sync(~0u, two, (lane * lanes) & 31);
+  } else {
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (e0 + i < a.E) rank[e0 + i] = x[i] == -CUDART_INF_F ? none : s[i] + (F)b[i];
+      if (e0 + i < a.E) rank[e0 + i] = r[i];
     __syncwarp();
     int G = 1, g_log = 0;
     while (G < a.groups) G *= 2, ++g_log;
     const int sub = 32 >> g_log, g = lane >> (5 - g_log);      // `sub` lanes a group
-    F one = none, two = none;
     if (g < a.groups)
       for (int i = lane & (sub - 1); i < per; i += sub) {
         const F v = rank[g * per + i];
@@ -106,29 +183,117 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&x)[N], 
       two = fmax(fmax(two, v2), fmin(one, v));
       one = fmax(one, v);
     }
-    // lane g has group g's
-    const F worth = __shfl_sync(~0u, a.group_top == 2 ? one + two : one, (lane * sub) & 31);
-    int better = 0;
-    for (int j = 0; j < a.groups; ++j) {
-      const F v = __shfl_sync(~0u, worth, j);
-      better += v > worth || (v == worth && j < lane);
-    }
-    const bool in = lane < a.groups && better < a.group_k;
-    left = __ballot_sync(~0u, in);
-    if (sizeof(F) == 4 && a.group_k < a.groups) {
-      // the last group that stays and the first that does not
-      const F last = __shfl_sync(~0u, worth, __ffs(__ballot_sync(~0u, lane < a.groups && better == a.group_k - 1)) - 1);
-      const F next = __shfl_sync(~0u, worth, __ffs(__ballot_sync(~0u, lane < a.groups && better == a.group_k)) - 1);
-      sure = last - next > 4 * err + (F)0x1p-21 * (fabs(last) + fabs(next)) || next == none;
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      r[i] = e0 + i < a.E && !(left >> ((e0 + i) / per) & 1) ? none : x[i] == -CUDART_INF_F ? none : a.bias ? s[i] + (F)b[i] : (F)x[i];
+    one = __shfl_sync(~0u, one, (lane * sub) & 31), two = __shfl_sync(~0u, two, (lane * sub) & 31);
     __syncwarp();
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) r[i] = x[i] == -CUDART_INF_F ? none : a.bias ? s[i] + (F)b[i] : (F)x[i];
   }
+  F worth = one;
+  if (a.group_top == 2) {
+    // logits: their scores, up to a softmax's sum
+    const auto score_of = [&](F v) {
+      return v == none ? none : a.score == QMV_SCORE_SIGMOID ? sigmoid(v) : v == (F)top ? (F)1 : exp_of(v - (F)top);
+    };
+    worth = a.bias ? one + two : score_of(one) + score_of(two);
+  }
+  int better = 0;
+  for (int j = 0; j < a.groups; ++j) {
+    const F v = __shfl_sync(~0u, worth, j);
+    better += v > worth || (v == worth && j < lane);
+  }
+  if (sizeof(F) == 4 && a.group_k < a.groups && (a.bias || a.group_top == 2)) {
+    // the last group that stays and the first that does not: apart, or truly equal
+    const int l = __ffs(__ballot_sync(~0u, lane < a.groups && better == a.group_k - 1)) - 1,
+              m = __ffs(__ballot_sync(~0u, lane < a.groups && better == a.group_k)) - 1;
+    const F last = __shfl_sync(~0u, worth, l), next = __shfl_sync(~0u, worth, m);
+    const bool same = !a.bias && __shfl_sync(~0u, one, l) == __shfl_sync(~0u, one, m) &&
+                      __shfl_sync(~0u, two, l) == __shfl_sync(~0u, two, m);
+    const F err = 4 * score_error<F>(a.score) + (F)0x1p-22 * (fabs(last) + fabs(next));
+    known->sure = last - next > err || next == none || same;
+    // a group's best two in exact arithmetic are among those that reach the second less their errors
+    known->worth = worth, known->reach = (a.group_top == 2 ? two : one) - err, known->low = next - err, known->high = last + err;
+  }
+  return __ballot_sync(~0u, lane < a.groups && better < a.group_k);
+}
+
+// Ranks of the groups that do not remain become -inf.
+template <typename F, int N>
+__device__ __forceinline__ void leave_groups(const RouteArgs& a, F (&r)[N], uint32_t left, int lane) {
+  // a lane's experts lie in groups that follow each other
+  const int e0 = lane * N, per = a.per;
+  int g = group_of(a, e0), next = (g + 1) * per;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (e0 + i == next) ++g, next += per;
+    if (!(left >> (g & 31) & 1)) r[i] = (F)(-CUDART_INF_F);
+  }
+}
+
+// The choice of groups in 64 bits.
+template <int N>
+__device__ __noinline__ uint32_t groups_wide(const RouteArgs& a, const float* xb, int lane, double* rank) {
+  float x[N];
+  double r[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = xb[i];
+  double whole;
+  const float top = scores<double, N>(x, a.score, r, &whole);
+#pragma unroll
+  for (int i = 0; i < N; ++i) r[i] = x[i] == -CUDART_INF_F ? (double)x[i] : a.bias ? r[i] + (double)xb[N + i] : (double)x[i];
+  Groups<double> known;
+  return choose_groups<double, N>(a, r, top, lane, rank, &known);
+}
+
+// The same where a few groups are near each other: only their best experts' ranks are formed in 64 bits,
+// one a lane (sigmoid scores and a bias).  Returns 0 where these are more than 32.
+template <int N>
+__device__ __noinline__ uint32_t groups_near(const RouteArgs& a, const float* xb, const float* rb, const Groups<float>& known, int lane, Few* few) {
+  const uint32_t near = __ballot_sync(~0u, lane < a.groups && known.worth >= known.low && known.worth <= known.high);
+  uint32_t in = __ballot_sync(~0u, lane < a.groups && known.worth > known.high);
+  int n = 0;
+  for (int i = 0; i < N; ++i) {
+    const int e = lane * N + i, g = group_of(a, e) & 31;
+    const bool one = __shfl_sync(~0u, known.reach, g) <= rb[i] && e < a.E && (near >> g & 1) && rb[i] > -CUDART_INF_F;
+    const uint32_t all = __ballot_sync(~0u, one);
+    const int at = n + __popc(all & ((1u << lane) - 1));
+    if (one && at < 32) few[at] = Few{0.0f, xb[i], xb[N + i], g};
+    n += __popc(all);
+  }
+  __syncwarp();
+  if (n > 32) return 0;
+  double rank = -CUDART_INF, one = -CUDART_INF, two = -CUDART_INF;
+  if (lane < n) rank = sigmoid((double)few[lane].x) + (double)few[lane].b;
+  for (int j = 0; j < n; ++j) {
+    const double v = __shfl_sync(~0u, rank, j);
+    if (few[j].e == lane) two = fmax(two, fmin(one, v)), one = fmax(one, v);
+  }
+  const double worth = a.group_top == 2 ? one + two : one;
+  const bool mine = lane < a.groups && (near >> lane & 1);
+  int better = 0;
+  for (int j = 0; j < a.groups; ++j) {
+    const double v = __shfl_sync(~0u, worth, j);
+    better += (near >> j & 1) && (v > worth || (v == worth && j < lane));
+  }
+  const int room = a.group_k - __popc(in);
+  in |= __ballot_sync(~0u, mine && better < room);
+  __syncwarp();                            // few is written again
+  return in;
+}
+
+// Experts one after another, of the groups `left`, with ranks in F: lane t % 32 receives pick t (place
+// t / 32) with its logit.  Returns whether F could tell.
+template <typename F, int N>
+__device__ __noinline__ bool choose_each(const RouteArgs& a, const float* xb, uint32_t left, int lane, int (&id)[2], float (&of)[2]) {
+  const F none = (F)(-CUDART_INF_F), err = score_error<F>(a.score);
+  const int e0 = lane * N;
+  float x[N], b[N];
+  F s[N], r[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = xb[i], b[i] = xb[N + i];
+  F whole;
+  scores<F, N>(x, a.score, s, &whole);
+#pragma unroll
+  for (int i = 0; i < N; ++i) r[i] = x[i] == -CUDART_INF_F ? none : a.bias ? s[i] + (F)b[i] : (F)x[i];
+  leave_groups<F, N>(a, r, left, lane);
+  bool sure = true;
   F before = none;
   float x_before = 0.0f, b_before = 0.0f;
   for (int t = 0; t <= a.T; ++t) {                   // one more than is wanted, to tell the last apart
@@ -138,69 +303,199 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&x)[N], 
     for (int i = 1; i < N; ++i) best = fmax(best, r[i]);
     const F top = warp_max(best);
     if (top == none) {
-      if (lane == (t & 31) && t < a.T) id[t >> 5] = -1, w[t >> 5] = 0.0f;
+      if (lane == (t & 31) && t < a.T) id[t >> 5] = -1;
       continue;
     }
     const int owner = __ffs(__ballot_sync(~0u, best == top)) - 1;
     int at = 0;
-    float sv = 0.0f, xv = 0.0f, bv = 0.0f;
+    float xv = 0.0f, bv = 0.0f;
     bool found = false;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const bool hit = !found && lane == owner && r[i] == top;
-      if (hit) at = e0 + i, sv = (float)s[i], xv = x[i], bv = b[i], r[i] = none;
+      if (hit) at = e0 + i, xv = x[i], bv = b[i], r[i] = none;
       found |= hit;
     }
+    at = __shfl_sync(~0u, at, owner), xv = __shfl_sync(~0u, xv, owner);
     if (a.bias && sizeof(F) == 4) {
-      xv = __shfl_sync(~0u, xv, owner), bv = __shfl_sync(~0u, bv, owner);
+      bv = __shfl_sync(~0u, bv, owner);
       // equal ones of the same logit and bias are truly equal
       if (t > 0 && !(before - top > 2 * err + (F)0x1p-22 * (fabs(before) + fabs(top))) && !(xv == x_before && bv == b_before))
         sure = false;
       before = top, x_before = xv, b_before = bv;
     }
-    at = __shfl_sync(~0u, at, owner), sv = __shfl_sync(~0u, sv, owner);
-    if (lane == (t & 31) && t < a.T) id[t >> 5] = at, w[t >> 5] = sv;
+    if (lane == (t & 31) && t < a.T) id[t >> 5] = at, of[t >> 5] = xv;
   }
   return sure;
 }
 
-template <int N>
-__device__ __noinline__ void choose_wide(const RouteArgs& a, const float* xb, int lane, double* rank, int (&id)[2], float (&w)[2]) {
-  float x[N], b[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = xb[i], b[i] = xb[N + i];
-  choose<double, N>(a, x, b, lane, rank, id, w);
+// The order of the few in 64 bits (sigmoid scores): lane t has pick t.
+__device__ __noinline__ void order_wide(const RouteArgs& a, const Few* few, int n, int lane, int* id, float* of) {
+  const Few f = few[lane];
+  double rank = -CUDART_INF;
+  if (lane < n) rank = sigmoid((double)f.x) + (double)f.b;
+  uint32_t who = (lane < n ? f.e : MAX_E) << 5 | lane;
+  sort_lanes(rank, who, n, lane);
+  const bool in = lane < a.T && rank > -CUDART_INF;
+  *id = in ? (int)(who >> 5) : -1;
+  *of = few[who & 31].x;
 }
 
-template <typename X, int N>
-__global__ void __launch_bounds__(WARPS * 32) route_kernel(RouteArgs a) {
+template <typename X, int N, bool VEC>
+__global__ void __launch_bounds__(WARPS * 32, N <= 8 ? 10 : 4) route_kernel(RouteArgs a) {
   __shared__ double ranks[WARPS][N * 32];
+  __shared__ Few all_few[WARPS][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = lane * N;
   pdl_begin();
   const int64_t m = (int64_t)blockIdx.x * WARPS + warp;
   if (m >= a.M) return;
   const X* row = (const X*)a.x + m * a.ldx;
-  float xb[2 * N];
+  float x[N], b[N];
+  // loads without conditions, so that none waits for another
+  X raw[N];
+  constexpr int EACH = 16 / sizeof(X);
+  if constexpr (VEC) {                               // rows and E are whole 16-byte words
+    const int last = a.E - EACH;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int e = e0 + i;
-    float x = -CUDART_INF_F, b = 0.0f;
-    if (e < a.E) {
-      x = to_f<X>(row[e]);
-      if (a.bias) b = a.bias[e];
+    for (int i = 0; i < N; i += EACH) {
+      const uint4 v = *reinterpret_cast<const uint4*>(row + min(e0 + i, last));
+      memcpy(raw + i, &v, 16);
     }
-    // what cannot be chosen: NaN or -inf in either
-    if (isnan(x) || isnan(b) || b == -CUDART_INF_F) x = -CUDART_INF_F, b = 0.0f;
-    xb[i] = x, xb[N + i] = b;
-  }
-  int id[2] = {-1, -1};
-  float w[2] = {0.0f, 0.0f};
-  {
-    float x[N], b[N];
+  } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = xb[i], b[i] = xb[N + i];
-    if (!choose<float, N>(a, x, b, lane, reinterpret_cast<float*>(ranks[warp]), id, w))
-      choose_wide<N>(a, xb, lane, ranks[warp], id, w);
+    for (int i = 0; i < N; ++i) raw[i] = row[min(e0 + i, a.E - 1)];
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) b[i] = 0.0f;
+  if (a.bias) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) b[i] = a.bias[min(e0 + i, a.E - 1)];
+  }
+  // what cannot be chosen: NaN or -inf in either
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = to_f<X>(raw[i]) > -CUDART_INF_F ? to_f<X>(raw[i]) : -CUDART_INF_F;
+  if (a.bias) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (!(b[i] > -CUDART_INF_F)) x[i] = -CUDART_INF_F;
+  }
+  if (a.E < 32 * N) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (e0 + i >= a.E) x[i] = -CUDART_INF_F;
+  }
+  float s[N], r[N];
+  float whole = 1.0f;
+  const float top = scores<float, N>(x, a.score, s, &whole), none = -CUDART_INF_F;
+#pragma unroll
+  for (int i = 0; i < N; ++i) r[i] = a.bias && x[i] != none ? s[i] + b[i] : x[i];
+  const auto spill = [&](float (&xb)[2 * N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) xb[i] = x[i], xb[N + i] = b[i];
+  };
+  uint32_t left = ~0u;
+  if (a.groups > 1) {
+    Groups<float> known;
+    known.sure = true;
+    left = choose_groups<float, N>(a, r, top, lane, reinterpret_cast<float*>(ranks[warp]), &known);
+    if (!known.sure) {
+      float xb[2 * N], rb[N];
+      spill(xb);
+#pragma unroll
+      for (int i = 0; i < N; ++i) rb[i] = r[i];
+      left = a.bias && a.score == QMV_SCORE_SIGMOID ? groups_near<N>(a, xb, rb, known, lane, all_few[warp]) : 0;
+      if (left == 0) left = groups_wide<N>(a, xb, lane, ranks[warp]);
+    }
+    leave_groups<float, N>(a, r, left, lane);
+  }
+
+  int id[2] = {-1, -1};
+  float of[2] = {0.0f, 0.0f};                        // their logits
+  const float err2 = 2 * score_error<float>(a.score);
+  int n = 33;
+  Few* few = all_few[warp];
+  if (a.T <= MAX_SORTED) {
+    // T + 1 experts reach the (T / k + 1)-th of the lanes' k-th largest.  The first alone will do where
+    // experts are left in many lanes; in few the others give a higher bound.
+    float best = r[0], bound = -3.402823466e38f;
+#pragma unroll
+    for (int i = 1; i < N; ++i) best = fmaxf(best, r[i]);
+    uint32_t used = 0;
+    int mine = 0, at = 0;
+#pragma unroll 1
+    for (int k = 1; k <= N; ++k) {
+      float reach = __shfl_sync(~0u, sort_lanes(best, lane), k == 1 ? a.T : a.T / k);
+      if (a.bias) reach -= err2 + 0x1p-21f * fabsf(reach);     // and those that may do so but for their errors
+      bound = fmaxf(bound, reach);                             // (-inf, or inf - inf: as it was)
+      mine = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) mine += r[i] >= bound;
+      at = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(~0u, at, o);
+        if (lane >= o) at += v;
+      }
+      n = __shfl_sync(~0u, at, 31);
+      if (n <= 32) break;
+      bool found = false;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (!found && !(used >> i & 1) && r[i] == best) found = true, used |= 1u << i;
+      best = none;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (!(used >> i & 1)) best = fmaxf(best, r[i]);
+    }
+    at -= mine;
+    if (n <= 32) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (r[i] >= bound) few[at++] = Few{r[i], x[i], b[i], e0 + i};
+    }
+    __syncwarp();
+  }
+  if (n <= 32) {
+    // by rank, then by number: a lane each
+    float key = lane < n ? few[lane].rank : none;
+    uint32_t who = (lane < n ? few[lane].e : MAX_E) << 5 | lane;
+    sort_lanes(key, who, n, lane);
+    const bool in = lane < a.T && key > none;
+    const Few f = few[who & 31];
+    id[0] = in ? (int)(who >> 5) : -1;
+    of[0] = f.x;
+    if (a.bias) {
+      const float key2 = __shfl_down_sync(~0u, key, 1);
+      const bool near = in && lane < 31 && key2 > none && !(key - key2 > err2 + 0x1p-22f * (fabsf(key) + fabsf(key2)));
+      if (__any_sync(~0u, near)) {
+        // equal ones of the same logit and bias are truly equal
+        const float x2 = __shfl_down_sync(~0u, f.x, 1), b2 = __shfl_down_sync(~0u, f.b, 1);
+        if (__any_sync(~0u, near && !(f.x == x2 && f.b == b2))) {
+          if (a.score == QMV_SCORE_SIGMOID)
+            order_wide(a, few, n, lane, &id[0], &of[0]);
+          else
+            n = 34;
+        }
+      }
+    }
+  }
+  if (n > 32) {
+    float xb[2 * N];
+    spill(xb);
+    int id2[2] = {-1, -1};
+    float of2[2] = {0.0f, 0.0f};
+    if (n == 34 || !choose_each<float, N>(a, xb, left, lane, id2, of2)) choose_each<double, N>(a, xb, left, lane, id2, of2);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) id[p] = id2[p], of[p] = of2[p];
+  }
+  float w[2];
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    w[p] = 0.0f;
+    if (lane + 32 * p < a.T && id[p] >= 0) {
+      const float v = of[p], e = expf(a.score == QMV_SCORE_SIGMOID ? -fabsf(v) : v - top);
+      w[p] = a.score == QMV_SCORE_SIGMOID ? (v >= 0.0f ? 1.0f : e) / (1.0f + e) : v == top ? 1.0f / whole : e / whole;
+    }
   }
   float f = a.scale;
   if (a.renorm) {
@@ -215,15 +510,25 @@ __global__ void __launch_bounds__(WARPS * 32) route_kernel(RouteArgs a) {
     }
 }
 
+template <typename X, int N>
+cudaError_t run(const RouteArgs& a, cudaStream_t s) {
+  const dim3 grid((unsigned)(((int64_t)a.M + WARPS - 1) / WARPS));
+  constexpr int EACH = 16 / sizeof(X);
+  if constexpr (N % EACH == 0) {
+    if (a.E % EACH == 0 && (uintptr_t)a.x % 16 == 0 && (a.M == 1 || a.ldx % EACH == 0))
+      return launch_step(route_kernel<X, N, true>, grid, WARPS * 32, 0, s, 1, a);
+  }
+  return launch_step(route_kernel<X, N, false>, grid, WARPS * 32, 0, s, 1, a);
+}
+
 template <typename X>
 cudaError_t typed(const RouteArgs& a, cudaStream_t s) {
-  const dim3 grid((unsigned)(((int64_t)a.M + WARPS - 1) / WARPS));
-  if (a.E <= 32) return launch_step(route_kernel<X, 1>, grid, WARPS * 32, 0, s, 1, a);
-  if (a.E <= 64) return launch_step(route_kernel<X, 2>, grid, WARPS * 32, 0, s, 1, a);
-  if (a.E <= 128) return launch_step(route_kernel<X, 4>, grid, WARPS * 32, 0, s, 1, a);
-  if (a.E <= 256) return launch_step(route_kernel<X, 8>, grid, WARPS * 32, 0, s, 1, a);
-  if (a.E <= 512) return launch_step(route_kernel<X, 16>, grid, WARPS * 32, 0, s, 1, a);
-  return launch_step(route_kernel<X, 32>, grid, WARPS * 32, 0, s, 1, a);
+  if (a.E <= 32) return run<X, 1>(a, s);
+  if (a.E <= 64) return run<X, 2>(a, s);
+  if (a.E <= 128) return run<X, 4>(a, s);
+  if (a.E <= 256) return run<X, 8>(a, s);
+  if (a.E <= 512) return run<X, 16>(a, s);
+  return run<X, 32>(a, s);
 }
 
 }  // namespace

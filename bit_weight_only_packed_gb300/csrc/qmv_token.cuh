@@ -33,6 +33,8 @@ struct RouteArgs {
   float scale;
   int* ids;
   float* w;
+  int per;                      // experts a group
+  uint32_t per_inv;             // above 1: e / per is the upper half of e * per_inv, for e below 1024
 };
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t s);
 

@@ -115,7 +115,8 @@ int qmv_route(int M, int E, int T, const void* logits, int ldl, int dtype, int s
   const Span in = span(logits, M, ldl, E, dsize(dtype)), b = flat(bias, E, 4), oi = flat(ids, (int64_t)M * T, 4),
              ow = flat(weights, (int64_t)M * T, 4);
   if (meets(oi, in, b, ow) || meets(ow, in, b)) return QMV_ERR_INVALID_ARG;
-  qmv::RouteArgs a{M, E, T, logits, ldl, dtype, score, bias, groups, group_k, group_top, renormalise != 0, scale, ids, weights};
+  qmv::RouteArgs a{M, E, T, logits, ldl, dtype, score, bias, groups, group_k, group_top, renormalise != 0, scale, ids, weights,
+                   E / groups, E == groups ? 0 : (uint32_t)(((uint64_t)1 << 32) / (E / groups) + 1)};
   return done(qmv::launch_route(a, (cudaStream_t)stream));
 }
 
