@@ -7,6 +7,10 @@
 // sines belong to the token, and a warp takes B heads at a time of one token, so they are formed
 // once for all its heads.  The angle is position * turns modulo 2^64, exact at any
 // position; its upper 32 bits go to sincospi.
+//
+// The gammas go into the cosines and sines, so that an element of a head costs three operations, its
+// square and its conversions.  The next heads are on their way while one batch is worked on, by loads
+// without conditions (one under a condition waits for those before it).
 #include "qmv_token.cuh"
 
 namespace qmv {
@@ -18,17 +22,22 @@ struct alignas(W * sizeof(T) < 16 ? W * sizeof(T) : 16) Run {
   T v[W];
 };
 
+// Two neighbours rounded by one instruction.
+__device__ __forceinline__ void pair_of(float a, float b, __half* to) { *reinterpret_cast<__half2*>(to) = __floats2half2_rn(a, b); }
+__device__ __forceinline__ void pair_of(float a, float b, __nv_bfloat16* to) {
+  *reinterpret_cast<__nv_bfloat162*>(to) = __floats2bfloat162_rn(a, b);
+}
+
 template <typename X, typename T, int W, int U, int B, bool SIDE>
-__global__ void __launch_bounds__(128) rope_kernel(RopeArgs a, int lanes_log, int units, int splits, int per) {
+__global__ void __launch_bounds__(128, U <= 1 ? 4 : 1) rope_kernel(RopeArgs a, int lanes_log, int units, int splits, int per) {
   const int lane = threadIdx.x & 31, L = 1 << lanes_log, l = lane & (L - 1), hpw = 32 >> lanes_log;
   const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int m = (int)(item / splits), part = (int)(item - (int64_t)m * splits), H = a.nq + a.nk;
   pdl_begin();
   if (m >= a.M) return;
-  // this lane's units: where their two halves begin, and their cosines and sines
+  // this lane's units: where their two halves begin (the head's first elements, where it has none)
   const int turned = a.rot / (2 * W);
   int ea[U], eb[U];
-  float c[U][W], s[U][W];
   bool on[U], both[U];
 #pragma unroll
   for (int j = 0; j < U; ++j) {
@@ -38,91 +47,120 @@ __global__ void __launch_bounds__(128) rope_kernel(RopeArgs a, int lanes_log, in
     ea[j] = half ? u * W : 2 * u * W;
     eb[j] = half ? a.rot / 2 + u * W : (2 * u + 1) * W;
     both[j] = on[j] && (W > 1 || eb[j] < a.D);
+    if (!on[j]) ea[j] = 0;
+    if (!both[j]) eb[j] = 0;
+  }
+  const X* x = (const X*)a.x + (int64_t)m * a.ld;
+  const int first = part * per * hpw * B, h_end = min(H, first + per * hpw * B), own = lane >> lanes_log;
+  Run<X, W> xa[B][U], xb[B][U];
+  const auto load = [&](int h0) {
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const X* head = x + (int64_t)min(h0 + own + b * hpw, H - 1) * a.D;
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        xa[b][j] = *reinterpret_cast<const Run<X, W>*>(head + ea[j]);
+        xb[b][j] = *reinterpret_cast<const Run<X, W>*>(head + eb[j]);
+      }
+    }
+  };
+  load(first);
+  // and their cosines and sines
+  float c[U][W], s[U][W];
+#pragma unroll
+  for (int j = 0; j < U; ++j)
 #pragma unroll
     for (int i = 0; i < W; ++i) c[j][i] = 1.0f, s[j][i] = 0.0f;
-    if (u < turned) {
-      const uint64_t pos = (uint64_t)(int64_t)a.positions[m];
+  if (turned) {
+    const uint64_t pos = (uint64_t)(int64_t)a.positions[m];
 #pragma unroll
-      for (int i = 0; i < W; ++i) {
-        const int t = (int)((pos * (uint64_t)a.turns[u * W + i]) >> 32);       // turns, in 2^-32
-        sincospif((float)t * 0x1p-31f, &s[j][i], &c[j][i]);
-        s[j][i] *= a.amplitude;
-        c[j][i] *= a.amplitude;
+    for (int j = 0; j < U; ++j) {
+      const int u = l + j * L;
+      uint64_t turns[W];
+#pragma unroll
+      for (int i = 0; i < W; ++i) turns[i] = (uint64_t)a.turns[min(u, turned - 1) * W + i];
+      if (u < turned) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          const int t = (int)((pos * turns[i]) >> 32);           // turns, in 2^-32
+          sincospif((float)t * 0x1p-31f, &s[j][i], &c[j][i]);
+          s[j][i] *= a.amplitude;
+          c[j][i] *= a.amplitude;
+        }
       }
     }
   }
-  const X* x = (const X*)a.x + (int64_t)m * a.ld;
   const float inv_d = 1.0f / (float)a.D;
-  const int h_end = min(H, (part + 1) * per * hpw * B);
-  for (int h0 = part * per * hpw * B + (lane >> lanes_log); h0 < h_end + (lane >> lanes_log); h0 += hpw * B) {
-    Run<X, W> xa[B][U], xb[B][U];
+  // pair i of a unit: element first_of(i) and its second, of the W in a and the W in b
+  constexpr bool BESIDE = SIDE && W > 1;
+  const auto first_of = [](int i) { return BESIDE ? 2 * i : i; };
+  const auto second_of = [](int i) { return BESIDE ? 2 * i + 1 : W + i; };
+  float p1[U][W], p2[U][W], q1[U][W], q2[U][W];
+  int of = -1;                   // whose they are: 1 queries', 0 keys'
+  const auto coefficients = [&](bool is_q) {
+    const T* gamma = (const T*)(is_q ? a.gamma_q : a.gamma_k);
 #pragma unroll
-    for (int b = 0; b < B; ++b) {
-      const int h = h0 + b * hpw;
+    for (int j = 0; j < U; ++j) {
+      float g[2 * W];
 #pragma unroll
-      for (int j = 0; j < U; ++j) {
+      for (int i = 0; i < 2 * W; ++i) g[i] = 1.0f;
+      if (gamma) {
+        const Run<T, W> ga = *reinterpret_cast<const Run<T, W>*>(gamma + ea[j]), gb = *reinterpret_cast<const Run<T, W>*>(gamma + eb[j]);
 #pragma unroll
-        for (int i = 0; i < W; ++i) xa[b][j].v[i] = xb[b][j].v[i] = from_f<X>(0.0f);
-        if (h < h_end && on[j]) xa[b][j] = *reinterpret_cast<const Run<X, W>*>(x + (int64_t)h * a.D + ea[j]);
-        if (h < h_end && both[j]) xb[b][j] = *reinterpret_cast<const Run<X, W>*>(x + (int64_t)h * a.D + eb[j]);
+        for (int i = 0; i < W; ++i) g[i] = to_f<T>(ga.v[i]) + a.goff, g[W + i] = to_f<T>(gb.v[i]) + a.goff;
+      }
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        const float gp = g[first_of(i)], gq = g[second_of(i)];
+        p1[j][i] = gp * c[j][i], p2[j][i] = gq * s[j][i], q1[j][i] = gq * c[j][i], q2[j][i] = gp * s[j][i];
       }
     }
+    of = is_q;
+  };
+  for (int h0 = first; h0 < h_end; h0 += hpw * B) {
+    Run<X, W> ya[B][U], yb[B][U];
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+#pragma unroll
+      for (int j = 0; j < U; ++j) ya[b][j] = xa[b][j], yb[b][j] = xb[b][j];
+    // (in place, the next heads lie outside what this batch writes)
+    if (h0 + hpw * B < h_end) load(h0 + hpw * B);
 #pragma unroll
     for (int b = 0; b < B; ++b) {
-      const int h = h0 + b * hpw;
+      const int h = h0 + own + b * hpw;
       const bool is_q = h < a.nq;
-      const T* gamma = (const T*)(is_q ? a.gamma_q : a.gamma_k);
-      float va[U][W], vb[U][W], ss = 0.0f;
+      if (of != (int)is_q) coefficients(is_q);
+      float v[U][2 * W], ss = 0.0f;
 #pragma unroll
       for (int j = 0; j < U; ++j)
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-          va[j][i] = to_f<X>(xa[b][j].v[i]);
-          vb[j][i] = to_f<X>(xb[b][j].v[i]);
-          ss = fmaf(va[j][i], va[j][i], ss);
-          ss = fmaf(vb[j][i], vb[j][i], ss);
+          v[j][i] = to_f<X>(ya[b][j].v[i]);
+          v[j][W + i] = to_f<X>(yb[b][j].v[i]);
+          ss = on[j] ? fmaf(v[j][i], v[j][i], ss) : ss;
+          ss = both[j] ? fmaf(v[j][W + i], v[j][W + i], ss) : ss;
         }
       for (int o = L >> 1; o; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
-      if (h >= h_end) continue;
-      if (gamma) {
-        const float r = 1.0f / sqrtf(fmaf(ss, inv_d, a.eps));
-#pragma unroll
-        for (int j = 0; j < U; ++j) {
-          Run<T, W> ga, gb;
-#pragma unroll
-          for (int i = 0; i < W; ++i) ga.v[i] = gb.v[i] = from_f<T>(0.0f);
-          if (on[j]) ga = *reinterpret_cast<const Run<T, W>*>(gamma + ea[j]);
-          if (both[j]) gb = *reinterpret_cast<const Run<T, W>*>(gamma + eb[j]);
-#pragma unroll
-          for (int i = 0; i < W; ++i) {
-            va[j][i] = va[j][i] * r * (to_f<T>(ga.v[i]) + a.goff);
-            vb[j][i] = vb[j][i] * r * (to_f<T>(gb.v[i]) + a.goff);
-          }
-        }
-      }
+      const float r = (is_q ? a.gamma_q : a.gamma_k) ? rsqrtf(fmaf(ss, inv_d, a.eps)) : 1.0f;
       T* out = is_q ? (T*)a.q + (int64_t)m * a.ldq + (int64_t)h * a.D : (T*)a.k + (int64_t)m * a.ldk + (int64_t)(h - a.nq) * a.D;
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        Run<T, W> oa, ob;
-        if (SIDE && W > 1) {
+        float y[2 * W];
 #pragma unroll
-          for (int i = 0; i < W; ++i) {
-            // pair i: the first W / 2 lie in a, the others in b
-            float(&v)[W] = i < W / 2 ? va[j] : vb[j];
-            Run<T, W>& o = i < W / 2 ? oa : ob;
-            const int k = 2 * (i % (W / 2));
-            o.v[k] = from_f<T>(v[k] * c[j][i] - v[(k + 1) % W] * s[j][i]);
-            o.v[(k + 1) % W] = from_f<T>(v[(k + 1) % W] * c[j][i] + v[k] * s[j][i]);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < W; ++i) {
-            oa.v[i] = from_f<T>(va[j][i] * c[j][i] - vb[j][i] * s[j][i]);
-            ob.v[i] = from_f<T>(vb[j][i] * c[j][i] + va[j][i] * s[j][i]);
-          }
+        for (int i = 0; i < W; ++i) {
+          const float p = v[j][first_of(i)], q = v[j][second_of(i)];
+          y[first_of(i)] = (p * p1[j][i] - q * p2[j][i]) * r;
+          y[second_of(i)] = (q * q1[j][i] + p * q2[j][i]) * r;
         }
-        if (on[j]) *reinterpret_cast<Run<T, W>*>(out + ea[j]) = oa;
-        if (both[j]) *reinterpret_cast<Run<T, W>*>(out + eb[j]) = ob;
+        Run<T, W> oa, ob;
+        if constexpr (W > 1) {
+#pragma unroll
+          for (int i = 0; i < W; i += 2) pair_of(y[i], y[i + 1], oa.v + i), pair_of(y[W + i], y[W + i + 1], ob.v + i);
+        } else {
+          oa.v[0] = from_f<T>(y[0]), ob.v[0] = from_f<T>(y[1]);
+        }
+        if (h < h_end && on[j]) *reinterpret_cast<Run<T, W>*>(out + ea[j]) = oa;
+        if (h < h_end && both[j]) *reinterpret_cast<Run<T, W>*>(out + eb[j]) = ob;
       }
     }
   }
@@ -155,12 +193,12 @@ cudaError_t typed(const RopeArgs& a, cudaStream_t s) {
     return a.D % (2 * w) == 0 && a.rot % (2 * w) == 0 && at(a.x, a.ld, sizeof(X)) && at(a.q, a.ldq, 2) && at(a.k, a.ldk, 2) &&
            at(a.gamma_q, 0, 2) && at(a.gamma_k, 0, 2);
   };
-  constexpr int B = sizeof(X) == 4 ? 2 : 4;
+  constexpr int B = sizeof(X) == 4 ? 1 : 2;
   if (a.D <= 512 && whole(8)) return side ? run<X, T, 8, 1, B, true>(a, s) : run<X, T, 8, 1, B, false>(a, s);
   if (a.D <= 256 && whole(4)) return side ? run<X, T, 4, 1, B, true>(a, s) : run<X, T, 4, 1, B, false>(a, s);
   // single elements: the layouts differ in places only
-  if (a.D <= 64) return side ? run<X, T, 1, 1, 4, true>(a, s) : run<X, T, 1, 1, 4, false>(a, s);
-  if (a.D <= 256) return side ? run<X, T, 1, 4, 2, true>(a, s) : run<X, T, 1, 4, 2, false>(a, s);
+  if (a.D <= 64) return side ? run<X, T, 1, 1, 2, true>(a, s) : run<X, T, 1, 1, 2, false>(a, s);
+  if (a.D <= 256) return side ? run<X, T, 1, 4, 1, true>(a, s) : run<X, T, 1, 4, 1, false>(a, s);
   return side ? run<X, T, 1, 16, 1, true>(a, s) : run<X, T, 1, 16, 1, false>(a, s);
 }
 
