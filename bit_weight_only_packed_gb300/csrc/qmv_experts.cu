@@ -1,6 +1,8 @@
 // qmv_experts.cu -- around the experts' products (qmv_experts.cuh): the pairs of token and expert in
 // the order of experts, x in fp16 with the activation in front of it, and the weighted sum
 // behind them.
+#include <algorithm>
+
 #include "qmv_experts.cuh"
 
 namespace qmv {
@@ -12,60 +14,53 @@ extern template cudaError_t run_experts<128>(const ExpertsArgs&, const ExpertsPl
 extern template cudaError_t read_x_error<32>(int, int*);
 extern template cudaError_t read_x_error<64>(int, int*);
 extern template cudaError_t read_x_error<128>(int, int*);
+// read_x_error<0>: this file's
 
 }  // namespace w4
 
-static __device__ int g_experts_error = 0;
-
 int read_experts_error(int clear, int* out) {
-  int v[4] = {};
-  cudaError_t (*const read[])(int, int*) = {w4::read_x_error<32>, w4::read_x_error<64>, w4::read_x_error<128>};
-  for (int i = 0; i < 3; ++i) {
-    const cudaError_t e = read[i](clear, &v[i]);
+  cudaError_t (*const read[])(int, int*) = {w4::read_x_error<32>, w4::read_x_error<64>, w4::read_x_error<128>, w4::read_x_error<0>};
+  *out = 0;
+  for (const auto f : read) {
+    int v = 0;
+    const cudaError_t e = f(clear, &v);
     if (e != cudaSuccess) return (int)e;
+    if (v) *out = v;
   }
-  cudaError_t e = cudaMemcpyFromSymbol(&v[3], g_experts_error, sizeof(int));
-  if (e == cudaSuccess && clear && v[3]) {
-    const int z = 0;
-    e = cudaMemcpyToSymbol(g_experts_error, &z, sizeof(int));
-  }
-  *out = v[0] ? v[0] : v[1] ? v[1] : v[2] ? v[2] : v[3];
-  return (int)e;
+  return 0;
 }
 
 namespace {
 
 using namespace w4;
 
-constexpr int PREP_NT = 512, PREP_W = PREP_NT / 32;
-
-// The pairs in the order of their experts, pairs of one expert as they came, and the tasks.  A warp
-// counts a contiguous part of the pairs in counters of its own, [warp][expert], which then
-// become the places where it puts them.
-__device__ void sort_pairs(const ExpertsArgs& a, int cols, int* head, int* order, Task* tasks, int* counts) {
-  __shared__ int sums[PREP_W], t_sums[PREP_W], totals[2];
+// The pairs in the order of their experts, pairs of one expert as they came, and the tasks.  Each of nw
+// warps counts a contiguous part of the pairs in counters of its own, [warp][expert], which then become
+// the places where it puts them.  EACH: experts a thread.
+template <int EACH>
+__device__ __forceinline__ void sort_each(const ExpertsArgs& a, int cols, int* head, int* order, Task* tasks, int* counts) {
+  __shared__ int sums[X_W], t_sums[X_W];
   const int P = a.M * a.T, E1 = a.E + 1, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int i = tid; i < PREP_W * E1; i += PREP_NT) counts[i] = 0;
+  const int nw = min(X_W, cdiv(P, 32)), per = cdiv(cdiv(P, nw), 32) * 32, p0 = min(P, warp * per), p1 = min(P, p0 + per);
+  const auto expert_of = [&](int e) { return (unsigned)e < (unsigned)a.E ? e : a.E; };    // those without one come last
+  // the first of a warp's ids, for both of its passes, is on its way meanwhile
+  const int first = p0 + lane < p1 ? a.ids[p0 + lane] : -1;
+  for (int i = tid; i < nw * E1; i += X_NT) counts[i] = 0;
   __syncthreads();
-  const int per = cdiv(cdiv(P, PREP_W), 32) * 32, p0 = min(P, warp * per), p1 = min(P, p0 + per);
-  const auto expert_of = [&](int p) {
-    const int e = a.ids[p];
-    return (unsigned)e < (unsigned)a.E ? e : a.E;          // those without one come last
-  };
   for (int p = p0 + lane; p < p1; p += 32) {
-    const int e = a.ids[p];
-    if (e < -1 || e >= a.E) atomicCAS(&g_experts_error, 0, pipe::ERR_BAD_EXPERT);
-    atomicAdd(&counts[warp * E1 + expert_of(p)], 1);
+    const int e = p < p0 + 32 ? first : a.ids[p];
+    if (e < -1 || e >= a.E) atomicCAS(&g_x_error, 0, pipe::ERR_BAD_EXPERT);
+    atomicAdd(&counts[warp * E1 + expert_of(e)], 1);
   }
   __syncthreads();
-  // running sums over the experts, of pairs and of tasks; E1 <= 1025: three experts a thread
-  int n[3], tn[3], all = 0, t_all = 0;
+  // running sums over the experts, of pairs and of tasks
+  int n[EACH], tn[EACH], all = 0, t_all = 0;
 #pragma unroll
-  for (int j = 0; j < 3; ++j) {
-    const int e = tid * 3 + j;
+  for (int j = 0; j < EACH; ++j) {
+    const int e = tid * EACH + j;
     n[j] = 0;
     if (e < E1)
-      for (int w = 0; w < PREP_W; ++w) n[j] += counts[w * E1 + e];
+      for (int w = 0; w < nw; ++w) n[j] += counts[w * E1 + e];
     tn[j] = e < a.E ? cdiv(n[j], cols) : 0;
     all += n[j];
     t_all += tn[j];
@@ -78,17 +73,17 @@ __device__ void sort_pairs(const ExpertsArgs& a, int cols, int* head, int* order
   }
   if (lane == 31) sums[warp] = run, t_sums[warp] = t_run;
   __syncthreads();
-  for (int w = 0; w < warp; ++w) run += sums[w], t_run += t_sums[w];
-  run -= all, t_run -= t_all;
+  run += __reduce_add_sync(~0u, lane < warp ? sums[lane] : 0) - all;
+  t_run += __reduce_add_sync(~0u, lane < warp ? t_sums[lane] : 0) - t_all;
 #pragma unroll
-  for (int j = 0; j < 3; ++j) {
-    const int e = tid * 3 + j;
+  for (int j = 0; j < EACH; ++j) {
+    const int e = tid * EACH + j;
     if (e < a.E)
-      for (int i = 0; i < tn[j]; ++i) tasks[t_run + i] = Task{e, run + i * cols, min(cols, n[j] - i * cols), 0};
-    if (e == a.E) totals[0] = t_run, totals[1] = run;
+      for (int i = 0; i < tn[j]; ++i) tasks[t_run + i] = Task(e, run + i * cols, min(cols, n[j] - i * cols));
+    if (e == a.E) head[0] = t_run, head[1] = run;
     t_run += tn[j];
     if (e < E1)
-      for (int w = 0, at = run; w < PREP_W; ++w) {
+      for (int w = 0, at = run; w < nw; ++w) {
         const int c = counts[w * E1 + e];
         counts[w * E1 + e] = at;
         at += c;
@@ -96,9 +91,8 @@ __device__ void sort_pairs(const ExpertsArgs& a, int cols, int* head, int* order
     run += n[j];
   }
   __syncthreads();
-  if (tid == 0) head[0] = totals[0], head[1] = totals[1];
   for (int b = p0; b < p1; b += 32) {
-    const int p = b + lane, e = p < p1 ? expert_of(p) : -1;
+    const int p = b + lane, e = p < p1 ? expert_of(b == p0 ? first : a.ids[p]) : -1;
     const unsigned same = __match_any_sync(~0u, e);
     const int before = __popc(same & ((1u << lane) - 1));
     int at = 0;
@@ -112,28 +106,36 @@ __device__ void sort_pairs(const ExpertsArgs& a, int cols, int* head, int* order
   }
 }
 
-// CTA 0 sorts the pairs; each of the others makes a row of x: the activation, then fp16, for bf16
+__device__ __forceinline__ void sort_pairs(const ExpertsArgs& a, int cols, int* head, int* order, Task* tasks, int* counts) {
+  static_assert(3 * X_NT > EXPERTS_MAX_E, "a thread for every three experts");
+  if (a.E < X_NT)
+    sort_each<1>(a, cols, head, order, tasks, counts);
+  else
+    sort_each<3>(a, cols, head, order, tasks, counts);
+}
+
+// CTA 0 sorts the pairs where they are many; each of the others makes a row of x: the activation, then fp16, for bf16
 // scaled by a power of two that puts the row's largest value at 2^14 (as the 4-bit matvec does).
-__global__ void __launch_bounds__(PREP_NT) prepare_kernel(ExpertsArgs a, int cols, int* head, int* order, Task* tasks,
+__global__ void __launch_bounds__(X_NT) prepare_kernel(ExpertsArgs a, int sort, int cols, int* head, int* order, Task* tasks,
                                                           int* exps, uint16_t* xh, int64_t ldxh) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint32_t s_top;
   if (threadIdx.x == 0) s_top = 0;
   __syncthreads();
   pdl_begin();
-  if (blockIdx.x == 0) return sort_pairs(a, cols, head, order, tasks, reinterpret_cast<int*>(smem));
-  const int row = blockIdx.x - 1;
+  if (sort && blockIdx.x == 0) return sort_pairs(a, cols, head, order, tasks, reinterpret_cast<int*>(smem));
+  const int row = blockIdx.x - sort;
   const uint16_t* x = (const uint16_t*)a.x + (int64_t)row * a.ldx;
   uint16_t* v = reinterpret_cast<uint16_t*>(smem);
   uint32_t top = 0;
-  for (int k = threadIdx.x; k < a.K; k += PREP_NT) {
+  for (int k = threadIdx.x; k < a.K; k += X_NT) {
     uint32_t b = x[k];
     if (a.act != QMV_ACT_NONE) b = gated_bits(f16_f(b, a.x_bf16), f16_f(x[a.K + k], a.x_bf16), a.act, a.x_bf16);
     v[k] = (uint16_t)b;
     top = max(top, b & 0x7fffu);
   }
   if (!a.x_bf16) {
-    for (int k = threadIdx.x; k < a.K; k += PREP_NT) xh[row * ldxh + k] = v[k];
+    for (int k = threadIdx.x; k < a.K; k += X_NT) xh[row * ldxh + k] = v[k];
     return;
   }
   top = __reduce_max_sync(~0u, top);
@@ -142,7 +144,7 @@ __global__ void __launch_bounds__(PREP_NT) prepare_kernel(ExpertsArgs a, int col
   const int e = column_exp(s_top);
   const float f = pow2_f(e);
   if (threadIdx.x == 0) exps[row] = e;
-  for (int k = threadIdx.x; k < a.K; k += PREP_NT)
+  for (int k = threadIdx.x; k < a.K; k += X_NT)
     xh[row * ldxh + k] = __half_as_ushort(__float2half_rn(__uint_as_float((uint32_t)v[k] << 16) * f));
 }
 
@@ -153,13 +155,15 @@ __global__ void __launch_bounds__(128) combine_kernel(ExpertsArgs a, const float
   if (r >= a.R) return;
   for (int m = blockIdx.y; m < a.M; m += gridDim.y) {
     float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
+    // loads without conditions, so that none waits for another
+#pragma unroll 8
     for (int j = 0; j < a.T; ++j) {
       const int p = m * a.T + j;
-      if ((unsigned)a.ids[p] >= (unsigned)a.E) continue;
+      const bool in = (unsigned)a.ids[p] < (unsigned)a.E;
       const float w = a.weights[p];
       const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)p * a.R + r);
-      y.x = fmaf(w, v.x, y.x), y.y = fmaf(w, v.y, y.y), y.z = fmaf(w, v.z, y.z), y.w = fmaf(w, v.w, y.w);
+      y.x = in ? fmaf(w, v.x, y.x) : y.x, y.y = in ? fmaf(w, v.y, y.y) : y.y;
+      y.z = in ? fmaf(w, v.z, y.z) : y.z, y.w = in ? fmaf(w, v.w, y.w) : y.w;
     }
     const int64_t at = (int64_t)m * a.ldy + r;
     store_y(a.y, at, a.y_dtype, y.x), store_y(a.y, at + 1, a.y_dtype, y.y);
@@ -193,8 +197,11 @@ bool lay_out(const ExpertsArgs& a, int cols, ExpertsPlan* P) {
   P->pitch = P->KB * 256 + 64;
   P->x_size = (int)up((int64_t)P->pitch * cols);
   P->xs_size = (int)up((int64_t)P->KB * (BK / a.group) * X_COLS * 4);
-  const int64_t part = (int64_t)X_W * 2 * cols * ROWS * 4;
-  const int64_t left = (int64_t)dev_info().max_smem_optin - 4096 - (2 * P->x_size + 256 + 2 * P->xs_size + part);
+  const int64_t part = (int64_t)X_W * cols * ROWS * 4;
+  const int pairs = a.M * a.T, tasks = std::min(pairs, pairs / cols + std::min(pairs, a.E));
+  P->own = pairs <= X_OWN;
+  const int own = P->own ? (int)(up(pairs * 2) + up(tasks * sizeof(OwnTask))) : 0;
+  const int64_t left = (int64_t)dev_info().max_smem_optin - 4096 - (2 * P->x_size + 256 + 2 * P->xs_size + part + own);
   const int64_t fit = left / ((int64_t)X_W * bb);         // blocks a warp's ring can hold
   if (left < 0 || fit < 2) return false;
   P->stage = fit >= 4 ? 2 : 1;
@@ -203,7 +210,9 @@ bool lay_out(const ExpertsArgs& a, int cols, ExpertsPlan* P) {
   P->zero_off = P->x_off + 2 * P->x_size;
   P->xs_off = P->zero_off + 256;
   P->part_off = P->xs_off + 2 * P->xs_size;
-  P->smem = P->part_off + (int)part;
+  P->order_off = P->part_off + (int)part;
+  P->tasks_off = P->order_off + (P->own ? (int)up(pairs * 2) : 0);
+  P->smem = P->order_off + own;
   return true;
 }
 
@@ -229,13 +238,18 @@ cudaError_t launch_experts(const ExpertsArgs& a, cudaStream_t s) {
   P.x = as_is ? (const uint16_t*)a.x : xh;
   P.ldx = as_is ? a.ldx : a.K;
   const int rows = as_is ? 0 : a.per_pair ? a.M * a.T : a.M;
-  const size_t sort = (size_t)PREP_W * (a.E + 1) * 4, smem = sort > (size_t)a.K * 2 ? sort : (size_t)a.K * 2;
-  static thread_local KernCache c;
-  cudaError_t e = prep_kernel(prepare_kernel, c, PREP_NT, smem, nullptr);
-  if (e == cudaSuccess)
-    e = launch_step(prepare_kernel, dim3(1 + rows), PREP_NT, smem, s, 1, a, cols, (int*)(ws + at.head), (int*)(ws + at.order),
-                    (Task*)(ws + at.tasks), (int*)(ws + at.exps), xh, (int64_t)a.K);
-  if (e != cudaSuccess) return e;
+  const int sort = !P.own;
+  P.prepared = sort || rows;
+  cudaError_t e = cudaSuccess;
+  if (P.prepared) {
+    const size_t counts = sort ? (size_t)X_W * (a.E + 1) * 4 : 0, smem = std::max(counts, (size_t)a.K * 2);
+    static thread_local KernCache c;
+    e = prep_kernel(prepare_kernel, c, X_NT, smem, nullptr);
+    if (e == cudaSuccess)
+      e = launch_step(prepare_kernel, dim3(sort + rows), X_NT, smem, s, 1, a, sort, cols, (int*)(ws + at.head),
+                      (int*)(ws + at.order), (Task*)(ws + at.tasks), (int*)(ws + at.exps), xh, (int64_t)a.K);
+    if (e != cudaSuccess) return e;
+  }
   e = a.group == 32 ? run_experts<32>(a, P, s) : a.group == 64 ? run_experts<64>(a, P, s) : run_experts<128>(a, P, s);
   if (e != cudaSuccess || !a.weights) return e;
   return launch_step(combine_kernel, dim3(cdiv(a.R, 512), a.M), 128, 0, s, 1, a, (const float*)P.part);
