@@ -148,27 +148,31 @@ __global__ void __launch_bounds__(X_NT) prepare_kernel(ExpertsArgs a, int sort, 
     xh[row * ldxh + k] = __half_as_ushort(__float2half_rn(__uint_as_float((uint32_t)v[k] << 16) * f));
 }
 
-// y[m] = sum_j weights[m][j] * part[m][j], in the order of j.
+// y[m] = sum_j weights[m][j] * part[m][j], in the order of j.  All that came before the products has
+// ended when this starts, so ids and weights are read ahead of the wait for those.
 __global__ void __launch_bounds__(128) combine_kernel(ExpertsArgs a, const float* part) {
-  pdl_begin();
-  const int r = (blockIdx.x * 128 + threadIdx.x) * 4;
-  if (r >= a.R) return;
-  for (int m = blockIdx.y; m < a.M; m += gridDim.y) {
-    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    // loads without conditions, so that none waits for another
-#pragma unroll 8
-    for (int j = 0; j < a.T; ++j) {
-      const int p = m * a.T + j;
-      const bool in = (unsigned)a.ids[p] < (unsigned)a.E;
-      const float w = a.weights[p];
-      const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)p * a.R + r);
-      y.x = in ? fmaf(w, v.x, y.x) : y.x, y.y = in ? fmaf(w, v.y, y.y) : y.y;
-      y.z = in ? fmaf(w, v.z, y.z) : y.z, y.w = in ? fmaf(w, v.w, y.w) : y.w;
-    }
-    const int64_t at = (int64_t)m * a.ldy + r;
-    store_y(a.y, at, a.y_dtype, y.x), store_y(a.y, at + 1, a.y_dtype, y.y);
-    store_y(a.y, at + 2, a.y_dtype, y.z), store_y(a.y, at + 3, a.y_dtype, y.w);
+  __shared__ float w[64];
+  __shared__ int in[64];
+  const int m = blockIdx.y, r = (blockIdx.x * 128 + threadIdx.x) * 4;
+  if (threadIdx.x < a.T) {
+    in[threadIdx.x] = (unsigned)a.ids[m * a.T + threadIdx.x] < (unsigned)a.E;
+    w[threadIdx.x] = a.weights[m * a.T + threadIdx.x];
   }
+  pdl_begin();
+  __syncthreads();
+  if (r >= a.R) return;
+  float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  // loads without conditions, so that none waits for another
+#pragma unroll 8
+  for (int j = 0; j < a.T; ++j) {
+    const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)(m * a.T + j) * a.R + r);
+    const bool is = in[j];
+    y.x = is ? fmaf(w[j], v.x, y.x) : y.x, y.y = is ? fmaf(w[j], v.y, y.y) : y.y;
+    y.z = is ? fmaf(w[j], v.z, y.z) : y.z, y.w = is ? fmaf(w[j], v.w, y.w) : y.w;
+  }
+  const int64_t at = (int64_t)m * a.ldy + r;
+  store_y(a.y, at, a.y_dtype, y.x), store_y(a.y, at + 1, a.y_dtype, y.y);
+  store_y(a.y, at + 2, a.y_dtype, y.z), store_y(a.y, at + 3, a.y_dtype, y.w);
 }
 
 // Where things lie in the workspace.

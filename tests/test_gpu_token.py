@@ -438,7 +438,8 @@ def draw_ref(x, u, t, k, p, m):
 
 def logits_like(seed, rows, V):
     x = randn(seed, rows, V) * 2
-    x.scatter_add_(1, torch.randint(0, V, (rows, 8), generator=gen(seed + 1), device="cuda"), 6 + 5 * torch.rand(rows, 8, device="cuda"))
+    g = gen(seed + 1)
+    x.scatter_add_(1, torch.randint(0, V, (rows, 8), generator=g, device="cuda"), 6 + 5 * torch.rand(rows, 8, generator=g, device="cuda"))
     return x
 
 
