@@ -1,16 +1,20 @@
 // qmv_rope.cu -- norms of query and key heads and their position rotation (qmv_qk_norm_rope):
 //   u = x / sqrt(mean x^2 + eps) * gamma;  (a, b) -> amplitude * (a cos t - b sin t, b cos t + a sin t).
 //
-// A lane owns whole pairs: W neighbouring elements of the first half of what is turned and the
-// W that they pair with (or 2 W neighbours, where pairs lie side by side or nothing is
-// turned), so a head costs no exchange but the sum of its squares.  Its cosines and
-// sines belong to the token, and a warp takes B heads at a time of one token, so they are formed
-// once for all its heads.  The angle is position * turns modulo 2^64, exact at any
-// position; its upper 32 bits go to sincospi.
+// A lane owns whole pairs: W neighbouring elements of the first half of what is turned and the W that they
+// pair with (or 2 W neighbours, where pairs lie side by side or nothing is turned), so a head costs no
+// exchange but the sum of its squares.  Its cosines and sines belong to the token, whose heads a warp takes one
+// after another, so they are formed once for all of them.  The angle is position * turns modulo 2^64, exact at
+// any position; its upper 32 bits go to sincospi.  The gammas go into the cosines and sines, so that an element
+// of a head costs three operations, its square and its conversions.
 //
-// The gammas go into the cosines and sines, so that an element of a head costs three operations, its
-// square and its conversions.  The next heads are on their way while one batch is worked on, by loads
-// without conditions (one under a condition waits for those before it).
+// Bound by HBM where tokens are many, which takes more heads on their way than registers hold: with the next
+// head in registers (loads without conditions, since one under a condition waits for those before it) 8192
+// tokens of 32 + 8 heads of 256 took 91 us, with the next two 76; with three in shared memory, copied by each
+// thread for itself so that nobody waits for another, 55 (6.1 TB/s; a copy of the same bytes takes 51), and
+// 1024 tokens of 32 + 8 heads of 128 8.3 us against 10.4.  Runs of other sizes than 16 bytes gain nothing by that
+// (3000 tokens of 68 heads of 64 in fp32: 20.0 us and 18.1; of 15 heads of 72: 10.3 both) and keep to registers.
+// A few tokens are bound by latency: 1.9 us.
 #include "qmv_token.cuh"
 
 namespace qmv {
@@ -28,8 +32,19 @@ __device__ __forceinline__ void pair_of(float a, float b, __nv_bfloat16* to) {
   *reinterpret_cast<__nv_bfloat162*>(to) = __floats2bfloat162_rn(a, b);
 }
 
-template <typename X, typename T, int W, int U, int B, bool SIDE>
-__global__ void __launch_bounds__(128, U <= 1 ? 4 : 1) rope_kernel(RopeArgs a, int lanes_log, int units, int splits, int per) {
+// 16 bytes from global to shared memory, on their way.
+__device__ __forceinline__ void copy_ahead(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
+
+constexpr int STAGES = 4;
+
+// Heads on their way in shared memory: where a run is one copy of 16 bytes.
+template <typename X, int W>
+constexpr bool RINGED = W * sizeof(X) == 16;
+
+template <typename X, typename T, int W, int U, bool SIDE>
+__global__ void __launch_bounds__(128, RINGED<X, W> ? 5 : U <= 1 ? 4 : 1) rope_kernel(RopeArgs a, int lanes_log, int units, int splits, int per) {
   const int lane = threadIdx.x & 31, L = 1 << lanes_log, l = lane & (L - 1), hpw = 32 >> lanes_log;
   const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int m = (int)(item / splits), part = (int)(item - (int64_t)m * splits), H = a.nq + a.nk;
@@ -51,20 +66,31 @@ __global__ void __launch_bounds__(128, U <= 1 ? 4 : 1) rope_kernel(RopeArgs a, i
     if (!both[j]) eb[j] = 0;
   }
   const X* x = (const X*)a.x + (int64_t)m * a.ld;
-  const int first = part * per * hpw * B, h_end = min(H, first + per * hpw * B), own = lane >> lanes_log;
-  Run<X, W> xa[B][U], xb[B][U];
+  const int first = part * per * hpw, h_end = min(H, first + per * hpw), own = lane >> lanes_log;
+  Run<X, W> xa[U], xb[U];
   const auto load = [&](int h0) {
+    const X* head = x + (int64_t)min(h0 + own, H - 1) * a.D;
 #pragma unroll
-    for (int b = 0; b < B; ++b) {
-      const X* head = x + (int64_t)min(h0 + own + b * hpw, H - 1) * a.D;
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        xa[b][j] = *reinterpret_cast<const Run<X, W>*>(head + ea[j]);
-        xb[b][j] = *reinterpret_cast<const Run<X, W>*>(head + eb[j]);
-      }
+    for (int j = 0; j < U; ++j) {
+      xa[j] = *reinterpret_cast<const Run<X, W>*>(head + ea[j]);
+      xb[j] = *reinterpret_cast<const Run<X, W>*>(head + eb[j]);
     }
   };
-  load(first);
+  constexpr bool RING = RINGED<X, W>;
+  __shared__ uint4 ring[RING ? STAGES : 1][2][RING ? 128 : 1];           // a thread's two runs
+  const auto copy = [&](int h0, int stage) {
+    if (h0 < h_end) {
+      const X* head = x + (int64_t)min(h0 + own, H - 1) * a.D;
+      copy_ahead(&ring[stage][0][threadIdx.x], head + ea[0]);
+      copy_ahead(&ring[stage][1][threadIdx.x], head + eb[0]);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if constexpr (RING) {
+    for (int i = 0; i < STAGES - 1; ++i) copy(first + i * hpw, i);
+  } else {
+    load(first);
+  }
   // and their cosines and sines
   float c[U][W], s[U][W];
 #pragma unroll
@@ -117,68 +143,75 @@ __global__ void __launch_bounds__(128, U <= 1 ? 4 : 1) rope_kernel(RopeArgs a, i
     }
     of = is_q;
   };
-  for (int h0 = first; h0 < h_end; h0 += hpw * B) {
-    Run<X, W> ya[B][U], yb[B][U];
+  int stage = 0;
+  for (int h0 = first; h0 < h_end; h0 += hpw) {
+    // (in place, the heads ahead lie outside what this one writes)
+    Run<X, W> ya[U], yb[U];
+    if constexpr (RING) {
+      copy(h0 + (STAGES - 1) * hpw, stage ? stage - 1 : STAGES - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+      memcpy(ya[0].v, &ring[stage][0][threadIdx.x], 16);
+      memcpy(yb[0].v, &ring[stage][1][threadIdx.x], 16);
+      stage = stage + 1 < STAGES ? stage + 1 : 0;
+    } else {
 #pragma unroll
-    for (int b = 0; b < B; ++b)
+      for (int j = 0; j < U; ++j) ya[j] = xa[j], yb[j] = xb[j];
+      if (h0 + hpw < h_end) load(h0 + hpw);
+    }
+    const int h = h0 + own;
+    const bool is_q = h < a.nq;
+    if (of != (int)is_q) coefficients(is_q);
+    float v[U][2 * W], ss = 0.0f;
 #pragma unroll
-      for (int j = 0; j < U; ++j) ya[b][j] = xa[b][j], yb[b][j] = xb[b][j];
-    // (in place, the next heads lie outside what this batch writes)
-    if (h0 + hpw * B < h_end) load(h0 + hpw * B);
+    for (int j = 0; j < U; ++j)
 #pragma unroll
-    for (int b = 0; b < B; ++b) {
-      const int h = h0 + own + b * hpw;
-      const bool is_q = h < a.nq;
-      if (of != (int)is_q) coefficients(is_q);
-      float v[U][2 * W], ss = 0.0f;
-#pragma unroll
-      for (int j = 0; j < U; ++j)
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-          v[j][i] = to_f<X>(ya[b][j].v[i]);
-          v[j][W + i] = to_f<X>(yb[b][j].v[i]);
-          ss = on[j] ? fmaf(v[j][i], v[j][i], ss) : ss;
-          ss = both[j] ? fmaf(v[j][W + i], v[j][W + i], ss) : ss;
-        }
-      for (int o = L >> 1; o; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
-      const float r = (is_q ? a.gamma_q : a.gamma_k) ? rsqrtf(fmaf(ss, inv_d, a.eps)) : 1.0f;
-      T* out = is_q ? (T*)a.q + (int64_t)m * a.ldq + (int64_t)h * a.D : (T*)a.k + (int64_t)m * a.ldk + (int64_t)(h - a.nq) * a.D;
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        float y[2 * W];
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-          const float p = v[j][first_of(i)], q = v[j][second_of(i)];
-          y[first_of(i)] = (p * p1[j][i] - q * p2[j][i]) * r;
-          y[second_of(i)] = (q * q1[j][i] + p * q2[j][i]) * r;
-        }
-        Run<T, W> oa, ob;
-        if constexpr (W > 1) {
-#pragma unroll
-          for (int i = 0; i < W; i += 2) pair_of(y[i], y[i + 1], oa.v + i), pair_of(y[W + i], y[W + i + 1], ob.v + i);
-        } else {
-          oa.v[0] = from_f<T>(y[0]), ob.v[0] = from_f<T>(y[1]);
-        }
-        if (h < h_end && on[j]) *reinterpret_cast<Run<T, W>*>(out + ea[j]) = oa;
-        if (h < h_end && both[j]) *reinterpret_cast<Run<T, W>*>(out + eb[j]) = ob;
+      for (int i = 0; i < W; ++i) {
+        v[j][i] = to_f<X>(ya[j].v[i]);
+        v[j][W + i] = to_f<X>(yb[j].v[i]);
+        ss = on[j] ? fmaf(v[j][i], v[j][i], ss) : ss;
+        ss = both[j] ? fmaf(v[j][W + i], v[j][W + i], ss) : ss;
       }
+    for (int o = L >> 1; o; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
+    const float r = (is_q ? a.gamma_q : a.gamma_k) ? rsqrtf(fmaf(ss, inv_d, a.eps)) : 1.0f;
+    T* out = is_q ? (T*)a.q + (int64_t)m * a.ldq + (int64_t)h * a.D : (T*)a.k + (int64_t)m * a.ldk + (int64_t)(h - a.nq) * a.D;
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      float y[2 * W];
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        const float p = v[j][first_of(i)], q = v[j][second_of(i)];
+        float y1 = p * p1[j][i], y2 = q * q1[j][i];
+        // (not 0 times the other one, which may be infinite)
+        if (l + j * L < turned) y1 = fmaf(-q, p2[j][i], y1), y2 = fmaf(p, q2[j][i], y2);
+        y[first_of(i)] = y1 * r;
+        y[second_of(i)] = y2 * r;
+      }
+      Run<T, W> oa, ob;
+      if constexpr (W > 1) {
+#pragma unroll
+        for (int i = 0; i < W; i += 2) pair_of(y[i], y[i + 1], oa.v + i), pair_of(y[W + i], y[W + i + 1], ob.v + i);
+      } else {
+        oa.v[0] = from_f<T>(y[0]), ob.v[0] = from_f<T>(y[1]);
+      }
+      if (h < h_end && on[j]) *reinterpret_cast<Run<T, W>*>(out + ea[j]) = oa;
+      if (h < h_end && both[j]) *reinterpret_cast<Run<T, W>*>(out + eb[j]) = ob;
     }
   }
 }
 
-template <typename X, typename T, int W, int U, int B, bool SIDE>
+template <typename X, typename T, int W, int U, bool SIDE>
 cudaError_t run(const RopeArgs& a, cudaStream_t s) {
   const int units = W > 1 ? a.D / (2 * W) : a.rot / 2 + (a.D - a.rot + 1) / 2;
   int lanes_log = 0;
   while (lanes_log < 5 && (U << lanes_log) < units) ++lanes_log;
   // a warp for all heads of a token where tokens are many, for fewer heads otherwise
-  const int heads = (32 >> lanes_log) * B, batches = (a.nq + a.nk + heads - 1) / heads;
+  const int heads = 32 >> lanes_log, batches = (a.nq + a.nk + heads - 1) / heads;
   const int64_t want = (int64_t)dev_info().sms * 16;
   int splits = (int)((want + a.M - 1) / a.M);
   splits = splits < batches ? splits : batches;
   const int per = (batches + splits - 1) / splits;
   splits = (batches + per - 1) / per;
-  return launch_step(rope_kernel<X, T, W, U, B, SIDE>, dim3((unsigned)(((int64_t)a.M * splits + 3) / 4)), 128, 0, s, 1, a,
+  return launch_step(rope_kernel<X, T, W, U, SIDE>, dim3((unsigned)(((int64_t)a.M * splits + 3) / 4)), 128, 0, s, 1, a,
                      lanes_log, units, splits, per);
 }
 
@@ -193,13 +226,12 @@ cudaError_t typed(const RopeArgs& a, cudaStream_t s) {
     return a.D % (2 * w) == 0 && a.rot % (2 * w) == 0 && at(a.x, a.ld, sizeof(X)) && at(a.q, a.ldq, 2) && at(a.k, a.ldk, 2) &&
            at(a.gamma_q, 0, 2) && at(a.gamma_k, 0, 2);
   };
-  constexpr int B = sizeof(X) == 4 ? 1 : 2;
-  if (a.D <= 512 && whole(8)) return side ? run<X, T, 8, 1, B, true>(a, s) : run<X, T, 8, 1, B, false>(a, s);
-  if (a.D <= 256 && whole(4)) return side ? run<X, T, 4, 1, B, true>(a, s) : run<X, T, 4, 1, B, false>(a, s);
+  if (a.D <= 512 && whole(8)) return side ? run<X, T, 8, 1, true>(a, s) : run<X, T, 8, 1, false>(a, s);
+  if (a.D <= 256 && whole(4)) return side ? run<X, T, 4, 1, true>(a, s) : run<X, T, 4, 1, false>(a, s);
   // single elements: the layouts differ in places only
-  if (a.D <= 64) return side ? run<X, T, 1, 1, 2, true>(a, s) : run<X, T, 1, 1, 2, false>(a, s);
-  if (a.D <= 256) return side ? run<X, T, 1, 4, 1, true>(a, s) : run<X, T, 1, 4, 1, false>(a, s);
-  return side ? run<X, T, 1, 16, 1, true>(a, s) : run<X, T, 1, 16, 1, false>(a, s);
+  if (a.D <= 64) return side ? run<X, T, 1, 1, true>(a, s) : run<X, T, 1, 1, false>(a, s);
+  if (a.D <= 256) return side ? run<X, T, 1, 4, true>(a, s) : run<X, T, 1, 4, false>(a, s);
+  return side ? run<X, T, 1, 16, true>(a, s) : run<X, T, 1, 16, false>(a, s);
 }
 
 }  // namespace

@@ -114,6 +114,28 @@ def test_rope_in_place_and_values_stay():
         assert torch.equal(a[0][0], fq[m]) and torch.equal(a[1][0], fk[m])
 
 
+@pytest.mark.parametrize("layout", [0, 1])
+@pytest.mark.parametrize("D,rot", [(128, 64), (72, 40), (70, 20), (300, 100)])
+@pytest.mark.parametrize("M", [3, 3000])
+def test_rope_leaves_what_it_does_not_turn(M, D, rot, layout):
+    # an infinity there shows in its own place alone; one that is turned, in its pair's
+    q = qmv()
+    nq, nk = 9, 2
+    x = randn(D, M, (nq + nk) * D).to(F16)
+    h = x.view(M, nq + nk, D)
+    h[:, 1, rot + 3] = math.inf
+    h[:, 4, D - 1] = -math.inf
+    h[:, 10, rot] = math.nan
+    h[:, 2, 6] = math.inf
+    pos = torch.full((M,), 12345, device="cuda", dtype=torch.int32)
+    fq, fk = q.qmv_qk_norm_rope(x, nq, nk, D, q.Rope(rot, layout=layout), pos)
+    y = torch.cat((fq.reshape(M, nq, D), fk.reshape(M, nk, D)), 1)
+    assert torch.equal(torch.nan_to_num(y[:, :, rot:], 7.0), torch.nan_to_num(h[:, :, rot:], 7.0))
+    odd = torch.zeros(nq + nk, rot, dtype=torch.bool, device="cuda")
+    odd[2, 6] = odd[2, 7 if layout else (6 + rot // 2) % rot] = True
+    assert torch.equal(~torch.isfinite(y[:, :, :rot]), odd.expand(M, -1, -1))
+
+
 @pytest.mark.parametrize("scaling", ["NONE", "LINEAR", "NTK", "YARN"])
 @pytest.mark.parametrize("far", [1, 100_000, 2 ** 31 - 1])
 def test_rope_far_positions(scaling, far):
@@ -463,7 +485,7 @@ def test_sample(rows, V, k, p, m, dt):
 
 @pytest.mark.parametrize("dt", [F32, BF16])
 @pytest.mark.parametrize("k,p,m", [(50, 0.9, 0.0), (0, 0.9, 0.0), (0, 0.999, 0.001), (3000, 0.8, 0.0), (0, 1.0, 0.0), (2000, 1.0, 0.02)])
-@pytest.mark.parametrize("rows,V", [(320, 5001), (160, 20000), (40, 100_000), (1, 300_001), (2, 1 << 20)])
+@pytest.mark.parametrize("rows,V", [(320, 5001), (160, 20000), (40, 100_000), (1, 300_001), (2, 1 << 20), (6, 25601), (5, 8200)])
 def test_sample_many_and_long_rows(rows, V, k, p, m, dt):
     x = logits_like(V, rows, V).to(dt)
     check_sample(x, torch.rand(rows, generator=gen(V + k), device="cuda"), 0.8, k, p, m)
