@@ -1,19 +1,20 @@
 // qmv_route.cu -- the experts of each token and their weights (qmv_route).
 //
-// A warp takes a token and its lanes N neighbouring experts each, all in registers.  A group's
-// worth comes by exchanges within the warp where its experts are whole lanes', otherwise through shared
-// memory.  The lanes' largest ranks, sorted, give a bound that T + 1 experts reach; the few that
-// reach it, one a lane, are sorted into the answer.  Where T is large, or ties make them more than 32,
-// experts are taken one after another, each with a maximum over the warp.
+// A warp takes a token and its lanes N neighbouring experts each, all in registers.  A group's worth comes by
+// exchanges within the warp where its experts are whole lanes', otherwise through shared memory.  The lanes'
+// largest ranks, sorted, give a bound that T + 1 experts reach; the few that reach it, one a lane, are sorted
+// into the answer.  Where T is large, or ties make them more than 32, experts are taken one after another, each
+// with a maximum over the warp.
 //
-// Bound by instructions (16384 tokens of 256 experts: 62 us with a maximum over the warp an expert
-// and conditional loads, 36 with the sort, 43 % of that the tail of tokens ranked again in 64 bits).
+// Ranks are compared as exact arithmetic has them.  Without a bias they follow the logits, which are compared
+// themselves.  Otherwise fp32 ranks decide where neighbours in the order are further apart than their errors add
+// up to.  Where they are not (about one token in a thousand of 256 experts) the choice of groups, or the order
+// of the few, is formed again in 64 bits, or all of it where a softmax needs that.
 //
-// Ranks are compared as exact arithmetic has them.  Without a bias they follow the
-// logits, which are compared themselves.  Otherwise fp32 ranks decide where neighbours in
-// the order are further apart than their errors add up to.  Where they are not (about one token in a
-// thousand of 256 experts) the choice of groups, or the order of the few, is formed again in 64
-// bits, or all of it where a softmax needs that.
+// Bound by instructions where tokens are many, about a thousand a token: 16384 tokens of 256 experts in 8 groups
+// took 62 us with a maximum over the warp an expert and loads under conditions, 36 with unconditional loads and
+// the sort, 28 since only ranks that are near each other are formed in 64 bits (exchanges and compares; HBM
+// would take 2.6).  One token is bound by latency: 2.9 us.
 #include <math_constants.h>
 
 #include "qmv_token.cuh"
@@ -98,11 +99,12 @@ __device__ __forceinline__ float over(float a, float b) {
 
 // What a score may be off by in fp32.  A sigmoid 1 / (1 + e): e's error counts s (1 - s) times, and
 // x s (1 - s) is below 1/4, so 2^-25 + 2^-24; the sum 2^-24, the reciprocal 2^-23, the product 2^-24.  A
-// softmax, relative to itself: (x - max) 2^-22 (times p: below 2^-23), 2^-22, the sum of 32 sums of up
-// to 32 such terms, 2^-22.
+// softmax p = largest e^-d, d = max - x, relative to itself: d 2^-24 for its argument, expf's 2^-23, the sum of
+// 32 sums of up to 32 terms 37 2^-24, over() 2^-22: (43 + d) 2^-24.  As a number it is greatest for d = 0:
+// below 2^-18 of `largest`, what a score is at most.
 template <typename F>
-__device__ __forceinline__ F score_error(int score) {
-  return sizeof(F) == 8 ? (F)0 : score == QMV_SCORE_SIGMOID ? (F)0x1p-21 : (F)0x1p-18;
+__device__ __forceinline__ F score_error(int score, F largest) {
+  return sizeof(F) == 8 ? (F)0 : score == QMV_SCORE_SIGMOID ? (F)0x1p-21 : (F)0x1p-18 * largest;
 }
 
 template <typename F>
@@ -148,7 +150,7 @@ struct Groups {
 // The groups that remain, a bit each.  r: ranks, or logits without a bias; top: as scores() gives it;
 // rank: a warp's [E] in shared memory.
 template <typename F, int N>
-__device__ __forceinline__ uint32_t choose_groups(const RouteArgs& a, const F (&r)[N], float top, int lane, F* rank, Groups<F>* known) {
+__device__ __forceinline__ uint32_t choose_groups(const RouteArgs& a, const F (&r)[N], float top, F largest, int lane, F* rank, Groups<F>* known) {
   const F none = (F)(-CUDART_INF_F);
   const int per = a.per, lanes = per / N, e0 = lane * N;
   F one = none, two = none;                          // lane g: the largest of group g
@@ -206,7 +208,7 @@ __device__ __forceinline__ uint32_t choose_groups(const RouteArgs& a, const F (&
     const F last = __shfl_sync(~0u, worth, l), next = __shfl_sync(~0u, worth, m);
     const bool same = !a.bias && __shfl_sync(~0u, one, l) == __shfl_sync(~0u, one, m) &&
                       __shfl_sync(~0u, two, l) == __shfl_sync(~0u, two, m);
-    const F err = 4 * score_error<F>(a.score) + (F)0x1p-22 * (fabs(last) + fabs(next));
+    const F err = 4 * score_error<F>(a.score, a.bias ? largest : (F)1) + (F)0x1p-22 * (fabs(last) + fabs(next));
     known->sure = last - next > err || next == none || same;
     // a group's best two in exact arithmetic are among those that reach the second less their errors
     known->worth = worth, known->reach = (a.group_top == 2 ? two : one) - err, known->low = next - err, known->high = last + err;
@@ -239,7 +241,7 @@ __device__ __noinline__ uint32_t groups_wide(const RouteArgs& a, const float* xb
 #pragma unroll
   for (int i = 0; i < N; ++i) r[i] = x[i] == -CUDART_INF_F ? (double)x[i] : a.bias ? r[i] + (double)xb[N + i] : (double)x[i];
   Groups<double> known;
-  return choose_groups<double, N>(a, r, top, lane, rank, &known);
+  return choose_groups<double, N>(a, r, top, 1.0, lane, rank, &known);
 }
 
 // The same where a few groups are near each other: only their best experts' ranks are formed in 64 bits,
@@ -282,14 +284,15 @@ __device__ __noinline__ uint32_t groups_near(const RouteArgs& a, const float* xb
 // t / 32) with its logit.  Returns whether F could tell.
 template <typename F, int N>
 __device__ __noinline__ bool choose_each(const RouteArgs& a, const float* xb, uint32_t left, int lane, int (&id)[2], float (&of)[2]) {
-  const F none = (F)(-CUDART_INF_F), err = score_error<F>(a.score);
+  const F none = (F)(-CUDART_INF_F);
   const int e0 = lane * N;
   float x[N], b[N];
   F s[N], r[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) x[i] = xb[i], b[i] = xb[N + i];
-  F whole;
+  F whole = 1;
   scores<F, N>(x, a.score, s, &whole);
+  const F err = score_error<F>(a.score, 1 / whole);
 #pragma unroll
   for (int i = 0; i < N; ++i) r[i] = x[i] == -CUDART_INF_F ? none : a.bias ? s[i] + (F)b[i] : (F)x[i];
   leave_groups<F, N>(a, r, left, lane);
@@ -387,6 +390,7 @@ __global__ void __launch_bounds__(WARPS * 32, N <= 8 ? 10 : 4) route_kernel(Rout
   float s[N], r[N];
   float whole = 1.0f;
   const float top = scores<float, N>(x, a.score, s, &whole), none = -CUDART_INF_F;
+  const float largest = a.score == QMV_SCORE_SIGMOID ? 1.0f : whole > 0.0f ? 1.0f / whole : 0.0f;
 #pragma unroll
   for (int i = 0; i < N; ++i) r[i] = a.bias && x[i] != none ? s[i] + b[i] : x[i];
   const auto spill = [&](float (&xb)[2 * N]) {
@@ -397,7 +401,7 @@ __global__ void __launch_bounds__(WARPS * 32, N <= 8 ? 10 : 4) route_kernel(Rout
   if (a.groups > 1) {
     Groups<float> known;
     known.sure = true;
-    left = choose_groups<float, N>(a, r, top, lane, reinterpret_cast<float*>(ranks[warp]), &known);
+    left = choose_groups<float, N>(a, r, top, largest, lane, reinterpret_cast<float*>(ranks[warp]), &known);
     if (!known.sure) {
       float xb[2 * N], rb[N];
       spill(xb);
@@ -411,7 +415,7 @@ __global__ void __launch_bounds__(WARPS * 32, N <= 8 ? 10 : 4) route_kernel(Rout
 
   int id[2] = {-1, -1};
   float of[2] = {0.0f, 0.0f};                        // their logits
-  const float err2 = 2 * score_error<float>(a.score);
+  const float err2 = 2 * score_error<float>(a.score, largest);
   int n = 33;
   Few* few = all_few[warp];
   if (a.T <= MAX_SORTED) {
@@ -466,7 +470,12 @@ __global__ void __launch_bounds__(WARPS * 32, N <= 8 ? 10 : 4) route_kernel(Rout
     of[0] = f.x;
     if (a.bias) {
       const float key2 = __shfl_down_sync(~0u, key, 1);
-      const bool near = in && lane < 31 && key2 > none && !(key - key2 > err2 + 0x1p-22f * (fabsf(key) + fabsf(key2)));
+      float err = err2;
+      if (a.score != QMV_SCORE_SIGMOID) {            // by their own d, and what p itself is off by here
+        const float d = top - f.x, own = exp_of(-d) * largest * (48.0f + d) * 0x1p-24f + 0x1p-120f;
+        err = own + __shfl_down_sync(~0u, own, 1);
+      }
+      const bool near = in && lane < 31 && key2 > none && !(key - key2 > err + 0x1p-23f * (fabsf(key) + fabsf(key2)));
       if (__any_sync(~0u, near)) {
         // equal ones of the same logit and bias are truly equal
         const float x2 = __shfl_down_sync(~0u, f.x, 1), b2 = __shfl_down_sync(~0u, f.b, 1);
