@@ -3,7 +3,7 @@
 // A warp takes a token and its lanes N neighbouring experts each, all in registers.  A group's worth comes by
 // exchanges within the warp where its experts are whole lanes', otherwise through shared memory.  The lanes'
 // largest ranks, sorted, give a bound that T + 1 experts reach; the few that reach it, one a lane, are sorted
-// into the answer.  Where T is large, or ties make them more than 32, experts are taken one after another, each
+// into the answer.  Where T is 32 or more, or ties leave no bound that 32 reach, experts are taken one after another, each
 // with a maximum over the warp.
 //
 // Ranks are compared as exact arithmetic has them.  Without a bias they follow the logits, which are compared
@@ -24,7 +24,7 @@ namespace {
 
 typedef unsigned long long u64;
 constexpr int WARPS = 4, MAX_E = 1024;
-constexpr int MAX_SORTED = 24;     // picks by sorting: some more than T have to fit in 32
+constexpr int MAX_SORTED = 31;     // picks by sorting: one more than T have to fit in 32
 
 // One of the experts that may be chosen.
 struct alignas(16) Few {
@@ -419,37 +419,44 @@ __global__ void __launch_bounds__(WARPS * 32, N <= 8 ? 10 : 4) route_kernel(Rout
   int n = 33;
   Few* few = all_few[warp];
   if (a.T <= MAX_SORTED) {
-    // T + 1 experts reach the (T / k + 1)-th of the lanes' k-th largest.  The first alone will do where
-    // experts are left in many lanes; in few the others give a higher bound.
-    float best = r[0], bound = -3.402823466e38f;
+    // T + 1 experts reach the (T + 1)-th of the lanes' largest ranks.  Where more than 32 do, or experts are left
+    // in few lanes, halves of what lies between that and the largest rank of all lead to another bound.
+    float best = r[0];
 #pragma unroll
     for (int i = 1; i < N; ++i) best = fmaxf(best, r[i]);
-    uint32_t used = 0;
-    int mine = 0, at = 0;
-#pragma unroll 1
-    for (int k = 1; k <= N; ++k) {
-      float reach = __shfl_sync(~0u, sort_lanes(best, lane), k == 1 ? a.T : a.T / k);
-      if (a.bias) reach -= err2 + 0x1p-21f * fabsf(reach);     // and those that may do so but for their errors
-      bound = fmaxf(bound, reach);                             // (-inf, or inf - inf: as it was)
-      mine = 0;
+    best = sort_lanes(best, lane);
+    const auto reach = [&](float v) {
+      int c = 0;
 #pragma unroll
-      for (int i = 0; i < N; ++i) mine += r[i] >= bound;
-      at = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(~0u, at, o);
-        if (lane >= o) at += v;
+      for (int i = 0; i < N; ++i) c += r[i] >= v;
+      return c;
+    };
+    // and those that may do so but for their errors (-inf, or inf - inf: all that may be chosen)
+    const auto less = [&](float v) { return fmaxf(a.bias ? v - (err2 + 0x1p-21f * fabsf(v)) : v, -3.402823466e38f); };
+    float bound = less(__shfl_sync(~0u, best, a.T));
+    int mine = reach(bound);
+    n = __reduce_add_sync(~0u, mine);
+    if (n > 32) {
+      uint32_t low = ordered(__shfl_sync(~0u, best, a.T)), high = ordered(__shfl_sync(~0u, best, 0)) + 1;
+      while (high - low > 1) {             // T + 1 reach low, and not high
+        const uint32_t mid = low + (high - low) / 2;
+        const float v = unordered(mid);
+        if (__reduce_add_sync(~0u, reach(v)) <= a.T) {
+          high = mid;
+          continue;
+        }
+        low = mid;
+        bound = less(v);
+        mine = reach(bound);
+        n = __reduce_add_sync(~0u, mine);
+        if (n <= 32) break;
       }
-      n = __shfl_sync(~0u, at, 31);
-      if (n <= 32) break;
-      bool found = false;
+    }
+    int at = mine;
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (!found && !(used >> i & 1) && r[i] == best) found = true, used |= 1u << i;
-      best = none;
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (!(used >> i & 1)) best = fmaxf(best, r[i]);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(~0u, at, o);
+      if (lane >= o) at += v;
     }
     at -= mine;
     if (n <= 32) {

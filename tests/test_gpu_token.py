@@ -207,6 +207,7 @@ ROUTES = [
     (1, 1, 1, 1, 1, 1), (1, 64, 8, 1, 1, 1), (7, 5, 5, 1, 1, 1), (33, 100, 64, 1, 1, 1), (129, 156, 6, 12, 3, 2),
     (50, 256, 8, 8, 4, 2), (20, 512, 16, 4, 2, 1), (11, 1024, 33, 32, 7, 2), (9, 31, 2, 31, 5, 1), (300, 128, 1, 16, 16, 2),
     (5, 6, 3, 2, 1, 2), (64, 60, 10, 3, 2, 1), (3, 999, 40, 9, 4, 2),
+    (400, 384, 16, 1, 1, 1), (200, 512, 31, 1, 1, 1), (200, 1024, 24, 8, 2, 2), (100, 1024, 32, 1, 1, 1), (100, 300, 20, 2, 1, 1),
 ]
 
 
