@@ -13,7 +13,7 @@
 //
 // Bound by instructions where tokens are many, about a thousand a token: 16384 tokens of 256 experts in 8 groups
 // took 62 us with a maximum over the warp an expert and loads under conditions, 36 with unconditional loads and
-// the sort, 28 since only ranks that are near each other are formed in 64 bits (exchanges and compares; HBM
+// the sort, 27 since only ranks that are near each other are formed in 64 bits (exchanges and compares; HBM
 // would take 2.6).  One token is bound by latency: 2.9 us.
 #include <math_constants.h>
 

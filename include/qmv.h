@@ -720,7 +720,8 @@ QMV_API int qmv_w4_experts(const qmv_w4pack *p, int rows_per_expert, int M, int 
  *   logits  device [rows][V] of dtype (QMV_F32, QMV_F16 or QMV_BF16), row stride ldl.
  *   d_temperature, d_top_k, d_top_p, d_min_p  nullable device [rows] (int32 for top_k, fp32
  *           otherwise): a row's own setting; NULL takes the number beside it for all.
- *           Their values act as the nearest allowed ones, NaN as 0 (top_p: as 1).
+ *           Their values act as the nearest allowed ones, NaN as 0 (top_p: as 1); a T below 2^-100 that
+ *           is not 0 as that.
  *   u       device fp32 [rows] in [0, 1).
  *   tokens  device int32 [rows].
  *   rows >= 1; V 1 .. 2^20; temperature >= 0, top_k >= 0, top_p and min_p 0 .. 1.

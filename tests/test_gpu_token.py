@@ -400,6 +400,23 @@ def test_experts_rows_are_their_own():
         assert bool(((a[fin] - b[fin]).abs() <= tol).all())
 
 
+@pytest.mark.parametrize("M,T", [(3, 8), (16, 8), (17, 8), (64, 5)])
+def test_experts_that_a_token_has_twice(M, T):
+    # an id may stand more than once in a row, or none at all
+    q = qmv()
+    p, _, w = make_w4(6 * 64, 256, 64, True, F16, 8, exact=True)
+    x = torch.randint(-2, 3, (M, 256), generator=gen(M), device="cuda").to(F16)
+    ids = torch.randint(-1, 6, (M, T), generator=gen(T), device="cuda", dtype=torch.int32)
+    ids[0], ids[M - 1] = 4, -1
+    y = q.qmv_w4_experts(p, 64, ids, x)
+    # whole numbers: every partial sum is exact
+    all_of = torch.cat(((x.double() @ w.t()).view(M, 6, 64), torch.zeros(M, 1, 64, dtype=torch.float64, device="cuda")), 1)
+    ref = all_of.gather(1, torch.where(ids < 0, 6, ids).long()[:, :, None].expand(-1, -1, 64))
+    assert torch.equal(y.double(), ref)
+    none = q.qmv_w4_experts(p, 64, torch.full_like(ids, -1), x, weights=torch.ones(M, T, device="cuda"))
+    assert not bool(none.any()) and q.qmv_device_error(clear=True) == 0
+
+
 def test_experts_ids_out_of_range():
     q = qmv()
     p, _, w = make_w4(4 * 32, 128, 128, True, F16, 3)
