@@ -54,6 +54,7 @@ ROPE_SHAPES = [
     (4, 5, 0, 80, 16), (6, 0, 3, 96, 96), (3, 12, 4, 100, 50), (2, 32, 8, 256, 64), (33, 1, 1, 512, 512), (2, 3, 1, 1024, 1024),
     (2, 2, 2, 1023, 510), (300, 9, 3, 48, 48), (1000, 4, 1, 32, 30), (7, 1, 2, 1, 0), (5, 6, 2, 200, 0), (2500, 2, 1, 256, 256),
     (17, 40, 8, 16, 16), (3, 4, 4, 520, 8),
+    (2600, 20, 5, 72, 40), (2600, 20, 5, 128, 128), (2500, 11, 2, 256, 96),
 ]
 
 

@@ -247,6 +247,29 @@ def test_views_that_the_fast_form_leaves_to_the_other():
         q.qmv_route(wide.t(), 4)
 
 
+def test_the_python_form_gives_the_same(monkeypatch):
+    q = qmv()
+    assert not isinstance(q._host, q._NoHost)
+    p, _, _ = make_w4(6 * 64, 256, 64, True, BF16, 2)
+    x, g = randn(1, 9, 512), (randn(2, 64) * 0.2).to(BF16)
+    r, pos = q.Rope(64, scaling=q.QMV_SCALE_NTK, factor=4.0), torch.arange(9, device="cuda", dtype=torch.int32)
+    bias, lg = randn(3, 6), logits_like(4, 9, 5003)
+    u, per = torch.rand(9, generator=gen(5), device="cuda"), torch.rand(9, generator=gen(6), device="cuda")
+
+    def run():
+        out = list(q.qmv_qk_norm_rope(x, 4, 2, 64, r, pos, g, g, 1.0, 1e-5, q.QMV_BF16))
+        out += q.qmv_qk_norm_rope(x.to(F16), 4, 0, 64)[:1]
+        ids, w = q.qmv_route(x[:, :6].contiguous(), 2, q.QMV_SCORE_SIGMOID, bias, 3, 2, 2, True, 2.5)
+        out += [ids, w, q.qmv_w4_experts(p, 64, ids, x[:, :256].to(BF16).contiguous()),
+                q.qmv_w4_experts(p, 64, ids, x.to(BF16), weights=w, act=q.QMV_ACT_SILU, y_dtype=q.QMV_BF16)]
+        return out + [q.qmv_sample(lg, u, 0.7, 40, 0.9, 0.01), q.qmv_sample(lg, u, per, 0, per, per * 0.1)]
+
+    ref = run()
+    monkeypatch.setattr(q, "_host", q._NoHost())
+    for a, b in zip(run(), ref):
+        assert a.dtype == b.dtype and a.shape == b.shape and torch.equal(a, b)
+
+
 # As for the calls before these: the legacy stream may not be used while a stream that waits for it is
 # captured, so the runtime refuses the launch and nothing runs on the device.
 REFUSED = """

@@ -212,3 +212,8 @@ def test_binding_refuses_before_any_call(q):
         with pytest.raises(ValueError, match=text):
             f()
             raise AssertionError(f"case {i} ({text}) was not refused")
+
+
+def test_binding_refuses_the_same_without_its_cpp_form(q, monkeypatch):
+    monkeypatch.setattr(q, "_host", q._NoHost())
+    test_binding_refuses_before_any_call(q)
