@@ -116,9 +116,9 @@ struct Shared {
   u64 told[2][MAX_C][3];         // what the CTAs of the cluster tell each other
   u64 octaves[MAX_C][OCTAVES];   // and of the octaves of weights: ids, and sums of their bins
   uint32_t ends[2 << SUB_LOG];   // the bins of the two octaves that hold a range's ends
-  uint32_t start[NT];            // where buckets begin
+  uint32_t start[NT];            // where buckets begin; the threads' largest logits
   u64 cut;
-  uint32_t sub[256];
+  uint32_t sub[NW];
   uint32_t top, bound, n;
   int o[2], i[2];                // the octaves, and the bins that end the range
 };
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(NT, 2) draw_kernel(DrawArgs a, int C, int four
   const bool short_row = C == 1 && V <= MAX_CAND;
   const int part = NW * fours * 128, here = max(0, min(part, V + shift - rank * part));
   const int most_per = (int)(((int64_t)k * min(part, V) + V - 1) / V);   // the same for all CTAs
-  const bool few = !greedy && (short_row || (k_on && k <= MAX_FEW && most_per <= 128));
+  const bool few = !greedy && (short_row || (k_on && k <= MAX_FEW && most_per <= NT / 2));
   const int per = few ? (int)(((int64_t)k * min(here, V) + V - 1) / V) : 0;
   float most = -CUDART_INF_F;
   each(ahead, [&](int, const float(&w)[4]) { most = fmaxf(fmaxf(most, fmaxf(w[0], w[1])), fmaxf(w[2], w[3])); });
@@ -297,22 +297,28 @@ __global__ void __launch_bounds__(NT, 2) draw_kernel(DrawArgs a, int C, int four
   if (lane == 0) atomicMax(&S.top, warp_top);
   uint32_t bound = 0;
   if (few && !short_row) {
-    // the largest of every warp, eight lanes or two: twice as many as are wanted, or more
-    const int lanes = most_per <= 8 ? 32 : most_per <= 32 ? 8 : 2, n = NT / lanes;
-    if (tid == 0) S.bound = ~0u;           // of a CTA that has no share
-    __syncthreads();
-    uint32_t m = key;
-    for (int o = 1; o < lanes; o <<= 1) m = max(m, __shfl_xor_sync(~0u, m, o));
-    if (lane % lanes == 0) S.sub[tid / lanes] = m;
-    __syncthreads();
-    if (tid < n) {
-      const uint32_t own = S.sub[tid];
-      int above = 0;
-      for (int i = 0; i < n; ++i) above += S.sub[i] > own || (S.sub[i] == own && i < tid);
-      if (above == per - 1) S.bound = own;
+    if (most_per > 32) {
+      // the largest of every thread, of which twice as many as are wanted: the bits of the last wanted one
+#pragma unroll 1
+      for (uint32_t bit = 1u << 31; bit; bit >>= 1)
+        if (__syncthreads_count(key >= (bound | bit)) >= per) bound |= bit;
+    } else {
+      // the largest of every warp or eight lanes
+      const int lanes = most_per <= 8 ? 32 : 8, n = NT / lanes;
+      if (tid == 0) S.bound = ~0u;         // of a CTA that has no share
+      uint32_t m = key;
+      for (int o = 1; o < lanes; o <<= 1) m = max(m, __shfl_xor_sync(~0u, m, o));
+      if (lane % lanes == 0) S.start[tid / lanes] = m;
+      __syncthreads();
+      if (tid < n) {
+        const uint32_t own = S.start[tid];
+        int above = 0;
+        for (int i = 0; i < n; ++i) above += S.start[i] > own || (S.start[i] == own && i < tid);
+        if (above == per - 1) S.bound = own;
+      }
+      __syncthreads();
+      bound = S.bound;
     }
-    __syncthreads();
-    bound = S.bound;
   } else {
     __syncthreads();
   }
@@ -812,6 +818,10 @@ cudaError_t run(const DrawArgs& a, int C, int fours, cudaStream_t s) {
 // CTAs a row: so many that each thread has two fours, but no more than run at once, or twice as many
 // while a thread has more than 16 (128 rows of 262144: 205 us with two CTAs a row, 186 with four, 210 with
 // eight; 32 rows: 75, 60 and 103 with four, eight and sixteen; 512 rows of 32000: 101 and 134 with one and two).
+// One CTA is enough where a thread has four fours at most, since its barriers cost less than a
+// cluster's (a row of 6000 with top-k 50: 11.3 us, 12.6 with two).  A cluster of 16 keeps one of the eight parts of the
+// GPU to itself, so more rows than these have them only for long rows (9 rows of 50257, top-k 50: 14.7 us with sixteen
+// CTAs and 12.0 with eight; one row 11.2 and 11.5).
 template <typename X>
 cudaError_t typed(const DrawArgs& a, cudaStream_t s) {
   const bool even = (a.rows == 1 || a.ldx % 4 == 0) && (uintptr_t)a.x % (4 * sizeof(X)) == 0;
@@ -819,7 +829,10 @@ cudaError_t typed(const DrawArgs& a, cudaStream_t s) {
   const auto fours = [&](int C) { return (elements + C * NT * 4 - 1) / (C * NT * 4); };
   int C = 1;
   const int64_t at_once = 2 * dev_info().sms;
-  while (C < MAX_C && (fours(C) > 2 && C * 2 * (int64_t)a.rows <= at_once || fours(C) > 16 && C * (int64_t)a.rows <= at_once)) C *= 2;
+  if (fours(1) > 4)
+    while (C < MAX_C && (fours(C) > 2 && C * 2 * (int64_t)a.rows <= at_once || fours(C) > 16 && C * (int64_t)a.rows <= at_once) &&
+           !(C == 8 && a.rows > 8 && fours(C) <= 4))
+      C *= 2;
   return run<X>(a, C, fours(C), s);
 }
 

@@ -503,8 +503,8 @@ def test_sample(rows, V, k, p, m, dt):
 
 
 @pytest.mark.parametrize("dt", [F32, BF16])
-@pytest.mark.parametrize("k,p,m", [(50, 0.9, 0.0), (0, 0.9, 0.0), (0, 0.999, 0.001), (3000, 0.8, 0.0), (0, 1.0, 0.0), (2000, 1.0, 0.02)])
-@pytest.mark.parametrize("rows,V", [(320, 5001), (160, 20000), (40, 100_000), (1, 300_001), (2, 1 << 20), (6, 25601), (5, 8200)])
+@pytest.mark.parametrize("k,p,m", [(50, 0.9, 0.0), (0, 0.9, 0.0), (0, 0.999, 0.001), (3000, 0.8, 0.0), (0, 1.0, 0.0), (2000, 1.0, 0.02), (200, 0.95, 0.0), (256, 1.0, 0.0)])
+@pytest.mark.parametrize("rows,V", [(320, 5001), (160, 20000), (40, 100_000), (1, 300_001), (2, 1 << 20), (6, 25601), (5, 8200), (6, 7000)])
 def test_sample_many_and_long_rows(rows, V, k, p, m, dt):
     x = logits_like(V, rows, V).to(dt)
     check_sample(x, torch.rand(rows, generator=gen(V + k), device="cuda"), 0.8, k, p, m)
