@@ -344,6 +344,18 @@ __device__ __noinline__ void order_wide(const RouteArgs& a, const Few* few, int 
   *of = few[who & 31].x;
 }
 
+// Weights over their sum where that is small: each relative to the largest of them, so that scores below
+// the smallest fp32 number keep their shares (a score that fp32 holds to 2^-150 is off by
+// 2^-126 of a sum of 2^-24).  v: logits of a lane's two picks, -inf where there is none.
+__device__ __noinline__ float2 small_shares(const RouteArgs& a, float v0, float v1, float top, bool sigmoids) {
+  const float m = warp_max(fmaxf(v0, v1));
+  const auto share_of = [&](float v) { return v == -CUDART_INF_F ? 0.0f : expf(v - m) / (sigmoids ? 1.0f + expf(v) : 1.0f); };
+  const float w0 = share_of(v0), w1 = share_of(v1), sum = warp_total(w0 + w1);
+  // the sum is 0 where it is so in 64 bits
+  const float f = exp((double)m - (sigmoids ? 0.0 : (double)top)) > 0.0 ? a.scale / sum : 0.0f;
+  return make_float2(w0 * f, w1 * f);
+}
+
 template <typename X, int N, bool VEC>
 __global__ void __launch_bounds__(WARPS * 32, N <= 8 ? 10 : 4) route_kernel(RouteArgs a) {
   __shared__ double ranks[WARPS][N * 32];
@@ -516,7 +528,12 @@ __global__ void __launch_bounds__(WARPS * 32, N <= 8 ? 10 : 4) route_kernel(Rout
   float f = a.scale;
   if (a.renorm) {
     const float sum = warp_total(w[0] + w[1]);
-    f = sum > 0.0f ? a.scale / sum : 0.0f;
+    if (sum >= 0x1p-24f) {
+      f = a.scale / sum;
+    } else {
+      const float2 v = small_shares(a, id[0] >= 0 ? of[0] : none, id[1] >= 0 ? of[1] : none, top, a.score == QMV_SCORE_SIGMOID);
+      w[0] = v.x, w[1] = v.y, f = 1.0f;
+    }
   }
 #pragma unroll
   for (int p = 0; p < 2; ++p)

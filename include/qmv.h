@@ -649,7 +649,7 @@ QMV_API int qmv_qk_norm_rope(int M, int n_q, int n_k, int D, const void *qkv, in
  *   with groups > 1 (of E / groups neighbouring experts): a group counts the sum of its
  *   group_top largest r, and only the experts of the best group_k groups remain;
  *   ids = the T largest r, the largest first;  weights = s of those, over their sum where
- *   renormalise is not 0 (0 where that sum is 0), times scale.
+ *   renormalise is not 0 (0 where that sum is 0 in 64 bits), times scale.
  * Equal ones go to the lowest index.  r is compared as 64-bit arithmetic would have it: where
  * fp32 cannot tell two apart they are formed again in 64 bits; without bias the
  * logits themselves are compared.  Weights are fp32, within 2^-20 of themselves.

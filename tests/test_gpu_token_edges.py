@@ -1,0 +1,50 @@
+"""Edges of the decode-step operators that their other tests leave out, each against 64 bits or
+the definition in the header."""
+import math
+
+import pytest
+import torch
+
+from gpu_util import GuardBuf, qmv
+from test_gpu_step import BF16, EPS, F16, F32, TINY, gen, make_w4
+from test_gpu_token import act_ref, distinct, randn, route_ref
+
+pytestmark = pytest.mark.gpu
+
+
+# ----------------------------------------------------------------- route --
+
+def check_shares(x, T, score, bias=None, renorm=True, scale=1.0):
+    """check_route without its smallest sum of 1e-300: weights over their sum in 64 bits, 0 where that is 0."""
+    q = qmv()
+    ids, w = q.qmv_route(x, T, score=score, bias=bias, renormalise=renorm, scale=scale)
+    ref, _ = route_ref(x, T, score, bias, 1, 1, 1, renorm, scale)
+    assert torch.equal(ids, ref)
+    v = x.double()
+    s = 1 / (1 + torch.exp(-v)) if score else torch.softmax(v, 1)
+    rw = s.gather(1, ref.long())
+    if renorm:
+        total = rw.sum(1, keepdim=True)
+        rw = torch.where(total > 0, rw / total, 0.0)
+    tol = rw * scale * 2.0 ** -20 + 2.0 ** -126 * scale
+    assert bool(((w.double() - rw * scale).abs() <= tol).all()), float(((w.double() - rw * scale).abs() / tol).max())
+
+
+@pytest.mark.parametrize("T", [1, 8, 40])
+@pytest.mark.parametrize("scale", [1.0, 2.5])
+@pytest.mark.parametrize("level", [-5.0, -17.0, -40.0, -87.0, -89.0, -100.0, -104.0, -150.0, -700.0, -800.0])
+def test_route_weights_of_small_scores(level, scale, T):
+    # scores near or below the smallest fp32 number: their shares of their sum are as large as any
+    E = 64
+    x = level - 3 * torch.rand(20, E, generator=gen(T), device="cuda")
+    check_shares(x, T, 1, None, True, scale)
+    check_shares(x, T, 1, None, False, scale)
+    # the same of a softmax, where the bias takes experts far below the largest: every row has one logit of 0
+    y = torch.cat((torch.zeros(20, 1, device="cuda"), x), 1)
+    bias = torch.ones(E + 1, device="cuda") + 0.1 * torch.rand(E + 1, generator=gen(9), device="cuda")
+    bias[0] = -5.0
+    check_shares(y, T, 0, bias, True, scale)
+    check_shares(y, T, 1, bias, True, scale)
+    # and small ones beside one that is not
+    bias[0] = 5.0
+    check_shares(y, T, 1, bias, True, scale)
