@@ -344,12 +344,21 @@ __device__ __noinline__ void order_wide(const RouteArgs& a, const Few* few, int 
   *of = few[who & 31].x;
 }
 
+// exp(v - top), v <= top, within 2^-21 of itself: what the difference is rounded by, up to 2^-18 of a distance
+// of 64, is put right behind it.
+__device__ __forceinline__ float exp_below(float v, float top) {
+  const float d = v - top, back = d + top;                 // d = v - top + (what follows)
+  const float off = (v - back) - (top - (back - d));
+  const float e = expf(d);
+  return e > 0.0f ? fmaf(e, off, e) : 0.0f;
+}
+
 // Weights over their sum where that is small: each relative to the largest of them, so that scores below
 // the smallest fp32 number keep their shares (a score that fp32 holds to 2^-150 is off by
 // 2^-126 of a sum of 2^-24).  v: logits of a lane's two picks, -inf where there is none.
 __device__ __noinline__ float2 small_shares(const RouteArgs& a, float v0, float v1, float top, bool sigmoids) {
   const float m = warp_max(fmaxf(v0, v1));
-  const auto share_of = [&](float v) { return v == -CUDART_INF_F ? 0.0f : expf(v - m) / (sigmoids ? 1.0f + expf(v) : 1.0f); };
+  const auto share_of = [&](float v) { return v == -CUDART_INF_F ? 0.0f : exp_below(v, m) / (sigmoids ? 1.0f + expf(v) : 1.0f); };
   const float w0 = share_of(v0), w1 = share_of(v1), sum = warp_total(w0 + w1);
   // the sum is 0 where it is so in 64 bits
   const float f = exp((double)m - (sigmoids ? 0.0 : (double)top)) > 0.0 ? a.scale / sum : 0.0f;
@@ -521,8 +530,8 @@ __global__ void __launch_bounds__(WARPS * 32, N <= 8 ? 10 : 4) route_kernel(Rout
   for (int p = 0; p < 2; ++p) {
     w[p] = 0.0f;
     if (lane + 32 * p < a.T && id[p] >= 0) {
-      const float v = of[p], e = expf(a.score == QMV_SCORE_SIGMOID ? -fabsf(v) : v - top);
-      w[p] = a.score == QMV_SCORE_SIGMOID ? (v >= 0.0f ? 1.0f : e) / (1.0f + e) : v == top ? 1.0f / whole : e / whole;
+      const float v = of[p], e = a.score == QMV_SCORE_SIGMOID ? expf(-fabsf(v)) : v == top ? 1.0f : exp_below(v, top);
+      w[p] = a.score == QMV_SCORE_SIGMOID ? (v >= 0.0f ? 1.0f : e) / (1.0f + e) : e / whole;
     }
   }
   float f = a.scale;

@@ -48,3 +48,19 @@ def test_route_weights_of_small_scores(level, scale, T):
     # and small ones beside one that is not
     bias[0] = 5.0
     check_shares(y, T, 1, bias, True, scale)
+
+
+@pytest.mark.parametrize("T", [8, 40])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_weights_far_below_the_largest(renorm, T):
+    # the distance to the largest logit has to be known to 2^-21, which its fp32 difference does not say beyond 8
+    E = 41
+    x = -16 - 60 * torch.rand(300, E, generator=gen(T), device="cuda")
+    x[:, 7] = torch.rand(300, generator=gen(1), device="cuda") + 0.3
+    check_shares(x, T, 0, None, renorm)
+    bias = torch.zeros(E, device="cuda")
+    bias[7] = -5.0
+    bias[20:] = 1.0
+    check_shares(x, min(T, 20), 0, bias, renorm)
+    x[:, 7] = -20 - torch.rand(300, generator=gen(2), device="cuda")
+    check_shares(x, T, 1, None, renorm)
