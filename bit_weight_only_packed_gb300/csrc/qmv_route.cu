@@ -194,7 +194,7 @@ __device__ __forceinline__ uint32_t choose_groups(const RouteArgs& a, const F (&
     const auto score_of = [&](F v) {
       return v == none ? none : a.score == QMV_SCORE_SIGMOID ? sigmoid(v) : v == (F)top ? (F)1 : exp_of(v - (F)top);
     };
-    worth = a.bias ? one + two : score_of(one) + score_of(two);
+    worth = two == none ? none : a.bias ? one + two : score_of(one) + score_of(two);
   }
   int better = 0;
   for (int j = 0; j < a.groups; ++j) {
@@ -267,7 +267,7 @@ __device__ __noinline__ uint32_t groups_near(const RouteArgs& a, const float* xb
     const double v = __shfl_sync(~0u, rank, j);
     if (few[j].e == lane) two = fmax(two, fmin(one, v)), one = fmax(one, v);
   }
-  const double worth = a.group_top == 2 ? one + two : one;
+  const double worth = a.group_top == 1 ? one : two == -CUDART_INF ? two : one + two;
   const bool mine = lane < a.groups && (near >> lane & 1);
   int better = 0;
   for (int j = 0; j < a.groups; ++j) {

@@ -654,8 +654,8 @@ QMV_API int qmv_qk_norm_rope(int M, int n_q, int n_k, int D, const void *qkv, in
  * fp32 cannot tell two apart they are formed again in 64 bits; without bias the
  * logits themselves are compared.  Weights are fp32, within 2^-20 of themselves.
  * An expert whose logit or bias is NaN or -inf is never chosen (nor counted in a
- * group, as -inf); places that are left over hold id -1 and weight 0.  Logits of +inf
- * share a softmax evenly.
+ * group, as -inf: with group_top 2 a group of one expert alone counts as -inf); places
+ * that are left over hold id -1 and weight 0.  Logits of +inf share a softmax evenly.
  *   logits   device [M][E] of dtype (QMV_F32, QMV_F16 or QMV_BF16), row stride ldl.
  *   bias     nullable device fp32 [E].
  *   ids      device int32 [M][T], as qmv_w4_experts and (a row at a time) qmv_gemv_gather take them.

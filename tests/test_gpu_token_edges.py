@@ -64,3 +64,22 @@ def test_route_weights_far_below_the_largest(renorm, T):
     check_shares(x, min(T, 20), 0, bias, renorm)
     x[:, 7] = -20 - torch.rand(300, generator=gen(2), device="cuda")
     check_shares(x, T, 1, None, renorm)
+
+
+@pytest.mark.parametrize("per", [4, 8, 5])
+@pytest.mark.parametrize("score", [0, 1])
+def test_route_groups_with_fewer_than_two_experts(score, per):
+    # such a group counts as -inf, whatever its only expert's rank is
+    q = qmv()
+    groups, M = 4, 6
+    E = groups * per
+    x = randn(per, M, E)
+    x[:, 1:per] = -math.inf                     # the first group has its first expert alone
+    bias = torch.zeros(E, device="cuda")
+    bias[0] = math.inf
+    for group_k in (1, 2, 3):
+        ids, w = q.qmv_route(x, 3, score=score, bias=bias, groups=groups, group_k=group_k, group_top=2)
+        rest, rw = q.qmv_route(x[:, per:].contiguous(), 3, score=score, bias=bias[per:].contiguous(), groups=3, group_k=group_k, group_top=2)
+        assert torch.equal(ids, rest + per), (ids, rest)
+    ids, _ = q.qmv_route(x, 3, score=score, bias=bias, groups=groups, group_k=4, group_top=2)
+    assert bool((ids[:, 0] == 0).all())         # where all groups stay it comes first
