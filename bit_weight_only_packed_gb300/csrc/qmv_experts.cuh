@@ -55,15 +55,12 @@ struct ExpertsPlan {
 // The error word of this translation unit.
 static __device__ int g_x_error = 0;
 
-// act(gate) * up, rounded to x's type: its bits, and its value.
+// act(gate) * up, rounded to x's type: its bits, and its value.  Both are g / (1 + e^-t), t = g or, since
+// (1 + tanh s) / 2 = 1 / (1 + e^-2s), twice GELU's argument: no difference takes bits away, and e^-|t|
+// does not overflow (1 + tanh s in fp32 has lost all of them at g = -5.5, g / (1 + e^-g) at -89).
 __device__ __forceinline__ uint32_t gated_bits(float g, float u, int act, int bf16) {
-  float v;
-  if (act == QMV_ACT_SILU) {
-    v = g / (1.0f + expf(-g)) * u;
-  } else {
-    const float t = 0.7978845608028654f * (g + 0.044715f * g * g * g);
-    v = 0.5f * g * (1.0f + tanhf(t)) * u;
-  }
+  const float t = act == QMV_ACT_SILU ? g : 1.5957691216057308f * (g + 0.044715f * g * g * g), e = expf(-fabsf(t));
+  const float v = (t >= 0.0f ? g : g * e) / (1.0f + e) * u;
   return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
 }
 __device__ __forceinline__ float gated(float g, float u, int act, int bf16) {

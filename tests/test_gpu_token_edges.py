@@ -83,3 +83,35 @@ def test_route_groups_with_fewer_than_two_experts(score, per):
         assert torch.equal(ids, rest + per), (ids, rest)
     ids, _ = q.qmv_route(x, 3, score=score, bias=bias, groups=groups, group_k=4, group_top=2)
     assert bool((ids[:, 0] == 0).all())         # where all groups stay it comes first
+
+
+# --------------------------------------------------------------- experts --
+
+def one_to_one(dt):
+    """A pack whose product with x is x: 32 rows of 32, code 9 on the diagonal and 8, which is zero, elsewhere."""
+    codes = torch.full((32, 32), 8, device="cuda", dtype=torch.uint8)
+    codes.fill_diagonal_(9)
+    return qmv().W4Pack(32, 32, 32, dt, False).pack_weights(codes, torch.ones(32, 1, device="cuda", dtype=dt))
+
+
+@pytest.mark.parametrize("dt", [F16, BF16])
+@pytest.mark.parametrize("act", [1, 2])
+@pytest.mark.parametrize("M", [16, 700])
+def test_experts_gates_far_below_zero(M, act, dt):
+    # the activation there is a small number, and as many bits of it are right as of any other
+    q = qmv()
+    g = torch.linspace(-95.0 if act == 1 else -10.0, 3.0, M, device="cuda").to(dt)
+    x = torch.cat((g[:, None].expand(M, 32), torch.ones(M, 32, device="cuda", dtype=dt)), 1).contiguous()
+    y = q.qmv_w4_experts(one_to_one(dt), 32, torch.zeros(M, 1, device="cuda", dtype=torch.int32), x[:, None], act=act)[:, 0].double()
+    v = act_ref(x, act)
+    if act == 2:                                # (1 + tanh t) / 2 = 1 / (1 + exp(-2 t)), without its cancellation
+        a = x[:, :32].double()
+        v = a / (1 + torch.exp(-2 * math.sqrt(2 / math.pi) * (a + 0.044715 * a ** 3)))
+    # The exponent t is formed by up to five roundings: t 2^-21 of the exponential; that itself, a sum, a product,
+    # a quotient: 2^-21 in all.  An exponential below 2^-126 is a multiple of 2^-149, of which g are taken.
+    a = x[:, :32].double().abs()
+    t = a if act == 1 else 2 * math.sqrt(2 / math.pi) * (a + 0.044715 * a ** 3)
+    near = v.abs() * (t * 2.0 ** -21 + 2.0 ** -21) + a * 2.0 ** -149
+    tol = near + (v.abs() + near) * EPS[dt] + TINY[dt]
+    err = (y - v).abs()
+    assert bool((err <= tol).all()), (float((err / tol).max()), x[(err / tol).max(1).values.argmax(), 0].item())
