@@ -168,8 +168,8 @@ __global__ void __launch_bounds__(128) combine_kernel(ExpertsArgs a, const float
   __shared__ int in[64];
   const int m = blockIdx.y, r = (blockIdx.x * 128 + threadIdx.x) * 4;
   if (threadIdx.x < a.T) {
-    in[threadIdx.x] = (unsigned)a.ids[m * a.T + threadIdx.x] < (unsigned)a.E;
-    w[threadIdx.x] = a.weights[m * a.T + threadIdx.x];
+    in[threadIdx.x] = (unsigned)ld_early(a.ids + m * a.T + threadIdx.x) < (unsigned)a.E;
+    w[threadIdx.x] = ld_early(a.weights + m * a.T + threadIdx.x);
   }
   pdl_begin();
   __syncthreads();

@@ -76,7 +76,7 @@ __device__ __forceinline__ void sort_own(const ExpertsArgs& a, int cols, int* he
   int e = INT32_MAX;                       // behind all
   if (tid < X_OWN) {
     if (tid < P) {
-      e = a.ids[tid];
+      e = ld_early(a.ids + tid);
       if (e < -1 || e >= a.E) atomicCAS(&g_x_error, 0, pipe::ERR_BAD_EXPERT);
       if ((unsigned)e >= (unsigned)a.E) e = a.E;           // those without an expert come last
     }

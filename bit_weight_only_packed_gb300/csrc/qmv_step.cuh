@@ -107,10 +107,15 @@ cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s);
 // A launch on s in clusters of `cluster` CTAs along x, as a programmatic
 // dependent of the kernel before it: its CTAs may start while that one still
 // drains, and every kernel launched here waits for it (griddepcontrol.wait)
-// before it touches global memory, so that only the launch itself overlaps.  (The
-// matvec with early weights reads those before it waits.)  Each lets its own dependents
-// start after that wait and not before, so what runs early runs ahead of one kernel
-// only: all before that one have ended, and what they wrote can be read.
+// before it touches global memory, so that only the launch itself overlaps.  Each lets
+// its own dependents start after that wait and not before, so what runs early runs ahead
+// of one kernel only: all before that one have ended.  Three read something before their
+// wait, and so need a kernel right before them that waits before it lets them start:
+//   the matvec with early weights (qmv_set_pdl): packed weights, by bulk copies;
+//   the experts' products behind the kernel that makes x: ids (ld_early) and packed weights, by bulk copies;
+//   the sums of the experts' products: ids and their weights (ld_early).
+// None of these is what the kernel right before writes.  Ids and their weights change at every
+// step, in place, so they are read from L2, where all that has ended has left its writes.
 // (43008x5376 for one token, call after call: 28.7 us without, 25.8 us with.)
 template <typename... P, typename... A>
 inline cudaError_t launch_step(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, int cluster,

@@ -6,6 +6,19 @@
 
 namespace qmv {
 
+// What is read before the wait for the kernel before (see launch_step): from L2, past lines of L1 that
+// may be older than a write two kernels back.
+__device__ __forceinline__ int ld_early(const int* p) {
+  int v;
+  asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ float ld_early(const float* p) {
+  float v;
+  asm volatile("ld.relaxed.gpu.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
+
 struct RopeArgs {
   int M, nq, nk, D;
   const void* x;

@@ -115,3 +115,26 @@ def test_experts_gates_far_below_zero(M, act, dt):
     tol = near + (v.abs() + near) * EPS[dt] + TINY[dt]
     err = (y - v).abs()
     assert bool((err <= tol).all()), (float((err / tol).max()), x[(err / tol).max(1).values.argmax(), 0].item())
+
+
+@pytest.mark.parametrize("dt", [F16, BF16])
+def test_experts_ids_and_weights_written_again_in_place(dt):
+    # a decode loop keeps its buffers: each step's ids and weights lie where the last one's lay
+    q = qmv()
+    M, E, T, R, K, steps = 4, 32, 4, 64, 256, 150
+    p, _, _ = make_w4(E * R, K, 64, True, dt, 6)
+    x = randn(1, M, K).to(dt)
+    logits = randn(2, steps, M, E)
+    ids, w = torch.empty(M, T, device="cuda", dtype=torch.int32), torch.empty(M, T, device="cuda")
+    ws = q.qmv_w4_experts_workspace(p, R, M, T)
+    torch.cuda.synchronize()
+    outs = []
+    for i in range(steps):
+        q.qmv_route(logits[i], T, ids=ids, weights=w)
+        outs.append((q.qmv_w4_experts(p, R, ids, x, weights=w, workspace=ws), q.qmv_w4_experts(p, R, ids, x, workspace=ws)))
+    torch.cuda.synchronize()
+    for i in range(steps):
+        a, b = q.qmv_route(logits[i], T)
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i][0], q.qmv_w4_experts(p, R, a, x, weights=b)), i
+        assert torch.equal(outs[i][1], q.qmv_w4_experts(p, R, a, x)), i
