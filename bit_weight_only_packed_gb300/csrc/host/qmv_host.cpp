@@ -29,12 +29,15 @@ decltype(&qmv_qk_norm_rope) f_rope;
 decltype(&qmv_route) f_route;
 decltype(&qmv_w4_experts) f_experts;
 decltype(&qmv_w4_experts_workspace_bytes) f_experts_ws;
+decltype(&qmv_w4_experts_form) f_experts_form;
+decltype(&qmv_w4_experts_form_bytes) f_experts_form_ws;
 decltype(&qmv_sample) f_sample;
 
 // init(function addresses): the library is loaded by the binding
 PyObject* init(PyObject*, PyObject* args) {
-  unsigned long long f[9];
-  if (!PyArg_ParseTuple(args, "KKKKKKKKK", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7], &f[8])) return nullptr;
+  unsigned long long f[11];
+  if (!PyArg_ParseTuple(args, "KKKKKKKKKKK", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7], &f[8], &f[9], &f[10]))
+    return nullptr;
   f_w4 = reinterpret_cast<decltype(f_w4)>(f[0]);
   f_norm = reinterpret_cast<decltype(f_norm)>(f[1]);
   f_softmax = reinterpret_cast<decltype(f_softmax)>(f[2]);
@@ -43,7 +46,9 @@ PyObject* init(PyObject*, PyObject* args) {
   f_route = reinterpret_cast<decltype(f_route)>(f[5]);
   f_experts = reinterpret_cast<decltype(f_experts)>(f[6]);
   f_experts_ws = reinterpret_cast<decltype(f_experts_ws)>(f[7]);
-  f_sample = reinterpret_cast<decltype(f_sample)>(f[8]);
+  f_experts_form = reinterpret_cast<decltype(f_experts_form)>(f[8]);
+  f_experts_form_ws = reinterpret_cast<decltype(f_experts_form_ws)>(f[9]);
+  f_sample = reinterpret_cast<decltype(f_sample)>(f[10]);
   Py_RETURN_NONE;
 }
 
@@ -288,23 +293,25 @@ PyObject* w4_experts(PyObject* const* a, Py_ssize_t n) {
   const int xd = type_of(*x);
   void *w, *st, *ws = nullptr;
   if ((xd != QMV_F16 && xd != QMV_BF16) || !of(a[6], dev, at::kFloat, {M, T}, true, &w) || !stream_of(dev, &st)) return leave();
-  const size_t need = f_experts_ws(p, R, static_cast<int>(M), static_cast<int>(T));
-  size_t have = need;
+  size_t have;
   at::Tensor made;
-  if (a[9] != Py_None) {
+  const bool own = a[9] == Py_None;        // scratch for this call's form alone
+  if (!own) {
     const at::Tensor* given = tensor(a[9], dev);
     if (!given) return leave();
     have = given->nbytes();
     ws = given->data_ptr();
-    if (have < need) return leave();
-  } else if (need) {
-    made = fresh(*x, at::kByte, {static_cast<int64_t>(need)});
+    if (have < f_experts_ws(p, R, static_cast<int>(M), static_cast<int>(T))) return leave();
+  } else if ((have = f_experts_form_ws(p, R, static_cast<int>(M), static_cast<int>(T), w != nullptr, x->data_ptr(),
+                                       static_cast<int>(width), per_pair, xd, act))) {
+    made = fresh(*x, at::kByte, {static_cast<int64_t>(have)});
     ws = made.data_ptr();
   }
   at::Tensor y = w ? fresh(*x, TYPES[yd], {M, R}) : fresh(*x, TYPES[yd], {M, T, R});
-  return one(f_experts(p, R, static_cast<int>(M), static_cast<int>(T), static_cast<const int*>(ids->data_ptr()),
-                       static_cast<const float*>(w), x->data_ptr(), static_cast<int>(width), per_pair, xd, act, y.data_ptr(), R,
-                       yd, ws, have, st),
+  return one((own ? f_experts_form : f_experts)(p, R, static_cast<int>(M), static_cast<int>(T),
+                                                static_cast<const int*>(ids->data_ptr()), static_cast<const float*>(w),
+                                                x->data_ptr(), static_cast<int>(width), per_pair, xd, act, y.data_ptr(), R, yd,
+                                                ws, have, st),
              std::move(y));
 }
 

@@ -188,20 +188,27 @@ __global__ void __launch_bounds__(128) combine_kernel(ExpertsArgs a, const float
   store_y(a.y, at + 2, a.y_dtype, y.z), store_y(a.y, at + 3, a.y_dtype, y.w);
 }
 
-// Where things lie in the workspace.
+bool sorted_before(const ExpertsArgs& a) { return a.M * a.T > X_OWN; }
+// x as it is where the copies can take it; otherwise so many rows of it are made.
+bool x_as_is(const ExpertsArgs& a) { return !a.x_bf16 && a.act == QMV_ACT_NONE && (uintptr_t)a.x % 16 == 0 && a.ldx % 8 == 0; }
+int rows_made(const ExpertsArgs& a) { return x_as_is(a) ? 0 : a.per_pair ? a.M * a.T : a.M; }
+
+// Where things lie in the workspace: the pairs in order where a kernel before sorts them, the rows of x that are
+// made, and the products where they are summed afterwards.
 struct Places {
   size_t head, order, tasks, exps, x, part, bytes;
-  Places(int K, int R, int M, int T) {
+  Places(size_t sorted, size_t rows, size_t K, size_t parts, size_t R) {
     const auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
-    const size_t P = (size_t)M * T;
     head = 0;
-    order = 256;
-    tasks = order + up(P * 4);
-    exps = tasks + up(P * sizeof(Task));
-    x = exps + up(P * 4);
-    part = x + up(P * K * 2);
-    bytes = part + up(P * R * 4);
+    order = sorted ? 256 : 0;
+    tasks = order + up(sorted * 4);
+    exps = tasks + up(sorted * sizeof(Task));
+    x = exps + up(rows * 4);
+    part = x + up(rows * K * 2);
+    bytes = part + up(parts * R * 4);
   }
+  explicit Places(const ExpertsArgs& a)
+      : Places(sorted_before(a) ? (size_t)a.M * a.T : 0, rows_made(a), a.K, a.weights ? (size_t)a.M * a.T : 0, a.R) {}
 };
 
 // The shared memory of the products with up to `cols` tokens a task, or false where it does not fit.
@@ -216,7 +223,7 @@ bool lay_out(const ExpertsArgs& a, int cols, ExpertsPlan* P) {
   P->xs_size = (int)up((int64_t)P->KB * (BK / a.group) * X_COLS * 4);
   const int64_t part = (int64_t)X_W * cols * ROWS * 4;
   const int pairs = a.M * a.T, tasks = std::min(pairs, pairs / cols + std::min(pairs, a.E));
-  P->own = pairs <= X_OWN;
+  P->own = !sorted_before(a);
   const int own = P->own ? (int)(up(pairs * 2) + up(tasks * sizeof(OwnTask))) : 0;
   const int64_t left = (int64_t)dev_info().max_smem_optin - 4096 - (2 * P->x_size + 256 + 2 * P->xs_size + part + own);
   const int64_t fit = left / ((int64_t)X_W * bb);         // blocks a warp's ring can hold
@@ -235,27 +242,28 @@ bool lay_out(const ExpertsArgs& a, int cols, ExpertsPlan* P) {
 
 }  // namespace
 
-size_t experts_workspace(int K, int R, int M, int T) { return Places(K, R, M, T).bytes; }
+size_t experts_workspace(int K, int R, int M, int T) {
+  const size_t P = (size_t)M * T;
+  return Places(P, P, K, P, R).bytes;
+}
+size_t experts_workspace(const ExpertsArgs& a) { return Places(a).bytes; }
 
 cudaError_t launch_experts(const ExpertsArgs& a, cudaStream_t s) {
   ExpertsPlan P;
   int cols = X_COLS;
   while (!lay_out(a, cols, &P))
     if ((cols /= 2) == 0) return cudaErrorInvalidConfiguration;       // not reached: one column of EXPERTS_MAX_K fits
-  const Places at(a.K, a.R, a.M, a.T);
+  const Places at(a);
   uint8_t* ws = (uint8_t*)a.ws;
   P.head = (int*)(ws + at.head);
   P.order = (int*)(ws + at.order);
   P.tasks = (Task*)(ws + at.tasks);
   P.exps = (int*)(ws + at.exps);
   P.part = a.weights ? (float*)(ws + at.part) : nullptr;
-  // x as it is where the copies can take it
-  const bool as_is = !a.x_bf16 && a.act == QMV_ACT_NONE && (uintptr_t)a.x % 16 == 0 && a.ldx % 8 == 0;
   uint16_t* xh = (uint16_t*)(ws + at.x);
-  P.x = as_is ? (const uint16_t*)a.x : xh;
-  P.ldx = as_is ? a.ldx : a.K;
-  const int rows = as_is ? 0 : a.per_pair ? a.M * a.T : a.M;
-  const int sort = !P.own;
+  const int rows = rows_made(a), sort = !P.own;
+  P.x = rows ? xh : (const uint16_t*)a.x;
+  P.ldx = rows ? a.K : a.ldx;
   P.prepared = sort || rows;
   cudaError_t e = cudaSuccess;
   if (P.prepared) {

@@ -66,7 +66,9 @@ struct ExpertsArgs {
 // One column of the longest row fits twice beside the rings; strips of all tasks are counted in int.
 constexpr int EXPERTS_MAX_K = 16384, EXPERTS_MAX_PAIRS = 32768, EXPERTS_MAX_E = 1024, EXPERTS_MAX_R = 1 << 20;
 static_assert((int64_t)EXPERTS_MAX_PAIRS * (EXPERTS_MAX_R / 32) <= (int64_t)1 << 30, "strips");
+// Scratch of any call of these sizes, and of the one call (ids, y and the scratch itself do not count).
 size_t experts_workspace(int K, int R, int M, int T);
+size_t experts_workspace(const ExpertsArgs& a);
 cudaError_t launch_experts(const ExpertsArgs& a, cudaStream_t s);
 // The device error word of the experts' products (bounded waits, ids out of range).
 int read_experts_error(int clear, int* out);

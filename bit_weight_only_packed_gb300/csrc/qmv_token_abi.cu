@@ -24,6 +24,33 @@ bool experts_fit(const qmv_w4pack* p, int E, int M, int T) {
          p->K <= qmv::EXPERTS_MAX_K && p->N / E <= qmv::EXPERTS_MAX_R;
 }
 
+// form: the workspace has to hold this call's own scratch only.
+int experts_call(const qmv_w4pack* p, int rows_per_expert, int M, int T, const int* ids, const float* weights, const void* x,
+                 int ldx, int per_pair, int x_dtype, int act, void* y, int ldy, int y_dtype, void* d_workspace,
+                 size_t workspace_bytes, bool form, void* stream) {
+  if (!p || p->magic != QMV_W4_MAGIC || !p->d_packed || !ids || !x || !y || M < 1 || T < 1) return QMV_ERR_INVALID_ARG;
+  if (!dtype16(x_dtype) || !dtype_ok(y_dtype) || act < QMV_ACT_NONE || act > QMV_ACT_GELU) return QMV_ERR_INVALID_ARG;
+  const int E = experts_of(p, rows_per_expert), R = rows_per_expert;
+  if (!E) return QMV_ERR_SHAPE;
+  if (!experts_fit(p, E, M, T)) return QMV_ERR_UNSUPPORTED;
+  const int width = act == QMV_ACT_NONE ? p->K : 2 * p->K;
+  if (ldx < width || ldy < R) return QMV_ERR_SHAPE;
+  const qmv::ExpertsArgs a{p->d_packed, p->K, p->scale_bf16, p->group, p->zeros, E, R, M, T, ids, weights, x, ldx, per_pair != 0,
+                           x_dtype == QMV_BF16, act, y, ldy, y_dtype, d_workspace};
+  const size_t need = form ? qmv::experts_workspace(a) : qmv::experts_workspace(p->K, R, M, T);
+  if (!aligned(ids, 4) || !aligned(weights, 4) || !aligned(x, 2) || !aligned(y, dsize(y_dtype)) ||
+      (need && d_workspace && !aligned(d_workspace, 256)))
+    return QMV_ERR_ALIGNMENT;
+  if (need && (!d_workspace || workspace_bytes < need)) return QMV_ERR_WORKSPACE;
+  const int64_t pairs = (int64_t)M * T;
+  const Span in = span(x, per_pair ? pairs : M, ldx, width, 2), i = flat(ids, pairs, 4), w = flat(weights, pairs, 4),
+             packed = flat(p->d_packed, p->bytes, 1), out = span(y, weights ? M : pairs, ldy, R, dsize(y_dtype)),
+             ws = flat(need ? d_workspace : nullptr, need, 1);
+  if (meets(out, in, i, w, packed, ws) || meets(ws, in, i, w, packed)) return QMV_ERR_INVALID_ARG;
+  return done(qmv::launch_experts(a, (cudaStream_t)stream));
+}
+constexpr float NO_WEIGHT = 0.0f;          // stands for weights in a question for sizes
+
 }  // namespace
 
 extern "C" {
@@ -127,29 +154,28 @@ size_t qmv_w4_experts_workspace_bytes(const qmv_w4pack* p, int rows_per_expert, 
   return qmv::experts_workspace(p->K, rows_per_expert, M, T);
 }
 
+size_t qmv_w4_experts_form_bytes(const qmv_w4pack* p, int rows_per_expert, int M, int T, int weighted, const void* x, int ldx,
+                                 int per_pair, int x_dtype, int act) {
+  if (qmv_w4_experts_workspace_bytes(p, rows_per_expert, M, T) == 0) return 0;
+  qmv::ExpertsArgs a = {};
+  a.K = p->K, a.R = rows_per_expert, a.M = M, a.T = T;
+  a.weights = weighted ? &NO_WEIGHT : nullptr;
+  a.x = x, a.ldx = ldx, a.per_pair = per_pair != 0, a.x_bf16 = x_dtype == QMV_BF16, a.act = act;
+  return qmv::experts_workspace(a);
+}
+
 int qmv_w4_experts(const qmv_w4pack* p, int rows_per_expert, int M, int T, const int* ids, const float* weights,
                    const void* x, int ldx, int per_pair, int x_dtype, int act, void* y, int ldy, int y_dtype,
                    void* d_workspace, size_t workspace_bytes, void* stream) {
-  if (!p || p->magic != QMV_W4_MAGIC || !p->d_packed || !ids || !x || !y || M < 1 || T < 1) return QMV_ERR_INVALID_ARG;
-  if (!dtype16(x_dtype) || !dtype_ok(y_dtype) || act < QMV_ACT_NONE || act > QMV_ACT_GELU) return QMV_ERR_INVALID_ARG;
-  const int E = experts_of(p, rows_per_expert), R = rows_per_expert;
-  if (!E) return QMV_ERR_SHAPE;
-  if (!experts_fit(p, E, M, T)) return QMV_ERR_UNSUPPORTED;
-  const int width = act == QMV_ACT_NONE ? p->K : 2 * p->K;
-  if (ldx < width || ldy < R) return QMV_ERR_SHAPE;
-  if (!aligned(ids, 4) || !aligned(weights, 4) || !aligned(x, 2) || !aligned(y, dsize(y_dtype)) ||
-      (d_workspace && !aligned(d_workspace, 256)))
-    return QMV_ERR_ALIGNMENT;
-  const int64_t pairs = (int64_t)M * T;
-  const size_t need = qmv::experts_workspace(p->K, R, M, T);
-  if (need && (!d_workspace || workspace_bytes < need)) return QMV_ERR_WORKSPACE;
-  const Span in = span(x, per_pair ? pairs : M, ldx, width, 2), i = flat(ids, pairs, 4), w = flat(weights, pairs, 4),
-             packed = flat(p->d_packed, p->bytes, 1), out = span(y, weights ? M : pairs, ldy, R, dsize(y_dtype)),
-             ws = flat(need ? d_workspace : nullptr, need, 1);
-  if (meets(out, in, i, w, packed, ws) || meets(ws, in, i, w, packed)) return QMV_ERR_INVALID_ARG;
-  qmv::ExpertsArgs a{p->d_packed, p->K, p->scale_bf16, p->group, p->zeros, E, R, M, T, ids, weights, x, ldx, per_pair != 0,
-                     x_dtype == QMV_BF16, act, y, ldy, y_dtype, d_workspace};
-  return done(qmv::launch_experts(a, (cudaStream_t)stream));
+  return experts_call(p, rows_per_expert, M, T, ids, weights, x, ldx, per_pair, x_dtype, act, y, ldy, y_dtype, d_workspace,
+                      workspace_bytes, false, stream);
+}
+
+int qmv_w4_experts_form(const qmv_w4pack* p, int rows_per_expert, int M, int T, const int* ids, const float* weights,
+                        const void* x, int ldx, int per_pair, int x_dtype, int act, void* y, int ldy, int y_dtype,
+                        void* d_workspace, size_t workspace_bytes, void* stream) {
+  return experts_call(p, rows_per_expert, M, T, ids, weights, x, ldx, per_pair, x_dtype, act, y, ldy, y_dtype, d_workspace,
+                      workspace_bytes, true, stream);
 }
 
 int qmv_sample(int rows, int V, const void* logits, int ldl, int dtype, const float* d_temperature, float temperature,

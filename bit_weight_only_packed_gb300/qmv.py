@@ -84,6 +84,8 @@ SIGNATURES = {
     "qmv_route": (_I, [_I, _I, _I, _P, _I, _I, _I, _P, _I, _I, _I, _I, _F, _P, _P, _P]),
     "qmv_w4_experts_workspace_bytes": (ctypes.c_size_t, [_P, _I, _I, _I]),
     "qmv_w4_experts": (_I, [_P, _I, _I, _I, _P, _P, _P, _I, _I, _I, _I, _P, _I, _I, _P, ctypes.c_size_t, _P]),
+    "qmv_w4_experts_form_bytes": (ctypes.c_size_t, [_P, _I, _I, _I, _I, _P, _I, _I, _I, _I]),
+    "qmv_w4_experts_form": (_I, [_P, _I, _I, _I, _P, _P, _P, _I, _I, _I, _I, _P, _I, _I, _P, ctypes.c_size_t, _P]),
     "qmv_sample": (_I, [_I, _I, _P, _I, _I, _P, _F, _P, _I, _P, _F, _P, _F, _P, _P, _P]),
 }
 
@@ -542,7 +544,8 @@ def _load_host():
     addr = lambda f: ctypes.cast(f, _P).value
     mod.init(*(addr(f) for f in (_lib.qmv_w4_gemv, _lib.qmv_block_norm, _lib.qmv_softmax, _lib.qmv_verify_draft,
                                  _lib.qmv_qk_norm_rope, _lib.qmv_route, _lib.qmv_w4_experts,
-                                 _lib.qmv_w4_experts_workspace_bytes, _lib.qmv_sample)))
+                                 _lib.qmv_w4_experts_workspace_bytes, _lib.qmv_w4_experts_form,
+                                 _lib.qmv_w4_experts_form_bytes, _lib.qmv_sample)))
     return mod
 
 
@@ -963,12 +966,13 @@ def qmv_route(logits, top_k, score=QMV_SCORE_SOFTMAX, bias=None, groups=1, group
 
 
 def qmv_w4_experts_workspace_bytes(p: W4Pack, rows_per_expert: int, M: int, T: int) -> int:
-    """Device scratch bytes that qmv_w4_experts needs for up to M tokens of T experts (0 for none)."""
+    """Device scratch bytes that are enough for every form of qmv_w4_experts of up to M tokens of
+    T experts (0 where such a call is refused)."""
     return int(_lib.qmv_w4_experts_workspace_bytes(p.handle, rows_per_expert, M, T))
 
 
 def qmv_w4_experts_workspace(p: W4Pack, rows_per_expert: int, M: int, T: int, device=None):
-    """A workspace tensor for such calls (None when they need none)."""
+    """A workspace tensor for such calls (None where they are refused)."""
     n = qmv_w4_experts_workspace_bytes(p, rows_per_expert, M, T)
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda") if n else None
 
@@ -977,7 +981,8 @@ def qmv_w4_experts(p: W4Pack, rows_per_expert, ids, x, weights=None, act=QMV_ACT
                    workspace=None, stream=None):
     """Products of the experts ids int32 [M, T] with x: y [M, T, R], or summed by weights fp32
     [M, T] y [M, R].  x is [M, K], or [M, T, K] for a row a pair; with act its rows
-    are gate and up, 2 K wide."""
+    are gate and up, 2 K wide.  workspace: one for every form of call (qmv_w4_experts_workspace);
+    without it the call takes fresh scratch for its own form, which is often none."""
     if y is None and stream is None:
         r = _host.w4_experts(p._address, p._dev, p.K, rows_per_expert, ids, x, weights, act, y_dtype, workspace)
         if r is not None:
@@ -1003,20 +1008,22 @@ def qmv_w4_experts(p: W4Pack, rows_per_expert, ids, x, weights=None, act=QMV_ACT
     ldy = R
     if y is not None:
         ldy = _rows("y", y, (ydt,), M, R) if weights is not None else _heads_rows("y", y, (ydt,), M, T, R)
-    n = qmv_w4_experts_workspace_bytes(p, R, M, T)
     if workspace is not None:
+        call, n = _lib.qmv_w4_experts, qmv_w4_experts_workspace_bytes(p, R, M, T)
         _need_bytes("workspace", workspace, n)
         if not workspace.is_contiguous():
             raise ValueError("workspace: expected a contiguous tensor")
     st = _place(stream, x, p.packed, ids, weights, y, workspace)
     if y is None:
         y = _fresh((M, T, R) if weights is None else (M, R), ydt, x.device, stream)
-    if workspace is None and n:
-        workspace = _fresh((n,), torch.uint8, x.device, stream)
-    rc = _lib.qmv_w4_experts(p.handle, R, M, T, ids.data_ptr(), None if weights is None else weights.data_ptr(), x.data_ptr(),
-                             ldx, 1 if per_pair else 0, _DTYPE[x.dtype], act, y.data_ptr(), ldy, y_dtype,
-                             None if workspace is None else workspace.data_ptr(),
-                             0 if workspace is None else workspace.numel() * workspace.element_size(), st)
+    if workspace is None:
+        call, n = _lib.qmv_w4_experts_form, int(_lib.qmv_w4_experts_form_bytes(
+            p.handle, R, M, T, 0 if weights is None else 1, x.data_ptr(), ldx, 1 if per_pair else 0, _DTYPE[x.dtype], act))
+        workspace = _fresh((n,), torch.uint8, x.device, stream) if n else None
+    rc = call(p.handle, R, M, T, ids.data_ptr(), None if weights is None else weights.data_ptr(), x.data_ptr(),
+              ldx, 1 if per_pair else 0, _DTYPE[x.dtype], act, y.data_ptr(), ldy, y_dtype,
+              None if workspace is None else workspace.data_ptr(),
+              0 if workspace is None else workspace.numel() * workspace.element_size(), st)
     if rc:
         _check("qmv_w4_experts", rc)
     return y

@@ -688,8 +688,9 @@ QMV_API int qmv_route(int M, int E, int T, const void *logits, int ldl, int dtyp
  *   x        device, M or M * T rows of K (2 K with act) of x_dtype (QMV_F16 or QMV_BF16), row stride ldx.
  *   y        device [M][T][R], or [M][R] with weights, of y_dtype, row stride ldy (of M * T or M rows of R).
  *   d_workspace, workspace_bytes  caller scratch, 256-byte aligned, at least
- *            qmv_w4_experts_workspace_bytes(p, rows_per_expert, M, T) bytes; its contents on entry
- *            do not matter; calls that share a workspace must not overlap.
+ *            qmv_w4_experts_workspace_bytes(p, rows_per_expert, M, T) bytes, which is enough for calls of
+ *            every form of up to M tokens and T experts (0 where such a call is refused); its contents on
+ *            entry do not matter; calls that share a workspace must not overlap.
  *   M 1 .. 4096; T 1 .. 64; M * T <= 32768; E <= 1024; K <= 16384; R <= 2^20.
  * Errors: INVALID_ARG, SHAPE (rows_per_expert, strides), UNSUPPORTED (sizes), ALIGNMENT, WORKSPACE, CUDA.
  */
@@ -698,6 +699,22 @@ QMV_API int qmv_w4_experts(const qmv_w4pack *p, int rows_per_expert, int M, int 
                            const float *weights, const void *x, int ldx, int per_pair, int x_dtype,
                            int act, void *y, int ldy, int y_dtype, void *d_workspace,
                            size_t workspace_bytes, void *stream);
+
+/*
+ * qmv_w4_experts_form -- the same call with scratch for its own form alone: at least
+ * qmv_w4_experts_form_bytes of its arguments.  That counts the pairs in order where M * T > 128, the rows of
+ * x that are made (none for fp16 without act, x 16-byte aligned and ldx a multiple of 8; M, or with
+ * per_pair M * T, of K otherwise) and the products that are summed (M * T of R, weights only).  It may be 0,
+ * and d_workspace NULL then.  (4096 tokens of 8 experts of 4096 rows, K = 2048, fp16 without weights: 0.7 MB;
+ * for every form 672 MB.)
+ *   weighted  not 0 where the call has weights.   x  read for its alignment alone.
+ */
+QMV_API size_t qmv_w4_experts_form_bytes(const qmv_w4pack *p, int rows_per_expert, int M, int T, int weighted,
+                                         const void *x, int ldx, int per_pair, int x_dtype, int act);
+QMV_API int qmv_w4_experts_form(const qmv_w4pack *p, int rows_per_expert, int M, int T, const int *ids,
+                                const float *weights, const void *x, int ldx, int per_pair, int x_dtype,
+                                int act, void *y, int ldy, int y_dtype, void *d_workspace,
+                                size_t workspace_bytes, void *stream);
 
 /*
  * qmv_sample -- one token a row of logits, from given random numbers.  In a row, with T its

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from gpu_util import GuardBuf, qmv
-from test_gpu_step import BF16, EPS, F16, F32, TINY, gen, make_w4
+from test_gpu_step import BF16, EPS, F16, TINY, code, gen, make_w4
 from test_gpu_token import act_ref, distinct, randn, route_ref
 
 pytestmark = pytest.mark.gpu
@@ -138,3 +138,54 @@ def test_experts_ids_and_weights_written_again_in_place(dt):
         torch.cuda.synchronize()
         assert torch.equal(outs[i][0], q.qmv_w4_experts(p, R, a, x, weights=b)), i
         assert torch.equal(outs[i][1], q.qmv_w4_experts(p, R, a, x)), i
+
+
+@pytest.mark.parametrize("xdt", [F16, BF16])
+@pytest.mark.parametrize("M,T,weighted,per_pair,act", [
+    (3, 2, False, False, 0), (3, 2, True, False, 0), (40, 4, True, True, 1), (40, 4, False, False, 0), (40, 4, False, False, 2), (200, 4, True, False, 0),
+])
+def test_experts_scratch_of_its_form_is_enough(M, T, weighted, per_pair, act, xdt):
+    # the form's own bytes, any contents, nothing written outside; the same bits as with a workspace for every form
+    q = qmv()
+    E, R, K = 12, 64, 320
+    p, _, _ = make_w4(E * R, K, 32, True, xdt, 3)
+    ids = distinct(M, T, E, 2)
+    width = K * (2 if act else 1)
+    x = randn(1, *((M, T, width) if per_pair else (M, width))).to(xdt)
+    w = torch.rand(M, T, generator=gen(5), device="cuda") if weighted else None
+    ref = q.qmv_w4_experts(p, R, ids, x, weights=w, act=act, workspace=q.qmv_w4_experts_workspace(p, R, M, T))
+    n = q.lib().qmv_w4_experts_form_bytes(p.handle, R, M, T, int(weighted), x.data_ptr(), width, int(per_pair), code(xdt), act)
+    st = torch.cuda.current_stream().cuda_stream
+    for fill in (0x00, 0x5A, 0xFF):
+        ws = GuardBuf(n, fill=fill) if n else None
+        y = torch.full_like(ref, 7.0)
+        rc = q.lib().qmv_w4_experts_form(p.handle, R, M, T, ids.data_ptr(), w.data_ptr() if weighted else None, x.data_ptr(), width,
+                                         int(per_pair), code(xdt), act, y.data_ptr(), R, q.QMV_F32,
+                                         ws.view(torch.uint8, (n,)).data_ptr() if n else None, n, st)
+        torch.cuda.synchronize()
+        assert rc == 0 and torch.equal(y, ref)
+        if n:
+            ws.check("workspace")
+    assert torch.equal(q.qmv_w4_experts(p, R, ids, x, weights=w, act=act), ref)
+
+
+@pytest.mark.parametrize("form", ["cpp", "python"])
+def test_experts_take_no_more_memory_than_their_form(form, monkeypatch):
+    q = qmv()
+    if form == "python":
+        monkeypatch.setattr(q, "_host", q._NoHost())
+    M, T, E, R, K = 1024, 8, 16, 1024, 512
+    p, _, _ = make_w4(E * R, K, 128, False, F16, 3)
+    ids = distinct(M, T, E, 2)
+    w = torch.rand(M, T, generator=gen(5), device="cuda")
+    # rows of y, and what the call may take beside them: the pairs in order, rows of x, products
+    order = 256 + 20 * M * T
+    for dt, weights, most in ((F16, None, order), (BF16, None, order + M * (2 * K + 4)), (F16, w, order + M * T * R * 4)):
+        x = randn(1, M, K).to(dt)
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_allocated()
+        torch.cuda.reset_peak_memory_stats()
+        y = q.qmv_w4_experts(p, R, ids, x, weights=weights)
+        taken = torch.cuda.max_memory_allocated() - before - y.numel() * 4
+        assert taken <= most + 2048, (dt, taken, most)         # rounded up to 256 and 512 bytes a region and an allocation
+        del y, x
