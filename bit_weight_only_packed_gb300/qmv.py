@@ -833,11 +833,18 @@ def qmv_verify_draft(target, draft_probs, draft, u_accept, u_sample, n_draft=Non
 
 def _matrix(name, t):
     """(rows, columns) of a [rows, columns] tensor; [columns] is one row."""
-    if t.dim() == 2:
-        return t.shape
-    if t.dim() == 1:
-        return 1, t.shape[0]
-    raise ValueError(f"{name}: expected a [rows, columns] tensor, got {tuple(t.shape)}")
+    if t.dim() not in (1, 2):
+        raise ValueError(f"{name}: expected a [rows, columns] tensor, got {tuple(t.shape)}")
+    rows, columns = t.shape if t.dim() == 2 else (1, t.shape[0])
+    _whole(**{f"{name}'s rows": rows, f"{name}'s columns": columns})
+    return rows, columns
+
+
+def _whole(**numbers):
+    """Checks that numbers are whole ones of 32 bits: ctypes would cut others off to that."""
+    for name, v in numbers.items():
+        if int(v) != v or not -(1 << 31) <= v < 1 << 31:
+            raise ValueError(f"{name}: expected a whole number of 32 bits, got {v!r}")
 
 
 def _heads(name, t, dt, M, n, D):
@@ -864,6 +871,7 @@ class Rope:
             raise ValueError(f"layout: unknown value {layout!r}")
         if rot < 2 or rot > 1024 or rot % 2:
             raise ValueError(f"rot: expected an even number from 2 to 1024, got {rot}")
+        _whole(scaling=scaling)
         n, amp = rot // 2, ctypes.c_float(1.0)
         w, turns = (ctypes.c_double * n)(), (ctypes.c_int64 * n)()
         if inv_freq is None:
@@ -896,6 +904,7 @@ def qmv_qk_norm_rope(qkv, n_q, n_k, head_dim, rope=None, positions=None, gamma_q
                                gamma_k, gamma_offset, eps, y_dtype)
         if r is not None:
             return _done("qmv_qk_norm_rope", r)
+    _whole(n_q=n_q, n_k=n_k, head_dim=head_dim)
     M, C = _matrix("qkv", qkv)
     D = head_dim
     if n_q < 0 or n_k < 0 or D < 1 or C < (n_q + n_k) * D:
@@ -944,6 +953,7 @@ def qmv_route(logits, top_k, score=QMV_SCORE_SOFTMAX, bias=None, groups=1, group
         r = _host.route(logits, top_k, score, bias, groups, group_k, group_top, renormalise, scale)
         if r is not None:
             return _done("qmv_route", r)
+    _whole(top_k=top_k, score=score, groups=groups, group_k=group_k, group_top=group_top)
     M, E = _matrix("logits", logits)
     ldl = _rows("logits", logits, _FLOAT, M, E)
     if bias is not None:
@@ -968,6 +978,7 @@ def qmv_route(logits, top_k, score=QMV_SCORE_SOFTMAX, bias=None, groups=1, group
 def qmv_w4_experts_workspace_bytes(p: W4Pack, rows_per_expert: int, M: int, T: int) -> int:
     """Device scratch bytes that are enough for every form of qmv_w4_experts of up to M tokens of
     T experts (0 where such a call is refused)."""
+    _whole(rows_per_expert=rows_per_expert, M=M, T=T)
     return int(_lib.qmv_w4_experts_workspace_bytes(p.handle, rows_per_expert, M, T))
 
 
@@ -990,6 +1001,7 @@ def qmv_w4_experts(p: W4Pack, rows_per_expert, ids, x, weights=None, act=QMV_ACT
     if ids.dim() != 2:
         raise ValueError(f"ids: expected [tokens, experts], got {tuple(ids.shape)}")
     M, T = ids.shape
+    _whole(rows_per_expert=rows_per_expert, act=act, tokens=M, experts=T)
     R, K = rows_per_expert, p.K
     _vec("ids", ids, torch.int32, M * T)
     if weights is not None:
@@ -1058,6 +1070,8 @@ def qmv_sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tokens
             at.append(v.data_ptr())
             num.append(0)
         else:
+            if name == "top_k":
+                _whole(top_k=v)
             at.append(None)
             num.append(v)
     if tokens is not None:

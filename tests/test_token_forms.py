@@ -1,5 +1,6 @@
-"""Scratch of the experts' products by the form of the call: host checks."""
+"""Scratch of the experts' products by the form of the call, and numbers past 32 bits: host checks."""
 import pytest
+import torch
 
 F32, F16, BF16 = 0, 1, 2
 
@@ -61,3 +62,30 @@ def test_experts_form_calls(q):
     for kw in (dict(ldx=K - 1), dict(ldy=R - 1)):
         assert call(**kw) == -4, kw
     assert call(M=4097) == call(T=65) == -2
+
+
+def test_numbers_past_32_bits_are_refused_not_cut_off(q):
+    far = 1 << 32
+    f16 = lambda *s: torch.zeros(*s, dtype=torch.float16)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    p = q.W4Pack(128, 256, 128)
+    rows = torch.empty(far + 1, 1, device="meta")
+    cases = [
+        (lambda: q.qmv_sample(torch.zeros(2, 64), torch.zeros(2), top_k=far + 5), "top_k"),
+        (lambda: q.qmv_sample(torch.zeros(2, 64), torch.zeros(2), top_k=2.5), "top_k"),
+        (lambda: q.qmv_sample(rows, torch.empty(far + 1, device="meta")), "logits's rows"),
+        (lambda: q.qmv_route(rows, 1), "logits's rows"),
+        (lambda: q.qmv_route(torch.zeros(2, 64), far + 2), "top_k"),
+        (lambda: q.qmv_route(torch.zeros(2, 64), 2, groups=far + 1), "groups"),
+        (lambda: q.qmv_route(torch.zeros(2, 64), 2, score=far), "score"),
+        (lambda: q.qmv_qk_norm_rope(rows, 1, 0, 1), "qkv's rows"),
+        (lambda: q.qmv_qk_norm_rope(f16(2, 192), far + 2, 1, 64), "n_q"),
+        (lambda: q.qmv_w4_experts(p, far + 64, i32(2, 2), f16(2, 256)), "rows_per_expert"),
+        (lambda: q.qmv_w4_experts(p, 64, i32(2, 2), f16(2, 256), act=far), "act"),
+        (lambda: q.qmv_w4_experts_workspace_bytes(p, 64, far + 1, 1), "M"),
+        (lambda: q.Rope(64, scaling=far, device="cpu"), "scaling"),
+    ]
+    for i, (f, text) in enumerate(cases):
+        with pytest.raises(ValueError, match=text):
+            f()
+            raise AssertionError(f"case {i} ({text}) was not refused")
