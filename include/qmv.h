@@ -651,8 +651,11 @@ QMV_API int qmv_qk_norm_rope(int M, int n_q, int n_k, int D, const void *qkv, in
  *   ids = the T largest r, the largest first;  weights = s of those, over their sum where
  *   renormalise is not 0 (0 where that sum is 0 in 64 bits), times scale.
  * Equal ones go to the lowest index.  r is compared as 64-bit arithmetic would have it: where
- * fp32 cannot tell two apart they are formed again in 64 bits; without bias the
- * logits themselves are compared.  Weights are fp32, within 2^-20 of themselves.
+ * fp32 cannot tell two apart they are formed again in 64 bits.  Without bias experts are compared
+ * by their logits, which is the order of exact scores also where those of 64 bits are equal: of
+ * sigmoid logits 40 and 41, both scores 1 there, 41 comes first, with a bias of 0 the lower
+ * index.  The sums of two that groups count are of 64-bit scores, with a bias or without.
+ * Weights are fp32, within 2^-20 of themselves.
  * An expert whose logit or bias is NaN or -inf is never chosen (nor counted in a
  * group, as -inf: with group_top 2 a group of one expert alone counts as -inf); places
  * that are left over hold id -1 and weight 0.  Logits of +inf share a softmax evenly.

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from gpu_util import GuardBuf, qmv
-from test_gpu_step import BF16, EPS, F16, TINY, code, gen, make_w4
+from test_gpu_step import BF16, EPS, F16, F32, TINY, code, gen, make_w4
 from test_gpu_token import act_ref, distinct, randn, route_ref
 
 pytestmark = pytest.mark.gpu
@@ -83,6 +83,24 @@ def test_route_groups_with_fewer_than_two_experts(score, per):
         assert torch.equal(ids, rest + per), (ids, rest)
     ids, _ = q.qmv_route(x, 3, score=score, bias=bias, groups=groups, group_k=4, group_top=2)
     assert bool((ids[:, 0] == 0).all())         # where all groups stay it comes first
+
+
+@pytest.mark.parametrize("dt", [F32, F16, BF16])
+def test_route_scores_that_64_bits_cannot_tell_apart(dt):
+    q = qmv()
+    # sigmoid scores of 1, softmax scores of 0, in 64 bits: without a bias the logit decides, with a bias of 0 the index
+    x = torch.tensor([[41.0, 43.0, 40.0, 42.0, -3.0, 44.0, 40.0, 43.0]], device="cuda").to(dt)
+    zero = torch.zeros(8, device="cuda")
+    assert q.qmv_route(x, 4, score=1)[0].tolist() == [[5, 1, 7, 3]]
+    assert q.qmv_route(x, 4, score=1, bias=zero)[0].tolist() == [[0, 1, 2, 3]]
+    y = torch.tensor([[2.0, -1.0, 3.0, 900.0, 4.0, 1.0, 5.0, 0.0]], device="cuda").to(dt)
+    assert q.qmv_route(y, 4, score=0)[0].tolist() == [[3, 6, 4, 2]]
+    assert q.qmv_route(y, 4, score=0, bias=zero)[0].tolist() == [[3, 0, 1, 2]]
+    # groups of two go by their scores' sum, where the first of those that are equal stays; of one by the logit
+    for bias, first in ((None, 1), (zero, 0)):
+        assert q.qmv_route(x, 2, score=1, bias=bias, groups=4, group_k=1, group_top=2)[0].tolist() == [[first, 1 - first]]
+    assert q.qmv_route(x, 2, score=1, groups=4, group_k=1, group_top=1)[0].tolist() == [[5, 4]]
+    assert q.qmv_route(x, 2, score=1, bias=zero, groups=4, group_k=1, group_top=1)[0].tolist() == [[0, 1]]
 
 
 # --------------------------------------------------------------- experts --
