@@ -299,14 +299,14 @@ __device__ __noinline__ bool choose_each(const RouteArgs& a, const float* xb, ui
   bool sure = true;
   F before = none;
   float x_before = 0.0f, b_before = 0.0f;
-  for (int t = 0; t <= a.T; ++t) {                   // one more than is wanted, to tell the last apart
-    if (t == a.T && (!a.bias || sizeof(F) == 8)) break;
+  for (int t = 0; t < a.T; ++t) {
     F best = r[0];
 #pragma unroll
     for (int i = 1; i < N; ++i) best = fmax(best, r[i]);
     const F top = warp_max(best);
     if (top == none) {
-      if (lane == (t & 31) && t < a.T) id[t >> 5] = -1;
+      if (lane == (t & 31)) id[t >> 5] = -1;
+      before = none;
       continue;
     }
     const int owner = __ffs(__ballot_sync(~0u, best == top)) - 1;
@@ -327,7 +327,15 @@ __device__ __noinline__ bool choose_each(const RouteArgs& a, const float* xb, ui
         sure = false;
       before = top, x_before = xv, b_before = bv;
     }
-    if (lane == (t & 31) && t < a.T) id[t >> 5] = at, of[t >> 5] = xv;
+    if (lane == (t & 31)) id[t >> 5] = at, of[t >> 5] = xv;
+  }
+  if (a.bias && sizeof(F) == 4 && before > none) {
+    // the last one and the largest of those left that are not truly equal to it
+    F best = none;
+#pragma unroll
+    for (int i = 0; i < N; ++i) best = x[i] == x_before && b[i] == b_before ? best : fmax(best, r[i]);
+    const F top = warp_max(best);
+    if (top > none && !(before - top > 2 * err + (F)0x1p-22 * (fabs(before) + fabs(top)))) sure = false;
   }
   return sure;
 }
@@ -497,16 +505,19 @@ __global__ void __launch_bounds__(WARPS * 32, N <= 8 ? 10 : 4) route_kernel(Rout
     id[0] = in ? (int)(who >> 5) : -1;
     of[0] = f.x;
     if (a.bias) {
-      const float key2 = __shfl_down_sync(~0u, key, 1);
+      // each pick and the next, and the last pick and each of those behind it
+      const int with = lane < a.T - 1 ? lane + 1 : a.T - 1;
+      const float key2 = __shfl_sync(~0u, key, with);
       float err = err2;
       if (a.score != QMV_SCORE_SIGMOID) {            // by their own d, and what p itself is off by here
         const float d = top - f.x, own = exp_of(-d) * largest * (48.0f + d) * 0x1p-24f + 0x1p-120f;
-        err = own + __shfl_down_sync(~0u, own, 1);
+        err = own + __shfl_sync(~0u, own, with);
       }
-      const bool near = in && lane < 31 && key2 > none && !(key - key2 > err + 0x1p-23f * (fabsf(key) + fabsf(key2)));
+      const bool near = lane != a.T - 1 && key > none && key2 > none &&
+                        !(fabsf(key - key2) > err + 0x1p-23f * (fabsf(key) + fabsf(key2)));
       if (__any_sync(~0u, near)) {
         // equal ones of the same logit and bias are truly equal
-        const float x2 = __shfl_down_sync(~0u, f.x, 1), b2 = __shfl_down_sync(~0u, f.b, 1);
+        const float x2 = __shfl_sync(~0u, f.x, with), b2 = __shfl_sync(~0u, f.b, with);
         if (__any_sync(~0u, near && !(f.x == x2 && f.b == b2))) {
           if (a.score == QMV_SCORE_SIGMOID)
             order_wide(a, few, n, lane, &id[0], &of[0]);

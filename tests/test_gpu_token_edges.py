@@ -7,7 +7,7 @@ import torch
 
 from gpu_util import GuardBuf, qmv
 from test_gpu_step import BF16, EPS, F16, F32, TINY, code, gen, make_w4
-from test_gpu_token import act_ref, distinct, randn, route_ref
+from test_gpu_token import act_ref, check_route, distinct, randn, route_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -101,6 +101,19 @@ def test_route_scores_that_64_bits_cannot_tell_apart(dt):
         assert q.qmv_route(x, 2, score=1, bias=bias, groups=4, group_k=1, group_top=2)[0].tolist() == [[first, 1 - first]]
     assert q.qmv_route(x, 2, score=1, groups=4, group_k=1, group_top=1)[0].tolist() == [[5, 4]]
     assert q.qmv_route(x, 2, score=1, bias=zero, groups=4, group_k=1, group_top=1)[0].tolist() == [[0, 1]]
+
+
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("E,T", [(8, 1), (30, 3), (64, 1), (64, 8), (300, 5), (300, 31), (1000, 16), (64, 40), (1000, 33)])
+def test_route_equal_experts_hide_no_larger_one(E, T, score):
+    # a few logits many times over, and a bias beside which fp32 cannot tell them apart: equal ones fill
+    # the last places and the next, behind which one that is larger in 64 bits may follow
+    step = 2.0 ** -14 if score else 2.0 ** -8
+    x = torch.randint(0, 4, (400, E), generator=gen(E + T), device="cuda").float() * step
+    check_route(x, T, score, torch.full((E,), 1024.0, device="cuda"))
+    few = torch.full((400, E), -30.0, device="cuda")
+    few[:, :: max(E // 8, 1)] = x[:, :: max(E // 8, 1)]
+    check_route(few, min(T, 7), score, torch.full((E,), 1024.0, device="cuda"))
 
 
 # --------------------------------------------------------------- experts --
