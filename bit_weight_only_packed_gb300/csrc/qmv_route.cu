@@ -202,14 +202,15 @@ __device__ __forceinline__ uint32_t choose_groups(const RouteArgs& a, const F (&
     better += v > worth || (v == worth && j < lane);
   }
   if (sizeof(F) == 4 && a.group_k < a.groups && (a.bias || a.group_top == 2)) {
-    // the last group that stays and the first that does not: apart, or truly equal
+    // the last group that stays and the first that does not: apart, or all that are near them truly equal
     const int l = __ffs(__ballot_sync(~0u, lane < a.groups && better == a.group_k - 1)) - 1,
               m = __ffs(__ballot_sync(~0u, lane < a.groups && better == a.group_k)) - 1;
-    const F last = __shfl_sync(~0u, worth, l), next = __shfl_sync(~0u, worth, m);
-    const bool same = !a.bias && __shfl_sync(~0u, one, l) == __shfl_sync(~0u, one, m) &&
-                      __shfl_sync(~0u, two, l) == __shfl_sync(~0u, two, m);
+    const F last = __shfl_sync(~0u, worth, l), next = __shfl_sync(~0u, worth, m), one_l = __shfl_sync(~0u, one, l),
+            two_l = __shfl_sync(~0u, two, l);
+    const bool same = !a.bias && one == one_l && two == two_l;
     const F err = 4 * score_error<F>(a.score, a.bias ? largest : (F)1) + (F)0x1p-22 * (fabs(last) + fabs(next));
-    known->sure = last - next > err || next == none || same;
+    const bool odd = __any_sync(~0u, lane < a.groups && !(worth < next - err) && !(worth > last + err) && !same);
+    known->sure = last - next > err || next == none || !odd;
     // a group's best two in exact arithmetic are among those that reach the second less their errors
     known->worth = worth, known->reach = (a.group_top == 2 ? two : one) - err, known->low = next - err, known->high = last + err;
   }

@@ -116,6 +116,18 @@ def test_route_equal_experts_hide_no_larger_one(E, T, score):
     check_route(few, min(T, 7), score, torch.full((E,), 1024.0, device="cuda"))
 
 
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("groups,per,group_k", [(4, 2, 1), (8, 4, 3), (8, 8, 1), (5, 3, 2), (32, 8, 12)])
+def test_route_equal_groups_hide_no_larger_one(groups, per, group_k, score):
+    # groups of the same two logits, and some whose sum of scores is larger by less than fp32 can tell
+    g = gen(groups + per)
+    x = torch.full((400, groups, per), -4.0, device="cuda")
+    x[:, :, 0], x[:, :, 1] = 3 + torch.rand(400, 1, generator=g, device="cuda"), 2 + torch.rand(400, 1, generator=g, device="cuda")
+    x[:, :, 1] += 2.0 ** -22 * torch.randint(0, 2, (400, groups), generator=g, device="cuda")
+    order = torch.rand(400, groups, per, generator=g, device="cuda").argsort(2)
+    check_route(x.gather(2, order).view(400, -1), 2, score, None, groups, group_k, 2)
+
+
 # --------------------------------------------------------------- experts --
 
 def one_to_one(dt):
