@@ -210,7 +210,9 @@ __device__ __forceinline__ uint32_t choose_groups(const RouteArgs& a, const F (&
     const bool same = !a.bias && one == one_l && two == two_l;
     const F err = 4 * score_error<F>(a.score, a.bias ? largest : (F)1) + (F)0x1p-22 * (fabs(last) + fabs(next));
     const bool odd = __any_sync(~0u, lane < a.groups && !(worth < next - err) && !(worth > last + err) && !same);
-    known->sure = last - next > err || next == none || !odd;
+    // (a sum of two large biases may be infinite in fp32: that is no proof either)
+    const bool none_out = !__any_sync(~0u, lane < a.groups && better >= a.group_k && (a.group_top == 2 ? two : one) != none);
+    known->sure = last - next > err || none_out || !odd;
     // a group's best two in exact arithmetic are among those that reach the second less their errors
     known->worth = worth, known->reach = (a.group_top == 2 ? two : one) - err, known->low = next - err, known->high = last + err;
   }
@@ -246,9 +248,10 @@ __device__ __noinline__ uint32_t groups_wide(const RouteArgs& a, const float* xb
 }
 
 // The same where a few groups are near each other: only their best experts' ranks are formed in 64 bits,
-// one a lane (sigmoid scores and a bias).  Returns 0 where these are more than 32.
+// one a lane (sigmoid scores and a bias).  Returns 0 where these are more than 32, or what is near infinite.
 template <int N>
 __device__ __noinline__ uint32_t groups_near(const RouteArgs& a, const float* xb, const float* rb, const Groups<float>& known, int lane, Few* few) {
+  if (!(known.high - known.low < CUDART_INF_F)) return 0;
   const uint32_t near = __ballot_sync(~0u, lane < a.groups && known.worth >= known.low && known.worth <= known.high);
   uint32_t in = __ballot_sync(~0u, lane < a.groups && known.worth > known.high);
   int n = 0;

@@ -128,6 +128,23 @@ def test_route_equal_groups_hide_no_larger_one(groups, per, group_k, score):
     check_route(x.gather(2, order).view(400, -1), 2, score, None, groups, group_k, 2)
 
 
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("groups,per,group_k,group_top", [(1, 64, 1, 1), (8, 8, 1, 1), (8, 8, 3, 2), (32, 2, 5, 2), (4, 250, 2, 1), (5, 3, 2, 2),
+                                                            (3, 1, 1, 1), (8, 1, 2, 1), (6, 4, 2, 1), (4, 4, 1, 2)])
+def test_route_biases_of_any_size(groups, per, group_k, group_top, score):
+    # infinite ones, and such whose sum of two is infinite in fp32 and not in 64 bits
+    E = groups * per
+    x = randn(E, 50, E)
+    for seed, some in enumerate((0.03, 0.3, 0.9)):
+        for sizes in ([math.inf], [3e38], [-3e38], [3e38, -3e38, 2e38], [math.inf, 3e38, -2e38], [1e30, -1e30]):
+            g = gen(seed)
+            bias = 0.1 * torch.randn(E, generator=g, device="cuda")
+            at = torch.rand(E, generator=g, device="cuda") < some
+            which = torch.randint(0, len(sizes), (E,), generator=g, device="cuda")
+            bias = torch.where(at, torch.tensor(sizes, device="cuda")[which], bias)
+            check_route(x, min(6, group_k * per), score, bias, groups, group_k, group_top)
+
+
 # --------------------------------------------------------------- experts --
 
 def one_to_one(dt):
