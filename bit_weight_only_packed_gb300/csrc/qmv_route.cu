@@ -107,8 +107,12 @@ __device__ __forceinline__ F score_error(int score, F largest) {
   return sizeof(F) == 8 ? (F)0 : score == QMV_SCORE_SIGMOID ? (F)0x1p-21 : (F)0x1p-18 * largest;
 }
 
-template <typename F>
-__device__ __forceinline__ F sigmoid(F x) { return over((F)1, (F)1 + exp_of(-x)); }
+__device__ __forceinline__ float sigmoid(float x) { return over(1.0f, 1.0f + exp_of(-x)); }
+// (e^-x is infinite below -709, where the score is still a number)
+__device__ __forceinline__ double sigmoid(double x) {
+  const double e = exp_of(-fabs(x));
+  return (x < 0.0 ? e : 1.0) / (1.0 + e);
+}
 
 // Scores of a lane's N experts.  x: logits, those that cannot be chosen -inf.  Returns the largest logit,
 // and in *whole the sum of exp(x - that) (softmax).

@@ -145,6 +145,18 @@ def test_route_biases_of_any_size(groups, per, group_k, group_top, score):
             check_route(x, min(6, group_k * per), score, bias, groups, group_k, group_top)
 
 
+@pytest.mark.parametrize("groups,group_k,group_top", [(1, 1, 1), (4, 2, 2)])
+@pytest.mark.parametrize("T", [4, 12, 33])
+def test_route_scores_near_the_smallest_numbers(T, groups, group_k, group_top):
+    # sigmoid scores from e^-690 to e^-744, which a bias of 0 leaves as they are
+    q = qmv()
+    E = 128
+    x = -690 - torch.rand(60, E, generator=gen(T), device="cuda").mul(27).round() * 2
+    bias = torch.zeros(E, device="cuda")
+    ids, _ = q.qmv_route(x, T, score=1, bias=bias, groups=groups, group_k=group_k, group_top=group_top)
+    assert torch.equal(ids, route_ref(x, T, 1, bias, groups, group_k, group_top, False, 1.0)[0])
+
+
 # --------------------------------------------------------------- experts --
 
 def one_to_one(dt):
