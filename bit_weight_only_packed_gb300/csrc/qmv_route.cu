@@ -370,8 +370,8 @@ __device__ __forceinline__ float exp_below(float v, float top) {
 }
 
 // Weights over their sum where that is small: each relative to the largest of them, so that scores below
-// the smallest fp32 number keep their shares (a score that fp32 holds to 2^-150 is off by
-// 2^-126 of a sum of 2^-24).  v: logits of a lane's two picks, -inf where there is none.
+// the smallest fp32 number keep their shares (an exponential, a quotient and their sum below 2^-126 are
+// off by 2^-148 in all, which is 2^-128 of a sum of 2^-20).  v: logits of a lane's two picks, -inf where there is none.
 __device__ __noinline__ float2 small_shares(const RouteArgs& a, float v0, float v1, float top, bool sigmoids) {
   const float m = warp_max(fmaxf(v0, v1));
   const auto share_of = [&](float v) { return v == -CUDART_INF_F ? 0.0f : exp_below(v, m) / (sigmoids ? 1.0f + expf(v) : 1.0f); };
@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(WARPS * 32, N <= 8 ? 10 : 4) route_kernel(Rout
   float f = a.scale;
   if (a.renorm) {
     const float sum = warp_total(w[0] + w[1]);
-    if (sum >= 0x1p-24f) {
+    if (sum >= 0x1p-20f) {
       f = a.scale / sum;
     } else {
       const float2 v = small_shares(a, id[0] >= 0 ? of[0] : none, id[1] >= 0 ? of[1] : none, top, a.score == QMV_SCORE_SIGMOID);

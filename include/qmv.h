@@ -655,7 +655,7 @@ QMV_API int qmv_qk_norm_rope(int M, int n_q, int n_k, int D, const void *qkv, in
  * by their logits, which is the order of exact scores also where those of 64 bits are equal: of
  * sigmoid logits 40 and 41, both scores 1 there, 41 comes first, with a bias of 0 the lower
  * index.  The sums of two that groups count are of 64-bit scores, with a bias or without.
- * Weights are fp32, within 2^-20 of themselves.
+ * Weights are fp32, within 2^-20 of themselves, or 2^-126 of scale.
  * An expert whose logit or bias is NaN or -inf is never chosen (nor counted in a
  * group, as -inf: with group_top 2 a group of one expert alone counts as -inf); places
  * that are left over hold id -1 and weight 0.  Logits of +inf share a softmax evenly.

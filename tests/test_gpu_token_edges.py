@@ -50,6 +50,19 @@ def test_route_weights_of_small_scores(level, scale, T):
     check_shares(y, T, 1, bias, True, scale)
 
 
+@pytest.mark.parametrize("level", [-12.2, -14.9, -16.4])
+@pytest.mark.parametrize("score", [0, 1])
+def test_route_small_weights_beside_a_small_sum(level, score):
+    # shares that are numbers, of scores that are not quite: e^-80 and less of a sum of about 2^-20 or 2^-24
+    x = level - 80 - 8 * torch.rand(400, 28, generator=gen(3), device="cuda")
+    x[:, 5] = level - 0.1 * torch.rand(400, generator=gen(4), device="cuda")
+    x[:, 23:] = -0.3 * torch.rand(400, 5, generator=gen(5), device="cuda")
+    bias = torch.ones(28, device="cuda") + 0.1 * torch.rand(28, generator=gen(9), device="cuda")
+    bias[23:] = -5.0
+    for scale in (1.0, 1e-3):
+        check_shares(x, 20, score, bias, True, scale)
+
+
 @pytest.mark.parametrize("T", [8, 40])
 @pytest.mark.parametrize("renorm", [False, True])
 def test_route_weights_far_below_the_largest(renorm, T):
