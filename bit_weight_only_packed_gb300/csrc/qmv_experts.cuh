@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(X_NT, 1)
     const auto place = [&](int w) { return reinterpret_cast<float*>(smem + P.part_off + (size_t)w * (P.cols * ROWS * 4)); };
     // column m and row `row` of the segment; what a lane needs of a column comes from global memory once
     const auto emit = [&](int row, int pair, float scale, float v) {
-      v *= scale;
+      v = v * 2097152.0f * scale;          // one after the other: their product may be infinite where v's is not
       if (!(fabsf(v) <= 3.402823466e38f)) v = plain_product(a, pair, task.expert * a.R + s0 * ROWS + row);
       if (abort_flag) return;
       if (P.part)
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(X_NT, 1)
         store_y(a.y, (int64_t)pair * a.ldy + s0 * ROWS + row, a.y_dtype, v);
     };
     const auto pair_of = [&](int m) { return order_of(task.first + m); };
-    const auto scale_of = [&](int pair) { return a.x_bf16 ? 2097152.0f * pow2_f(-P.exps[a.per_pair ? pair : pair / a.T]) : 2097152.0f; };
+    const auto scale_of = [&](int pair) { return a.x_bf16 ? pow2_f(-P.exps[a.per_pair ? pair : pair / a.T]) : 1.0f; };
     int my_pair[2] = {0, 0};               // of the columns 2 t and 2 t + 1, whose sums this lane has
     float my_scale[2] = {0.0f, 0.0f};
 #pragma unroll

@@ -274,3 +274,21 @@ def test_experts_take_no_more_memory_than_their_form(form, monkeypatch):
         taken = torch.cuda.max_memory_allocated() - before - y.numel() * 4
         assert taken <= most + 2048, (dt, taken, most)         # rounded up to 256 and 512 bytes a region and an allocation
         del y, x
+
+
+@pytest.mark.parametrize("M,T", [(3, 2), (100, 2)])
+def test_experts_of_the_largest_x(M, T):
+    # bf16 rows from 2^121 on, whose products are numbers again
+    q = qmv()
+    E, R, K, group = 4, 64, 512, 64
+    p, _, w = make_w4(E * R, K, group, True, BF16, 5)
+    ids = distinct(M, T, E, 2)
+    x = (randn(3, M, K) * 2.0 ** torch.linspace(115, 125, M, device="cuda")[:, None]).to(BF16)
+    y = q.qmv_w4_experts(p, R, ids, x)
+    u, wr = x.double(), w.view(E, R, K)
+    ref, A = torch.einsum("mk,erk->mer", u, wr), torch.einsum("mk,erk->mer", u.abs(), wr.abs())
+    pick = ids.long()[:, :, None].expand(M, T, R)
+    # the products' fp32 sums, as for x of any size (test_experts_general)
+    tol = (A.gather(1, pick) + u.abs().sum(1)[:, None, None] * 30 * 0.02) * (17 * 8 + K // group + 32) * 2.0 ** -23
+    assert float((ref.abs().gather(1, pick) + tol).max()) < 3.4e38      # numbers of fp32, to the last bit of what they may be off
+    assert bool(((y.double() - ref.gather(1, pick)).abs() <= tol).all()), y[~torch.isfinite(y)].numel()
