@@ -7,14 +7,15 @@
 //   few    (a small top-k, or a row that is short anyway): the k largest come out of a few more candidates,
 //          those that reach a bound which k logits reach for certain; one CTA sorts them and finishes the
 //          row.  No weight of the other ids is formed.
-//   many   (top-p alone, or a large k): the ids are counted by weight in bins of 2^(1/256), which bound the sum
-//          above any bin to 0.3 %; in the bins that may hold the cut, about a thousand ids of 262144, one CTA
-//          sorts for the place.  Where ties make them more, a search by halves over their logits finds it.
+//   many   (top-p alone, or a large k): the ids are counted by weight in bins, 256 even steps an octave, whose edges
+//          differ by 1/256 to 1/512 of a weight and so bound the sum above any bin (weights below 2^8 units, whose
+//          bins are narrower than a unit, only from above); in the bins that may hold the cut, about a thousand ids of
+//          262144, one CTA sorts for the place.  Where ties make them more, a search by halves over their logits finds it.
 //   none   (no cut, or after it): every CTA sums what stays, and the one whose part the threshold falls into
 //          finds the id.
 //
 // A row of 262144 with top-k 64 and top-p 0.95 takes 13 us, a latency: the row is read twice, the cluster meets
-// three times, 1.5 us are the sorts.  128 rows of them with top-p 0.9 alone take 185 us (134 MB, 20 us from HBM):
+// three times, 1.5 us are the sorts.  128 rows of them with top-p 0.9 alone take 189 us (134 MB, 20 us from HBM):
 // 28 the largest logits, 50 each of the two passes that form the weights, by their instructions (some 40 a weight
 // and its bin), the rest the meetings and sorts of CTAs that run two to a multiprocessor.
 #include <math_constants.h>

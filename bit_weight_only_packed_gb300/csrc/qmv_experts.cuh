@@ -119,7 +119,8 @@ __device__ __forceinline__ void sort_own(const ExpertsArgs& a, int cols, int* he
   }
 }
 
-// A product by its definition, for results that are not finite.
+// A product by its definition, for results that are not finite: a lane a product, all of K.  (64 tokens of 8 experts,
+// 2048 x 2048: 64 us, with NaN in one token's row 7.5 ms, in every row 21 ms.)
 static __device__ __noinline__ float plain_product(const ExpertsArgs& a, int pair, int n) {
   const uint16_t* x = (const uint16_t*)a.x + (int64_t)(a.per_pair ? pair : pair / a.T) * a.ldx;
   const int KB = cdiv(a.K, BK), bb = block_bytes(a.group, a.zeros != 0), gpb = BK / a.group;

@@ -993,7 +993,8 @@ def qmv_w4_experts(p: W4Pack, rows_per_expert, ids, x, weights=None, act=QMV_ACT
     """Products of the experts ids int32 [M, T] with x: y [M, T, R], or summed by weights fp32
     [M, T] y [M, R].  x is [M, K], or [M, T, K] for a row a pair; with act its rows
     are gate and up, 2 K wide.  workspace: one for every form of call (qmv_w4_experts_workspace);
-    without it the call takes fresh scratch for its own form, which is often none."""
+    without it the call takes fresh scratch for its own form, which is often none.  Repeated
+    calls give the same bits; among other tokens a token's sums may be rounded in another way."""
     if y is None and stream is None:
         r = _host.w4_experts(p._address, p._dev, p.K, rows_per_expert, ids, x, weights, act, y_dtype, workspace)
         if r is not None:

@@ -625,7 +625,8 @@ QMV_API int qmv_rope_turns(int n, const double *inv_freq, int64_t *turns);
  *   pairs (a, b) of the first rot elements become amplitude * (a cos t - b sin t,
  *   b cos t + a sin t), t = position * frequency; the others stay u.
  * QMV_ROPE_HALF pairs element i with i + rot / 2, QMV_ROPE_INTERLEAVED 2 i with 2 i + 1.
- * Steps are fp32 with one rounding to dtype; cosines and sines are within 2^-21.
+ * Steps are fp32 with one rounding to dtype; cosines and sines are within 2^-21.  (So the squares of a
+ * normed head have to stay below 2^128: with values from 2^64 / sqrt(D) on it becomes 0.)
  *   qkv        device [M][(n_q + n_k) * D, at least] of x_dtype (QMV_F32, QMV_F16 or QMV_BF16),
  *              row stride ld.
  *   positions  device int32 [M] (negative ones turn back); NULL exactly when rot is 0.
@@ -682,8 +683,10 @@ QMV_API int qmv_route(int M, int E, int T, const void *logits, int ldl, int dtyp
  * x_dtype, as an activation of its own would leave it: QMV_ACT_SILU g / (1 + exp(-g)),
  * QMV_ACT_GELU g / 2 * (1 + tanh(sqrt(2 / pi) * (g + 0.044715 g^3))).
  * Exact products, fp32 sums in a fixed order, one rounding to y's type; x in bf16 as in
- * qmv_w4_gemv.  Repeated calls give the same bits.  Infinities and NaN of x act as the
- * definition has them, in their own row.
+ * qmv_w4_gemv.  Repeated calls give the same bits; among other tokens a token's fp32 sums may be
+ * split, and so rounded, in another way.  Infinities and NaN of x act as the definition has
+ * them, in their own row; products that are not finite are formed one by one, which takes some
+ * hundred times as long.
  *   rows_per_expert  divides the pack's N and is a multiple of 32.
  *   ids      device int32 [M][T]; may come from the kernel just before.  An id outside [0, E)
  *            has the product 0; but for -1 it sets the device error word (8).
