@@ -268,11 +268,12 @@ def test_experts_take_no_more_memory_than_their_form(form, monkeypatch):
     for dt, weights, most in ((F16, None, order), (BF16, None, order + M * (2 * K + 4)), (F16, w, order + M * T * R * 4)):
         x = randn(1, M, K).to(dt)
         torch.cuda.synchronize()
-        before = torch.cuda.memory_allocated()
+        # what was asked for: a block that is handed out may be up to 1 MB larger, since less is not split off
         torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_stats()["requested_bytes.all.current"]
         y = q.qmv_w4_experts(p, R, ids, x, weights=weights)
-        taken = torch.cuda.max_memory_allocated() - before - y.numel() * 4
-        assert taken <= most + 2048, (dt, taken, most)         # rounded up to 256 and 512 bytes a region and an allocation
+        taken = torch.cuda.memory_stats()["requested_bytes.all.peak"] - before - y.numel() * 4
+        assert taken <= most + 1280, (dt, taken, most)         # five regions, each rounded up to 256 bytes
         del y, x
 
 
